@@ -1,0 +1,379 @@
+"""Python binding of ``include/selective_scan.h``: the selective scan, the
+short convolution in front of it, and the 8-bit cache of states.
+
+Argument marshalling only, as in the rest of the package: tensors are checked
+for device, dtype and shape, outputs and workspaces are allocated with torch,
+and the library's kernels run on torch's current stream of the inputs' device.
+Activations may be slices of wider rows (their last dimension adjacent);
+parameters and states are contiguous.  Each call has a workspace of its own
+from torch's allocator, so calls on several streams and captured graphs share
+none.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+_i64, _i32, _vp, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_CACHE_CODE = {torch.int8: 3, torch.float8_e4m3fn: 4}
+
+
+class _ScanInputs(ctypes.Structure):
+    """``selective_scan_inputs``."""
+    _fields_ = ([(n, _i64) for n in ("batch", "seqlen", "channels", "dstate", "ngroups")]
+                + [("dtype", _i32), ("softplus", _i32)]
+                + [(n, _vp) for n in ("u", "dt", "z", "B", "C", "A", "D", "dt_bias", "h0", "seqlens")]
+                + [(n, _i64) for n in ("u_batch", "u_token", "dt_batch", "dt_token", "z_batch", "z_token",
+                                       "B_batch", "B_token", "B_group", "C_batch", "C_token", "C_group")])
+
+
+class _ScanGrads(ctypes.Structure):
+    """``selective_scan_grads``."""
+    _fields_ = ([("dy", _vp), ("dy_batch", _i64), ("dy_token", _i64)]
+                + [(n, _vp) for n in ("dh_final", "checkpoints", "du", "ddt", "dz", "dB", "dC", "dA", "dD",
+                                      "ddt_bias", "dh0")])
+
+
+class _ConvInputs(ctypes.Structure):
+    """``short_conv_inputs``."""
+    _fields_ = ([(n, _i64) for n in ("batch", "seqlen", "channels", "width")]
+                + [("dtype", _i32), ("silu", _i32), ("x", _vp), ("x_batch", _i64), ("x_token", _i64)]
+                + [(n, _vp) for n in ("weight", "bias", "initial_state", "seqlens")])
+
+
+def declare(lib: ctypes.CDLL) -> None:
+    """Sets the argument types of this header's functions."""
+    ps, pg, pc = (ctypes.POINTER(s) for s in (_ScanInputs, _ScanGrads, _ConvInputs))
+    for name, args, res in (
+            ("selective_scan_workspace_size", [_i64] * 5, _sz),
+            ("selective_scan_bwd_workspace_size", [_i64] * 5, _sz),
+            ("selective_scan_checkpoint_size", [_i64] * 4, _sz),
+            ("selective_scan_fwd", [ps, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+            ("selective_scan_bwd", [ps, pg, _vp, _sz, _vp], ctypes.c_int),
+            ("selective_scan_step", [ps, _vp, _vp, _vp], ctypes.c_int),
+            ("short_conv_fwd", [pc, _vp, _vp, _vp], ctypes.c_int),
+            ("short_conv_bwd_workspace_size", [_i64] * 4, _sz),
+            ("short_conv_bwd", [pc, _vp, _i64, _i64] + [_vp] * 6 + [_sz, _vp], ctypes.c_int),
+            ("short_conv_step", [pc, _vp, _vp, _vp], ctypes.c_int),
+            ("state_cache_write", [_vp, _vp] + [_i64] * 4 + [ctypes.c_int, _vp, _vp, _vp], ctypes.c_int),
+            ("state_cache_read", [_vp, _vp, _vp] + [_i64] * 4 + [ctypes.c_int, _vp, _vp], ctypes.c_int)):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, res
+
+
+def _lib():
+    from . import load_library
+    return load_library()
+
+
+def _ok(status: int, what: str) -> None:
+    if status != 0:
+        from . import SSDError
+        raise SSDError(status, what)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on(device):
+    """Makes the inputs' device the current one for the launches."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _check(name, t, device, dtype, shape, strided=False):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be on one GPU with the other tensors (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if strided:
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}'s last dimension must be adjacent in memory")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _activation(name, t, dims):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _CODE:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16")
+    if t.dim() != len(dims):
+        raise ValueError(f"{name} must be [{', '.join(dims)}]")
+    _check(name, t, t.device, t.dtype, t.shape, strided=True)
+
+
+def _seqlens(t, device, batch):
+    if t is not None:
+        _check("seqlens", t, device, torch.int32, (batch,))
+
+
+# ---------------------------------------------------------------------------
+# selective scan
+# ---------------------------------------------------------------------------
+def _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus, step=False) -> _ScanInputs:
+    _activation("u", u, ("batch", "channels") if step else ("batch", "seqlen", "channels"))
+    dev, kind, lead, ch = u.device, u.dtype, u.shape[:-1], u.shape[-1]
+    _check("dt", dt, dev, kind, u.shape, strided=True)
+    if z is not None:
+        _check("z", z, dev, kind, u.shape, strided=True)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be [channels, dstate]")
+    N = A.shape[1]
+    _check("A", A, dev, torch.float32, (ch, N))
+    if not isinstance(B, torch.Tensor) or B.dim() != len(lead) + 2:
+        raise ValueError("B must be [batch, ngroups, dstate]" if step else "B must be [batch, seqlen, ngroups, dstate]")
+    G = B.shape[-2]
+    _check("B", B, dev, kind, (*lead, G, N), strided=True)
+    _check("C", C, dev, kind, (*lead, G, N), strided=True)
+    if D is not None:
+        _check("D", D, dev, torch.float32, (ch,))
+    if dt_bias is not None:
+        _check("dt_bias", dt_bias, dev, torch.float32, (ch,))
+    if h0 is not None:
+        _check("h0", h0, dev, torch.float32, (lead[0], ch, N))
+    _seqlens(seqlens, dev, lead[0])
+    sz = u if z is None else z
+    tok = (lambda t: 0) if step else (lambda t: t.stride(1))
+    return _ScanInputs(lead[0], 1 if step else lead[1], ch, N, G, _CODE[kind], 1 if dt_softplus else 0,
+                       _at(u), _at(dt), _at(z), _at(B), _at(C), _at(A), _at(D), _at(dt_bias), _at(h0), _at(seqlens),
+                       u.stride(0), tok(u), dt.stride(0), tok(dt), sz.stride(0), tok(sz),
+                       B.stride(0), tok(B), B.stride(-2), C.stride(0), tok(C), C.stride(-2))
+
+
+def _tiles(lib, s):
+    return lib.selective_scan_checkpoint_size(s.batch, s.seqlen, s.channels, s.dstate) // (
+        4 * s.batch * s.channels * s.dstate)
+
+
+def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, seqlens=None, dt_softplus: bool = True,
+                   want_final_state: bool = True, want_checkpoints: bool = False, out: torch.Tensor | None = None):
+    """Selective scan over whole sequences.  With dt' = softplus(dt + dt_bias):
+
+        h_t = exp(dt'_t A) h_{t-1} + dt'_t B_t u_t,   y_t = (C_t . h_t + D u_t) silu(z_t)
+
+    for each channel, with a decay for each of its states.  u, dt and z
+    (optional) [Bt, L, channels] and B, C [Bt, L, groups, N] in fp32, bf16 or
+    fp16 (one dtype; slices of wider rows are fine); A [channels, N], D and
+    dt_bias [channels] and h0 [Bt, channels, N] in fp32 (the last three
+    optional); N is at most 64.  seqlens (int32 [Bt], on the GPU): tokens at
+    or past a sequence's length are padding; their y is zero.
+
+    Returns (y, h_final or None), and with want_checkpoints
+    (y, h_final or None, checkpoints), where checkpoints is what
+    ``selective_scan_bwd`` takes."""
+    lib = _lib()
+    s = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus)
+    dev = u.device
+    y = torch.empty(u.shape, dtype=u.dtype, device=dev) if out is None else out
+    _check("out", y, dev, u.dtype, u.shape)
+    hf = torch.empty((s.batch, s.channels, s.dstate), dtype=torch.float32, device=dev) if want_final_state else None
+    kept = None
+    if want_checkpoints:
+        kept = torch.empty((s.batch, _tiles(lib, s), s.dstate, s.channels), dtype=torch.float32, device=dev)
+    need = lib.selective_scan_workspace_size(s.batch, s.seqlen, s.channels, s.dstate, s.ngroups)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    with _on(dev):
+        _ok(lib.selective_scan_fwd(ctypes.byref(s), _at(y), _at(hf), _at(kept), _at(ws), need, _stream(dev)),
+            "selective_scan")
+    return (y, hf, kept) if want_checkpoints else (y, hf)
+
+
+def selective_scan_bwd(dy, u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, seqlens=None,
+                       dt_softplus: bool = True, checkpoints: torch.Tensor | None = None, dh_final=None) -> dict:
+    """Gradients of ``selective_scan``'s inputs from the gradient dy of its y
+    (and dh_final of its h_final), with the checkpoints of the forward pass
+    over the same inputs.  Returns a dict of "du", "ddt", "dB", "dC" (and
+    "dz") in u's dtype and "dA" (and "dD", "ddt_bias", "dh0") in fp32; those
+    in parentheses where the input was given.  dB and dC are summed over the
+    channels of a group.  Padding has zero gradients."""
+    lib = _lib()
+    s = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus)
+    dev, f32 = u.device, torch.float32
+    _check("dy", dy, dev, u.dtype, u.shape, strided=True)
+    state = (s.batch, s.channels, s.dstate)
+    if checkpoints is None:
+        raise ValueError("checkpoints: run selective_scan with want_checkpoints=True")
+    _check("checkpoints", checkpoints, dev, f32, (s.batch, _tiles(lib, s), s.dstate, s.channels))
+    if dh_final is not None:
+        _check("dh_final", dh_final, dev, f32, state)
+    like = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+    got = {"du": like(u.shape, u.dtype), "ddt": like(u.shape, u.dtype), "dA": like(A.shape, f32),
+           "dB": like(B.shape, u.dtype), "dC": like(C.shape, u.dtype)}
+    if D is not None:
+        got["dD"] = like(D.shape, f32)
+    if z is not None:
+        got["dz"] = like(u.shape, u.dtype)
+    if dt_bias is not None:
+        got["ddt_bias"] = like(dt_bias.shape, f32)
+    if h0 is not None:
+        got["dh0"] = like(state, f32)
+    g = _ScanGrads(_at(dy), dy.stride(0), dy.stride(1), _at(dh_final), _at(checkpoints),
+                   *(_at(got.get(k)) for k in ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0")))
+    need = lib.selective_scan_bwd_workspace_size(s.batch, s.seqlen, s.channels, s.dstate, s.ngroups)
+    ws = like((max(need, 16),), torch.uint8)
+    with _on(dev):
+        _ok(lib.selective_scan_bwd(ctypes.byref(s), ctypes.byref(g), _at(ws), ws.numel(), _stream(dev)),
+            "selective_scan_bwd")
+    return got
+
+
+def selective_scan_step(h, u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = True,
+                        out: torch.Tensor | None = None):
+    """One token of ``selective_scan`` for every sequence: updates the state h
+    [Bt, channels, N] (fp32) in place and returns y [Bt, channels].  u, dt and
+    z [Bt, channels], B and C [Bt, groups, N]; the rest as there."""
+    lib = _lib()
+    s = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, None, None, dt_softplus, step=True)
+    _check("h", h, u.device, torch.float32, (s.batch, s.channels, s.dstate))
+    y = torch.empty(u.shape, dtype=u.dtype, device=u.device) if out is None else out
+    _check("out", y, u.device, u.dtype, u.shape)
+    with _on(u.device):
+        _ok(lib.selective_scan_step(ctypes.byref(s), _at(h), _at(y), _stream(u.device)), "selective_scan_step")
+    return y
+
+
+# ---------------------------------------------------------------------------
+# short convolution
+# ---------------------------------------------------------------------------
+def _conv_inputs(x, weight, bias, initial_state, seqlens, silu, step=False) -> _ConvInputs:
+    _activation("x", x, ("batch", "channels") if step else ("batch", "seqlen", "channels"))
+    dev, ch, n = x.device, x.shape[-1], x.shape[0]
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [channels, width]")
+    W = weight.shape[1]
+    _check("weight", weight, dev, torch.float32, (ch, W))
+    if bias is not None:
+        _check("bias", bias, dev, torch.float32, (ch,))
+    if initial_state is not None:
+        _check("initial_state", initial_state, dev, x.dtype, (n, W - 1, ch))
+    _seqlens(seqlens, dev, n)
+    return _ConvInputs(n, 1 if step else x.shape[1], ch, W, _CODE[x.dtype], 1 if silu else 0, _at(x), x.stride(0),
+                       0 if step else x.stride(1), _at(weight), _at(bias), _at(initial_state), _at(seqlens))
+
+
+def short_conv(x, weight, bias=None, initial_state=None, seqlens=None, silu: bool = True,
+               want_final_state: bool = True, out: torch.Tensor | None = None):
+    """Causal convolution of each channel over its last `width` tokens, with
+    the activation silu (or none): x [Bt, L, channels] in fp32, bf16 or fp16
+    (slices of wider rows are fine), weight [channels, width] with width 2 to
+    4 and bias [channels] in fp32.  initial_state [Bt, width - 1, channels]
+    holds the inputs before the first token (oldest first; zeros without), and
+    the final state the last ones.  seqlens as in ``selective_scan``.  Returns
+    (y, final_state or None)."""
+    lib = _lib()
+    s = _conv_inputs(x, weight, bias, initial_state, seqlens, silu)
+    dev = x.device
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    _check("out", y, dev, x.dtype, x.shape)
+    last = torch.empty((s.batch, s.width - 1, s.channels), dtype=x.dtype, device=dev) if want_final_state else None
+    with _on(dev):
+        _ok(lib.short_conv_fwd(ctypes.byref(s), _at(y), _at(last), _stream(dev)), "short_conv")
+    return y, last
+
+
+def short_conv_bwd(dy, x, weight, bias=None, initial_state=None, seqlens=None, silu: bool = True,
+                   dfinal_state=None) -> dict:
+    """Gradients of ``short_conv``'s inputs from the gradient dy of its y (and
+    dfinal_state of its final state): a dict of "dx" in x's dtype, "dweight"
+    in fp32, and "dbias" (fp32) and "dinitial_state" where those were given."""
+    lib = _lib()
+    s = _conv_inputs(x, weight, bias, initial_state, seqlens, silu)
+    dev = x.device
+    _check("dy", dy, dev, x.dtype, x.shape, strided=True)
+    if dfinal_state is not None:
+        _check("dfinal_state", dfinal_state, dev, x.dtype, (s.batch, s.width - 1, s.channels))
+    got = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev), "dweight": torch.empty_like(weight)}
+    if bias is not None:
+        got["dbias"] = torch.empty_like(bias)
+    if initial_state is not None:
+        got["dinitial_state"] = torch.empty_like(initial_state)
+    need = lib.short_conv_bwd_workspace_size(s.batch, s.seqlen, s.channels, s.width)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        _ok(lib.short_conv_bwd(ctypes.byref(s), _at(dy), dy.stride(0), dy.stride(1), _at(dfinal_state), _at(got["dx"]),
+                               _at(got["dweight"]), _at(got.get("dbias")), _at(got.get("dinitial_state")), _at(ws),
+                               ws.numel(), _stream(dev)), "short_conv_bwd")
+    return got
+
+
+def short_conv_step(state, x, weight, bias=None, silu: bool = True, out: torch.Tensor | None = None):
+    """One token of ``short_conv`` for every sequence: state
+    [Bt, width - 1, channels] (x's dtype) takes x [Bt, channels] in and drops
+    its oldest row, in place; returns y [Bt, channels]."""
+    lib = _lib()
+    s = _conv_inputs(x, weight, bias, None, None, silu, step=True)
+    _check("state", state, x.device, x.dtype, (s.batch, s.width - 1, s.channels))
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    _check("out", y, x.device, x.dtype, x.shape)
+    with _on(x.device):
+        _ok(lib.short_conv_step(ctypes.byref(s), _at(state), _at(y), _stream(x.device)), "short_conv_step")
+    return y
+
+
+# ---------------------------------------------------------------------------
+# 8-bit cache of states
+# ---------------------------------------------------------------------------
+def _cache_args(cache, scales, slots):
+    if not isinstance(cache, torch.Tensor) or cache.dtype not in _CACHE_CODE:
+        raise TypeError("cache must be int8 or float8_e4m3fn")
+    if cache.dim() < 2:
+        raise ValueError("cache must be [slots, ..., dstate]")
+    dev = cache.device
+    _check("cache", cache, dev, cache.dtype, cache.shape)
+    _check("scales", scales, dev, torch.float32, cache.shape[:-1])
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be [batch]")
+    _check("slots", slots, dev, torch.int32, slots.shape)
+    rows = 1
+    for n in cache.shape[1:-1]:
+        rows *= n
+    return dev, (slots.shape[0], rows, cache.shape[-1], cache.shape[0], _CACHE_CODE[cache.dtype])
+
+
+def state_cache_write(h, cache, scales, slots) -> None:
+    """Keeps the states h [Bt, ..., dstate] (fp32: a final state of
+    ``ssd_fwd`` or ``selective_scan``, or the state of a step) in 8 bits, state
+    i in slot slots[i] (int32 [Bt], on the GPU) of cache [slots, ..., dstate]
+    (int8 or float8_e4m3fn), with a scale for each row of dstate values in
+    scales [slots, ...] (fp32).  A state whose slot is out of range is not
+    written; of several that name one slot the last is."""
+    lib = _lib()
+    dev, sizes = _cache_args(cache, scales, slots)
+    _check("h", h, dev, torch.float32, (sizes[0], *cache.shape[1:]))
+    with _on(dev):
+        _ok(lib.state_cache_write(_at(h), _at(slots), *sizes, _at(cache), _at(scales), _stream(dev)),
+            "state_cache_write")
+
+
+def state_cache_read(cache, scales, slots, out: torch.Tensor | None = None):
+    """The states in the given slots of a cache that ``state_cache_write``
+    filled, as fp32 [Bt, ..., dstate]: the h0 of ``ssd_fwd`` or
+    ``selective_scan``, or the state of a step.  A slot out of range gives a
+    state of zeros."""
+    lib = _lib()
+    dev, sizes = _cache_args(cache, scales, slots)
+    shape = (sizes[0], *cache.shape[1:])
+    h = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else out
+    _check("out", h, dev, torch.float32, shape)
+    with _on(dev):
+        _ok(lib.state_cache_read(_at(cache), _at(scales), _at(slots), *sizes, _at(h), _stream(dev)),
+            "state_cache_read")
+    return h
+
+
+__all__ = ["selective_scan", "selective_scan_bwd", "selective_scan_step", "short_conv", "short_conv_bwd",
+           "short_conv_step", "state_cache_write", "state_cache_read"]
