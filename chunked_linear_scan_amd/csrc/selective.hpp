@@ -39,9 +39,8 @@ __device__ __forceinline__ float softplus(float x) {
     const float e = fexp(-fabsf(x));
     const float w = 1.0f + e;
     const float d = w - 1.0f;
-    const float l = __builtin_amdgcn_logf(w) * kLn2 * e * __builtin_amdgcn_rcpf(d);
-    const float r = fmaxf(x, 0.0f) + (d == 0.0f ? e : l);
-    return x != x ? x : r;  // the maximum drops a NaN
+    const float l = __builtin_amdgcn_logf(w) * kLn2 * (e * __builtin_amdgcn_rcpf(d));
+    return fmaxf(x, 0.0f) + (d == 0.0f ? e : l);  // the maximum drops a NaN, the other term does not
 }
 
 // d silu(x) / dx with s = sigmoid(x)

@@ -50,7 +50,7 @@ int scan_sizes(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
 ScanCut scan_cut(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
     const int64_t tile = cls::scan_tile(N);
     const int64_t waves = batch * G * ceil_div(ch / G, cls::kScanCh) * cls::scan_waves(N);
-    int64_t nseg = waves >= 1024 ? 1 : ceil_div(2048, waves);
+    int64_t nseg = waves >= 1024 ? 1 : ceil_div(8192, waves);
     if (nseg > cls::kScanMaxSegs) nseg = cls::kScanMaxSegs;
     int64_t len = ceil_div(ceil_div(L, nseg), tile) * tile;
     if (len < 4 * tile) len = 4 * tile;
@@ -80,6 +80,8 @@ int scan_check(const selective_scan_inputs* in) {
     const int64_t strides[] = {in->u_batch, in->u_token, in->dt_batch, in->dt_token, in->z_batch, in->z_token,
                                in->B_batch, in->B_token, in->B_group, in->C_batch, in->C_token, in->C_group};
     if (!strides_ok(strides, 12)) return SSD_ERR_SHAPE;
+    for (int64_t s : {in->u_token, in->dt_token, in->z_token, in->B_token, in->C_token})
+        if (s > cls::kScanMaxTokenStride) return SSD_ERR_SHAPE;
     for (const void* p : {in->u, in->dt, in->z, in->B, in->C})
         if (!aligned(p, elem_size(in->dtype))) return SSD_ERR_ALIGN;
     for (const float* p : {in->A, in->D, in->dt_bias, in->h0})
@@ -187,7 +189,7 @@ int selective_scan_bwd(const selective_scan_inputs* in, const selective_scan_gra
         (in->z && !g->dz))
         return SSD_ERR_NULL;
     const int64_t strides[] = {g->dy_batch, g->dy_token};
-    if (!strides_ok(strides, 2)) return SSD_ERR_SHAPE;
+    if (!strides_ok(strides, 2) || g->dy_token > cls::kScanMaxTokenStride) return SSD_ERR_SHAPE;
     for (const void* p : {g->dy, static_cast<const void*>(g->du), static_cast<const void*>(g->ddt),
                           static_cast<const void*>(g->dz), static_cast<const void*>(g->dB), static_cast<const void*>(g->dC)})
         if (!aligned(p, elem_size(in->dtype))) return SSD_ERR_ALIGN;

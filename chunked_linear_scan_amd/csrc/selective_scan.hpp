@@ -10,6 +10,8 @@
 // (y) crosses waves, through LDS, once per tile of tokens.
 #pragma once
 
+#include <utility>
+
 #include "selective.hpp"
 
 namespace cls {
@@ -17,6 +19,7 @@ namespace cls {
 constexpr int kScanCh = 64;       // channels of a workgroup
 constexpr int kScanMaxStates = 64;
 constexpr int kScanMaxSegs = 64;
+constexpr int64_t kScanMaxTokenStride = int64_t(1) << 26;  // a tile's rows stay within 32-bit offsets
 
 // Tokens per tile, and between checkpoints: the backward pass holds a tile's
 // states and decays in registers, and its partial sums in LDS.
@@ -54,6 +57,130 @@ struct ScanParams {
     float* part_bc;  // [blocks of the group][batch][L][G][2][N]: dB and dC of one channel block
     float* part_a;   // [batch * nseg][N + 2][ch]: dA, then dD, then ddt_bias
 };
+
+// An element at a wave-uniform pointer and a lane's byte offset.
+template <typename T>
+__device__ __forceinline__ const T& at_bytes(const T* p, uint32_t bytes) {
+    return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + bytes);
+}
+template <typename T>
+__device__ __forceinline__ T& at_bytes(T* p, uint32_t bytes) {
+    return *reinterpret_cast<T*>(reinterpret_cast<char*>(p) + bytes);
+}
+
+// Where a workgroup works.
+struct ScanPlace {
+    int64_t b;
+    int g, seg, ch;
+    bool on;              // the lane has a channel; one past its group computes the group's last, unseen
+    int64_t first, stop;  // the segment's tokens
+    int64_t last;         // the end of those that count
+};
+
+__device__ __forceinline__ ScanPlace scan_place(const ScanParams& p, int seg0 = 0) {
+    ScanPlace a;
+    const uint32_t blocks = uint32_t(p.bpg) * uint32_t(p.G);
+    const uint32_t row = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+    a.g = int(blk / uint32_t(p.bpg));
+    a.b = row % uint32_t(p.batch);
+    a.seg = int(row / uint32_t(p.batch)) + seg0;
+    const int c = int(blk % uint32_t(p.bpg)) * kScanCh + int(threadIdx.x & 63);
+    a.on = c < p.cpg;
+    a.ch = a.g * p.cpg + (a.on ? c : p.cpg - 1);
+    const int end = seq_end(p.seqlens, a.b, p.L);
+    a.first = int64_t(a.seg) * p.seg_len;
+    a.stop = a.first + p.seg_len < p.L ? a.first + p.seg_len : p.L;
+    a.last = a.stop < end ? a.stop : end;
+    return a;
+}
+
+// The rows of B or C of a tile for one wave: lane l holds token l / 4 (of up
+// to 16) and state n0 + l % 4, which is how a 4x4x1 matrix instruction takes
+// the 4 rows of its A operand, block by block; see outer() and dot().
+template <typename E, int TT>
+struct ScanRows {
+    typedef typename E::raw raw;
+    const raw* at;    // the tile to be loaded, the same for all lanes
+    int stride, row;  // of a token; the lane's token
+    uint32_t off;     // the lane's byte offset
+    bool on;
+    raw r;
+
+    __device__ __forceinline__ ScanRows(const void* v, const ScanStride& s, int64_t b, int g, int64_t first, int n0, int N,
+                                        int lane) {
+        at = static_cast<const raw*>(v) + b * s.b + g * s.g + first * s.t;
+        stride = int(s.t);
+        row = (lane >> 2) & (TT - 1);
+        const int n = n0 + (lane & 3);
+        on = n < N;
+        off = uint32_t(row * stride + (on ? n : 0)) * uint32_t(sizeof(raw));
+    }
+    // Loads the tile; rem: the last of its rows that may be read (below 0: before the tile).
+    __device__ __forceinline__ void load(int rem) {
+        if (rem >= TT - 1) r = at_bytes(at, off);
+        else r = *(&at_bytes(at, off) - int64_t(row > rem ? row - rem : 0) * stride);
+    }
+    __device__ __forceinline__ float get() const { return on ? E::get(r) : 0.0f; }
+};
+
+// rows: as ScanRows gives them.  c[k] + value(T, k) v for the wave's four states k, where v is the lane's own: the
+// matrix instruction multiplies 16 blocks of 4 rows by 4 columns (the lanes), with the rows of block T in all blocks.
+template <int T>
+__device__ __forceinline__ f32x4 outer(float rows, float v, f32x4 c = f32x4{0.f, 0.f, 0.f, 0.f}) {
+    return __builtin_amdgcn_mfma_f32_4x4x1f32(rows, v, c, 4, T, 0);
+}
+
+// The same rows as operands of vector instructions: register r holds, in each
+// row of 16 lanes, tokens 4 r to 4 r + 3, and the instruction that uses one of
+// its values broadcasts it within the row as it reads it (a DPP operand).
+template <typename E, int TT>
+struct ScanQuads {
+    typedef typename E::raw raw;
+    const raw* at;
+    int stride, row;
+    uint32_t off;
+    bool on;
+    raw r[TT / 4];
+
+    __device__ __forceinline__ ScanQuads(const void* v, const ScanStride& s, int64_t b, int g, int64_t first, int n0,
+                                         int N, int lane) {
+        at = static_cast<const raw*>(v) + b * s.b + g * s.g + first * s.t;
+        stride = int(s.t);
+        row = (lane >> 2) & 3;
+        const int n = n0 + (lane & 3);
+        on = n < N;
+        off = uint32_t(row * stride + (on ? n : 0)) * uint32_t(sizeof(raw));
+    }
+    __device__ __forceinline__ void load(int rem) {
+#pragma unroll
+        for (int i = 0; i < TT / 4; ++i) {
+            const raw* q = at + 4 * i * stride;
+            if (rem >= TT - 1) r[i] = at_bytes(q, off);
+            else r[i] = *(&at_bytes(q, off) - int64_t(4 * i + row > rem ? 4 * i + row - rem : 0) * stride);
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[TT / 4]) const {
+#pragma unroll
+        for (int i = 0; i < TT / 4; ++i) f[i] = on ? E::get(r[i]) : 0.0f;
+    }
+};
+
+// sum_k value(T, k) v[k].  The compiler does not fold a DPP operand into a
+// multiply-add, hence the instructions themselves; s_nop: a DPP operand may be
+// read no sooner than two wait states after a vector instruction wrote it.
+template <int T>
+__device__ __forceinline__ float dot(const float* rows, const float (&v)[4]) {
+    constexpr int I = (T & 3) * 4;
+    float y;
+    asm("s_nop 1\n\t"
+        "v_mul_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+        : "=&v"(y)
+        : "v"(rows[T >> 2]), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "n"(I), "n"(I + 1), "n"(I + 2), "n"(I + 3));
+    return y;
+}
 
 // The segments that a sequence is cut into, and their length in tokens (a
 // multiple of the tile).

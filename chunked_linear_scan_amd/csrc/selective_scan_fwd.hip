@@ -8,35 +8,22 @@ namespace {
 
 // AGG: a segment's own contribution only (state from zero, summed steps).
 template <typename E, int NW, bool AGG>
-__global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanParams p) {
-    constexpr int K = kScanK, NP = NW * K;
+__global__ __launch_bounds__(NW * 64, 4) void scan_fwd_kernel(ScanParams p) {
+    constexpr int K = kScanK;
     constexpr int TT = NW > 8 ? 8 : 16;
     constexpr int R = TT >= NW ? TT / NW : 1;  // token rows that a wave stages and finishes
     typedef typename E::raw raw;
     __shared__ float2 s_d[TT][kScanCh];        // dt', dt' u
-    __shared__ float s_bc[2][TT][NP];
-    __shared__ float s_y[AGG ? 1 : NW][AGG ? 1 : TT][kScanCh];
+    __shared__ float s_y[NW][AGG ? 1 : TT][kScanCh];  // each wave's share of the sum over the states
 
+    const ScanPlace at = scan_place(p);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t wg = blockIdx.x;
-    const int cb = int(wg % p.bpg); wg /= p.bpg;
-    const int g = int(wg % p.G); wg /= p.G;
-    const int64_t b = wg % p.batch;
-    const int seg = int(wg / p.batch);
-    const int c = cb * kScanCh + lane;
-    const bool on = c < p.cpg;
-    const int ch = g * p.cpg + (on ? c : p.cpg - 1);  // lanes past the group compute its last channel, unseen
-    const int L_end = seq_end(p.seqlens, b, p.L);
-    const int64_t first = int64_t(seg) * p.seg_len;
-    const int64_t stop = first + p.seg_len < p.L ? first + p.seg_len : p.L;   // of the segment
-    const int64_t last = stop < L_end ? stop : L_end;                         // of its tokens that count
-
-    const raw* u = static_cast<const raw*>(p.u) + b * p.su.b + ch;
-    const raw* dt = static_cast<const raw*>(p.dt) + b * p.sdt.b + ch;
-    const raw* z = p.z ? static_cast<const raw*>(p.z) + b * p.sz.b + ch : nullptr;
-    const raw* B = static_cast<const raw*>(p.B) + b * p.sB.b + g * p.sB.g;
-    const raw* C = static_cast<const raw*>(p.C) + b * p.sC.b + g * p.sC.g;
+    const int64_t b = at.b;
+    const bool on = at.on;
+    const uint32_t ch = uint32_t(at.ch);
+    const int seg = at.seg;
+    const int64_t first = at.first, last = at.last;
     const float bias = p.dt_bias ? p.dt_bias[ch] : 0.0f;
     const float Dc = p.D ? p.D[ch] : 0.0f;
 
@@ -64,22 +51,39 @@ __global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanParams p) {
     }
     float sum_dt = 0.0f;
 
+    // rows of the tile to come, from wave-uniform pointers that step from tile to tile
+    const raw* u = static_cast<const raw*>(p.u) + b * p.su.b + first * p.su.t;
+    const raw* dt = static_cast<const raw*>(p.dt) + b * p.sdt.b + first * p.sdt.t;
+    const raw* z = p.z ? static_cast<const raw*>(p.z) + b * p.sz.b + first * p.sz.t : nullptr;
+    ScanRows<E, TT> B(p.B, p.sB, b, at.g, first, n0, p.N, lane);
+    ScanQuads<E, TT> C(p.C, p.sC, b, at.g, first, n0, p.N, lane);
+    const uint32_t lane_off = ch * uint32_t(sizeof(raw));
+    const int u_t = int(p.su.t), dt_t = int(p.sdt.t), z_t = int(p.sz.t);
     raw ru[R], rdt[R], rz[R];
     auto load = [&](int64_t t0) {
+        // past the end: the last token that counts, whose values are read and not used
+        const int rem = int(last - 1 - t0 < TT ? last - 1 - t0 : TT);
+        B.load(rem);
+        if (!AGG) C.load(rem);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int row = wave + r * NW;
-            const int64_t t = t0 + row;
-            ru[r] = rdt[r] = rz[r] = 0;
-            if (row < TT && t < last) {
-                ru[r] = u[t * p.su.t];
-                rdt[r] = dt[t * p.sdt.t];
-                if (!AGG && z) rz[r] = z[t * p.sz.t];
-            }
+            const int row = wave + r * NW < rem ? wave + r * NW : rem;
+            ru[r] = at_bytes(u + row * u_t, lane_off);
+            rdt[r] = at_bytes(dt + row * dt_t, lane_off);
+            rz[r] = 0;
+            if (!AGG && z) rz[r] = at_bytes(z + row * z_t, lane_off);
         }
+        u += TT * int64_t(u_t);
+        dt += TT * int64_t(dt_t);
+        if (!AGG && z) z += TT * int64_t(z_t);
+        B.at += TT * int64_t(B.stride);
+        C.at += TT * int64_t(C.stride);
     };
-    load(first);
+    raw* y = AGG ? nullptr : static_cast<raw*>(p.y) + (b * p.L + first) * p.ch;
+    float* ckpt = AGG || !p.ckpt ? nullptr : p.ckpt + ((b * ((p.L + TT - 1) / TT) + first / TT) * p.N + n0) * p.ch;
+    if (last > first) load(first);
     for (int64_t t0 = first; t0 < last; t0 += TT) {
+        const int nt = int(last - t0 < TT ? last - t0 : TT);
         float uc[R], zc[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -88,70 +92,68 @@ __global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanParams p) {
             zc[r] = E::get(rz[r]);
             float d = E::get(rdt[r]) + bias;
             if (p.softplus) d = softplus(d);
-            if (t0 + row >= last) d = 0.0f;  // no step
-            if (row < TT) s_d[row][lane] = make_float2(d, d * uc[r]);
+            float du = d * uc[r];
+            if (row >= nt) d = du = 0.0f;  // no step
+            if (AGG && row < TT) sum_dt += d;
+            if (row < TT) s_d[row][lane] = make_float2(d, du);
         }
-        for (int i = threadIdx.x; i < 2 * TT * NP; i += NW * 64) {
-            const int n = i % NP, row = (i / NP) % TT, w = i / (NP * TT);
-            float v = 0.0f;
-            if (n < p.N && t0 + row < last && !(AGG && w))
-                v = E::get(w ? C[(t0 + row) * p.sC.t + n] : B[(t0 + row) * p.sB.t + n]);
-            s_bc[w][row][n] = v;
-        }
+        const float fB = B.get();
+        float fC[TT / 4];
+        if (!AGG) C.get(fC);
         load(t0 + TT);
         __syncthreads();
-        if constexpr (!AGG) {
-            if (p.ckpt && on) {
-                const int64_t tiles = (p.L + TT - 1) / TT;
+        if (!AGG && ckpt) {
+            if (on) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (n0 + k < p.N) p.ckpt[((b * tiles + t0 / TT) * p.N + n0 + k) * p.ch + ch] = h[k];
+                    if (n0 + k < p.N) at_bytes(ckpt + k * p.ch, ch * 4) = h[k];
             }
+            ckpt += int64_t(p.N) * p.ch;
         }
+        [&]<int... T>(std::integer_sequence<int, T...>) {
+            (
+                [&] {
+                    const float2 d = s_d[T][lane];
+                    const f32x4 b4 = outer<T>(fB, d.y);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const float2 d = s_d[t][lane];
-            const f32x4 bv = *reinterpret_cast<const f32x4*>(&s_bc[0][t][n0]);
-            float yv = 0.0f;
-            if constexpr (AGG) {
-                sum_dt += d.x;
-#pragma unroll
-                for (int k = 0; k < K; ++k) h[k] = fmaf(fexp2(d.x * A2[k]), h[k], d.y * bv[k]);
-            } else {
-                const f32x4 cv = *reinterpret_cast<const f32x4*>(&s_bc[1][t][n0]);
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    h[k] = fmaf(fexp2(d.x * A2[k]), h[k], d.y * bv[k]);
-                    yv = fmaf(cv[k], h[k], yv);
-                }
-                s_y[wave][t][lane] = yv;
-            }
-        }
+                    for (int k = 0; k < K; ++k) h[k] = fmaf(fexp2(d.x * A2[k]), h[k], b4[k]);
+                    if constexpr (!AGG) s_y[wave][T][lane] = dot<T>(fC, h);
+                }(),
+                ...);
+        }(std::make_integer_sequence<int, TT>{});
         __syncthreads();
         if constexpr (!AGG) {
-            raw* y = static_cast<raw*>(p.y) + b * p.L * p.ch + ch;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int row = wave + r * NW;
-                if (row >= TT || t0 + row >= last || !on) continue;
+                if (row >= nt) continue;
                 float v = Dc * uc[r];
 #pragma unroll
                 for (int w = 0; w < NW; ++w) v += s_y[w][row][lane];
-                if (z) v *= zc[r] * sigmoid(zc[r]);
-                y[(t0 + row) * p.ch] = E::put(v);
+                if (p.z) v *= zc[r] * sigmoid(zc[r]);
+                if (on) at_bytes(y + int64_t(row) * p.ch, lane_off) = E::put(v);
             }
+            y += int64_t(TT) * p.ch;
         }
     }
-    if (!on) return;
     if constexpr (AGG) {
+        s_y[wave][0][lane] = sum_dt;
+        __syncthreads();
+        if (!on) return;
         const int64_t sb = int64_t(seg) * p.batch + b;
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (n0 + k < p.N) p.seg_h[(sb * p.N + n0 + k) * p.ch + ch] = h[k];
-        if (wave == 0) p.seg_dt[sb * p.ch + ch] = sum_dt;
+        if (wave == 0) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) s += s_y[w][0][lane];
+            p.seg_dt[sb * p.ch + ch] = s;
+        }
     } else {
-        raw* y = static_cast<raw*>(p.y) + b * p.L * p.ch + ch;
-        for (int64_t t = (last > first ? last : first) + wave; t < stop; t += NW) y[t * p.ch] = E::put(0.0f);
+        if (!on) return;
+        y = static_cast<raw*>(p.y) + b * p.L * p.ch;
+        for (int64_t t = (last > first ? last : first) + wave; t < at.stop; t += NW) (y + t * p.ch)[ch] = E::put(0.0f);
         if (p.h_last && seg == p.nseg - 1) {
 #pragma unroll
             for (int k = 0; k < K; ++k)

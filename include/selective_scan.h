@@ -11,7 +11,8 @@
  *   - workspaces need no initial contents and keep nothing from call to call;
  *     calls that may overlap need a workspace each;
  *   - activations may be slices of wider rows: each has a batch and a token
- *     stride (in elements), its channels are adjacent;
+ *     stride (in elements, >= 0; the scan's token strides up to 2^26), its
+ *     channels are adjacent;
  *   - pointers are aligned to their element (16-bit: 2 bytes, fp32: 4 bytes),
  *     not to 16 bytes; workspaces and checkpoints to 16 bytes.
  * No kernel uses atomics: results are the same from run to run.
