@@ -48,12 +48,12 @@ int scan_sizes(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
 // Where the channels and states alone give the device too few waves, each
 // sequence is cut into segments.
 ScanCut scan_cut(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
-    const int64_t tile = cls::scan_tile(N);
+    const int64_t tile = cls::kScanTile;
     const int64_t waves = batch * G * ceil_div(ch / G, cls::kScanCh) * cls::scan_waves(N);
     int64_t nseg = waves >= 1024 ? 1 : ceil_div(8192, waves);
     if (nseg > cls::kScanMaxSegs) nseg = cls::kScanMaxSegs;
     int64_t len = ceil_div(ceil_div(L, nseg), tile) * tile;
-    if (len < 4 * tile) len = 4 * tile;
+    if (len < 8 * tile) len = 8 * tile;
     return ScanCut{ceil_div(L, len), len};
 }
 
@@ -159,7 +159,7 @@ size_t selective_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t 
 
 size_t selective_scan_checkpoint_size(int64_t batch, int64_t seqlen, int64_t channels, int64_t dstate) {
     if (scan_sizes(batch, seqlen, channels, dstate, 1) != SSD_OK) return 0;
-    return size_t(batch * ceil_div(seqlen, cls::scan_tile(dstate))) * size_t(dstate * channels) * 4;
+    return size_t(batch * ceil_div(seqlen, cls::kScanTile)) * size_t(dstate * channels) * 4;
 }
 
 int selective_scan_fwd(const selective_scan_inputs* in, void* y, float* h_final, void* checkpoints, void* workspace,

@@ -23,7 +23,7 @@ constexpr int64_t kScanMaxTokenStride = int64_t(1) << 26;  // a tile's rows stay
 
 // Tokens per tile, and between checkpoints: the backward pass holds a tile's
 // states and decays in registers, and its partial sums in LDS.
-inline __host__ __device__ constexpr int scan_tile(int64_t N) { return N > 32 ? 8 : 16; }
+constexpr int kScanTile = 8;
 // waves of a workgroup at 4 states each
 inline __host__ __device__ constexpr int scan_waves(int64_t N) {
     return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16;
@@ -180,6 +180,40 @@ __device__ __forceinline__ float dot(const float* rows, const float (&v)[4]) {
         : "=&v"(y)
         : "v"(rows[T >> 2]), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "n"(I), "n"(I + 1), "n"(I + 2), "n"(I + 3));
     return y;
+}
+
+// Folds segment s's contribution into v: exp(A sum dt') v + its own, for the wave's states.
+struct ScanFold {
+    float sd, own[kScanK];
+    __device__ __forceinline__ void load(const ScanParams& p, int s, int64_t b, int ch, int n0) {
+        const int64_t sb = int64_t(s) * p.batch + b;
+        sd = p.seg_dt[sb * p.ch + ch];
+#pragma unroll
+        for (int k = 0; k < kScanK; ++k) own[k] = n0 + k < p.N ? p.seg_h[(sb * p.N + n0 + k) * p.ch + ch] : 0.0f;
+    }
+    template <typename V>
+    __device__ __forceinline__ void apply(const float (&A2)[kScanK], V& v) const {
+#pragma unroll
+        for (int k = 0; k < kScanK; ++k) {
+            const float x = v[k];
+            v[k] = fmaf(fexp2(A2[k] * sd), x, own[k]);
+        }
+    }
+};
+
+// Segments from, from + step, ... (n of them), four at a time so that their loads are in flight together.
+template <typename V>
+__device__ __forceinline__ void scan_fold(const ScanParams& p, int from, int step, int n, int64_t b, int ch, int n0,
+                                          const float (&A2)[kScanK], V& v) {
+    for (int i = 0; i < n; i += 4) {
+        ScanFold f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < n) f[j].load(p, from + step * (i + j), b, ch, n0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < n) f[j].apply(A2, v);
+    }
 }
 
 // The segments that a sequence is cut into, and their length in tokens (a

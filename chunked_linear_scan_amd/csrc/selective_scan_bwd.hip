@@ -26,44 +26,32 @@ __device__ __forceinline__ float dpp_add(bool bit, float lo, float hi) {
     return (bit ? hi : lo) + dpp<CTRL>(bit ? lo : hi);
 }
 
+// AGG: what a segment alone hands back to the tokens before it (and its summed
+// steps), from no gradient behind it.
 template <typename E, int NW, bool AGG>
-__global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : 2) void scan_bwd_kernel(ScanParams p) {
-    constexpr int K = kScanK, NP = NW * K;
-    constexpr int TT = NW > 8 ? 8 : 16;
+__global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_kernel(ScanParams p) {
+    constexpr int K = kScanK;
+    constexpr int TT = kScanTile;
     constexpr int R = TT >= NW ? TT / NW : 1;
     typedef typename E::raw raw;
     __shared__ float2 s_d[TT][kScanCh];   // dt', dt' u
     __shared__ float s_dy[TT][kScanCh];   // the gradient of y before the gate
-    __shared__ float s_bc[2][TT][NP];
-    __shared__ float s_p[AGG ? 1 : NW][3][AGG ? 1 : TT][kScanCh];  // each wave's share of three sums over the states
+    __shared__ float s_p[NW][3][AGG ? 1 : TT][kScanCh];  // each wave's share of three sums over the states
 
+    const ScanPlace at = scan_place(p, AGG ? 1 : 0);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t wg = blockIdx.x;
-    const int cb = int(wg % p.bpg); wg /= p.bpg;
-    const int g = int(wg % p.G); wg /= p.G;
-    const int64_t b = wg % p.batch;
-    const int seg = int(wg / p.batch) + (AGG ? 1 : 0);
-    const int c = cb * kScanCh + lane;
-    const bool on = c < p.cpg;
-    const int ch = g * p.cpg + (on ? c : p.cpg - 1);
-    const int L_end = seq_end(p.seqlens, b, p.L);
-    const int64_t first = int64_t(seg) * p.seg_len;
-    const int64_t stop = first + p.seg_len < p.L ? first + p.seg_len : p.L;
-    const int64_t last = stop < L_end ? stop : L_end;
-    const int64_t tiles = (p.L + TT - 1) / TT;
-
-    const raw* u = static_cast<const raw*>(p.u) + b * p.su.b + ch;
-    const raw* dt = static_cast<const raw*>(p.dt) + b * p.sdt.b + ch;
-    const raw* z = p.z ? static_cast<const raw*>(p.z) + b * p.sz.b + ch : nullptr;
-    const raw* dy = static_cast<const raw*>(p.dy) + b * p.sdy.b + ch;
-    const raw* B = static_cast<const raw*>(p.B) + b * p.sB.b + g * p.sB.g;
-    const raw* C = static_cast<const raw*>(p.C) + b * p.sC.b + g * p.sC.g;
+    const int64_t b = at.b;
+    const bool on = at.on;
+    const uint32_t ch = uint32_t(at.ch), lane_off = ch * uint32_t(sizeof(raw));
+    const int seg = at.seg;
+    const int64_t first = at.first, last = at.last;
     const float bias = p.dt_bias ? p.dt_bias[ch] : 0.0f;
     const float Dc = p.D ? p.D[ch] : 0.0f;
 
     const int n0 = wave * K;
-    float A2[K], carry[K], dA[K];  // carry: the gradient that reaches the state from later tokens
+    float A2[K], dA[K];
+    f32x4 carry;  // the gradient that reaches the state from later tokens
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int n = n0 + k;
@@ -76,40 +64,66 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : 2) void scan_bwd_kernel(ScanP
             for (int k = 0; k < K; ++k)
                 if (n0 + k < p.N) carry[k] = p.dh_last[(b * p.ch + ch) * p.N + n0 + k];
         }
-        for (int s = p.nseg - 1; s > seg; --s) {
-            const int64_t sb = int64_t(s) * p.batch + b;
-            const float sd = p.seg_dt[sb * p.ch + ch];
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (n0 + k < p.N)
-                    carry[k] = fmaf(fexp2(A2[k] * sd), carry[k], p.seg_h[(sb * p.N + n0 + k) * p.ch + ch]);
-        }
+        scan_fold(p, p.nseg - 1, -1, p.nseg - 1 - seg, b, at.ch, n0, A2, carry);
     }
     float sum_dt = 0.0f, dD = 0.0f, dbias = 0.0f;
 
+    // the tiles from the last one back, from wave-uniform pointers that step with them
+    const int64_t tiles = last > first ? (last - first + TT - 1) / TT : 0;
+    const int64_t top = first + (tiles - 1) * TT;
+    const raw* u = static_cast<const raw*>(p.u) + b * p.su.b + top * p.su.t;
+    const raw* dt = static_cast<const raw*>(p.dt) + b * p.sdt.b + top * p.sdt.t;
+    const raw* z = p.z ? static_cast<const raw*>(p.z) + b * p.sz.b + top * p.sz.t : nullptr;
+    const raw* dy = static_cast<const raw*>(p.dy) + b * p.sdy.b + top * p.sdy.t;
+    ScanRows<E, TT> B(p.B, p.sB, b, at.g, top, n0, p.N, lane), C(p.C, p.sC, b, at.g, top, n0, p.N, lane);
+    ScanQuads<E, TT> Bq(p.B, p.sB, b, at.g, top, n0, p.N, lane), Cq(p.C, p.sC, b, at.g, top, n0, p.N, lane);
+    const int u_t = int(p.su.t), dt_t = int(p.sdt.t), z_t = int(p.sz.t), dy_t = int(p.sdy.t);
     raw ru[R], rdt[R], rz[R], rdy[R];
-    float hin[K];
+    // Loads the tile at t0 and steps back; before the segment there is none.
     auto load = [&](int64_t t0) {
+        if (t0 < first) return;
+        const int rem = int(last - 1 - t0 < TT ? last - 1 - t0 : TT);
+        C.load(rem);
+        if (!AGG) {
+            B.load(rem);
+            Bq.load(rem);
+            if (z) Cq.load(rem);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int row = wave + r * NW;
-            const int64_t t = t0 + row;
-            ru[r] = rdt[r] = rz[r] = rdy[r] = 0;
-            if (row < TT && t >= first && t < last) {
-                ru[r] = u[t * p.su.t];
-                rdt[r] = dt[t * p.sdt.t];
-                rdy[r] = dy[t * p.sdy.t];
-                if (z) rz[r] = z[t * p.sz.t];
-            }
+            const int row = wave + r * NW < rem ? wave + r * NW : rem;
+            ru[r] = at_bytes(u + row * u_t, lane_off);
+            rdt[r] = at_bytes(dt + row * dt_t, lane_off);
+            rdy[r] = at_bytes(dy + row * dy_t, lane_off);
+            rz[r] = 0;
+            if (z) rz[r] = at_bytes(z + row * z_t, lane_off);
         }
+        u -= TT * int64_t(u_t);
+        dt -= TT * int64_t(dt_t);
+        dy -= TT * int64_t(dy_t);
+        if (z) z -= TT * int64_t(z_t);
+        B.at -= TT * int64_t(B.stride);
+        C.at -= TT * int64_t(C.stride);
+        Bq.at -= TT * int64_t(B.stride);
+        Cq.at -= TT * int64_t(C.stride);
     };
-    const int64_t top = last > first ? (last - 1) / TT * TT : first - TT;
-    load(top);
+    const int64_t out0 = (b * p.L + top) * p.ch;
+    raw* du = static_cast<raw*>(p.du) + out0;
+    raw* ddt = static_cast<raw*>(p.ddt) + out0;
+    raw* dz = static_cast<raw*>(p.dz) + out0;
+    const float* ckpt = p.ckpt + ((b * ((p.L + TT - 1) / TT) + top / TT) * p.N + n0) * p.ch;
+    // the sums over the lanes of dB and dC end up in the lane (B or C, state, token of eight)
+    const int sum_n = n0 + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1), sum_t = lane & 7;
+    float* part = p.part_bc + ((((int64_t(blockIdx.x) % p.bpg * p.batch + b) * p.L + top + sum_t) * p.G + at.g) * 2 +
+                               (lane >> 5)) * p.N + sum_n;
+    const int64_t part_t = int64_t(p.G) * 2 * p.N;
+    if (tiles > 0) load(top);
     for (int64_t t0 = top; t0 >= first; t0 -= TT) {
+        const int nt = int(last - t0 < TT ? last - t0 : TT);
+        float hin[K];
         if constexpr (!AGG) {
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                hin[k] = n0 + k < p.N ? p.ckpt[((b * tiles + t0 / TT) * p.N + n0 + k) * p.ch + ch] : 0.0f;
+            for (int k = 0; k < K; ++k) hin[k] = n0 + k < p.N ? at_bytes(ckpt + k * p.ch, ch * 4) : 0.0f;
         }
         float uc[R], zc[R], xc[R], dc[R], oc[R], gc[R];
 #pragma unroll
@@ -120,158 +134,154 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : 2) void scan_bwd_kernel(ScanP
             oc[r] = E::get(rdy[r]);
             xc[r] = E::get(rdt[r]) + bias;
             dc[r] = p.softplus ? softplus(xc[r]) : xc[r];
-            if (t0 + row >= last) dc[r] = 0.0f;
             gc[r] = z ? oc[r] * zc[r] * sigmoid(zc[r]) : oc[r];
+            float d = dc[r], s = dc[r] * uc[r], gy = gc[r];
+            if (row >= nt) d = 0.0f;
+            if (row >= nt || !on) s = gy = 0.0f;  // nothing of a lane without a channel in the sums over the lanes
+            if (AGG && row < TT) sum_dt += d;
             if (row < TT) {
-                s_d[row][lane] = make_float2(dc[r], dc[r] * uc[r]);
-                s_dy[row][lane] = gc[r];
+                s_d[row][lane] = make_float2(d, s);
+                s_dy[row][lane] = gy;
             }
         }
-        for (int i = threadIdx.x; i < 2 * TT * NP; i += NW * 64) {
-            const int n = i % NP, row = (i / NP) % TT, w = i / (NP * TT);
-            float v = 0.0f;
-            if (n < p.N && t0 + row < last && !(AGG && !w))
-                v = E::get(w ? C[(t0 + row) * p.sC.t + n] : B[(t0 + row) * p.sB.t + n]);
-            s_bc[w][row][n] = v;
+        const float fC = C.get(), fB = AGG ? 0.0f : B.get();
+        float qB[TT / 4], qC[TT / 4];
+        if (!AGG) {
+            Bq.get(qB);
+            if (z) Cq.get(qC);
         }
         load(t0 - TT);
         __syncthreads();
         if constexpr (AGG) {
+            [&]<int... T>(std::integer_sequence<int, T...>) {
+                (
+                    [&] {
+                        constexpr int t = TT - 1 - T;
+                        const float d = s_d[t][lane].x;
+                        const f32x4 q = outer<t>(fC, s_dy[t][lane], carry);
 #pragma unroll
-            for (int t = TT - 1; t >= 0; --t) {
-                const float d = s_d[t][lane].x, gy = s_dy[t][lane];
-                const f32x4 cv = *reinterpret_cast<const f32x4*>(&s_bc[1][t][n0]);
-                sum_dt += d;
-#pragma unroll
-                for (int k = 0; k < K; ++k) carry[k] = fexp2(d * A2[k]) * fmaf(gy, cv[k], carry[k]);
-            }
+                        for (int k = 0; k < K; ++k) carry[k] = fexp2(d * A2[k]) * q[k];
+                    }(),
+                    ...);
+            }(std::make_integer_sequence<int, TT>{});
             __syncthreads();
         } else {
             float a[TT][K], hs[TT][K];
+            [&]<int... T>(std::integer_sequence<int, T...>) {
+                (
+                    [&] {
+                        const float2 d = s_d[T][lane];
+                        const f32x4 b4 = outer<T>(fB, d.y);
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const float2 d = s_d[t][lane];
-                const f32x4 bv = *reinterpret_cast<const f32x4*>(&s_bc[0][t][n0]);
-                float yv = 0.0f;
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    a[t][k] = fexp2(d.x * A2[k]);
-                    hs[t][k] = fmaf(a[t][k], t ? hs[t - 1][k] : hin[k], d.y * bv[k]);
-                }
-                if (z) {
-                    const f32x4 cv = *reinterpret_cast<const f32x4*>(&s_bc[1][t][n0]);
-#pragma unroll
-                    for (int k = 0; k < K; ++k) yv = fmaf(cv[k], hs[t][k], yv);
-                    s_p[wave][2][t][lane] = yv;
-                }
-            }
+                        for (int k = 0; k < K; ++k) {
+                            a[T][k] = fexp2(d.x * A2[k]);
+                            hs[T][k] = fmaf(a[T][k], T ? hs[T ? T - 1 : 0][k] : hin[k], b4[k]);
+                        }
+                        if (z) s_p[wave][2][T][lane] = dot<T>(qC, hs[T]);
+                    }(),
+                    ...);
+            }(std::make_integer_sequence<int, TT>{});
             const bool bit3 = lane & 8, bit2 = lane & 4, bit1 = lane & 2, bit0 = lane & 1;
+            float r8[8];
+            [&]<int... I>(std::integer_sequence<int, I...>) {
+                (
+                    [&] {
+                        constexpr int t = TT - 1 - I, i = t & 7;
+                        const float2 d = s_d[t][lane];
+                        const float gy = s_dy[t][lane];
+                        const f32x4 q4 = outer<t>(fC, gy, carry);
+                        float q[K], vB[K], vC[K], to_dt = 0.0f;
 #pragma unroll
-            for (int o = TT / 8 - 1; o >= 0; --o) {
-                float r8[8];
-#pragma unroll
-                for (int i = 7; i >= 0; --i) {
-                    const int t = o * 8 + i;
-                    const float2 d = s_d[t][lane];
-                    const float gy = s_dy[t][lane];
-                    const f32x4 bv = *reinterpret_cast<const f32x4*>(&s_bc[0][t][n0]);
-                    const f32x4 cv = *reinterpret_cast<const f32x4*>(&s_bc[1][t][n0]);
-                    float vB[K], vC[K], to_sig = 0.0f, to_dt = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        const float q = fmaf(gy, cv[k], carry[k]);
-                        carry[k] = q * a[t][k];
-                        const float qah = carry[k] * (t ? hs[t - 1][k] : hin[k]);
-                        dA[k] = fmaf(qah, d.x, dA[k]);
-                        to_dt = fmaf(qah, A2[k], to_dt);
-                        to_sig = fmaf(q, bv[k], to_sig);
-                        vB[k] = on ? q * d.y : 0.0f;
-                        vC[k] = on ? gy * hs[t][k] : 0.0f;
-                    }
-                    s_p[wave][0][t][lane] = to_sig;
-                    s_p[wave][1][t][lane] = to_dt;
-                    const float w0 = swap_add32(vB[0], vC[0]), w1 = swap_add32(vB[1], vC[1]);
-                    const float w2 = swap_add32(vB[2], vC[2]), w3 = swap_add32(vB[3], vC[3]);
-                    r8[i] = dpp_add<0x128>(bit3, swap_add16(w0, w2), swap_add16(w1, w3));
-                }
-                // the eight tokens' sums over the last three lane bits: half-row mirror, then within four lanes
-                const float x0 = dpp_add<0x141>(bit2, r8[0], r8[4]), x1 = dpp_add<0x141>(bit2, r8[1], r8[5]);
-                const float x2 = dpp_add<0x141>(bit2, r8[2], r8[6]), x3 = dpp_add<0x141>(bit2, r8[3], r8[7]);
-                const float y0 = dpp_add<0x4e>(bit1, x0, x2), y1 = dpp_add<0x4e>(bit1, x1, x3);
-                const float sum = dpp_add<0xb1>(bit0, y0, y1);
-                const int64_t t = t0 + o * 8 + (lane & 7);
-                const int n = n0 + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
-                if (t < last && n < p.N)
-                    p.part_bc[((((int64_t(cb) * p.batch + b) * p.L + t) * p.G + g) * 2 + (lane >> 5)) * p.N + n] = sum;
-            }
+                        for (int k = 0; k < K; ++k) {
+                            q[k] = q4[k];
+                            const float qa = q[k] * a[t][k];
+                            carry[k] = qa;
+                            const float qah = qa * (t ? hs[t ? t - 1 : 0][k] : hin[k]);
+                            dA[k] = fmaf(qah, d.x, dA[k]);
+                            to_dt = fmaf(qah, A2[k], to_dt);
+                            vB[k] = q[k] * d.y;
+                            vC[k] = gy * hs[t][k];
+                        }
+                        s_p[wave][0][t][lane] = dot<t>(qB, q);
+                        s_p[wave][1][t][lane] = to_dt;
+                        const float w0 = swap_add32(vB[0], vC[0]), w1 = swap_add32(vB[1], vC[1]);
+                        const float w2 = swap_add32(vB[2], vC[2]), w3 = swap_add32(vB[3], vC[3]);
+                        r8[i] = dpp_add<0x128>(bit3, swap_add16(w0, w2), swap_add16(w1, w3));
+                        if constexpr (i == 0) {
+                            // eight tokens' sums over the last three lane bits: half-row mirror, then within four lanes
+                            const float x0 = dpp_add<0x141>(bit2, r8[0], r8[4]), x1 = dpp_add<0x141>(bit2, r8[1], r8[5]);
+                            const float x2 = dpp_add<0x141>(bit2, r8[2], r8[6]), x3 = dpp_add<0x141>(bit2, r8[3], r8[7]);
+                            const float y0 = dpp_add<0x4e>(bit1, x0, x2), y1 = dpp_add<0x4e>(bit1, x1, x3);
+                            const float sum = dpp_add<0xb1>(bit0, y0, y1);
+                            if (t + sum_t < nt && sum_n < p.N) part[t * part_t] = sum;
+                        }
+                    }(),
+                    ...);
+            }(std::make_integer_sequence<int, TT>{});
+            part -= TT * part_t;
             __syncthreads();
-            raw* du = static_cast<raw*>(p.du) + b * p.L * p.ch + ch;
-            raw* ddt = static_cast<raw*>(p.ddt) + b * p.L * p.ch + ch;
-            raw* dz = static_cast<raw*>(p.dz) + b * p.L * p.ch + ch;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int row = wave + r * NW;
-                if (row >= TT || t0 + row >= last || !on) continue;
-                float to_sig = 0.0f, to_dt = 0.0f;
+                if (row >= nt) continue;
+                float to_sig = 0.0f, to_dt = 0.0f, y = Dc * uc[r];
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
                     to_sig += s_p[w][0][row][lane];
                     to_dt += s_p[w][1][row][lane];
+                    if (p.z) y += s_p[w][2][row][lane];
                 }
-                const int64_t at = (t0 + row) * p.ch;
-                du[at] = E::put(fmaf(Dc, gc[r], dc[r] * to_sig));
                 float d = fmaf(uc[r], to_sig, to_dt * kLn2);  // A2 is A log2(e)
                 if (p.softplus) d *= sigmoid(xc[r]);
-                ddt[at] = E::put(d);
                 dbias += d;
                 dD = fmaf(gc[r], uc[r], dD);
-                if (z) {
-                    float y = Dc * uc[r];
-#pragma unroll
-                    for (int w = 0; w < NW; ++w) y += s_p[w][2][row][lane];
-                    dz[at] = E::put(oc[r] * y * dsilu(zc[r], sigmoid(zc[r])));
-                }
+                if (!on) continue;
+                const int64_t o = int64_t(row) * p.ch;
+                at_bytes(du + o, lane_off) = E::put(fmaf(Dc, gc[r], dc[r] * to_sig));
+                at_bytes(ddt + o, lane_off) = E::put(d);
+                if (p.z) at_bytes(dz + o, lane_off) = E::put(oc[r] * y * dsilu(zc[r], sigmoid(zc[r])));
             }
+            du -= int64_t(TT) * p.ch;
+            ddt -= int64_t(TT) * p.ch;
+            dz -= int64_t(TT) * p.ch;
+            ckpt -= int64_t(p.N) * p.ch;
         }
     }
+    __syncthreads();
+    s_p[wave][0][0][lane] = AGG ? sum_dt : dD;
+    s_p[wave][1][0][lane] = dbias;
+    __syncthreads();
+    if (!on) return;
+    float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        sum0 += s_p[w][0][0][lane];
+        sum1 += s_p[w][1][0][lane];
+    }
     if constexpr (AGG) {
-        if (!on) return;
         const int64_t sb = int64_t(seg) * p.batch + b;
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (n0 + k < p.N) p.seg_h[(sb * p.N + n0 + k) * p.ch + ch] = carry[k];
-        if (wave == 0) p.seg_dt[sb * p.ch + ch] = sum_dt;
+        if (wave == 0) p.seg_dt[sb * p.ch + ch] = sum0;
     } else {
-        __syncthreads();
-        s_p[wave][0][0][lane] = dD;
-        s_p[wave][1][0][lane] = dbias;
-        __syncthreads();
-        if (!on) return;
         float* pa = p.part_a + (b * p.nseg + seg) * int64_t(p.N + 2) * p.ch + ch;
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (n0 + k < p.N) pa[int64_t(n0 + k) * p.ch] = dA[k];
         if (wave == 0) {
-            float sD = 0.0f, sb = 0.0f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                sD += s_p[w][0][0][lane];
-                sb += s_p[w][1][0][lane];
-            }
-            pa[int64_t(p.N) * p.ch] = sD;
-            pa[int64_t(p.N + 1) * p.ch] = sb;
+            pa[int64_t(p.N) * p.ch] = sum0;
+            pa[int64_t(p.N + 1) * p.ch] = sum1;
         }
         if (p.dh0 && seg == 0) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (n0 + k < p.N) p.dh0[(b * p.ch + ch) * p.N + n0 + k] = carry[k];
         }
-        raw* du = static_cast<raw*>(p.du) + b * p.L * p.ch + ch;
-        raw* ddt = static_cast<raw*>(p.ddt) + b * p.L * p.ch + ch;
-        raw* dz = static_cast<raw*>(p.dz) + b * p.L * p.ch + ch;
-        for (int64_t t = (last > first ? last : first) + wave; t < stop; t += NW) {
-            du[t * p.ch] = ddt[t * p.ch] = E::put(0.0f);
-            if (z) dz[t * p.ch] = E::put(0.0f);
+        const int64_t row0 = b * p.L * p.ch + ch;
+        for (int64_t t = (last > first ? last : first) + wave; t < at.stop; t += NW) {
+            static_cast<raw*>(p.du)[row0 + t * p.ch] = static_cast<raw*>(p.ddt)[row0 + t * p.ch] = E::put(0.0f);
+            if (p.z) static_cast<raw*>(p.dz)[row0 + t * p.ch] = E::put(0.0f);
         }
     }
 }
@@ -292,14 +302,24 @@ __global__ __launch_bounds__(256) void scan_bwd_bc_kernel(ScanParams p) {
     }
 }
 
-// dA, dD, ddt_bias: the sums over sequences and segments, one thread per value.
+// dA, dD, ddt_bias: the sums over sequences and segments.  A workgroup has 64
+// adjacent values, its four waves a quarter of the summands each.
 __global__ __launch_bounds__(256) void scan_bwd_a_kernel(ScanParams p) {
+    __shared__ float s_sum[4][64];
     const int64_t per = int64_t(p.N + 2) * p.ch;
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= per) return;
-    const int ch = int(i % p.ch), r = int(i / p.ch);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t i = int64_t(blockIdx.x) * 64 + lane;
+    const int rows = p.batch * p.nseg;
     float s = 0.0f;
-    for (int64_t q = 0; q < int64_t(p.batch) * p.nseg; ++q) s += p.part_a[q * per + i];
+    if (i < per) {
+#pragma unroll 8
+        for (int q = wave; q < rows; q += 4) s += p.part_a[q * per + i];
+    }
+    s_sum[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || i >= per) return;
+    s = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+    const int ch = int(i % p.ch), r = int(i / p.ch);
     if (r < p.N) p.dA[int64_t(ch) * p.N + r] = s;
     else if (r == p.N) { if (p.dD) p.dD[ch] = s; }
     else if (p.dbias) p.dbias[ch] = s;
@@ -320,7 +340,7 @@ int launch_bwd(const ScanParams& p, hipStream_t stream) {
     hipLaunchKernelGGL((scan_bwd_bc_kernel<E>), dim3(uint32_t(blocks < 65536 ? blocks : 65536)), dim3(256), 0, stream, p);
     if (hipGetLastError() != hipSuccess) return -7;
     const int64_t per = int64_t(p.N + 2) * p.ch;
-    hipLaunchKernelGGL(scan_bwd_a_kernel, dim3(uint32_t((per + 255) / 256)), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL(scan_bwd_a_kernel, dim3(uint32_t((per + 63) / 64)), dim3(256), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 

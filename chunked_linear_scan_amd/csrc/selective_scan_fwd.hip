@@ -10,7 +10,7 @@ namespace {
 template <typename E, int NW, bool AGG>
 __global__ __launch_bounds__(NW * 64, 4) void scan_fwd_kernel(ScanParams p) {
     constexpr int K = kScanK;
-    constexpr int TT = NW > 8 ? 8 : 16;
+    constexpr int TT = kScanTile;
     constexpr int R = TT >= NW ? TT / NW : 1;  // token rows that a wave stages and finishes
     typedef typename E::raw raw;
     __shared__ float2 s_d[TT][kScanCh];        // dt', dt' u
@@ -41,13 +41,7 @@ __global__ __launch_bounds__(NW * 64, 4) void scan_fwd_kernel(ScanParams p) {
             for (int k = 0; k < K; ++k)
                 if (n0 + k < p.N) h[k] = p.h0[(b * p.ch + ch) * p.N + n0 + k];
         }
-        for (int s = 0; s < seg; ++s) {  // what the earlier segments did to the state
-            const int64_t sb = int64_t(s) * p.batch + b;
-            const float sd = p.seg_dt[sb * p.ch + ch];
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (n0 + k < p.N) h[k] = fmaf(fexp2(A2[k] * sd), h[k], p.seg_h[(sb * p.N + n0 + k) * p.ch + ch]);
-        }
+        scan_fold(p, 0, 1, seg, b, at.ch, n0, A2, h);  // what the earlier segments did to the state
     }
     float sum_dt = 0.0f;
 

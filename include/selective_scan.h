@@ -57,7 +57,7 @@ extern "C" {
  *   h_final    [batch, channels, dstate]            fp32 (NULL = not written)
  *   checkpoints: what selective_scan_bwd needs of the forward pass, of
  *              selective_scan_checkpoint_size bytes (NULL = not written): the
- *              state before every 16th token (every 8th above 32 states)
+ *              state before every 8th token
  * dstate is 1..64 (SSD_ERR_UNSUPPORTED above), channels a multiple of
  * ngroups.  Decays above 1 (A > 0) are evaluated as they are.  Outputs must
  * not alias inputs.

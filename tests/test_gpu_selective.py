@@ -498,7 +498,7 @@ def test_binding_refuses_bad_tensors():
     with pytest.raises(ValueError, match="checkpoints"):
         cls.selective_scan_bwd(c["dy"], **args)
     with pytest.raises(ValueError, match="checkpoints"):
-        cls.selective_scan_bwd(c["dy"], **args, checkpoints=torch.zeros(2, 2, 4, 16, device="cuda"))
+        cls.selective_scan_bwd(c["dy"], **args, checkpoints=torch.zeros(2, 3, 4, 16, device="cuda"))
     with pytest.raises(cls.SSDError):
         big = torch.zeros(2, 9, 1, 65, dtype=torch.bfloat16, device="cuda")
         cls.selective_scan(c["u"], c["dt"], torch.zeros(16, 65, device="cuda"), big, big)

@@ -100,8 +100,8 @@ def test_scan_refuses_other_pointers():
 
 def test_scan_sizes():
     lib = cls.load_library()
-    # the state before every 16th token, every 8th above 32 states
-    assert lib.selective_scan_checkpoint_size(2, 33, 10, 16) == 2 * 3 * 10 * 16 * 4
+    # the state before every 8th token
+    assert lib.selective_scan_checkpoint_size(2, 33, 10, 16) == 2 * 5 * 10 * 16 * 4
     assert lib.selective_scan_checkpoint_size(2, 33, 10, 33) == 2 * 5 * 10 * 33 * 4
     assert lib.selective_scan_checkpoint_size(2, 33, 10, 65) == 0
     assert lib.selective_scan_workspace_size(64, 4096, 4096, 16, 1) == 0  # whole sequences fill the device
