@@ -94,10 +94,12 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanParams& p, int seg0 = 
     return a;
 }
 
-// The rows of B or C of a tile for one wave: lane l holds token l / 4 (of up
-// to 16) and state n0 + l % 4, which is how a 4x4x1 matrix instruction takes
-// the 4 rows of its A operand, block by block; see outer() and dot().
-template <typename E, int TT>
+// The rows of B or C of a tile for one wave: lane l holds token (l / 4) % 8 and
+// state n0 + l % 4, which is how a 4x4x1 matrix instruction takes the 4 rows of
+// its A operand, block by block; see outer().
+static_assert(kScanTile == 8 && kScanK == 4, "half a wave holds a tile");
+
+template <typename E>
 struct ScanRows {
     typedef typename E::raw raw;
     const raw* at;    // the tile to be loaded, the same for all lanes
@@ -110,18 +112,30 @@ struct ScanRows {
                                         int lane) {
         at = static_cast<const raw*>(v) + b * s.b + g * s.g + first * s.t;
         stride = int(s.t);
-        row = (lane >> 2) & (TT - 1);
+        row = (lane >> 2) & 7;
         const int n = n0 + (lane & 3);
         on = n < N;
         off = uint32_t(row * stride + (on ? n : 0)) * uint32_t(sizeof(raw));
     }
     // Loads the tile; rem: the last of its rows that may be read (below 0: before the tile).
     __device__ __forceinline__ void load(int rem) {
-        if (rem >= TT - 1) r = at_bytes(at, off);
+        if (rem >= kScanTile - 1) r = at_bytes(at, off);
         else r = *(&at_bytes(at, off) - int64_t(row > rem ? row - rem : 0) * stride);
     }
+    __device__ __forceinline__ void step(int dir) { at += dir * kScanTile * int64_t(stride); }
     __device__ __forceinline__ float get() const { return on ? E::get(r) : 0.0f; }
 };
+
+// The same rows as operands of vector instructions: each row of 16 lanes of
+// q[i] holds tokens 4 i to 4 i + 3, and the instruction that uses one of the
+// values broadcasts it within the row as it reads it (a DPP operand).  Rows 0
+// and 2 of a wave hold tokens 0 to 3, rows 1 and 3 tokens 4 to 7: swapping
+// them between two copies gives both.
+__device__ __forceinline__ void row_quads(float rows, float (&q)[2]) {
+    const auto r = __builtin_amdgcn_permlane16_swap(as_uint(rows), as_uint(rows), false, false);
+    q[0] = as_float(r[0]);
+    q[1] = as_float(r[1]);
+}
 
 // rows: as ScanRows gives them.  c[k] + value(T, k) v for the wave's four states k, where v is the lane's own: the
 // matrix instruction multiplies 16 blocks of 4 rows by 4 columns (the lanes), with the rows of block T in all blocks.
@@ -129,41 +143,6 @@ template <int T>
 __device__ __forceinline__ f32x4 outer(float rows, float v, f32x4 c = f32x4{0.f, 0.f, 0.f, 0.f}) {
     return __builtin_amdgcn_mfma_f32_4x4x1f32(rows, v, c, 4, T, 0);
 }
-
-// The same rows as operands of vector instructions: register r holds, in each
-// row of 16 lanes, tokens 4 r to 4 r + 3, and the instruction that uses one of
-// its values broadcasts it within the row as it reads it (a DPP operand).
-template <typename E, int TT>
-struct ScanQuads {
-    typedef typename E::raw raw;
-    const raw* at;
-    int stride, row;
-    uint32_t off;
-    bool on;
-    raw r[TT / 4];
-
-    __device__ __forceinline__ ScanQuads(const void* v, const ScanStride& s, int64_t b, int g, int64_t first, int n0,
-                                         int N, int lane) {
-        at = static_cast<const raw*>(v) + b * s.b + g * s.g + first * s.t;
-        stride = int(s.t);
-        row = (lane >> 2) & 3;
-        const int n = n0 + (lane & 3);
-        on = n < N;
-        off = uint32_t(row * stride + (on ? n : 0)) * uint32_t(sizeof(raw));
-    }
-    __device__ __forceinline__ void load(int rem) {
-#pragma unroll
-        for (int i = 0; i < TT / 4; ++i) {
-            const raw* q = at + 4 * i * stride;
-            if (rem >= TT - 1) r[i] = at_bytes(q, off);
-            else r[i] = *(&at_bytes(q, off) - int64_t(4 * i + row > rem ? 4 * i + row - rem : 0) * stride);
-        }
-    }
-    __device__ __forceinline__ void get(float (&f)[TT / 4]) const {
-#pragma unroll
-        for (int i = 0; i < TT / 4; ++i) f[i] = on ? E::get(r[i]) : 0.0f;
-    }
-};
 
 // sum_k value(T, k) v[k].  The compiler does not fold a DPP operand into a
 // multiply-add, hence the instructions themselves; s_nop: a DPP operand may be

@@ -6,6 +6,11 @@
 namespace cls {
 namespace {
 
+// Waves per SIMD that the backward kernel's registers are kept to: 3 (168
+// registers) measured 186 us where 2 took 198 and 4, with spills, 475.  With one
+// or two waves to a workgroup each stages more rows and needs more registers.
+constexpr int scan_bwd_waves(int NW, bool agg) { return NW > 8 || agg ? 4 : NW > 2 ? 3 : 2; }
+
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
@@ -26,17 +31,17 @@ __device__ __forceinline__ float dpp_add(bool bit, float lo, float hi) {
     return (bit ? hi : lo) + dpp<CTRL>(bit ? lo : hi);
 }
 
-// AGG: what a segment alone hands back to the tokens before it (and its summed
+// Z: with a gate.  AGG: what a segment alone hands back to the tokens before it (and its summed
 // steps), from no gradient behind it.
-template <typename E, int NW, bool AGG>
-__global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_kernel(ScanParams p) {
+template <typename E, int NW, bool AGG, bool Z>
+__global__ __launch_bounds__(NW * 64, scan_bwd_waves(NW, AGG)) void scan_bwd_kernel(ScanParams p) {
     constexpr int K = kScanK;
     constexpr int TT = kScanTile;
     constexpr int R = TT >= NW ? TT / NW : 1;
     typedef typename E::raw raw;
     __shared__ float2 s_d[TT][kScanCh];   // dt', dt' u
     __shared__ float s_dy[TT][kScanCh];   // the gradient of y before the gate
-    __shared__ float s_p[NW][3][AGG ? 1 : TT][kScanCh];  // each wave's share of three sums over the states
+    __shared__ float s_p[NW][Z ? 3 : 2][AGG ? 1 : TT][kScanCh];  // each wave's share of the sums over the states
 
     const ScanPlace at = scan_place(p, AGG ? 1 : 0);
     const int lane = threadIdx.x & 63;
@@ -73,10 +78,9 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_ke
     const int64_t top = first + (tiles - 1) * TT;
     const raw* u = static_cast<const raw*>(p.u) + b * p.su.b + top * p.su.t;
     const raw* dt = static_cast<const raw*>(p.dt) + b * p.sdt.b + top * p.sdt.t;
-    const raw* z = p.z ? static_cast<const raw*>(p.z) + b * p.sz.b + top * p.sz.t : nullptr;
+    const raw* z = static_cast<const raw*>(p.z) + (Z ? b * p.sz.b + top * p.sz.t : 0);
     const raw* dy = static_cast<const raw*>(p.dy) + b * p.sdy.b + top * p.sdy.t;
-    ScanRows<E, TT> B(p.B, p.sB, b, at.g, top, n0, p.N, lane), C(p.C, p.sC, b, at.g, top, n0, p.N, lane);
-    ScanQuads<E, TT> Bq(p.B, p.sB, b, at.g, top, n0, p.N, lane), Cq(p.C, p.sC, b, at.g, top, n0, p.N, lane);
+    ScanRows<E> B(p.B, p.sB, b, at.g, top, n0, p.N, lane), C(p.C, p.sC, b, at.g, top, n0, p.N, lane);
     const int u_t = int(p.su.t), dt_t = int(p.sdt.t), z_t = int(p.sz.t), dy_t = int(p.sdy.t);
     raw ru[R], rdt[R], rz[R], rdy[R];
     // Loads the tile at t0 and steps back; before the segment there is none.
@@ -84,11 +88,7 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_ke
         if (t0 < first) return;
         const int rem = int(last - 1 - t0 < TT ? last - 1 - t0 : TT);
         C.load(rem);
-        if (!AGG) {
-            B.load(rem);
-            Bq.load(rem);
-            if (z) Cq.load(rem);
-        }
+        if (!AGG) B.load(rem);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = wave + r * NW < rem ? wave + r * NW : rem;
@@ -96,16 +96,14 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_ke
             rdt[r] = at_bytes(dt + row * dt_t, lane_off);
             rdy[r] = at_bytes(dy + row * dy_t, lane_off);
             rz[r] = 0;
-            if (z) rz[r] = at_bytes(z + row * z_t, lane_off);
+            if (Z) rz[r] = at_bytes(z + row * z_t, lane_off);
         }
         u -= TT * int64_t(u_t);
         dt -= TT * int64_t(dt_t);
         dy -= TT * int64_t(dy_t);
-        if (z) z -= TT * int64_t(z_t);
-        B.at -= TT * int64_t(B.stride);
-        C.at -= TT * int64_t(C.stride);
-        Bq.at -= TT * int64_t(B.stride);
-        Cq.at -= TT * int64_t(C.stride);
+        if (Z) z -= TT * int64_t(z_t);
+        if (!AGG) B.step(-1);
+        C.step(-1);
     };
     const int64_t out0 = (b * p.L + top) * p.ch;
     raw* du = static_cast<raw*>(p.du) + out0;
@@ -134,7 +132,7 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_ke
             oc[r] = E::get(rdy[r]);
             xc[r] = E::get(rdt[r]) + bias;
             dc[r] = p.softplus ? softplus(xc[r]) : xc[r];
-            gc[r] = z ? oc[r] * zc[r] * sigmoid(zc[r]) : oc[r];
+            gc[r] = Z ? oc[r] * zc[r] * sigmoid(zc[r]) : oc[r];
             float d = dc[r], s = dc[r] * uc[r], gy = gc[r];
             if (row >= nt) d = 0.0f;
             if (row >= nt || !on) s = gy = 0.0f;  // nothing of a lane without a channel in the sums over the lanes
@@ -145,10 +143,10 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_ke
             }
         }
         const float fC = C.get(), fB = AGG ? 0.0f : B.get();
-        float qB[TT / 4], qC[TT / 4];
+        float qB[2], qC[2];
         if (!AGG) {
-            Bq.get(qB);
-            if (z) Cq.get(qC);
+            row_quads(fB, qB);
+            if (Z) row_quads(fC, qC);
         }
         load(t0 - TT);
         __syncthreads();
@@ -177,7 +175,7 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_ke
                             a[T][k] = fexp2(d.x * A2[k]);
                             hs[T][k] = fmaf(a[T][k], T ? hs[T ? T - 1 : 0][k] : hin[k], b4[k]);
                         }
-                        if (z) s_p[wave][2][T][lane] = dot<T>(qC, hs[T]);
+                        if constexpr (Z) s_p[wave][2][T][lane] = dot<T>(qC, hs[T]);
                     }(),
                     ...);
             }(std::make_integer_sequence<int, TT>{});
@@ -229,7 +227,7 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_ke
                 for (int w = 0; w < NW; ++w) {
                     to_sig += s_p[w][0][row][lane];
                     to_dt += s_p[w][1][row][lane];
-                    if (p.z) y += s_p[w][2][row][lane];
+                    if constexpr (Z) y += s_p[w][2][row][lane];
                 }
                 float d = fmaf(uc[r], to_sig, to_dt * kLn2);  // A2 is A log2(e)
                 if (p.softplus) d *= sigmoid(xc[r]);
@@ -239,7 +237,7 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_ke
                 const int64_t o = int64_t(row) * p.ch;
                 at_bytes(du + o, lane_off) = E::put(fmaf(Dc, gc[r], dc[r] * to_sig));
                 at_bytes(ddt + o, lane_off) = E::put(d);
-                if (p.z) at_bytes(dz + o, lane_off) = E::put(oc[r] * y * dsilu(zc[r], sigmoid(zc[r])));
+                if (Z) at_bytes(dz + o, lane_off) = E::put(oc[r] * y * dsilu(zc[r], sigmoid(zc[r])));
             }
             du -= int64_t(TT) * p.ch;
             ddt -= int64_t(TT) * p.ch;
@@ -281,7 +279,7 @@ __global__ __launch_bounds__(NW * 64, NW > 8 ? 4 : AGG ? 4 : 2) void scan_bwd_ke
         const int64_t row0 = b * p.L * p.ch + ch;
         for (int64_t t = (last > first ? last : first) + wave; t < at.stop; t += NW) {
             static_cast<raw*>(p.du)[row0 + t * p.ch] = static_cast<raw*>(p.ddt)[row0 + t * p.ch] = E::put(0.0f);
-            if (p.z) static_cast<raw*>(p.dz)[row0 + t * p.ch] = E::put(0.0f);
+            if (Z) static_cast<raw*>(p.dz)[row0 + t * p.ch] = E::put(0.0f);
         }
     }
 }
@@ -325,15 +323,15 @@ __global__ __launch_bounds__(256) void scan_bwd_a_kernel(ScanParams p) {
     else if (p.dbias) p.dbias[ch] = s;
 }
 
-template <typename E, int NW>
+template <typename E, int NW, bool Z>
 int launch_bwd(const ScanParams& p, hipStream_t stream) {
     const uint32_t per_seg = uint32_t(p.bpg) * uint32_t(p.G) * uint32_t(p.batch);
     const dim3 block{NW * 64u, 1u, 1u};
     if (p.nseg > 1) {
-        hipLaunchKernelGGL((scan_bwd_kernel<E, NW, true>), dim3(per_seg * uint32_t(p.nseg - 1)), block, 0, stream, p);
+        hipLaunchKernelGGL((scan_bwd_kernel<E, NW, true, Z>), dim3(per_seg * uint32_t(p.nseg - 1)), block, 0, stream, p);
         if (hipGetLastError() != hipSuccess) return -7;
     }
-    hipLaunchKernelGGL((scan_bwd_kernel<E, NW, false>), dim3(per_seg * uint32_t(p.nseg)), block, 0, stream, p);
+    hipLaunchKernelGGL((scan_bwd_kernel<E, NW, false, Z>), dim3(per_seg * uint32_t(p.nseg)), block, 0, stream, p);
     if (hipGetLastError() != hipSuccess) return -7;
     const int64_t values = int64_t(p.batch) * p.L * p.G * 2 * p.N;
     const int64_t blocks = (values + 255) / 256;
@@ -344,15 +342,20 @@ int launch_bwd(const ScanParams& p, hipStream_t stream) {
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
+template <typename E, bool Z>
+int launch_waves(const ScanParams& p, hipStream_t stream) {
+    switch (scan_waves(p.N)) {
+        case 1: return launch_bwd<E, 1, Z>(p, stream);
+        case 2: return launch_bwd<E, 2, Z>(p, stream);
+        case 4: return launch_bwd<E, 4, Z>(p, stream);
+        case 8: return launch_bwd<E, 8, Z>(p, stream);
+        default: return launch_bwd<E, 16, Z>(p, stream);
+    }
+}
+
 template <typename E>
 int launch_type(const ScanParams& p, hipStream_t stream) {
-    switch (scan_waves(p.N)) {
-        case 1: return launch_bwd<E, 1>(p, stream);
-        case 2: return launch_bwd<E, 2>(p, stream);
-        case 4: return launch_bwd<E, 4>(p, stream);
-        case 8: return launch_bwd<E, 8>(p, stream);
-        default: return launch_bwd<E, 16>(p, stream);
-    }
+    return p.z ? launch_waves<E, true>(p, stream) : launch_waves<E, false>(p, stream);
 }
 
 }  // namespace

@@ -49,8 +49,7 @@ __global__ __launch_bounds__(NW * 64, 4) void scan_fwd_kernel(ScanParams p) {
     const raw* u = static_cast<const raw*>(p.u) + b * p.su.b + first * p.su.t;
     const raw* dt = static_cast<const raw*>(p.dt) + b * p.sdt.b + first * p.sdt.t;
     const raw* z = p.z ? static_cast<const raw*>(p.z) + b * p.sz.b + first * p.sz.t : nullptr;
-    ScanRows<E, TT> B(p.B, p.sB, b, at.g, first, n0, p.N, lane);
-    ScanQuads<E, TT> C(p.C, p.sC, b, at.g, first, n0, p.N, lane);
+    ScanRows<E> B(p.B, p.sB, b, at.g, first, n0, p.N, lane), C(p.C, p.sC, b, at.g, first, n0, p.N, lane);
     const uint32_t lane_off = ch * uint32_t(sizeof(raw));
     const int u_t = int(p.su.t), dt_t = int(p.sdt.t), z_t = int(p.sz.t);
     raw ru[R], rdt[R], rz[R];
@@ -70,8 +69,8 @@ __global__ __launch_bounds__(NW * 64, 4) void scan_fwd_kernel(ScanParams p) {
         u += TT * int64_t(u_t);
         dt += TT * int64_t(dt_t);
         if (!AGG && z) z += TT * int64_t(z_t);
-        B.at += TT * int64_t(B.stride);
-        C.at += TT * int64_t(C.stride);
+        B.step(1);
+        if (!AGG) C.step(1);
     };
     raw* y = AGG ? nullptr : static_cast<raw*>(p.y) + (b * p.L + first) * p.ch;
     float* ckpt = AGG || !p.ckpt ? nullptr : p.ckpt + ((b * ((p.L + TT - 1) / TT) + first / TT) * p.N + n0) * p.ch;
@@ -92,8 +91,8 @@ __global__ __launch_bounds__(NW * 64, 4) void scan_fwd_kernel(ScanParams p) {
             if (row < TT) s_d[row][lane] = make_float2(d, du);
         }
         const float fB = B.get();
-        float fC[TT / 4];
-        if (!AGG) C.get(fC);
+        float fC[2];
+        if (!AGG) row_quads(C.get(), fC);
         load(t0 + TT);
         __syncthreads();
         if (!AGG && ckpt) {
