@@ -11,14 +11,21 @@ none.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import math
+import struct
 
 import torch
 
 _i64, _i32, _vp, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
 _CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _CACHE_CODE = {torch.int8: 3, torch.float8_e4m3fn: 4}
+
+# The header's structures, packed in one go: filling the ctypes fields one by
+# one takes longer than the smallest kernels.
+_PACK_SCAN = struct.Struct("5q2i10P12q")
+_PACK_GRADS = struct.Struct("P2q11P")
+_PACK_CONV = struct.Struct("4q2iP2q4P")
 
 
 class _ScanInputs(ctypes.Structure):
@@ -46,7 +53,7 @@ class _ConvInputs(ctypes.Structure):
 
 def declare(lib: ctypes.CDLL) -> None:
     """Sets the argument types of this header's functions."""
-    ps, pg, pc = (ctypes.POINTER(s) for s in (_ScanInputs, _ScanGrads, _ConvInputs))
+    ps = pg = pc = _vp  # packed bytes, or a reference to the structure
     for name, args, res in (
             ("selective_scan_workspace_size", [_i64] * 5, _sz),
             ("selective_scan_bwd_workspace_size", [_i64] * 5, _sz),
@@ -64,46 +71,49 @@ def declare(lib: ctypes.CDLL) -> None:
         f.argtypes, f.restype = args, res
 
 
+_library = None
+
+
 def _lib():
-    from . import load_library
-    return load_library()
+    global _library
+    if _library is None:
+        from . import load_library
+        _library = load_library()
+    return _library
 
 
-def _ok(status: int, what: str) -> None:
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _run(what, device, f, *args) -> None:
+    """Calls f on the device's current stream, with the device current."""
+    at = device.index
+    stream = torch._C._cuda_getCurrentRawStream(at)
+    if at == torch._C._cuda_getDevice():
+        status = f(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, stream)
     if status != 0:
         from . import SSDError
         raise SSDError(status, what)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _on(device):
-    """Makes the inputs' device the current one for the launches."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
 def _check(name, t, device, dtype, shape, strided=False):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device or device.type != "cuda":
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and (
+                t.is_contiguous() or (strided and (t.stride(-1) == 1 or t.shape[-1] == 1))):
+            return
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if t.device != device:
         raise ValueError(f"{name} must be on one GPU with the other tensors (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    if strided:
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name}'s last dimension must be adjacent in memory")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name}'s last dimension must be adjacent in memory" if strided else f"{name} must be contiguous")
 
 
 def _activation(name, t, dims):
@@ -113,6 +123,8 @@ def _activation(name, t, dims):
         raise TypeError(f"{name} must be float32, bfloat16 or float16")
     if t.dim() != len(dims):
         raise ValueError(f"{name} must be [{', '.join(dims)}]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU (got {t.device})")
     _check(name, t, t.device, t.dtype, t.shape, strided=True)
 
 
@@ -124,39 +136,50 @@ def _seqlens(t, device, batch):
 # ---------------------------------------------------------------------------
 # selective scan
 # ---------------------------------------------------------------------------
-def _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus, step=False) -> _ScanInputs:
-    _activation("u", u, ("batch", "channels") if step else ("batch", "seqlen", "channels"))
-    dev, kind, lead, ch = u.device, u.dtype, u.shape[:-1], u.shape[-1]
-    _check("dt", dt, dev, kind, u.shape, strided=True)
+_SEQ, _ONE = ("batch", "seqlen", "channels"), ("batch", "channels")
+
+
+def _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus, step=False):
+    """(the packed structure, its sizes)"""
+    _activation("u", u, _ONE if step else _SEQ)
+    dev, kind, shape = u.device, u.dtype, u.shape
+    n, ch = shape[0], shape[-1]
+    lead = shape[:-1]
+    _check("dt", dt, dev, kind, shape, True)
     if z is not None:
-        _check("z", z, dev, kind, u.shape, strided=True)
+        _check("z", z, dev, kind, shape, True)
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be [channels, dstate]")
     N = A.shape[1]
     _check("A", A, dev, torch.float32, (ch, N))
-    if not isinstance(B, torch.Tensor) or B.dim() != len(lead) + 2:
+    if not isinstance(B, torch.Tensor) or B.dim() != len(shape) + 1:
         raise ValueError("B must be [batch, ngroups, dstate]" if step else "B must be [batch, seqlen, ngroups, dstate]")
     G = B.shape[-2]
-    _check("B", B, dev, kind, (*lead, G, N), strided=True)
-    _check("C", C, dev, kind, (*lead, G, N), strided=True)
+    bc = (*lead, G, N)
+    _check("B", B, dev, kind, bc, True)
+    _check("C", C, dev, kind, bc, True)
     if D is not None:
         _check("D", D, dev, torch.float32, (ch,))
     if dt_bias is not None:
         _check("dt_bias", dt_bias, dev, torch.float32, (ch,))
     if h0 is not None:
-        _check("h0", h0, dev, torch.float32, (lead[0], ch, N))
-    _seqlens(seqlens, dev, lead[0])
-    sz = u if z is None else z
-    tok = (lambda t: 0) if step else (lambda t: t.stride(1))
-    return _ScanInputs(lead[0], 1 if step else lead[1], ch, N, G, _CODE[kind], 1 if dt_softplus else 0,
-                       _at(u), _at(dt), _at(z), _at(B), _at(C), _at(A), _at(D), _at(dt_bias), _at(h0), _at(seqlens),
-                       u.stride(0), tok(u), dt.stride(0), tok(dt), sz.stride(0), tok(sz),
-                       B.stride(0), tok(B), B.stride(-2), C.stride(0), tok(C), C.stride(-2))
+        _check("h0", h0, dev, torch.float32, (n, ch, N))
+    _seqlens(seqlens, dev, n)
+    L = 1 if step else shape[1]
+    us, ds, bs, cs = u.stride(), dt.stride(), B.stride(), C.stride()
+    zs = us if z is None else z.stride()
+    if step:
+        strides = (us[0], 0, ds[0], 0, zs[0], 0, bs[0], 0, bs[1], cs[0], 0, cs[1])
+    else:
+        strides = (us[0], us[1], ds[0], ds[1], zs[0], zs[1], bs[0], bs[1], bs[2], cs[0], cs[1], cs[2])
+    return _PACK_SCAN.pack(n, L, ch, N, G, _CODE[kind], 1 if dt_softplus else 0, u.data_ptr(), dt.data_ptr(), _at(z),
+                           B.data_ptr(), C.data_ptr(), A.data_ptr(), _at(D), _at(dt_bias), _at(h0), _at(seqlens),
+                           *strides), (n, L, ch, N, G)
 
 
-def _tiles(lib, s):
-    return lib.selective_scan_checkpoint_size(s.batch, s.seqlen, s.channels, s.dstate) // (
-        4 * s.batch * s.channels * s.dstate)
+def _checkpoint_shape(lib, sizes):
+    n, L, ch, N, _ = sizes
+    return (n, lib.selective_scan_checkpoint_size(n, L, ch, N) // max(4 * n * ch * N, 1), N, ch)
 
 
 def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, seqlens=None, dt_softplus: bool = True,
@@ -176,19 +199,19 @@ def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, seqlen
     (y, h_final or None, checkpoints), where checkpoints is what
     ``selective_scan_bwd`` takes."""
     lib = _lib()
-    s = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus)
-    dev = u.device
-    y = torch.empty(u.shape, dtype=u.dtype, device=dev) if out is None else out
-    _check("out", y, dev, u.dtype, u.shape)
-    hf = torch.empty((s.batch, s.channels, s.dstate), dtype=torch.float32, device=dev) if want_final_state else None
-    kept = None
-    if want_checkpoints:
-        kept = torch.empty((s.batch, _tiles(lib, s), s.dstate, s.channels), dtype=torch.float32, device=dev)
-    need = lib.selective_scan_workspace_size(s.batch, s.seqlen, s.channels, s.dstate, s.ngroups)
+    s, sizes = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus)
+    n, _, ch, N, _ = sizes
+    dev, f32 = u.device, torch.float32
+    if out is None:
+        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+    else:
+        y = out
+        _check("out", y, dev, u.dtype, u.shape)
+    hf = torch.empty((n, ch, N), dtype=f32, device=dev) if want_final_state else None
+    kept = torch.empty(_checkpoint_shape(lib, sizes), dtype=f32, device=dev) if want_checkpoints else None
+    need = lib.selective_scan_workspace_size(*sizes)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    with _on(dev):
-        _ok(lib.selective_scan_fwd(ctypes.byref(s), _at(y), _at(hf), _at(kept), _at(ws), need, _stream(dev)),
-            "selective_scan")
+    _run("selective_scan", dev, lib.selective_scan_fwd, s, y.data_ptr(), _at(hf), _at(kept), _at(ws), need)
     return (y, hf, kept) if want_checkpoints else (y, hf)
 
 
@@ -201,15 +224,15 @@ def selective_scan_bwd(dy, u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None
     in parentheses where the input was given.  dB and dC are summed over the
     channels of a group.  Padding has zero gradients."""
     lib = _lib()
-    s = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus)
+    s, sizes = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus)
+    n, _, ch, N, _ = sizes
     dev, f32 = u.device, torch.float32
-    _check("dy", dy, dev, u.dtype, u.shape, strided=True)
-    state = (s.batch, s.channels, s.dstate)
+    _check("dy", dy, dev, u.dtype, u.shape, True)
     if checkpoints is None:
         raise ValueError("checkpoints: run selective_scan with want_checkpoints=True")
-    _check("checkpoints", checkpoints, dev, f32, (s.batch, _tiles(lib, s), s.dstate, s.channels))
+    _check("checkpoints", checkpoints, dev, f32, _checkpoint_shape(lib, sizes))
     if dh_final is not None:
-        _check("dh_final", dh_final, dev, f32, state)
+        _check("dh_final", dh_final, dev, f32, (n, ch, N))
     like = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
     got = {"du": like(u.shape, u.dtype), "ddt": like(u.shape, u.dtype), "dA": like(A.shape, f32),
            "dB": like(B.shape, u.dtype), "dC": like(C.shape, u.dtype)}
@@ -220,14 +243,12 @@ def selective_scan_bwd(dy, u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None
     if dt_bias is not None:
         got["ddt_bias"] = like(dt_bias.shape, f32)
     if h0 is not None:
-        got["dh0"] = like(state, f32)
-    g = _ScanGrads(_at(dy), dy.stride(0), dy.stride(1), _at(dh_final), _at(checkpoints),
-                   *(_at(got.get(k)) for k in ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0")))
-    need = lib.selective_scan_bwd_workspace_size(s.batch, s.seqlen, s.channels, s.dstate, s.ngroups)
-    ws = like((max(need, 16),), torch.uint8)
-    with _on(dev):
-        _ok(lib.selective_scan_bwd(ctypes.byref(s), ctypes.byref(g), _at(ws), ws.numel(), _stream(dev)),
-            "selective_scan_bwd")
+        got["dh0"] = like((n, ch, N), f32)
+    g = _PACK_GRADS.pack(dy.data_ptr(), dy.stride(0), dy.stride(1), _at(dh_final), checkpoints.data_ptr(),
+                         *(_at(got.get(k)) for k in ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0")))
+    need = max(lib.selective_scan_bwd_workspace_size(*sizes), 16)
+    ws = like((need,), torch.uint8)
+    _run("selective_scan_bwd", dev, lib.selective_scan_bwd, s, g, ws.data_ptr(), need)
     return got
 
 
@@ -237,21 +258,26 @@ def selective_scan_step(h, u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
     [Bt, channels, N] (fp32) in place and returns y [Bt, channels].  u, dt and
     z [Bt, channels], B and C [Bt, groups, N]; the rest as there."""
     lib = _lib()
-    s = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, None, None, dt_softplus, step=True)
-    _check("h", h, u.device, torch.float32, (s.batch, s.channels, s.dstate))
-    y = torch.empty(u.shape, dtype=u.dtype, device=u.device) if out is None else out
-    _check("out", y, u.device, u.dtype, u.shape)
-    with _on(u.device):
-        _ok(lib.selective_scan_step(ctypes.byref(s), _at(h), _at(y), _stream(u.device)), "selective_scan_step")
+    s, (n, _, ch, N, _) = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, None, None, dt_softplus, True)
+    dev = u.device
+    _check("h", h, dev, torch.float32, (n, ch, N))
+    if out is None:
+        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+    else:
+        y = out
+        _check("out", y, dev, u.dtype, u.shape)
+    _run("selective_scan_step", dev, lib.selective_scan_step, s, h.data_ptr(), y.data_ptr())
     return y
 
 
 # ---------------------------------------------------------------------------
 # short convolution
 # ---------------------------------------------------------------------------
-def _conv_inputs(x, weight, bias, initial_state, seqlens, silu, step=False) -> _ConvInputs:
-    _activation("x", x, ("batch", "channels") if step else ("batch", "seqlen", "channels"))
-    dev, ch, n = x.device, x.shape[-1], x.shape[0]
+def _conv_inputs(x, weight, bias, initial_state, seqlens, silu, step=False):
+    """(the packed structure, its sizes)"""
+    _activation("x", x, _ONE if step else _SEQ)
+    dev, shape = x.device, x.shape
+    n, ch = shape[0], shape[-1]
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [channels, width]")
     W = weight.shape[1]
@@ -261,8 +287,9 @@ def _conv_inputs(x, weight, bias, initial_state, seqlens, silu, step=False) -> _
     if initial_state is not None:
         _check("initial_state", initial_state, dev, x.dtype, (n, W - 1, ch))
     _seqlens(seqlens, dev, n)
-    return _ConvInputs(n, 1 if step else x.shape[1], ch, W, _CODE[x.dtype], 1 if silu else 0, _at(x), x.stride(0),
-                       0 if step else x.stride(1), _at(weight), _at(bias), _at(initial_state), _at(seqlens))
+    L, xs = (1, x.stride()) if step else (shape[1], x.stride())
+    return _PACK_CONV.pack(n, L, ch, W, _CODE[x.dtype], 1 if silu else 0, x.data_ptr(), xs[0], 0 if step else xs[1],
+                           weight.data_ptr(), _at(bias), _at(initial_state), _at(seqlens)), (n, L, ch, W)
 
 
 def short_conv(x, weight, bias=None, initial_state=None, seqlens=None, silu: bool = True,
@@ -275,13 +302,15 @@ def short_conv(x, weight, bias=None, initial_state=None, seqlens=None, silu: boo
     the final state the last ones.  seqlens as in ``selective_scan``.  Returns
     (y, final_state or None)."""
     lib = _lib()
-    s = _conv_inputs(x, weight, bias, initial_state, seqlens, silu)
+    s, (n, _, ch, W) = _conv_inputs(x, weight, bias, initial_state, seqlens, silu)
     dev = x.device
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-    _check("out", y, dev, x.dtype, x.shape)
-    last = torch.empty((s.batch, s.width - 1, s.channels), dtype=x.dtype, device=dev) if want_final_state else None
-    with _on(dev):
-        _ok(lib.short_conv_fwd(ctypes.byref(s), _at(y), _at(last), _stream(dev)), "short_conv")
+    if out is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        y = out
+        _check("out", y, dev, x.dtype, x.shape)
+    last = torch.empty((n, W - 1, ch), dtype=x.dtype, device=dev) if want_final_state else None
+    _run("short_conv", dev, lib.short_conv_fwd, s, y.data_ptr(), _at(last))
     return y, last
 
 
@@ -291,22 +320,22 @@ def short_conv_bwd(dy, x, weight, bias=None, initial_state=None, seqlens=None, s
     dfinal_state of its final state): a dict of "dx" in x's dtype, "dweight"
     in fp32, and "dbias" (fp32) and "dinitial_state" where those were given."""
     lib = _lib()
-    s = _conv_inputs(x, weight, bias, initial_state, seqlens, silu)
+    s, sizes = _conv_inputs(x, weight, bias, initial_state, seqlens, silu)
+    n, _, ch, W = sizes
     dev = x.device
-    _check("dy", dy, dev, x.dtype, x.shape, strided=True)
+    _check("dy", dy, dev, x.dtype, x.shape, True)
     if dfinal_state is not None:
-        _check("dfinal_state", dfinal_state, dev, x.dtype, (s.batch, s.width - 1, s.channels))
+        _check("dfinal_state", dfinal_state, dev, x.dtype, (n, W - 1, ch))
     got = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev), "dweight": torch.empty_like(weight)}
     if bias is not None:
         got["dbias"] = torch.empty_like(bias)
     if initial_state is not None:
         got["dinitial_state"] = torch.empty_like(initial_state)
-    need = lib.short_conv_bwd_workspace_size(s.batch, s.seqlen, s.channels, s.width)
-    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        _ok(lib.short_conv_bwd(ctypes.byref(s), _at(dy), dy.stride(0), dy.stride(1), _at(dfinal_state), _at(got["dx"]),
-                               _at(got["dweight"]), _at(got.get("dbias")), _at(got.get("dinitial_state")), _at(ws),
-                               ws.numel(), _stream(dev)), "short_conv_bwd")
+    need = max(lib.short_conv_bwd_workspace_size(*sizes), 16)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _run("short_conv_bwd", dev, lib.short_conv_bwd, s, dy.data_ptr(), dy.stride(0), dy.stride(1), _at(dfinal_state),
+         got["dx"].data_ptr(), got["dweight"].data_ptr(), _at(got.get("dbias")), _at(got.get("dinitial_state")),
+         ws.data_ptr(), need)
     return got
 
 
@@ -315,12 +344,15 @@ def short_conv_step(state, x, weight, bias=None, silu: bool = True, out: torch.T
     [Bt, width - 1, channels] (x's dtype) takes x [Bt, channels] in and drops
     its oldest row, in place; returns y [Bt, channels]."""
     lib = _lib()
-    s = _conv_inputs(x, weight, bias, None, None, silu, step=True)
-    _check("state", state, x.device, x.dtype, (s.batch, s.width - 1, s.channels))
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    _check("out", y, x.device, x.dtype, x.shape)
-    with _on(x.device):
-        _ok(lib.short_conv_step(ctypes.byref(s), _at(state), _at(y), _stream(x.device)), "short_conv_step")
+    s, (n, _, ch, W) = _conv_inputs(x, weight, bias, None, None, silu, True)
+    dev = x.device
+    _check("state", state, dev, x.dtype, (n, W - 1, ch))
+    if out is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        y = out
+        _check("out", y, dev, x.dtype, x.shape)
+    _run("short_conv_step", dev, lib.short_conv_step, s, state.data_ptr(), y.data_ptr())
     return y
 
 
@@ -330,18 +362,19 @@ def short_conv_step(state, x, weight, bias=None, silu: bool = True, out: torch.T
 def _cache_args(cache, scales, slots):
     if not isinstance(cache, torch.Tensor) or cache.dtype not in _CACHE_CODE:
         raise TypeError("cache must be int8 or float8_e4m3fn")
-    if cache.dim() < 2:
+    shape = cache.shape
+    if len(shape) < 2:
         raise ValueError("cache must be [slots, ..., dstate]")
+    if not cache.is_cuda:
+        raise ValueError(f"cache must be on a GPU (got {cache.device})")
     dev = cache.device
-    _check("cache", cache, dev, cache.dtype, cache.shape)
-    _check("scales", scales, dev, torch.float32, cache.shape[:-1])
+    _check("cache", cache, dev, cache.dtype, shape)
+    _check("scales", scales, dev, torch.float32, shape[:-1])
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be [batch]")
-    _check("slots", slots, dev, torch.int32, slots.shape)
-    rows = 1
-    for n in cache.shape[1:-1]:
-        rows *= n
-    return dev, (slots.shape[0], rows, cache.shape[-1], cache.shape[0], _CACHE_CODE[cache.dtype])
+    n = slots.shape[0]
+    _check("slots", slots, dev, torch.int32, (n,))
+    return dev, (n, *shape[1:]), (n, math.prod(shape[1:-1]), shape[-1], shape[0], _CACHE_CODE[cache.dtype])
 
 
 def state_cache_write(h, cache, scales, slots) -> None:
@@ -351,12 +384,10 @@ def state_cache_write(h, cache, scales, slots) -> None:
     (int8 or float8_e4m3fn), with a scale for each row of dstate values in
     scales [slots, ...] (fp32).  A state whose slot is out of range is not
     written; of several that name one slot the last is."""
-    lib = _lib()
-    dev, sizes = _cache_args(cache, scales, slots)
-    _check("h", h, dev, torch.float32, (sizes[0], *cache.shape[1:]))
-    with _on(dev):
-        _ok(lib.state_cache_write(_at(h), _at(slots), *sizes, _at(cache), _at(scales), _stream(dev)),
-            "state_cache_write")
+    dev, shape, sizes = _cache_args(cache, scales, slots)
+    _check("h", h, dev, torch.float32, shape)
+    _run("state_cache_write", dev, _lib().state_cache_write, h.data_ptr(), slots.data_ptr(), *sizes, cache.data_ptr(),
+         scales.data_ptr())
 
 
 def state_cache_read(cache, scales, slots, out: torch.Tensor | None = None):
@@ -364,14 +395,14 @@ def state_cache_read(cache, scales, slots, out: torch.Tensor | None = None):
     filled, as fp32 [Bt, ..., dstate]: the h0 of ``ssd_fwd`` or
     ``selective_scan``, or the state of a step.  A slot out of range gives a
     state of zeros."""
-    lib = _lib()
-    dev, sizes = _cache_args(cache, scales, slots)
-    shape = (sizes[0], *cache.shape[1:])
-    h = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else out
-    _check("out", h, dev, torch.float32, shape)
-    with _on(dev):
-        _ok(lib.state_cache_read(_at(cache), _at(scales), _at(slots), *sizes, _at(h), _stream(dev)),
-            "state_cache_read")
+    dev, shape, sizes = _cache_args(cache, scales, slots)
+    if out is None:
+        h = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        h = out
+        _check("out", h, dev, torch.float32, shape)
+    _run("state_cache_read", dev, _lib().state_cache_read, cache.data_ptr(), scales.data_ptr(), slots.data_ptr(), *sizes,
+         h.data_ptr())
     return h
 
 

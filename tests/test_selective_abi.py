@@ -39,6 +39,18 @@ def test_structures_have_the_header_s_fields():
         body = re.search(r"typedef struct \{([^}]*)\} %s;" % name, text).group(1)
         fields = [re.sub(r"\W", "", f.split()[-1]) for d in body.split(";") for f in d.split(",") if f.strip()]
         assert fields == [f for f, _ in struct._fields_], name
+    assert sel._PACK_SCAN.size == ctypes.sizeof(sel._ScanInputs)
+    assert sel._PACK_GRADS.size == ctypes.sizeof(sel._ScanGrads)
+    assert sel._PACK_CONV.size == ctypes.sizeof(sel._ConvInputs)
+
+
+def test_packed_structures_are_the_ctypes_ones():
+    """The binding packs the structures as bytes: field by field the same as the declared layout."""
+    for pack, struct in ((sel._PACK_SCAN, sel._ScanInputs), (sel._PACK_GRADS, sel._ScanGrads),
+                         (sel._PACK_CONV, sel._ConvInputs)):
+        values = list(range(1, len(struct._fields_) + 1))
+        s = struct.from_buffer_copy(pack.pack(*values))
+        assert [getattr(s, f) for f, _ in struct._fields_] == values
 
 
 def scan_in(**k):
