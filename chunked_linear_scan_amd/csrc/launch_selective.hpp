@@ -16,8 +16,8 @@ int cls_selective_scan_fwd_launch(const cls::ScanParams& p, int dtype, hipStream
 int cls_selective_scan_bwd_launch(const cls::ScanParams& p, int dtype, hipStream_t stream);
 int cls_selective_scan_step_launch(const selective_scan_inputs& in, float* h, void* y, hipStream_t stream);
 
-// Token chunks that short_conv_bwd sums its weight gradients over (rows of its workspace).
-int64_t cls_short_conv_bwd_parts(int64_t batch, int64_t seqlen);
+// The most partial sums of weight gradients that short_conv_bwd adds up (rows of its workspace).
+int64_t cls_short_conv_bwd_parts(int64_t batch, int64_t seqlen, int64_t channels);
 int cls_short_conv_fwd_launch(const short_conv_inputs& in, void* y, void* final_state, hipStream_t stream);
 int cls_short_conv_bwd_launch(const short_conv_inputs& in, const void* dy, int64_t dy_batch, int64_t dy_token,
                               const void* dfinal, void* dx, float* dweight, float* dbias, void* dinitial, float* parts,

@@ -115,8 +115,8 @@ int conv_check(const short_conv_inputs* in) {
     if (in->batch <= 0 || in->seqlen <= 0 || in->channels <= 0 || in->width <= 0) return SSD_ERR_SHAPE;
     if (in->batch > kMaxDim || in->seqlen > kMaxTokens || in->channels > kMaxDim) return SSD_ERR_SHAPE;
     if (in->width < 2 || in->width > 4) return SSD_ERR_UNSUPPORTED;
-    // a thread per channel, the tokens of a run and the final state at least
-    if (in->batch * ceil_div(in->seqlen, 4) >= kMaxThreads / in->channels - in->batch) return SSD_ERR_SHAPE;
+    // a thread per channel and four tokens, and for the final state; workgroups of 256
+    if (in->batch * (ceil_div(in->seqlen, 4) + 1) >= (kMaxThreads - 256) / (in->channels + 64)) return SSD_ERR_SHAPE;
     const int64_t strides[] = {in->x_batch, in->x_token};
     if (!strides_ok(strides, 2)) return SSD_ERR_SHAPE;
     if (!aligned(in->x, elem_size(in->dtype)) || !aligned(in->initial_state, elem_size(in->dtype))) return SSD_ERR_ALIGN;
@@ -125,7 +125,7 @@ int conv_check(const short_conv_inputs* in) {
 }
 
 size_t conv_space(int64_t batch, int64_t L, int64_t ch, int64_t W) {
-    return size_t(cls_short_conv_bwd_parts(batch, L)) * size_t(ch) * size_t(W + 1) * 4;
+    return size_t(cls_short_conv_bwd_parts(batch, L, ch)) * size_t(ch) * size_t(W + 1) * 4;
 }
 
 int cache_check(const void* h, const int32_t* slots, int64_t batch, int64_t rows, int64_t S, int64_t nslots, int format,

@@ -12,27 +12,22 @@ template <typename E, int V>
 struct Vec {
     typedef typename E::raw raw;
     typedef raw vec __attribute__((ext_vector_type(V)));
-    static __device__ __forceinline__ void load(const raw* p, float (&f)[V]) {
-        if constexpr (V == 1) {
-            f[0] = E::get(*p);
-        } else {
-            const vec v = *reinterpret_cast<const vec*>(p);
+    static __device__ __forceinline__ vec load_raw(const raw* p) { return *reinterpret_cast<const vec*>(p); }
+    static __device__ __forceinline__ void widen(vec v, float (&f)[V]) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const raw x = v[e];
-                f[e] = E::get(x);
-            }
+        for (int e = 0; e < V; ++e) {
+            const raw x = v[e];
+            f[e] = E::get(x);
         }
     }
+    static __device__ __forceinline__ void load(const raw* p, float (&f)[V]) {
+        widen(load_raw(p), f);
+    }
     static __device__ __forceinline__ void store(raw* p, const float (&f)[V]) {
-        if constexpr (V == 1) {
-            *p = E::put(f[0]);
-        } else {
-            vec v;
+        vec v;
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = E::put(f[e]);
-            *reinterpret_cast<vec*>(p) = v;
-        }
+        for (int e = 0; e < V; ++e) v[e] = E::put(f[e]);
+        *reinterpret_cast<vec*>(p) = v;
     }
     static __device__ __forceinline__ void zero(float (&f)[V]) {
 #pragma unroll
@@ -55,12 +50,13 @@ struct ConvParams {
     float* parts;  // [parts][ch][W + 1]
     void* dinit;
     float *dw, *dbias;
-    int batch, L, ch, nvec, chunks, silu;
+    int batch, L, ch, nvec, silu;
+    int run, chunks;  // tokens of a thread, and how many such runs a sequence has
+    int lanes;        // backward: threads of a workgroup side by side in the channels, a power of two
     int64_t nparts;
 };
 
-constexpr int kConvRun = 8;      // tokens of a thread, forward
-constexpr int kConvBwdRun = 32;  // and backward
+constexpr int kConvGroup = 4;    // tokens that the backward pass loads together
 
 // The input at token t of sequence b (t >= 1 - W), zeros before a sequence without a start.
 template <typename E, int V, int W>
@@ -71,156 +67,243 @@ __device__ __forceinline__ void conv_input(const ConvParams& p, int64_t b, int64
     else Vec<E, V>::zero(f);
 }
 
+// V channels' weights and biases are adjacent: whole vectors where V allows.
 template <int V, int W>
 __device__ __forceinline__ void conv_weights(const ConvParams& p, int c, float (&w)[W][V], float (&bias)[V]) {
+    if constexpr (V % 4 == 0) {
+        float flat[V * W];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
+        for (int i = 0; i < V * W / 4; ++i) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(p.w + int64_t(c) * W + 4 * i);
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[k][e] = p.w[int64_t(c + e) * W + k];
-        bias[e] = p.bias ? p.bias[c + e] : 0.0f;
+            for (int e = 0; e < 4; ++e) flat[4 * i + e] = v[e];
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][e] = flat[e * W + k];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const f32x4 v = p.bias ? *reinterpret_cast<const f32x4*>(p.bias + c + 4 * i) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bias[4 * i + e] = v[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][e] = p.w[int64_t(c + e) * W + k];
+            bias[e] = p.bias ? p.bias[c + e] : 0.0f;
+        }
     }
 }
 
-// A thread: V channels, kConvRun tokens.  The chunk after the last (of each
-// sequence) writes the final state.
-template <typename E, int V, int W>
+// A thread: V channels, RUN tokens, all of whose rows are loaded before the
+// first is used.  The chunk after the last (of each sequence) writes the final
+// state.
+template <typename E, int V, int W, int RUN>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p) {
     typedef typename E::raw raw;
-    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    const int per = p.chunks + (p.fin ? 1 : 0);
-    if (id >= int64_t(p.batch) * per * p.nvec) return;
-    const int c = int(id % p.nvec) * V;
-    const int64_t j = id / p.nvec;
+    typedef Vec<E, V> vec;
+    const uint32_t id = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t per = uint32_t(p.chunks) + (p.fin ? 1u : 0u);
+    const uint32_t j = id / uint32_t(p.nvec);
+    const int c = int(id % uint32_t(p.nvec)) * V;
     const int chunk = int(j % per);
     const int64_t b = j / per;
+    if (b >= p.batch) return;
     const int end = seq_end(p.seqlens, b, p.L);
     if (chunk == p.chunks) {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
             float f[V];
             conv_input<E, V, W>(p, b, int64_t(end) - (W - 1) + k, c, f);
-            Vec<E, V>::store(static_cast<raw*>(p.fin) + (b * (W - 1) + k) * p.ch + c, f);
+            vec::store(static_cast<raw*>(p.fin) + (b * (W - 1) + k) * p.ch + c, f);
         }
         return;
     }
-    float w[W][V], bias[V], x[kConvRun + W - 1][V];
-    conv_weights<V, W>(p, c, w, bias);
-    const int t0 = chunk * kConvRun;
+    const int t0 = chunk * RUN;
+    const raw* x = static_cast<const raw*>(p.x) + b * p.x_b + t0 * p.x_t + c;
+    raw* y = static_cast<raw*>(p.y) + (b * p.L + t0) * p.ch + c;
+    typename vec::vec rx[RUN];
+    float w[W][V], bias[V], win[W][V];  // win: the last W inputs, the newest last
 #pragma unroll
-    for (int i = 0; i < kConvRun + W - 1; ++i) {
-        const int t = t0 + i - (W - 1);
-        if (t < end) conv_input<E, V, W>(p, b, t, c, x[i]);
-        else Vec<E, V>::zero(x[i]);
-    }
+    for (int i = 0; i < RUN; ++i)
+        if (t0 + i < end) rx[i] = vec::load_raw(x + i * p.x_t);
 #pragma unroll
-    for (int i = 0; i < kConvRun; ++i) {
-        const int t = t0 + i;
-        if (t >= p.L) break;
-        float y[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float s = bias[e];
-#pragma unroll
-            for (int k = 0; k < W; ++k) s = fmaf(w[k][e], x[i + k][e], s);
-            if (p.silu) s *= sigmoid(s);
-            y[e] = t < end ? s : 0.0f;
-        }
-        Vec<E, V>::store(static_cast<raw*>(p.y) + (b * p.L + t) * p.ch + c, y);
-    }
-}
-
-// A thread: V channels, kConvBwdRun tokens of which it owns the weight
-// gradients and the input gradients W - 1 tokens earlier; it walks the W - 1
-// tokens behind its run for their dp, too.
-template <typename E, int V, int W>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
-    typedef typename E::raw raw;
-    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (id >= int64_t(p.batch) * p.chunks * p.nvec) return;
-    const int c = int(id % p.nvec) * V;
-    const int64_t part = id / p.nvec;
-    const int chunk = int(part % p.chunks);
-    const int64_t b = part / p.chunks;
-    const int end = seq_end(p.seqlens, b, p.L);
-    const int t0 = chunk * kConvBwdRun;
-    float w[W][V], bias[V], dw[W][V], db[V], x[W][V], dp[W][V];  // x, dp: of the last W tokens, the newest last
+    for (int k = 1; k < W; ++k) conv_input<E, V, W>(p, b, t0 - W + k, c, win[k]);
     conv_weights<V, W>(p, c, w, bias);
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-        Vec<E, V>::zero(dw[k]);
-        Vec<E, V>::zero(x[k]);
-        Vec<E, V>::zero(dp[k]);
-    }
-    Vec<E, V>::zero(db);
-    if (t0 < end) {
-#pragma unroll
-        for (int k = 1; k < W; ++k) conv_input<E, V, W>(p, b, t0 - W + k, c, x[k]);
-    }
-    for (int i = 0; i < kConvBwdRun + W - 1; ++i) {
-        const int s = t0 + i;
+    for (int i = 0; i < RUN; ++i) {
+        if (t0 + i >= p.L) break;
 #pragma unroll
         for (int k = 0; k + 1 < W; ++k)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                x[k][e] = x[k + 1][e];
-                dp[k][e] = dp[k + 1][e];
-            }
-        Vec<E, V>::zero(dp[W - 1]);
-        if (s < end) {
-            float g[V];
-            conv_input<E, V, W>(p, b, s, c, x[W - 1]);
-            Vec<E, V>::load(static_cast<const raw*>(p.dy) + b * p.dy_b + s * p.dy_t + c, g);
+            for (int e = 0; e < V; ++e) win[k][e] = win[k + 1][e];
+        float out[V];
+        vec::zero(out);
+        if (t0 + i < end) {
+            vec::widen(rx[i], win[W - 1]);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                float q = bias[e];
+                float s = bias[e];
 #pragma unroll
-                for (int k = 0; k < W; ++k) q = fmaf(w[k][e], x[k][e], q);
-                const float d = p.silu ? g[e] * dsilu(q, sigmoid(q)) : g[e];
-                dp[W - 1][e] = d;
-                if (i < kConvBwdRun) {
-                    db[e] += d;
-#pragma unroll
-                    for (int k = 0; k < W; ++k) dw[k][e] = fmaf(d, x[k][e], dw[k][e]);
-                }
+                for (int k = 0; k < W; ++k) s = fmaf(w[k][e], win[k][e], s);
+                out[e] = p.silu ? s * sigmoid(s) : s;
             }
         }
-        // the input that token s is the last to see
-        const int t = s - (W - 1);
-        if ((i < W - 1 && chunk > 0) || t >= p.L) continue;
-        float dx[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float v = 0.0f;
-#pragma unroll
-            for (int k = 0; k < W; ++k) v = fmaf(w[W - 1 - k][e], dp[k][e], v);
-            dx[e] = v;
-        }
-        const int kept = t - (end - (W - 1));  // its place in the final state
-        if (p.dfin && kept >= 0 && t < end) {
-            float f[V];
-            Vec<E, V>::load(static_cast<const raw*>(p.dfin) + (b * (W - 1) + kept) * p.ch + c, f);
-#pragma unroll
-            for (int e = 0; e < V; ++e) dx[e] += f[e];
-        }
-        if (t >= 0) Vec<E, V>::store(static_cast<raw*>(p.dx) + (b * p.L + t) * p.ch + c, dx);
-        else if (p.dinit) Vec<E, V>::store(static_cast<raw*>(p.dinit) + (b * (W - 1) + t + W - 1) * p.ch + c, dx);
-    }
-    float* out = p.parts + (part * p.ch + c) * (W + 1);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-#pragma unroll
-        for (int k = 0; k < W; ++k) out[e * (W + 1) + k] = dw[k][e];
-        out[e * (W + 1) + W] = db[e];
+        vec::store(y + i * int64_t(p.ch), out);
     }
 }
 
+// A thread: V channels and a run of tokens, of which it owns the weight
+// gradients and the input gradients W - 1 tokens earlier; it walks the W - 1
+// tokens behind its run for their dp, too.  Tokens come kConvGroup at a time,
+// loaded while the group before them is computed.  The weight gradients of a
+// workgroup's runs are added in LDS.
+template <typename E, int V, int W>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
+    typedef typename E::raw raw;
+    typedef Vec<E, V> vec;
+    constexpr int U = kConvGroup, Q = V * (W + 1);
+    __shared__ float s_part[256 * (Q + 1)];
+    const int runs = 256 / p.lanes;  // of a workgroup
+    const int blocks = (p.nvec + p.lanes - 1) / p.lanes;
+    const int v = int(blockIdx.x % uint32_t(blocks)) * p.lanes + int(threadIdx.x) % p.lanes;
+    const int64_t group = blockIdx.x / uint32_t(blocks);
+    const int64_t part = group * runs + int(threadIdx.x) / p.lanes;
+    const bool on = v < p.nvec && part < int64_t(p.batch) * p.chunks;
+    const int c = (v < p.nvec ? v : 0) * V;
+    const int chunk = on ? int(part % p.chunks) : 0;
+    const int64_t b = on ? part / p.chunks : 0;
+    float dw[W][V], db[V];
+#pragma unroll
+    for (int k = 0; k < W; ++k) vec::zero(dw[k]);
+    vec::zero(db);
+    if (on) {
+        const int end = seq_end(p.seqlens, b, p.L);
+        const int t0 = chunk * p.run;
+        float w[W][V], bias[V], x[W][V], dp[W][V];  // x, dp: of the last W tokens, the newest last
+        conv_weights<V, W>(p, c, w, bias);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            vec::zero(x[k]);
+            vec::zero(dp[k]);
+        }
+        if (t0 < end) {
+#pragma unroll
+            for (int k = 1; k < W; ++k) conv_input<E, V, W>(p, b, t0 - W + k, c, x[k]);
+        }
+        const raw* px = static_cast<const raw*>(p.x) + b * p.x_b + c;
+        const raw* pg = static_cast<const raw*>(p.dy) + b * p.dy_b + c;
+        typename vec::vec rx[U], rg[U];
+        auto load = [&](int s) {
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (s + i < end) {
+                    rx[i] = vec::load_raw(px + (s + i) * p.x_t);
+                    rg[i] = vec::load_raw(pg + (s + i) * p.dy_t);
+                }
+        };
+        load(t0);
+        for (int i0 = 0; i0 < p.run + W - 1; i0 += U) {
+            typename vec::vec cx[U], cg[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                cx[i] = rx[i];
+                cg[i] = rg[i];
+            }
+            if (i0 + U < p.run + W - 1) load(t0 + i0 + U);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int i = i0 + j, s = t0 + i;
+                if (i >= p.run + W - 1) break;
+#pragma unroll
+                for (int k = 0; k + 1 < W; ++k)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        x[k][e] = x[k + 1][e];
+                        dp[k][e] = dp[k + 1][e];
+                    }
+                vec::zero(dp[W - 1]);
+                if (s < end) {
+                    float g[V];
+                    vec::widen(cx[j], x[W - 1]);
+                    vec::widen(cg[j], g);
+                    const bool own = i < p.run;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        float q = bias[e];
+#pragma unroll
+                        for (int k = 0; k < W; ++k) q = fmaf(w[k][e], x[k][e], q);
+                        const float d = p.silu ? g[e] * dsilu(q, sigmoid(q)) : g[e];
+                        dp[W - 1][e] = d;
+                    }
+                    if (own) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            db[e] += dp[W - 1][e];
+#pragma unroll
+                            for (int k = 0; k < W; ++k) dw[k][e] = fmaf(dp[W - 1][e], x[k][e], dw[k][e]);
+                        }
+                    }
+                }
+                // the input that token s is the last to see
+                const int t = s - (W - 1);
+                if ((i < W - 1 && chunk > 0) || t >= p.L) continue;
+                float dx[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float a = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) a = fmaf(w[W - 1 - k][e], dp[k][e], a);
+                    dx[e] = a;
+                }
+                const int kept = t - (end - (W - 1));  // its place in the final state
+                if (p.dfin && kept >= 0 && t < end) {
+                    float f[V];
+                    vec::load(static_cast<const raw*>(p.dfin) + (b * (W - 1) + kept) * p.ch + c, f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) dx[e] += f[e];
+                }
+                if (t >= 0) vec::store(static_cast<raw*>(p.dx) + (b * p.L + t) * p.ch + c, dx);
+                else if (p.dinit) vec::store(static_cast<raw*>(p.dinit) + (b * (W - 1) + t + W - 1) * p.ch + c, dx);
+            }
+        }
+    }
+    float* mine = s_part + threadIdx.x * (Q + 1);  // an odd stride: lanes on different banks
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) mine[e * (W + 1) + k] = dw[k][e];
+        mine[e * (W + 1) + W] = db[e];
+    }
+    __syncthreads();
+    const int first = int(blockIdx.x % uint32_t(blocks)) * p.lanes;
+    for (int i = threadIdx.x; i < p.lanes * Q; i += 256) {
+        if (first + i / Q >= p.nvec) continue;
+        float s = 0.0f;
+        for (int r = 0; r < runs; ++r) s += s_part[(r * p.lanes + i / Q) * (Q + 1) + i % Q];
+        p.parts[(group * p.ch + first * V) * (W + 1) + i] = s;
+    }
+}
+
+// A workgroup: 64 adjacent values, its four waves a quarter of the parts each.
 template <int W>
 __global__ __launch_bounds__(256) void conv_bwd_sum_kernel(ConvParams p) {
+    __shared__ float s_sum[4][64];
     const int64_t per = int64_t(p.ch) * (W + 1);
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= per) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t i = int64_t(blockIdx.x) * 64 + lane;
     float s = 0.0f;
-    for (int64_t q = 0; q < p.nparts; ++q) s += p.parts[q * per + i];
+    if (i < per) {
+#pragma unroll 8
+        for (int64_t q = wave; q < p.nparts; q += 4) s += p.parts[q * per + i];
+    }
+    s_sum[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || i >= per) return;
+    s = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
     const int64_t ch = i / (W + 1);
     const int k = int(i % (W + 1));
     if (k < W) { if (p.dw) p.dw[ch * W + k] = s; }
@@ -256,46 +339,71 @@ int launched() { return hipGetLastError() == hipSuccess ? 0 : -7; }
 
 dim3 blocks_for(int64_t threads) { return dim3(uint32_t((threads + 255) / 256)); }
 
-template <typename E, int V, int W>
-int launch(int what, ConvParams p, hipStream_t s) {
+int conv_bwd_run(int64_t batch, int64_t L, int64_t ch) {
+    // about 256k threads of 4 channels where there is work for them (16 tokens each measured 44.5 us where 48 took 49.6)
+    const int64_t run = batch * L * ((ch + 3) / 4) / (int64_t(1) << 18) / 16 * 16;
+    return int(run < 16 ? 16 : run > 512 ? 512 : run);
+}
+
+enum { kFwd, kBwd, kStep };
+
+template <int WHAT, typename E, int V, int W>
+int launch(ConvParams p, hipStream_t s) {
     p.nvec = p.ch / V;
     const int64_t row = int64_t(p.batch) * p.nvec;
-    if (what == 0) {
-        hipLaunchKernelGGL((conv_fwd_kernel<E, V, W>), blocks_for(row * (p.chunks + (p.fin ? 1 : 0))), dim3(256), 0, s, p);
+    if constexpr (WHAT == kFwd) {
+        // 16 tokens to a thread read 1.2 rows for one; 4 where that leaves the device without waves
+        p.run = row * ((p.L + 15) / 16) >= (int64_t(1) << 17) ? 16 : 4;
+        p.chunks = (p.L + p.run - 1) / p.run;
+        const dim3 grid = blocks_for(row * (p.chunks + (p.fin ? 1 : 0)));
+        if (p.run == 16) hipLaunchKernelGGL((conv_fwd_kernel<E, V, W, 16>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((conv_fwd_kernel<E, V, W, 4>), grid, dim3(256), 0, s, p);
         return launched();
-    }
-    if (what == 2) {
+    } else if constexpr (WHAT == kStep) {
         hipLaunchKernelGGL((conv_step_kernel<E, V, W>), blocks_for(row), dim3(256), 0, s, p);
         return launched();
+    } else {
+        p.lanes = 64;
+        while (p.lanes > 1 && p.lanes / 2 >= p.nvec) p.lanes /= 2;
+        const int64_t runs = 256 / p.lanes;
+        p.nparts = (int64_t(p.batch) * p.chunks + runs - 1) / runs;
+        const int64_t blocks = (p.nvec + p.lanes - 1) / p.lanes;
+        hipLaunchKernelGGL((conv_bwd_kernel<E, V, W>), dim3(uint32_t(blocks * p.nparts)), dim3(256), 0, s, p);
+        if (launched() != 0) return -7;
+        hipLaunchKernelGGL((conv_bwd_sum_kernel<W>), dim3(uint32_t((int64_t(p.ch) * (W + 1) + 63) / 64)), dim3(256), 0, s,
+                           p);
+        return launched();
     }
-    hipLaunchKernelGGL((conv_bwd_kernel<E, V, W>), blocks_for(row * p.chunks), dim3(256), 0, s, p);
-    if (launched() != 0) return -7;
-    hipLaunchKernelGGL((conv_bwd_sum_kernel<W>), blocks_for(int64_t(p.ch) * (W + 1)), dim3(256), 0, s, p);
-    return launched();
 }
 
-template <typename E, int V>
-int launch_width(int what, int64_t W, const ConvParams& p, hipStream_t s) {
-    return W == 2 ? launch<E, V, 2>(what, p, s) : W == 3 ? launch<E, V, 3>(what, p, s) : launch<E, V, 4>(what, p, s);
+template <int WHAT, typename E, int V>
+int launch_width(int64_t W, const ConvParams& p, hipStream_t s) {
+    return W == 2   ? launch<WHAT, E, V, 2>(p, s)
+           : W == 3 ? launch<WHAT, E, V, 3>(p, s)
+                    : launch<WHAT, E, V, 4>(p, s);
 }
 
-// Whole 16-byte vectors where every row of every tensor starts on one.
-template <typename E>
-int launch_type(int what, int64_t W, const ConvParams& p, hipStream_t s) {
-    constexpr int V = 16 / int(sizeof(typename E::raw));
+// Whole vectors (16 bytes; 8 for 16-bit elements in the backward pass and the
+// step, whose registers and threads 4 channels suit better) where every row of
+// every tensor starts on one.
+template <int WHAT, typename E>
+int launch_type(int64_t W, const ConvParams& p, hipStream_t s) {
+    constexpr int V = WHAT == kFwd ? 16 / int(sizeof(typename E::raw)) : 4;
     uintptr_t at = 0;
     for (const void* q : {p.x, p.init, p.dy, p.dfin, static_cast<const void*>(p.y), static_cast<const void*>(p.fin),
-                          static_cast<const void*>(p.dx), static_cast<const void*>(p.dinit)})
+                          static_cast<const void*>(p.dx), static_cast<const void*>(p.dinit),
+                          static_cast<const void*>(p.w), static_cast<const void*>(p.bias)})
         at |= reinterpret_cast<uintptr_t>(q);
     const bool whole = at % 16 == 0 && p.ch % V == 0 && p.x_b % V == 0 && p.x_t % V == 0 && p.dy_b % V == 0 &&
                        p.dy_t % V == 0;
-    return whole ? launch_width<E, V>(what, W, p, s) : launch_width<E, 1>(what, W, p, s);
+    return whole ? launch_width<WHAT, E, V>(W, p, s) : launch_width<WHAT, E, 1>(W, p, s);
 }
 
-int launch_any(int what, const short_conv_inputs& in, const ConvParams& p, hipStream_t s) {
-    return in.dtype == 0 ? launch_type<ElemF32>(what, in.width, p, s)
-         : in.dtype == 1 ? launch_type<ElemBF16>(what, in.width, p, s)
-                         : launch_type<ElemF16>(what, in.width, p, s);
+template <int WHAT>
+int launch_any(const short_conv_inputs& in, const ConvParams& p, hipStream_t s) {
+    return in.dtype == 0   ? launch_type<WHAT, ElemF32>(in.width, p, s)
+           : in.dtype == 1 ? launch_type<WHAT, ElemBF16>(in.width, p, s)
+                           : launch_type<WHAT, ElemF16>(in.width, p, s);
 }
 
 ConvParams params(const short_conv_inputs& in) {
@@ -309,15 +417,15 @@ ConvParams params(const short_conv_inputs& in) {
 }  // namespace
 }  // namespace cls
 
-int64_t cls_short_conv_bwd_parts(int64_t batch, int64_t seqlen) {
-    return batch * ((seqlen + cls::kConvBwdRun - 1) / cls::kConvBwdRun);
+int64_t cls_short_conv_bwd_parts(int64_t batch, int64_t seqlen, int64_t channels) {
+    const int64_t run = cls::conv_bwd_run(batch, seqlen, channels);
+    return (batch * ((seqlen + run - 1) / run) + 3) / 4;  // a workgroup adds four runs at least
 }
 
 int cls_short_conv_fwd_launch(const short_conv_inputs& in, void* y, void* final_state, hipStream_t stream) {
     cls::ConvParams p = cls::params(in);
     p.y = y; p.fin = final_state;
-    p.chunks = (p.L + cls::kConvRun - 1) / cls::kConvRun;
-    return cls::launch_any(0, in, p, stream);
+    return cls::launch_any<cls::kFwd>(in, p, stream);
 }
 
 int cls_short_conv_bwd_launch(const short_conv_inputs& in, const void* dy, int64_t dy_batch, int64_t dy_token,
@@ -326,14 +434,14 @@ int cls_short_conv_bwd_launch(const short_conv_inputs& in, const void* dy, int64
     cls::ConvParams p = cls::params(in);
     p.dy = dy; p.dy_b = dy_batch; p.dy_t = dy_token; p.dfin = dfinal;
     p.dx = dx; p.dw = dweight; p.dbias = dbias; p.dinit = dinitial; p.parts = parts;
-    p.chunks = (p.L + cls::kConvBwdRun - 1) / cls::kConvBwdRun;
-    p.nparts = cls_short_conv_bwd_parts(in.batch, in.seqlen);
-    return cls::launch_any(1, in, p, stream);
+    p.run = cls::conv_bwd_run(in.batch, in.seqlen, in.channels);
+    p.chunks = (p.L + p.run - 1) / p.run;
+    return cls::launch_any<cls::kBwd>(in, p, stream);
 }
 
 int cls_short_conv_step_launch(const short_conv_inputs& in, void* state, void* y, hipStream_t stream) {
     cls::ConvParams p = cls::params(in);
     p.init = nullptr; p.x_t = 0;
     p.fin = state; p.y = y;
-    return cls::launch_any(2, in, p, stream);
+    return cls::launch_any<cls::kStep>(in, p, stream);
 }
