@@ -1,4 +1,6 @@
 // Selective scan, one token, on gfx950.
+#include <type_traits>
+
 #include "selective.hpp"
 
 #include "launch_selective.hpp"
@@ -10,66 +12,184 @@ struct StepArgs {
     selective_scan_inputs in;
     float* h;
     void* y;
+    uint32_t blocks;  // workgroups side by side in the channels
 };
 
-// LS lanes hold a channel's states, four each.
-template <typename E, int LS>
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// The sum over LS adjacent lanes, in all of them: within four, then mirrored halves and rows.
+template <int LS>
+__device__ __forceinline__ float sum_lanes(float v) {
+    if constexpr (LS > 1) v += dpp<0xb1>(v);
+    if constexpr (LS > 2) v += dpp<0x4e>(v);
+    if constexpr (LS > 4) v += dpp<0x141>(v);
+    if constexpr (LS > 8) v += dpp<0x128>(v);
+    return v;
+}
+
+// Lane R of the LS, to all of them.
+template <int LS, int R>
+__device__ __forceinline__ float from_lane(float v) {
+    if constexpr (LS == 1) return v;
+    else if constexpr (LS == 4) return dpp<R * 0x55>(v);
+    else return __shfl(v, int(threadIdx.x & 63 & ~(LS - 1)) + R, 64);
+}
+
+// four values from n on; WIDE: an aligned vector, else element by element below N
+template <bool WIDE>
+__device__ __forceinline__ f32x4 load4(const float* p, int n, int N) {
+    if constexpr (WIDE) {
+        return n < N ? *reinterpret_cast<const f32x4*>(p + n) : f32x4{0.f, 0.f, 0.f, 0.f};
+    } else {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = n + e < N ? p[n + e] : 0.0f;
+        return v;
+    }
+}
+
+template <typename E, bool WIDE>
+__device__ __forceinline__ f32x4 load_row(const void* base, int64_t at, int n, int N) {
+    typedef typename E::raw raw4 __attribute__((ext_vector_type(4)));
+    const typename E::raw* p = static_cast<const typename E::raw*>(base) + at;
+    f32x4 v;
+    if constexpr (WIDE) {
+        const raw4 q = *reinterpret_cast<const raw4*>(p + (n < N ? n : 0));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const typename E::raw x = q[e];
+            v[e] = E::get(x);
+        }
+        return v;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = E::get(p[n + e < N ? n + e : 0]);
+    return v;
+}
+
+// LS lanes hold a channel's states, four each; a thread has U sequences, whose
+// loads are in flight together and which share A.  Sequence r's step and gate
+// are computed by lane r of the LS alone and handed to the others.
+template <typename E, int LS, int U, bool WIDE>
 __global__ __launch_bounds__(256) void scan_step_kernel(StepArgs s) {
     typedef typename E::raw raw;
+    static_assert(U == 1 || LS >= U, "a lane to each sequence");
     const selective_scan_inputs& p = s.in;
     const int N = int(p.dstate), l = threadIdx.x % LS;
-    const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LS;  // (b, ch)
-    const bool on = row < p.batch * p.channels;
-    const int64_t at = on ? row : p.batch * p.channels - 1;
-    const int64_t b = at / p.channels;
-    const int ch = int(at % p.channels);
+    const int64_t b0 = int64_t(blockIdx.x / s.blocks) * U;
+    const int c = int(blockIdx.x % s.blocks) * (256 / LS) + int(threadIdx.x) / LS;
+    const bool on = c < p.channels;
+    const int ch = on ? c : int(p.channels) - 1;
     const int g = ch / int(p.channels / p.ngroups);
-    const float u = E::get(static_cast<const raw*>(p.u)[b * p.u_batch + ch]);
-    float d = E::get(static_cast<const raw*>(p.dt)[b * p.dt_batch + ch]) + (p.dt_bias ? p.dt_bias[ch] : 0.0f);
-    if (p.softplus) d = softplus(d);
-    const float du = d * u;
-    const raw* B = static_cast<const raw*>(p.B) + b * p.B_batch + g * p.B_group;
-    const raw* C = static_cast<const raw*>(p.C) + b * p.C_batch + g * p.C_group;
-    float y = 0.0f;
+    const int n = 4 * l;
+    const int64_t mine = b0 + (U > 1 ? l & (U - 1) : 0);
+    const int64_t bm = mine < p.batch ? mine : p.batch - 1;
+    const float u = E::get(static_cast<const raw*>(p.u)[bm * p.u_batch + ch]);
+    float d = E::get(static_cast<const raw*>(p.dt)[bm * p.dt_batch + ch]) + (p.dt_bias ? p.dt_bias[ch] : 0.0f);
+    const float z = p.z ? E::get(static_cast<const raw*>(p.z)[bm * p.z_batch + ch]) : 0.0f;
+    f32x4 h[U], B[U], C[U];
+#pragma unroll
+    for (int r = 0; r < U; ++r) {
+        const int64_t b = b0 + r < p.batch ? b0 + r : p.batch - 1;
+        const float* src = s.h + (b * p.channels + ch) * N;
+        if constexpr (WIDE) {
+            // each state is touched once a token: past the caches
+            h[r] = n < N ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(src + n)) : f32x4{0.f, 0.f, 0.f, 0.f};
+        } else {
+            h[r] = load4<false>(src, n, N);
+        }
+        B[r] = load_row<E, WIDE>(p.B, b * p.B_batch + g * p.B_group, n, N);
+        C[r] = load_row<E, WIDE>(p.C, b * p.C_batch + g * p.C_group, n, N);
+    }
+    f32x4 A2 = load4<WIDE>(p.A + int64_t(ch) * N, n, N);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const int n = l * 4 + e;
-        if (n >= N || !on) continue;
-        const float a = fexp2(d * p.A[int64_t(ch) * N + n] * kLog2e);
-        const float h = fmaf(a, s.h[at * N + n], du * E::get(B[n]));
-        s.h[at * N + n] = h;
-        y = fmaf(E::get(C[n]), h, y);
+        const float a = A2[e];
+        A2[e] = a * kLog2e;
     }
+    if (p.softplus) d = softplus(d);
+    const float du = d * u;
+    float y = 0.0f;
+    const auto row = [&](auto R) {
+        constexpr int r = decltype(R)::value;
+        const float dr = from_lane<LS, r>(d), dur = from_lane<LS, r>(du);
+        float part = 0.0f;
+        f32x4 hn;
 #pragma unroll
-    for (int o = LS / 2; o >= 1; o >>= 1) y += __shfl_xor(y, o, 64);
-    if (l == 0 && on) {
-        y = fmaf(p.D ? p.D[ch] : 0.0f, u, y);
-        if (p.z) {
-            const float z = E::get(static_cast<const raw*>(p.z)[b * p.z_batch + ch]);
-            y *= z * sigmoid(z);
+        for (int e = 0; e < 4; ++e) {
+            const float a2 = A2[e], ho = h[r][e], b = B[r][e], c4 = C[r][e];
+            const float v = fmaf(fexp2(dr * a2), ho, dur * b);
+            hn[e] = v;
+            if (n + e < N) part = fmaf(c4, v, part);
         }
-        static_cast<raw*>(s.y)[at] = E::put(y);
+        part = sum_lanes<LS>(part);
+        if (U == 1 || (l & (U - 1)) == r) y = part;
+        if (on && b0 + r < p.batch) {
+            float* dst = s.h + ((b0 + r) * p.channels + ch) * N + n;
+            if constexpr (WIDE) {
+                if (n < N) __builtin_nontemporal_store(hn, reinterpret_cast<f32x4*>(dst));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < N) dst[e] = hn[e];
+            }
+        }
+    };
+    row(std::integral_constant<int, 0>{});
+    if constexpr (U > 1) {
+        row(std::integral_constant<int, 1>{});
+        row(std::integral_constant<int, 2>{});
+        row(std::integral_constant<int, 3>{});
     }
+    if (l < U && on && mine < p.batch) {
+        y = fmaf(p.D ? p.D[ch] : 0.0f, u, y);
+        if (p.z) y *= z * sigmoid(z);
+        static_cast<raw*>(s.y)[mine * p.channels + ch] = E::put(y);
+    }
+}
+
+template <typename E, int LS>
+int launch_lanes(StepArgs s, hipStream_t stream) {
+    const selective_scan_inputs& in = s.in;
+    s.blocks = uint32_t((in.channels * LS + 255) / 256);
+    // whole vectors of four states where every row of A, B and C starts on one
+    const uint64_t at = reinterpret_cast<uintptr_t>(in.B) | reinterpret_cast<uintptr_t>(in.C) |
+                        uint64_t(in.B_batch | in.B_group | in.C_batch | in.C_group) * sizeof(typename E::raw);
+    const bool wide = in.dstate % 4 == 0 && reinterpret_cast<uintptr_t>(in.A) % 16 == 0 &&
+                      at % (4 * sizeof(typename E::raw)) == 0;
+    const int64_t four = s.blocks * ((in.batch + 3) / 4);
+    const dim3 one(uint32_t(s.blocks * in.batch));
+    if constexpr (LS >= 4) {
+        // four sequences to a thread where that still leaves every CU a few workgroups
+        if (four >= 1024) {
+            if (wide) hipLaunchKernelGGL((scan_step_kernel<E, LS, 4, true>), dim3(uint32_t(four)), dim3(256), 0, stream, s);
+            else hipLaunchKernelGGL((scan_step_kernel<E, LS, 4, false>), dim3(uint32_t(four)), dim3(256), 0, stream, s);
+            return hipGetLastError() == hipSuccess ? 0 : -7;
+        }
+    }
+    if (wide) hipLaunchKernelGGL((scan_step_kernel<E, LS, 1, true>), one, dim3(256), 0, stream, s);
+    else hipLaunchKernelGGL((scan_step_kernel<E, LS, 1, false>), one, dim3(256), 0, stream, s);
+    return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
 template <typename E>
 int launch_type(const StepArgs& s, hipStream_t stream) {
     const int64_t lanes = (s.in.dstate + 3) / 4;
-    const int64_t rows = s.in.batch * s.in.channels;
-    const auto grid = [&](int64_t ls) { return dim3(uint32_t((rows * ls + 255) / 256)); };
-    if (lanes <= 1) hipLaunchKernelGGL((scan_step_kernel<E, 1>), grid(1), dim3(256), 0, stream, s);
-    else if (lanes <= 2) hipLaunchKernelGGL((scan_step_kernel<E, 2>), grid(2), dim3(256), 0, stream, s);
-    else if (lanes <= 4) hipLaunchKernelGGL((scan_step_kernel<E, 4>), grid(4), dim3(256), 0, stream, s);
-    else if (lanes <= 8) hipLaunchKernelGGL((scan_step_kernel<E, 8>), grid(8), dim3(256), 0, stream, s);
-    else hipLaunchKernelGGL((scan_step_kernel<E, 16>), grid(16), dim3(256), 0, stream, s);
-    return hipGetLastError() == hipSuccess ? 0 : -7;
+    return lanes <= 1   ? launch_lanes<E, 1>(s, stream)
+           : lanes <= 2 ? launch_lanes<E, 2>(s, stream)
+           : lanes <= 4 ? launch_lanes<E, 4>(s, stream)
+           : lanes <= 8 ? launch_lanes<E, 8>(s, stream)
+                        : launch_lanes<E, 16>(s, stream);
 }
 
 }  // namespace
 }  // namespace cls
 
 int cls_selective_scan_step_launch(const selective_scan_inputs& in, float* h, void* y, hipStream_t stream) {
-    const cls::StepArgs s{in, h, y};
+    const cls::StepArgs s{in, h, y, 0};
     return in.dtype == 0 ? cls::launch_type<cls::ElemF32>(s, stream)
          : in.dtype == 1 ? cls::launch_type<cls::ElemBF16>(s, stream)
                          : cls::launch_type<cls::ElemF16>(s, stream);

@@ -245,7 +245,8 @@ def test_scan_on_a_side_stream_and_in_a_graph():
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("nb,ch,N,G", [(1, 1, 1, 1), (3, 65, 16, 1), (2, 48, 5, 2), (5, 130, 20, 1), (2, 64, 64, 4),
-                                       (70, 192, 16, 1), (2, 24, 3, 3)])
+                                       (70, 192, 16, 1), (2, 24, 3, 3),
+                                       (87, 3001, 16, 1), (50, 2700, 18, 1)])
 def test_scan_step(nb, ch, N, G, kind):
     print(f"[scan step] {nb} {ch} {N} {G} {kind}", flush=True)
     c = scan_case(20 + nb + N, nb, 1, ch, N, G, kind=kind, start=True)
