@@ -63,55 +63,86 @@ __device__ __forceinline__ f32x4 load4(const float* row, int s, int S) {
     }
 }
 
-template <bool FP8, bool WIDE, int LS>
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    const uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, true));
+    return o > v ? o : v;
+}
+
+// The largest of LS adjacent lanes, in all of them: within rows of 16 lanes, then across rows.
+template <int LS>
+__device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
+    if constexpr (LS > 1) v = dpp_max<0xb1>(v);
+    if constexpr (LS > 2) v = dpp_max<0x4e>(v);
+    if constexpr (LS > 4) v = dpp_max<0x141>(v);
+    if constexpr (LS > 8) v = dpp_max<0x128>(v);
+    if constexpr (LS > 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = r[0] > r[1] ? r[0] : r[1];
+    }
+    if constexpr (LS > 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = r[0] > r[1] ? r[0] : r[1];
+    }
+    return v;
+}
+
+// A thread has a part of U rows, 256 / LS apart, whose loads are in flight together.
+template <bool FP8, bool WIDE, int LS, int U>
 __global__ __launch_bounds__(256) void cache_write_kernel(CacheParams p) {
-    const int64_t b = blockIdx.x / p.blocks, blk = blockIdx.x % p.blocks;
+    const int64_t b = blockIdx.x / uint32_t(p.blocks), blk = blockIdx.x % uint32_t(p.blocks);
+    const int l = threadIdx.x % LS;
+    const int64_t r0 = blk * (U * 256 / LS) + threadIdx.x / LS;
+    f32x4 v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int64_t r = r0 + i * (256 / LS);
+        v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (r < p.rows) v[i] = load4<WIDE>(p.h + (b * p.rows + r) * p.S, 4 * l, p.S);
+    }
     const int slot = p.slots[b];
     if (slot < 0 || slot >= p.nslots) return;
     // a later state that names the slot is the one to keep
     bool later = false;
     for (int i = int(b) + 1 + int(threadIdx.x); i < p.batch; i += 256) later |= p.slots[i] == slot;
     if (__syncthreads_or(later)) return;
-    const int l = threadIdx.x % LS;
-    const int64_t r = (blk * 256 + threadIdx.x) / LS;
-    if (r >= p.rows) return;
-    const f32x4 v = load4<WIDE>(p.h + (b * p.rows + r) * p.S, 4 * l, p.S);
-    // the largest magnitude by its bits: NaN is above infinity
-    uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float f = v[e];
-        const uint32_t a = as_uint(f) & 0x7fffffffu;
-        m = a > m ? a : m;
-    }
+    for (int i = 0; i < U; ++i) {
+        const int64_t r = r0 + i * (256 / LS);
+        // the largest magnitude by its bits: NaN is above infinity
+        uint32_t m = 0;
 #pragma unroll
-    for (int o = LS / 2; o >= 1; o >>= 1) {
-        const uint32_t a = __shfl_xor(m, o, 64);
-        m = a > m ? a : m;
-    }
-    const float top = FP8 ? 448.0f : 127.0f, big = as_float(m);
-    const bool held = !(big < kCacheSmallest);
-    const float scale = m >= 0x7f800000u ? as_float(0x7fc00000u) : held ? big / top : 0.0f;  // not finite: NaN
-    const float inv = held ? top / big : 0.0f;
-    const int64_t at = int64_t(slot) * p.rows + r;
-    if (l == 0) p.scales[at] = scale;
-    f32x4 q;
+        for (int e = 0; e < 4; ++e) {
+            const float f = v[i][e];
+            const uint32_t a = as_uint(f) & 0x7fffffffu;
+            m = a > m ? a : m;
+        }
+        m = max_lanes<LS>(m);
+        const float top = FP8 ? 448.0f : 127.0f, big = as_float(m);
+        const bool held = !(big < kCacheSmallest);
+        const float scale = m >= 0x7f800000u ? as_float(0x7fc00000u) : held ? big / top : 0.0f;  // not finite: NaN
+        const float inv = held ? top / big : 0.0f;
+        if (r >= p.rows) continue;
+        const int64_t at = int64_t(slot) * p.rows + r;
+        if (l == 0) p.scales[at] = scale;
+        f32x4 q;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = v[e] * inv;
-    const uint32_t bits = pack4<FP8>(q);
-    uint8_t* out = p.cache + at * p.S + 4 * l;
-    if constexpr (WIDE) {
-        if (4 * l < p.S) *reinterpret_cast<uint32_t*>(out) = bits;
-    } else {
+        for (int e = 0; e < 4; ++e) q[e] = v[i][e] * inv;
+        const uint32_t bits = pack4<FP8>(q);
+        uint8_t* out = p.cache + at * p.S + 4 * l;
+        if constexpr (WIDE) {
+            if (4 * l < p.S) *reinterpret_cast<uint32_t*>(out) = bits;
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (4 * l + e < p.S) out[e] = uint8_t(bits >> (8 * e));
+            for (int e = 0; e < 4; ++e)
+                if (4 * l + e < p.S) out[e] = uint8_t(bits >> (8 * e));
+        }
     }
 }
 
 template <bool FP8, bool WIDE, int LS>
 __global__ __launch_bounds__(256) void cache_read_kernel(CacheParams p) {
-    const int64_t b = blockIdx.x / p.blocks, blk = blockIdx.x % p.blocks;
+    const int64_t b = blockIdx.x / uint32_t(p.blocks), blk = blockIdx.x % uint32_t(p.blocks);
     const int slot = p.slots[b];
     const bool held = slot >= 0 && slot < p.nslots;
     const int l = threadIdx.x % LS;
@@ -146,10 +177,18 @@ __global__ __launch_bounds__(256) void cache_read_kernel(CacheParams p) {
 
 template <bool READ, bool FP8, bool WIDE, int LS>
 int launch(CacheParams p, hipStream_t s) {
-    p.blocks = (p.rows * LS + 255) / 256;
-    const dim3 grid(uint32_t(p.blocks * p.batch));
-    if constexpr (READ) hipLaunchKernelGGL((cache_read_kernel<FP8, WIDE, LS>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((cache_write_kernel<FP8, WIDE, LS>), grid, dim3(256), 0, s, p);
+    const auto blocks = [&](int64_t u) { return (p.rows + u * (256 / LS) - 1) / (u * (256 / LS)); };
+    p.blocks = blocks(1);
+    if constexpr (READ) {
+        hipLaunchKernelGGL((cache_read_kernel<FP8, WIDE, LS>), dim3(uint32_t(p.blocks * p.batch)), dim3(256), 0, s, p);
+    } else if (blocks(4) * p.batch >= 1024) {
+        // four rows to a thread where that leaves every CU a few workgroups: 32 states of 5120 rows of 128 in 21-23 us
+        // for 26 us with one, 4 states of 1536 rows of 16 in 4.2 for 3.2
+        p.blocks = blocks(4);
+        hipLaunchKernelGGL((cache_write_kernel<FP8, WIDE, LS, 4>), dim3(uint32_t(p.blocks * p.batch)), dim3(256), 0, s, p);
+    } else {
+        hipLaunchKernelGGL((cache_write_kernel<FP8, WIDE, LS, 1>), dim3(uint32_t(p.blocks * p.batch)), dim3(256), 0, s, p);
+    }
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 

@@ -364,7 +364,7 @@ CACHE = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("shape", [(1, 1, 1), (3, 5, 16), (2, 4, 64, 128), (2, 7, 3), (4, 33, 256), (2, 9, 100),
-                                   (3, 70, 20), (1, 3, 250), (2, 64, 8), (2, 40, 64)])
+                                   (3, 70, 20), (1, 3, 250), (2, 64, 8), (2, 40, 64), (37, 1003, 100)])
 def test_cache_bytes_and_scales(shape, kind):
     print(f"[cache] {shape} {kind}", flush=True)
     g = torch.Generator().manual_seed(40 + sum(shape))
