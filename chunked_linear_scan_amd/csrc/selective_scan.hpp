@@ -58,13 +58,18 @@ struct ScanParams {
     float* part_a;   // [batch * nseg][N + 2][ch]: dA, then dD, then ddt_bias
 };
 
-// An element at a wave-uniform pointer and a lane's byte offset.
+// An element at a wave-uniform pointer and a lane's byte offset.  The empty
+// statement keeps the offset a 32-bit register in the block that uses it, where
+// the compiler can see that the access takes it as such; widened once and for
+// all ahead of a loop, it would cost 64-bit address arithmetic at every access.
 template <typename T>
 __device__ __forceinline__ const T& at_bytes(const T* p, uint32_t bytes) {
+    asm volatile("" : "+v"(bytes));
     return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + bytes);
 }
 template <typename T>
 __device__ __forceinline__ T& at_bytes(T* p, uint32_t bytes) {
+    asm volatile("" : "+v"(bytes));
     return *reinterpret_cast<T*>(reinterpret_cast<char*>(p) + bytes);
 }
 
