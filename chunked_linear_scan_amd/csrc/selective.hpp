@@ -32,15 +32,16 @@ __device__ __forceinline__ float fexp(float x) { return fexp2(x * kLog2e); }
 // reciprocal is the right 0.
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + fexp(-x)); }
 
-// log(1 + exp(x)) = max(x, 0) + log1p(e) with e = exp(-|x|) <= 1.  log1p(e) is
-// log(w) e / (w - 1) with w = 1 + e rounded (Kahan): the rounding of w cancels,
-// so tiny steps keep their relative accuracy.
-__device__ __forceinline__ float softplus(float x) {
-    const float e = fexp(-fabsf(x));
-    const float w = 1.0f + e;
-    const float d = w - 1.0f;
-    const float l = __builtin_amdgcn_logf(w) * kLn2 * (e * __builtin_amdgcn_rcpf(d));
-    return fmaxf(x, 0.0f) + (d == 0.0f ? e : l);  // the maximum drops a NaN, the other term does not
+// log(1 + exp(x)) = max(x, 0) + log(1 + t) with t = exp(-|x|) <= 1.  What the
+// rounding of w = 1 + t lost, t - (w - 1), is exact and comes back to first
+// order, over w: tiny steps keep their relative accuracy.  s: sigmoid(x), the
+// derivative, from the same t and 1 / w.
+__device__ __forceinline__ float softplus(float x, float* s = nullptr) {
+    const float t = fexp(-fabsf(x));
+    const float w = 1.0f + t;
+    const float rw = __builtin_amdgcn_rcpf(w);
+    if (s) *s = x < 0.0f ? t * rw : rw;
+    return fmaxf(x, 0.0f) + fmaf(__builtin_amdgcn_logf(w), kLn2, (t - (w - 1.0f)) * rw);
 }
 
 // d silu(x) / dx with s = sigmoid(x)

@@ -123,16 +123,18 @@ __global__ __launch_bounds__(NW * 64, scan_bwd_waves(NW, AGG)) void scan_bwd_ker
 #pragma unroll
             for (int k = 0; k < K; ++k) hin[k] = n0 + k < p.N ? at_bytes(ckpt + k * p.ch, ch * 4) : 0.0f;
         }
-        float uc[R], zc[R], xc[R], dc[R], oc[R], gc[R];
+        float uc[R], zc[R], sz[R], sx[R], dc[R], oc[R], gc[R];  // sz, sx: the sigmoids of z and of dt + bias
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = wave + r * NW;
             uc[r] = E::get(ru[r]);
             zc[r] = E::get(rz[r]);
             oc[r] = E::get(rdy[r]);
-            xc[r] = E::get(rdt[r]) + bias;
-            dc[r] = p.softplus ? softplus(xc[r]) : xc[r];
-            gc[r] = Z ? oc[r] * zc[r] * sigmoid(zc[r]) : oc[r];
+            dc[r] = E::get(rdt[r]) + bias;
+            sx[r] = 1.0f;
+            if (p.softplus) dc[r] = softplus(dc[r], &sx[r]);
+            sz[r] = Z ? sigmoid(zc[r]) : 1.0f;
+            gc[r] = Z ? oc[r] * zc[r] * sz[r] : oc[r];
             float d = dc[r], s = dc[r] * uc[r], gy = gc[r];
             if (row >= nt) d = 0.0f;
             if (row >= nt || !on) s = gy = 0.0f;  // nothing of a lane without a channel in the sums over the lanes
@@ -229,15 +231,14 @@ __global__ __launch_bounds__(NW * 64, scan_bwd_waves(NW, AGG)) void scan_bwd_ker
                     to_dt += s_p[w][1][row][lane];
                     if constexpr (Z) y += s_p[w][2][row][lane];
                 }
-                float d = fmaf(uc[r], to_sig, to_dt * kLn2);  // A2 is A log2(e)
-                if (p.softplus) d *= sigmoid(xc[r]);
+                const float d = fmaf(uc[r], to_sig, to_dt * kLn2) * sx[r];  // A2 is A log2(e)
                 dbias += d;
                 dD = fmaf(gc[r], uc[r], dD);
                 if (!on) continue;
                 const int64_t o = int64_t(row) * p.ch;
                 at_bytes(du + o, lane_off) = E::put(fmaf(Dc, gc[r], dc[r] * to_sig));
                 at_bytes(ddt + o, lane_off) = E::put(d);
-                if (Z) at_bytes(dz + o, lane_off) = E::put(oc[r] * y * dsilu(zc[r], sigmoid(zc[r])));
+                if (Z) at_bytes(dz + o, lane_off) = E::put(oc[r] * y * dsilu(zc[r], sz[r]));
             }
             du -= int64_t(TT) * p.ch;
             ddt -= int64_t(TT) * p.ch;
