@@ -285,43 +285,55 @@ __global__ __launch_bounds__(NW * 64, scan_bwd_waves(NW, AGG)) void scan_bwd_ker
     }
 }
 
-// dB and dC: the sums of the group's channel blocks, one thread per value.
+// The sums that are left.  The first `blocks_a` workgroups: dA, dD and
+// ddt_bias over sequences and segments, 64 adjacent values each, a quarter of
+// the summands to a wave.  The others: dB and dC over the group's channel
+// blocks, a thread to a value.
 template <typename E>
-__global__ __launch_bounds__(256) void scan_bwd_bc_kernel(ScanParams p) {
+__global__ __launch_bounds__(256) void scan_bwd_sums_kernel(ScanParams p, uint32_t blocks_a) {
     typedef typename E::raw raw;
-    const int64_t per = int64_t(p.batch) * p.L * p.G * 2 * p.N;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < per; i += int64_t(gridDim.x) * 256) {
-        const int n = int(i % p.N);
-        const int64_t j = i / p.N, row = j >> 1;  // row: (b, t, g)
-        const int64_t bt = row / p.G;
+    if (blockIdx.x < blocks_a) {
+        __shared__ float s_sum[4][64];
+        const int64_t per = int64_t(p.N + 2) * p.ch;
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int64_t i = int64_t(blockIdx.x) * 64 + lane;
+        const int rows = p.batch * p.nseg;
         float s = 0.0f;
-        if (bt % p.L < seq_end(p.seqlens, bt / p.L, p.L))
-            for (int c = 0; c < p.bpg; ++c) s += p.part_bc[int64_t(c) * per + i];
-        static_cast<raw*>(j & 1 ? p.dC : p.dB)[row * p.N + n] = E::put(s);
-    }
-}
-
-// dA, dD, ddt_bias: the sums over sequences and segments.  A workgroup has 64
-// adjacent values, its four waves a quarter of the summands each.
-__global__ __launch_bounds__(256) void scan_bwd_a_kernel(ScanParams p) {
-    __shared__ float s_sum[4][64];
-    const int64_t per = int64_t(p.N + 2) * p.ch;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t i = int64_t(blockIdx.x) * 64 + lane;
-    const int rows = p.batch * p.nseg;
-    float s = 0.0f;
-    if (i < per) {
+        if (i < per) {
 #pragma unroll 8
-        for (int q = wave; q < rows; q += 4) s += p.part_a[q * per + i];
+            for (int q = wave; q < rows; q += 4) s += p.part_a[q * per + i];
+        }
+        s_sum[wave][lane] = s;
+        __syncthreads();
+        if (wave != 0 || i >= per) return;
+        s = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+        const int ch = int(i % p.ch), r = int(i / p.ch);
+        if (r < p.N) p.dA[int64_t(ch) * p.N + r] = s;
+        else if (r == p.N) { if (p.dD) p.dD[ch] = s; }
+        else if (p.dbias) p.dbias[ch] = s;
+        return;
     }
-    s_sum[wave][lane] = s;
-    __syncthreads();
-    if (wave != 0 || i >= per) return;
-    s = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
-    const int ch = int(i % p.ch), r = int(i / p.ch);
-    if (r < p.N) p.dA[int64_t(ch) * p.N + r] = s;
-    else if (r == p.N) { if (p.dD) p.dD[ch] = s; }
-    else if (p.dbias) p.dbias[ch] = s;
+    const int64_t per = int64_t(p.batch) * p.L * p.G * 2 * p.N;
+    const int64_t step = int64_t(gridDim.x - blocks_a) * 256;
+    for (int64_t base = int64_t(blockIdx.x - blocks_a) * 256; base < per; base += step) {
+        const int64_t i = base + threadIdx.x;
+        if (i >= per) return;
+        // the row (b, t, g) of the workgroup's first value, and from there in 32 bits
+        const uint32_t j = uint32_t(base % (2 * p.N)) + threadIdx.x;
+        const int64_t row = base / (2 * p.N) + j / uint32_t(2 * p.N);
+        const uint32_t at = j % uint32_t(2 * p.N), n = at % uint32_t(p.N);
+        bool counts = true;
+        if (p.seqlens) {
+            const int64_t bt = row / p.G;
+            counts = bt % p.L < seq_end(p.seqlens, bt / p.L, p.L);
+        }
+        float s = 0.0f;
+        if (counts) {
+#pragma unroll 8
+            for (int c = 0; c < p.bpg; ++c) s += p.part_bc[int64_t(c) * per + i];
+        }
+        static_cast<raw*>(at < uint32_t(p.N) ? p.dB : p.dC)[row * p.N + n] = E::put(s);
+    }
 }
 
 template <typename E, int NW, bool Z>
@@ -334,12 +346,10 @@ int launch_bwd(const ScanParams& p, hipStream_t stream) {
     }
     hipLaunchKernelGGL((scan_bwd_kernel<E, NW, false, Z>), dim3(per_seg * uint32_t(p.nseg)), block, 0, stream, p);
     if (hipGetLastError() != hipSuccess) return -7;
-    const int64_t values = int64_t(p.batch) * p.L * p.G * 2 * p.N;
-    const int64_t blocks = (values + 255) / 256;
-    hipLaunchKernelGGL((scan_bwd_bc_kernel<E>), dim3(uint32_t(blocks < 65536 ? blocks : 65536)), dim3(256), 0, stream, p);
-    if (hipGetLastError() != hipSuccess) return -7;
-    const int64_t per = int64_t(p.N + 2) * p.ch;
-    hipLaunchKernelGGL(scan_bwd_a_kernel, dim3(uint32_t((per + 63) / 64)), dim3(256), 0, stream, p);
+    const int64_t blocks_bc = (int64_t(p.batch) * p.L * p.G * 2 * p.N + 255) / 256;
+    const uint32_t blocks_a = uint32_t((int64_t(p.N + 2) * p.ch + 63) / 64);
+    hipLaunchKernelGGL((scan_bwd_sums_kernel<E>), dim3(blocks_a + uint32_t(blocks_bc < 65536 ? blocks_bc : 65536)),
+                       dim3(256), 0, stream, p, blocks_a);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 

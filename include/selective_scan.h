@@ -59,8 +59,9 @@ extern "C" {
  *              selective_scan_checkpoint_size bytes (NULL = not written): the
  *              state before every 8th token
  * dstate is 1..64 (SSD_ERR_UNSUPPORTED above), channels a multiple of
- * ngroups.  Decays above 1 (A > 0) are evaluated as they are.  Outputs must
- * not alias inputs.
+ * ngroups.  Decays above 1 (A > 0) are evaluated as they are.  An input that is
+ * not finite reaches its own channel's later outputs only (B and C: those of
+ * their group), which it makes infinite or NaN.  Outputs must not alias inputs.
  */
 typedef struct {
     int64_t batch, seqlen, channels, dstate, ngroups;

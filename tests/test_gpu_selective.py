@@ -194,6 +194,27 @@ def test_scan_inputs_shared_by_all_sequences():
     assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
 
 
+def test_scan_rows_far_apart():
+    """Sequences and tokens whose offsets pass 32 bits (in elements) within a large buffer."""
+    c = scan_case(17, 2, 70, 64, 16, 1, kind="bf16")
+    d = on_gpu(c)
+    base = torch.empty((1 << 32) + 70 * (1 << 25), dtype=torch.bfloat16, device="cuda")
+
+    def far(v, at):
+        f = base[at:].as_strided(v.shape, ((1 << 32), 1 << 25, *v.stride()[2:])) if v.dim() == 3 else base[at:].as_strided(
+            v.shape, (1 << 32, 1 << 25, 16, 1))
+        f.copy_(v)
+        return f
+
+    wide = {k: far(d[k], i * 4096) for i, k in enumerate(("u", "dt", "z", "B", "C", "dy"))}
+    runs = []
+    for a in (d, {**d, **wide}):
+        args = [a[k] for k in SCAN_KEYS]
+        y, h, kept = cls.selective_scan(*args, want_checkpoints=True)
+        runs.append([y, h, *cls.selective_scan_bwd(a["dy"], *args, checkpoints=kept).values()])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
 def test_scan_same_bits_every_run_and_stale_memory():
     """Gradients, too: no atomics.  Workspaces and outputs come from memory that held something else."""
     c = on_gpu(scan_case(15, 2, 400, 100, 16, 1, kind="bf16", start=True, ragged=True))
@@ -307,6 +328,41 @@ def test_conv(nb, L, ch, W, kind):
     check_conv(conv_case(30 + L, nb, L, ch, W, kind), label=f"{nb} {L} {ch} {W} {kind}")
 
 
+@pytest.mark.parametrize("nb,L,ch,W", [(4, 2050, 2048, 4), (1, 4097, 513, 3)])
+def test_conv_in_runs_of_16(nb, L, ch, W):
+    """Enough work for runs of 16 tokens forward, in whole vectors and channel by channel."""
+    print(f"[conv] {nb} {L} {ch} {W}", flush=True)
+    check_conv(conv_case(35, nb, L, ch, W, "bf16", ragged=True), label=f"{nb} {L} {ch} {W}")
+
+
+def test_conv_gradients_in_long_runs():
+    """Enough work for backward runs of 32 tokens, against float64 on whole tensors."""
+    g = torch.Generator(device="cuda").manual_seed(36)
+    nb, L, ch, W = 2, 4101, 4100, 4
+    x, dy = (torch.randn(nb, L, ch, generator=g, device="cuda") for _ in range(2))
+    w, b = torch.randn(ch, W, generator=g, device="cuda"), torch.randn(ch, generator=g, device="cuda")
+    got = cls.short_conv_bwd(dy, x, w, b)
+    pad = torch.zeros(nb, W - 1, ch, dtype=torch.float64, device="cuda")
+    xp = torch.cat([pad, x.double()], 1)
+    p = b.double() + sum(w[:, k].double() * xp[:, k:k + L] for k in range(W))
+    s = torch.sigmoid(p)
+    dp = dy.double() * s * (1 + p * (1 - s))
+    dpp = torch.cat([dp, pad], 1)
+    dx = sum(w[:, k].double() * dpp[:, W - 1 - k:W - 1 - k + L] for k in range(W))
+    # dp: 16 u of its largest term, the W + 2 roundings of p through a slope below 1/2; then W products and sums
+    big = sum(w[:, k].double().abs() * xp[:, k:k + L].abs() for k in range(W)) + b.double().abs()
+    e = dy.double().abs() * (16 * s * (1 + p.abs()) + 0.5 * (W + 2) * big)
+    ep, ap = (torch.cat([v, pad], 1) for v in (e, dp.abs()))
+    bound = sum(w[:, k].double().abs() * (ep + 8 * ap)[:, W - 1 - k:W - 1 - k + L] for k in range(W))
+    assert ((got["dx"].double() - dx).abs() <= 2 * U * bound + U * dx.abs()).all()
+    for k in range(W):
+        want, terms = (dp * xp[:, k:k + L]).sum((0, 1)), (dp * xp[:, k:k + L]).abs().sum((0, 1))
+        err = (e * xp[:, k:k + L].abs()).sum((0, 1))
+        # sums of 512 parts of 32 tokens: at most 640 additions deep
+        assert ((got["dweight"][:, k].double() - want).abs() <= 2 * U * (err + 640 * terms)).all(), k
+    assert ((got["dbias"].double() - dp.sum((0, 1))).abs() <= 2 * U * (e + 640 * dp.abs()).sum((0, 1))).all()
+
+
 @pytest.mark.parametrize("off", ["bias", "start", "silu", "aligned", "none"])
 def test_conv_options(off):
     print(f"[conv] without {off}", flush=True)
@@ -402,6 +458,21 @@ def test_cache_slots_out_of_range_and_named_twice(kind):
     back = cls.state_cache_read(cache, scales, torch.tensor([2, -1, 3, 2, 1], dtype=torch.int32, device="cuda"))
     assert torch.equal(back[0], back[3]) and back[0].any() and not back[1].any() and not back[2].any()
     assert not back[4].any()
+
+
+def test_cache_past_32_bits():
+    """Slots whose bytes lie beyond 4 GiB."""
+    nslots, rows, S = 70000, 4096, 16
+    cache = torch.empty(nslots, rows, S, dtype=torch.int8, device="cuda")
+    scales = torch.empty(nslots, rows, device="cuda")
+    h = torch.randn(2, rows, S, generator=torch.Generator().manual_seed(43)).cuda()
+    slots = torch.tensor([nslots - 1, 0], dtype=torch.int32, device="cuda")
+    cls.state_cache_write(h, cache, scales, slots)
+    small, smalls = torch.zeros(2, rows, S, dtype=torch.int8, device="cuda"), torch.zeros(2, rows, device="cuda")
+    cls.state_cache_write(h, small, smalls, torch.tensor([0, 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(cache[nslots - 1], small[0]) and torch.equal(cache[0], small[1])
+    back = cls.state_cache_read(cache, scales, slots)
+    assert torch.equal(back, cls.state_cache_read(small, smalls, torch.tensor([0, 1], dtype=torch.int32, device="cuda")))
 
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
