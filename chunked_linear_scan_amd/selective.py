@@ -100,6 +100,14 @@ def _run(what, device, f, *args) -> None:
         raise SSDError(status, what)
 
 
+# Outputs: the forms of torch.empty that take the least time to call.
+_DENSE = torch.contiguous_format
+
+
+def _like(t):
+    return torch.empty_like(t, memory_format=_DENSE)
+
+
 def _check(name, t, device, dtype, shape, strided=False):
     try:
         if t.dtype is dtype and t.shape == shape and t.device == device and (
@@ -203,12 +211,12 @@ def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, seqlen
     n, _, ch, N, _ = sizes
     dev, f32 = u.device, torch.float32
     if out is None:
-        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+        y = _like(u)
     else:
         y = out
         _check("out", y, dev, u.dtype, u.shape)
-    hf = torch.empty((n, ch, N), dtype=f32, device=dev) if want_final_state else None
-    kept = torch.empty(_checkpoint_shape(lib, sizes), dtype=f32, device=dev) if want_checkpoints else None
+    hf = torch.empty(n, ch, N, dtype=f32, device=dev) if want_final_state else None
+    kept = torch.empty(*_checkpoint_shape(lib, sizes), dtype=f32, device=dev) if want_checkpoints else None
     need = lib.selective_scan_workspace_size(*sizes)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _run("selective_scan", dev, lib.selective_scan_fwd, s, y.data_ptr(), _at(hf), _at(kept), _at(ws), need)
@@ -233,21 +241,19 @@ def selective_scan_bwd(dy, u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None
     _check("checkpoints", checkpoints, dev, f32, _checkpoint_shape(lib, sizes))
     if dh_final is not None:
         _check("dh_final", dh_final, dev, f32, (n, ch, N))
-    like = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
-    got = {"du": like(u.shape, u.dtype), "ddt": like(u.shape, u.dtype), "dA": like(A.shape, f32),
-           "dB": like(B.shape, u.dtype), "dC": like(C.shape, u.dtype)}
+    got = {"du": _like(u), "ddt": _like(u), "dA": _like(A), "dB": _like(B), "dC": _like(C)}
     if D is not None:
-        got["dD"] = like(D.shape, f32)
+        got["dD"] = _like(D)
     if z is not None:
-        got["dz"] = like(u.shape, u.dtype)
+        got["dz"] = _like(u)
     if dt_bias is not None:
-        got["ddt_bias"] = like(dt_bias.shape, f32)
+        got["ddt_bias"] = _like(dt_bias)
     if h0 is not None:
-        got["dh0"] = like((n, ch, N), f32)
+        got["dh0"] = _like(h0)
     g = _PACK_GRADS.pack(dy.data_ptr(), dy.stride(0), dy.stride(1), _at(dh_final), checkpoints.data_ptr(),
                          *(_at(got.get(k)) for k in ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0")))
     need = max(lib.selective_scan_bwd_workspace_size(*sizes), 16)
-    ws = like((need,), torch.uint8)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _run("selective_scan_bwd", dev, lib.selective_scan_bwd, s, g, ws.data_ptr(), need)
     return got
 
@@ -262,7 +268,7 @@ def selective_scan_step(h, u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
     dev = u.device
     _check("h", h, dev, torch.float32, (n, ch, N))
     if out is None:
-        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+        y = _like(u)
     else:
         y = out
         _check("out", y, dev, u.dtype, u.shape)
@@ -305,11 +311,11 @@ def short_conv(x, weight, bias=None, initial_state=None, seqlens=None, silu: boo
     s, (n, _, ch, W) = _conv_inputs(x, weight, bias, initial_state, seqlens, silu)
     dev = x.device
     if out is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = _like(x)
     else:
         y = out
         _check("out", y, dev, x.dtype, x.shape)
-    last = torch.empty((n, W - 1, ch), dtype=x.dtype, device=dev) if want_final_state else None
+    last = torch.empty(n, W - 1, ch, dtype=x.dtype, device=dev) if want_final_state else None
     _run("short_conv", dev, lib.short_conv_fwd, s, y.data_ptr(), _at(last))
     return y, last
 
@@ -326,11 +332,11 @@ def short_conv_bwd(dy, x, weight, bias=None, initial_state=None, seqlens=None, s
     _check("dy", dy, dev, x.dtype, x.shape, True)
     if dfinal_state is not None:
         _check("dfinal_state", dfinal_state, dev, x.dtype, (n, W - 1, ch))
-    got = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev), "dweight": torch.empty_like(weight)}
+    got = {"dx": _like(x), "dweight": _like(weight)}
     if bias is not None:
-        got["dbias"] = torch.empty_like(bias)
+        got["dbias"] = _like(bias)
     if initial_state is not None:
-        got["dinitial_state"] = torch.empty_like(initial_state)
+        got["dinitial_state"] = _like(initial_state)
     need = max(lib.short_conv_bwd_workspace_size(*sizes), 16)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _run("short_conv_bwd", dev, lib.short_conv_bwd, s, dy.data_ptr(), dy.stride(0), dy.stride(1), _at(dfinal_state),
@@ -348,7 +354,7 @@ def short_conv_step(state, x, weight, bias=None, silu: bool = True, out: torch.T
     dev = x.device
     _check("state", state, dev, x.dtype, (n, W - 1, ch))
     if out is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = _like(x)
     else:
         y = out
         _check("out", y, dev, x.dtype, x.shape)
@@ -397,7 +403,7 @@ def state_cache_read(cache, scales, slots, out: torch.Tensor | None = None):
     state of zeros."""
     dev, shape, sizes = _cache_args(cache, scales, slots)
     if out is None:
-        h = torch.empty(shape, dtype=torch.float32, device=dev)
+        h = torch.empty(*shape, dtype=torch.float32, device=dev)
     else:
         h = out
         _check("out", h, dev, torch.float32, shape)
