@@ -50,11 +50,12 @@ __device__ __forceinline__ f32x4 unpack4(uint32_t v) {
     return f;
 }
 
-// The lane's four values of a row; WIDE: whole aligned vectors.
+// The lane's four values of a row; WIDE: whole aligned vectors, past the caches (a state is written to the cache once:
+// write and read of 32 states of 5120 rows of 128 in 41.5 us for 49.4).
 template <bool WIDE>
 __device__ __forceinline__ f32x4 load4(const float* row, int s, int S) {
     if constexpr (WIDE) {
-        return s < S ? *reinterpret_cast<const f32x4*>(row + s) : f32x4{0.f, 0.f, 0.f, 0.f};
+        return s < S ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(row + s)) : f32x4{0.f, 0.f, 0.f, 0.f};
     } else {
         f32x4 v;
 #pragma unroll
