@@ -340,8 +340,10 @@ int launched() { return hipGetLastError() == hipSuccess ? 0 : -7; }
 dim3 blocks_for(int64_t threads) { return dim3(uint32_t((threads + 255) / 256)); }
 
 int conv_bwd_run(int64_t batch, int64_t L, int64_t ch) {
-    // about 256k threads of 4 channels where there is work for them (16 tokens each measured 44.5 us where 48 took 49.6)
-    const int64_t run = batch * L * ((ch + 3) / 4) / (int64_t(1) << 18) / 16 * 16;
+    // One round of three workgroups, what the registers leave room for, on each of 256 CUs, with 4 channels to a
+    // thread: 8 x 2048 x 1536 bf16 in runs of 32 (one round) took 39.5 us, of 16 (1.9 rounds) 45, of 48 (0.7) 49.6.
+    const int64_t threads = int64_t(3) * 256 * 256;
+    const int64_t run = (batch * L * ((ch + 3) / 4) + 8 * threads - 1) / (8 * threads) * 8;
     return int(run < 16 ? 16 : run > 512 ? 512 : run);
 }
 
