@@ -110,7 +110,7 @@ const char* ssd_strerror(int status) {
         case SSD_OK: return "ok";
         case SSD_ERR_NULL: return "a required pointer is NULL";
         case SSD_ERR_SHAPE: return "invalid shape (a size <= 0, too large, or heads % groups != 0)";
-        case SSD_ERR_DTYPE: return "dtype must be SSD_F32 or SSD_BF16";
+        case SSD_ERR_DTYPE: return "an element type that the call does not take";
         case SSD_ERR_CHUNK: return "chunk must be 16, 32, 64, 128 or 256";
         case SSD_ERR_ALIGN: return "a pointer is not 16-byte aligned";
         case SSD_ERR_WORKSPACE: return "workspace is NULL or smaller than required";
