@@ -231,7 +231,7 @@ int selective_scan_step(const selective_scan_inputs* in, float* h, void* y, void
     const int st = scan_check(&one);
     if (st != SSD_OK) return st;
     if (!aligned(h, 16) || !aligned(y, elem_size(one.dtype))) return SSD_ERR_ALIGN;
-    if (one.batch * one.channels >= kMaxThreads / 16) return SSD_ERR_SHAPE;
+    if (one.batch * (one.channels + 16) >= kMaxThreads / 16) return SSD_ERR_SHAPE;  // 16 lanes to a channel, whole workgroups
     return launched(cls_selective_scan_step_launch(one, h, y, static_cast<hipStream_t>(stream)));
 }
 

@@ -185,17 +185,19 @@ struct ScanFold {
     }
 };
 
-// Segments from, from + step, ... (n of them), four at a time so that their loads are in flight together.
+// Segments from, from + step, ... (n of them), kFoldAtOnce at a time so that their loads are in flight together.
+constexpr int kFoldAtOnce = 8;
+
 template <typename V>
 __device__ __forceinline__ void scan_fold(const ScanParams& p, int from, int step, int n, int64_t b, int ch, int n0,
                                           const float (&A2)[kScanK], V& v) {
-    for (int i = 0; i < n; i += 4) {
-        ScanFold f[4];
+    for (int i = 0; i < n; i += kFoldAtOnce) {
+        ScanFold f[kFoldAtOnce];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kFoldAtOnce; ++j)
             if (i + j < n) f[j].load(p, from + step * (i + j), b, ch, n0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kFoldAtOnce; ++j)
             if (i + j < n) f[j].apply(A2, v);
     }
 }
