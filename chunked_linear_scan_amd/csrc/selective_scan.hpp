@@ -185,8 +185,10 @@ struct ScanFold {
     }
 };
 
-// Segments from, from + step, ... (n of them), kFoldAtOnce at a time so that their loads are in flight together.
-constexpr int kFoldAtOnce = 8;
+// Segments from, from + step, ... (n of them), four at a time so that their
+// loads are in flight together (eight measured 5 % slower over a whole call:
+// registers).
+constexpr int kFoldAtOnce = 4;
 
 template <typename V>
 __device__ __forceinline__ void scan_fold(const ScanParams& p, int from, int step, int n, int64_t b, int ch, int n0,

@@ -108,14 +108,15 @@ def _like(t):
     return torch.empty_like(t, memory_format=_DENSE)
 
 
-def _check(name, t, device, dtype, shape, strided=False):
+def _check(name, t, at, dtype, shape, strided=False):
+    """t is on GPU number `at` with this dtype and shape, contiguous or (strided) its last dimension adjacent."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.device == device and (
+        if t.dtype is dtype and t.shape == shape and t.get_device() == at and (
                 t.is_contiguous() or (strided and (t.stride(-1) == 1 or t.shape[-1] == 1))):
             return
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor") from None
-    if t.device != device:
+    if t.get_device() != at:
         raise ValueError(f"{name} must be on one GPU with the other tensors (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
@@ -125,20 +126,30 @@ def _check(name, t, device, dtype, shape, strided=False):
 
 
 def _activation(name, t, dims):
+    """The GPU's number, the dtype and the shape of the tensor that the others are held to."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _CODE:
+    kind, shape = t.dtype, t.shape
+    if kind not in _CODE:
         raise TypeError(f"{name} must be float32, bfloat16 or float16")
-    if t.dim() != len(dims):
+    if len(shape) != len(dims):
         raise ValueError(f"{name} must be [{', '.join(dims)}]")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (got {t.device})")
-    _check(name, t, t.device, t.dtype, t.shape, strided=True)
+    if not (t.is_contiguous() or t.stride(-1) == 1 or shape[-1] == 1):
+        raise ValueError(f"{name}'s last dimension must be adjacent in memory")
+    return t.get_device(), kind, shape
 
 
-def _seqlens(t, device, batch):
+def _last_dim(name, t, dims):
+    if not isinstance(t, torch.Tensor) or t.dim() != len(dims):
+        raise ValueError(f"{name} must be [{', '.join(dims)}]")
+    return t.shape[-1]
+
+
+def _seqlens(t, at, batch):
     if t is not None:
-        _check("seqlens", t, device, torch.int32, (batch,))
+        _check("seqlens", t, at, torch.int32, (batch,))
 
 
 # ---------------------------------------------------------------------------
@@ -149,30 +160,25 @@ _SEQ, _ONE = ("batch", "seqlen", "channels"), ("batch", "channels")
 
 def _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus, step=False):
     """(the packed structure, its sizes)"""
-    _activation("u", u, _ONE if step else _SEQ)
-    dev, kind, shape = u.device, u.dtype, u.shape
+    at, kind, shape = _activation("u", u, _ONE if step else _SEQ)
     n, ch = shape[0], shape[-1]
-    lead = shape[:-1]
-    _check("dt", dt, dev, kind, shape, True)
+    _check("dt", dt, at, kind, shape, True)
     if z is not None:
-        _check("z", z, dev, kind, shape, True)
-    if not isinstance(A, torch.Tensor) or A.dim() != 2:
-        raise ValueError("A must be [channels, dstate]")
-    N = A.shape[1]
-    _check("A", A, dev, torch.float32, (ch, N))
-    if not isinstance(B, torch.Tensor) or B.dim() != len(shape) + 1:
-        raise ValueError("B must be [batch, ngroups, dstate]" if step else "B must be [batch, seqlen, ngroups, dstate]")
+        _check("z", z, at, kind, shape, True)
+    N = _last_dim("A", A, ("channels", "dstate"))
+    _check("A", A, at, torch.float32, (ch, N))
+    _last_dim("B", B, ("batch", "ngroups", "dstate") if step else ("batch", "seqlen", "ngroups", "dstate"))
     G = B.shape[-2]
-    bc = (*lead, G, N)
-    _check("B", B, dev, kind, bc, True)
-    _check("C", C, dev, kind, bc, True)
+    bc = (n, G, N) if step else (n, shape[1], G, N)
+    _check("B", B, at, kind, bc, True)
+    _check("C", C, at, kind, bc, True)
     if D is not None:
-        _check("D", D, dev, torch.float32, (ch,))
+        _check("D", D, at, torch.float32, (ch,))
     if dt_bias is not None:
-        _check("dt_bias", dt_bias, dev, torch.float32, (ch,))
+        _check("dt_bias", dt_bias, at, torch.float32, (ch,))
     if h0 is not None:
-        _check("h0", h0, dev, torch.float32, (n, ch, N))
-    _seqlens(seqlens, dev, n)
+        _check("h0", h0, at, torch.float32, (n, ch, N))
+    _seqlens(seqlens, at, n)
     L = 1 if step else shape[1]
     us, ds, bs, cs = u.stride(), dt.stride(), B.stride(), C.stride()
     zs = us if z is None else z.stride()
@@ -214,7 +220,7 @@ def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, seqlen
         y = _like(u)
     else:
         y = out
-        _check("out", y, dev, u.dtype, u.shape)
+        _check("out", y, dev.index, u.dtype, u.shape)
     hf = torch.empty(n, ch, N, dtype=f32, device=dev) if want_final_state else None
     kept = torch.empty(*_checkpoint_shape(lib, sizes), dtype=f32, device=dev) if want_checkpoints else None
     need = lib.selective_scan_workspace_size(*sizes)
@@ -235,12 +241,12 @@ def selective_scan_bwd(dy, u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None
     s, sizes = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, h0, seqlens, dt_softplus)
     n, _, ch, N, _ = sizes
     dev, f32 = u.device, torch.float32
-    _check("dy", dy, dev, u.dtype, u.shape, True)
+    _check("dy", dy, dev.index, u.dtype, u.shape, True)
     if checkpoints is None:
         raise ValueError("checkpoints: run selective_scan with want_checkpoints=True")
-    _check("checkpoints", checkpoints, dev, f32, _checkpoint_shape(lib, sizes))
+    _check("checkpoints", checkpoints, dev.index, f32, _checkpoint_shape(lib, sizes))
     if dh_final is not None:
-        _check("dh_final", dh_final, dev, f32, (n, ch, N))
+        _check("dh_final", dh_final, dev.index, f32, (n, ch, N))
     got = {"du": _like(u), "ddt": _like(u), "dA": _like(A), "dB": _like(B), "dC": _like(C)}
     if D is not None:
         got["dD"] = _like(D)
@@ -266,12 +272,12 @@ def selective_scan_step(h, u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
     lib = _lib()
     s, (n, _, ch, N, _) = _scan_inputs(u, dt, A, B, C, D, z, dt_bias, None, None, dt_softplus, True)
     dev = u.device
-    _check("h", h, dev, torch.float32, (n, ch, N))
+    _check("h", h, dev.index, torch.float32, (n, ch, N))
     if out is None:
         y = _like(u)
     else:
         y = out
-        _check("out", y, dev, u.dtype, u.shape)
+        _check("out", y, dev.index, u.dtype, u.shape)
     _run("selective_scan_step", dev, lib.selective_scan_step, s, h.data_ptr(), y.data_ptr())
     return y
 
@@ -281,20 +287,17 @@ def selective_scan_step(h, u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
 # ---------------------------------------------------------------------------
 def _conv_inputs(x, weight, bias, initial_state, seqlens, silu, step=False):
     """(the packed structure, its sizes)"""
-    _activation("x", x, _ONE if step else _SEQ)
-    dev, shape = x.device, x.shape
+    at, kind, shape = _activation("x", x, _ONE if step else _SEQ)
     n, ch = shape[0], shape[-1]
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
-        raise ValueError("weight must be [channels, width]")
-    W = weight.shape[1]
-    _check("weight", weight, dev, torch.float32, (ch, W))
+    W = _last_dim("weight", weight, ("channels", "width"))
+    _check("weight", weight, at, torch.float32, (ch, W))
     if bias is not None:
-        _check("bias", bias, dev, torch.float32, (ch,))
+        _check("bias", bias, at, torch.float32, (ch,))
     if initial_state is not None:
-        _check("initial_state", initial_state, dev, x.dtype, (n, W - 1, ch))
-    _seqlens(seqlens, dev, n)
+        _check("initial_state", initial_state, at, kind, (n, W - 1, ch))
+    _seqlens(seqlens, at, n)
     L, xs = (1, x.stride()) if step else (shape[1], x.stride())
-    return _PACK_CONV.pack(n, L, ch, W, _CODE[x.dtype], 1 if silu else 0, x.data_ptr(), xs[0], 0 if step else xs[1],
+    return _PACK_CONV.pack(n, L, ch, W, _CODE[kind], 1 if silu else 0, x.data_ptr(), xs[0], 0 if step else xs[1],
                            weight.data_ptr(), _at(bias), _at(initial_state), _at(seqlens)), (n, L, ch, W)
 
 
@@ -314,7 +317,7 @@ def short_conv(x, weight, bias=None, initial_state=None, seqlens=None, silu: boo
         y = _like(x)
     else:
         y = out
-        _check("out", y, dev, x.dtype, x.shape)
+        _check("out", y, dev.index, x.dtype, x.shape)
     last = torch.empty(n, W - 1, ch, dtype=x.dtype, device=dev) if want_final_state else None
     _run("short_conv", dev, lib.short_conv_fwd, s, y.data_ptr(), _at(last))
     return y, last
@@ -329,9 +332,9 @@ def short_conv_bwd(dy, x, weight, bias=None, initial_state=None, seqlens=None, s
     s, sizes = _conv_inputs(x, weight, bias, initial_state, seqlens, silu)
     n, _, ch, W = sizes
     dev = x.device
-    _check("dy", dy, dev, x.dtype, x.shape, True)
+    _check("dy", dy, dev.index, x.dtype, x.shape, True)
     if dfinal_state is not None:
-        _check("dfinal_state", dfinal_state, dev, x.dtype, (n, W - 1, ch))
+        _check("dfinal_state", dfinal_state, dev.index, x.dtype, (n, W - 1, ch))
     got = {"dx": _like(x), "dweight": _like(weight)}
     if bias is not None:
         got["dbias"] = _like(bias)
@@ -352,12 +355,12 @@ def short_conv_step(state, x, weight, bias=None, silu: bool = True, out: torch.T
     lib = _lib()
     s, (n, _, ch, W) = _conv_inputs(x, weight, bias, None, None, silu, True)
     dev = x.device
-    _check("state", state, dev, x.dtype, (n, W - 1, ch))
+    _check("state", state, dev.index, x.dtype, (n, W - 1, ch))
     if out is None:
         y = _like(x)
     else:
         y = out
-        _check("out", y, dev, x.dtype, x.shape)
+        _check("out", y, dev.index, x.dtype, x.shape)
     _run("short_conv_step", dev, lib.short_conv_step, s, state.data_ptr(), y.data_ptr())
     return y
 
@@ -374,12 +377,11 @@ def _cache_args(cache, scales, slots):
     if not cache.is_cuda:
         raise ValueError(f"cache must be on a GPU (got {cache.device})")
     dev = cache.device
-    _check("cache", cache, dev, cache.dtype, shape)
-    _check("scales", scales, dev, torch.float32, shape[:-1])
-    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
-        raise ValueError("slots must be [batch]")
-    n = slots.shape[0]
-    _check("slots", slots, dev, torch.int32, (n,))
+    at = dev.index
+    _check("cache", cache, at, cache.dtype, shape)
+    _check("scales", scales, at, torch.float32, shape[:-1])
+    n = _last_dim("slots", slots, ("batch",))
+    _check("slots", slots, at, torch.int32, (n,))
     return dev, (n, *shape[1:]), (n, math.prod(shape[1:-1]), shape[-1], shape[0], _CACHE_CODE[cache.dtype])
 
 
@@ -391,7 +393,7 @@ def state_cache_write(h, cache, scales, slots) -> None:
     scales [slots, ...] (fp32).  A state whose slot is out of range is not
     written; of several that name one slot the last is."""
     dev, shape, sizes = _cache_args(cache, scales, slots)
-    _check("h", h, dev, torch.float32, shape)
+    _check("h", h, dev.index, torch.float32, shape)
     _run("state_cache_write", dev, _lib().state_cache_write, h.data_ptr(), slots.data_ptr(), *sizes, cache.data_ptr(),
          scales.data_ptr())
 
@@ -406,7 +408,7 @@ def state_cache_read(cache, scales, slots, out: torch.Tensor | None = None):
         h = torch.empty(*shape, dtype=torch.float32, device=dev)
     else:
         h = out
-        _check("out", h, dev, torch.float32, shape)
+        _check("out", h, dev.index, torch.float32, shape)
     _run("state_cache_read", dev, _lib().state_cache_read, cache.data_ptr(), scales.data_ptr(), slots.data_ptr(), *sizes,
          h.data_ptr())
     return h
