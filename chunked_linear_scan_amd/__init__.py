@@ -15,7 +15,7 @@ import threading
 
 import torch
 
-from . import selective as _selective
+from . import selective
 from .selective import (selective_scan, selective_scan_bwd, selective_scan_step, short_conv, short_conv_bwd,
                         short_conv_step, state_cache_read, state_cache_write)
 
@@ -113,7 +113,6 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.linear_scan_plan.restype = ctypes.c_int
         lib.linear_scan_autotune_reset.argtypes = []
         lib.linear_scan_autotune_reset.restype = None
-        _selective.declare(lib)
         _lib = lib
         return lib
 
@@ -523,4 +522,4 @@ def ssd_step(h, x, dt, A, B, C, D=None, out: torch.Tensor | None = None):
 
 __all__ = ["linear_scan", "linear_scan_hillis_steele", "linear_scan_three_pass", "ssd_fwd", "ssd_fwd_autotune", "ssd_fwd_plan",
            "ssd_fwd_autotune_reset", "ssd_fwd_planned", "plan_request", "ssd_step", "load_library", "strerror",
-           "workspace_errors", "SSDError", "LIB_PATH", "SSD_F32", "SSD_BF16", "SSD_F16", *_selective.__all__]
+           "workspace_errors", "SSDError", "LIB_PATH", "SSD_F32", "SSD_BF16", "SSD_F16", *selective.__all__]

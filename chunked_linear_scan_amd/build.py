@@ -2,7 +2,9 @@
 
 Every HIP translation unit is compiled with hipcc for gfx950 only, with
 packed-fp32 instruction generation switched off, then linked into one
-shared library that exports the C ABI of ``include/chunked_linear_scan.h``.
+shared library that exports the C ABI of ``include/chunked_linear_scan.h`` and
+``include/selective_scan.h``.  The native Python binding of the latter (host
+code only, on torch's C++ API) becomes ``_selective_binding.so`` beside it.
 """
 from __future__ import annotations
 
@@ -11,12 +13,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libchunked_linear_scan.so")
+BINDING = os.path.join(HERE, "_selective_binding.so")
+BINDING_SRC = os.path.join(HERE, "binding", "selective_binding.cpp")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -44,6 +49,36 @@ def _compile(src):
     return obj
 
 
+def _compile_binding(obj):
+    """Host code: g++ with torch's headers."""
+    import torch
+    from torch.utils import cpp_extension
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
+                                           os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", BINDING_SRC, "-o", obj,
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for i in inc:
+        cmd += ["-isystem", i]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj):
+    from torch.utils import cpp_extension
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN"]
+    cmd += ["-L" + p for p in cpp_extension.library_paths()]
+    cmd += ["-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = True, jobs: int | None = None) -> str:
     if shutil.which(HIPCC) is None and not os.path.exists(HIPCC):
         raise RuntimeError(f"hipcc not found at {HIPCC}")
@@ -51,15 +86,18 @@ def build(verbose: bool = True, jobs: int | None = None) -> str:
     srcs = sources()
     jobs = jobs or min(8, os.cpu_count() or 4)
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding, os.path.join(BUILD, "selective_binding.o"))
         objs = list(ex.map(_compile, srcs))
+        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     if verbose:
-        print(f"built {LIB} from {len(srcs)} sources", file=sys.stderr)
+        print(f"built {LIB} from {len(srcs)} sources, and {BINDING}", file=sys.stderr)
     return LIB
 
 

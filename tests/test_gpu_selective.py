@@ -131,7 +131,11 @@ def test_scan_lengths_and_nan_in_the_padding(lens, N):
     print(f"[scan] lengths {lens} N={N}", flush=True)
     L = 700
     c = scan_case(9, 3, L, 40, N, 1, kind="f32", start=True)
-    assert cls.load_library().selective_scan_workspace_size(3, L, 40, N, 1) > 0
+    import ctypes
+    lib = ctypes.CDLL(cls.LIB_PATH)
+    lib.selective_scan_workspace_size.argtypes = [ctypes.c_int64] * 5
+    lib.selective_scan_workspace_size.restype = ctypes.c_size_t
+    assert lib.selective_scan_workspace_size(3, L, 40, N, 1) > 0
     c["seqlens"] = torch.tensor(lens, dtype=torch.int32)
     for i, n in enumerate(lens):
         for k in ("u", "dt", "z", "B", "C", "dy"):

@@ -9,7 +9,6 @@ import pytest
 import torch
 
 import chunked_linear_scan_amd as cls
-from chunked_linear_scan_amd import selective as sel
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "selective_scan.h")
@@ -18,6 +17,50 @@ pytestmark = pytest.mark.skipif(not os.path.exists(cls.LIB_PATH),
                                 reason="library not built (run __graft_entry__.build())")
 
 AT = 0x10000  # 16-byte aligned, never dereferenced on error paths
+I64, I32, VP, SZ = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+
+
+class ScanInputs(ctypes.Structure):
+    """``selective_scan_inputs``."""
+    _fields_ = ([(n, I64) for n in ("batch", "seqlen", "channels", "dstate", "ngroups")]
+                + [("dtype", I32), ("softplus", I32)]
+                + [(n, VP) for n in ("u", "dt", "z", "B", "C", "A", "D", "dt_bias", "h0", "seqlens")]
+                + [(n, I64) for n in ("u_batch", "u_token", "dt_batch", "dt_token", "z_batch", "z_token",
+                                      "B_batch", "B_token", "B_group", "C_batch", "C_token", "C_group")])
+
+
+class ScanGrads(ctypes.Structure):
+    """``selective_scan_grads``."""
+    _fields_ = ([("dy", VP), ("dy_batch", I64), ("dy_token", I64)]
+                + [(n, VP) for n in ("dh_final", "checkpoints", "du", "ddt", "dz", "dB", "dC", "dA", "dD",
+                                     "ddt_bias", "dh0")])
+
+
+class ConvInputs(ctypes.Structure):
+    """``short_conv_inputs``."""
+    _fields_ = ([(n, I64) for n in ("batch", "seqlen", "channels", "width")]
+                + [("dtype", I32), ("silu", I32), ("x", VP), ("x_batch", I64), ("x_token", I64)]
+                + [(n, VP) for n in ("weight", "bias", "initial_state", "seqlens")])
+
+
+def library():
+    lib = ctypes.CDLL(cls.LIB_PATH)
+    for name, args, res in (
+            ("selective_scan_workspace_size", [I64] * 5, SZ),
+            ("selective_scan_bwd_workspace_size", [I64] * 5, SZ),
+            ("selective_scan_checkpoint_size", [I64] * 4, SZ),
+            ("selective_scan_fwd", [VP] * 5 + [SZ, VP], ctypes.c_int),
+            ("selective_scan_bwd", [VP] * 3 + [SZ, VP], ctypes.c_int),
+            ("selective_scan_step", [VP] * 4, ctypes.c_int),
+            ("short_conv_fwd", [VP] * 4, ctypes.c_int),
+            ("short_conv_bwd_workspace_size", [I64] * 4, SZ),
+            ("short_conv_bwd", [VP, VP, I64, I64] + [VP] * 6 + [SZ, VP], ctypes.c_int),
+            ("short_conv_step", [VP] * 4, ctypes.c_int),
+            ("state_cache_write", [VP, VP] + [I64] * 4 + [ctypes.c_int] + [VP] * 3, ctypes.c_int),
+            ("state_cache_read", [VP] * 3 + [I64] * 4 + [ctypes.c_int, VP, VP], ctypes.c_int)):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, res
+    return lib
 
 
 def test_library_exports_every_declared_symbol():
@@ -34,30 +77,18 @@ def test_library_exports_every_declared_symbol():
 
 def test_structures_have_the_header_s_fields():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
-    for name, struct in (("selective_scan_inputs", sel._ScanInputs), ("selective_scan_grads", sel._ScanGrads),
-                         ("short_conv_inputs", sel._ConvInputs)):
+    for name, struct in (("selective_scan_inputs", ScanInputs), ("selective_scan_grads", ScanGrads),
+                         ("short_conv_inputs", ConvInputs)):
         body = re.search(r"typedef struct \{([^}]*)\} %s;" % name, text).group(1)
         fields = [re.sub(r"\W", "", f.split()[-1]) for d in body.split(";") for f in d.split(",") if f.strip()]
         assert fields == [f for f, _ in struct._fields_], name
-    assert sel._PACK_SCAN.size == ctypes.sizeof(sel._ScanInputs)
-    assert sel._PACK_GRADS.size == ctypes.sizeof(sel._ScanGrads)
-    assert sel._PACK_CONV.size == ctypes.sizeof(sel._ConvInputs)
-
-
-def test_packed_structures_are_the_ctypes_ones():
-    """The binding packs the structures as bytes: field by field the same as the declared layout."""
-    for pack, struct in ((sel._PACK_SCAN, sel._ScanInputs), (sel._PACK_GRADS, sel._ScanGrads),
-                         (sel._PACK_CONV, sel._ConvInputs)):
-        values = list(range(1, len(struct._fields_) + 1))
-        s = struct.from_buffer_copy(pack.pack(*values))
-        assert [getattr(s, f) for f, _ in struct._fields_] == values
 
 
 def scan_in(**k):
     a = dict(batch=2, seqlen=100, channels=64, dstate=16, ngroups=1, dtype=1, softplus=1, u=AT, dt=AT, z=AT, B=AT, C=AT,
              A=AT, D=AT, dt_bias=AT, h0=AT, seqlens=AT)
     a.update(k)
-    return sel._ScanInputs(**a)
+    return ScanInputs(**a)
 
 
 BAD_SCAN = [(dict(u=None), -1), (dict(A=None), -1), (dict(B=None), -1), (dict(C=None), -1), (dict(dt=None), -1),
@@ -70,20 +101,20 @@ BAD_LENGTH = [(dict(seqlen=0), -2), (dict(seqlen=1 << 31), -2), (dict(seqlens=AT
 
 @pytest.mark.parametrize("bad,status", BAD_SCAN + BAD_LENGTH)
 def test_scan_refuses(bad, status):
-    lib, s = cls.load_library(), scan_in(**bad)
+    lib, s = library(), scan_in(**bad)
     assert lib.selective_scan_fwd(ctypes.byref(s), AT, AT, AT, AT, 1 << 50, None) == status
-    g = sel._ScanGrads(**{k: AT for k in ("dy", "checkpoints", "du", "ddt", "dz", "dB", "dC", "dA")})
+    g = ScanGrads(**{k: AT for k in ("dy", "checkpoints", "du", "ddt", "dz", "dB", "dC", "dA")})
     assert lib.selective_scan_bwd(ctypes.byref(s), ctypes.byref(g), AT, 1 << 50, None) == status
 
 
 @pytest.mark.parametrize("bad,status", BAD_SCAN)
 def test_step_refuses(bad, status):
-    lib, s = cls.load_library(), scan_in(**bad)
+    lib, s = library(), scan_in(**bad)
     assert lib.selective_scan_step(ctypes.byref(s), AT, AT, None) == status
 
 
 def test_scan_refuses_other_pointers():
-    lib, s = cls.load_library(), scan_in()
+    lib, s = library(), scan_in()
     ref = ctypes.byref(s)
     big = 1 << 50
     assert lib.selective_scan_fwd(None, AT, AT, AT, AT, big, None) == -1
@@ -100,18 +131,18 @@ def test_scan_refuses_other_pointers():
     assert lib.selective_scan_step(ref, AT + 8, AT, None) == -5
     full = {k: AT for k in ("dy", "checkpoints", "du", "ddt", "dz", "dB", "dC", "dA")}
     for k in full:
-        g = sel._ScanGrads(**{**full, k: None})
+        g = ScanGrads(**{**full, k: None})
         assert lib.selective_scan_bwd(ref, ctypes.byref(g), AT, big, None) == -1, k
-    g = sel._ScanGrads(**full)
+    g = ScanGrads(**full)
     need = lib.selective_scan_bwd_workspace_size(2, 100, 64, 16, 1)
     assert lib.selective_scan_bwd(ref, ctypes.byref(g), AT, need - 1, None) == -6
     assert lib.selective_scan_bwd(ref, ctypes.byref(g), None, big, None) == -1
-    g = sel._ScanGrads(**full, dy_token=-4)
+    g = ScanGrads(**full, dy_token=-4)
     assert lib.selective_scan_bwd(ref, ctypes.byref(g), AT, big, None) == -2
 
 
 def test_scan_sizes():
-    lib = cls.load_library()
+    lib = library()
     # the state before every 8th token
     assert lib.selective_scan_checkpoint_size(2, 33, 10, 16) == 2 * 5 * 10 * 16 * 4
     assert lib.selective_scan_checkpoint_size(2, 33, 10, 33) == 2 * 5 * 10 * 33 * 4
@@ -124,7 +155,7 @@ def conv_in(**k):
     a = dict(batch=2, seqlen=100, channels=64, width=4, dtype=1, silu=1, x=AT, x_batch=6400, x_token=64, weight=AT,
              bias=AT, initial_state=AT, seqlens=AT)
     a.update(k)
-    return sel._ConvInputs(**a)
+    return ConvInputs(**a)
 
 
 @pytest.mark.parametrize("bad,status", [(dict(x=None), -1), (dict(weight=None), -1), (dict(dtype=4), -3),
@@ -132,7 +163,7 @@ def conv_in(**k):
                                         (dict(width=5), -8), (dict(x=AT + 1), -5), (dict(weight=AT + 2), -5),
                                         (dict(x_batch=-1), -2), (dict(batch=1 << 22, channels=1 << 22), -2)])
 def test_conv_refuses(bad, status):
-    lib, s = cls.load_library(), conv_in(**bad)
+    lib, s = library(), conv_in(**bad)
     ref, big = ctypes.byref(s), 1 << 50
     assert lib.short_conv_fwd(ref, AT, AT, None) == status
     assert lib.short_conv_step(ref, AT, AT, None) == status
@@ -140,7 +171,7 @@ def test_conv_refuses(bad, status):
 
 
 def test_conv_refuses_other_pointers():
-    lib, s = cls.load_library(), conv_in()
+    lib, s = library(), conv_in()
     ref, big = ctypes.byref(s), 1 << 50
     assert lib.short_conv_fwd(ref, None, AT, None) == -1
     assert lib.short_conv_fwd(ref, AT, AT + 1, None) == -5
@@ -159,7 +190,7 @@ def test_conv_refuses_other_pointers():
                                          ((2, 8, 16, 4, 1), -3), ((2, 1 << 33, 16, 4, 4), -2),
                                          ((1 << 20, 1 << 20, 16, 4, 4), -2)])
 def test_cache_refuses(args, status):
-    lib = cls.load_library()
+    lib = library()
     if status == 0:  # the sizes are fine, the pointers are not
         for k in range(4):
             p = [AT] * 4
