@@ -49,18 +49,26 @@ int scan_sizes(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
 
 // Where the channels and states alone give the device too few waves (below one
 // per SIMD), each sequence is cut into segments, to 8 waves per SIMD where its
-// length allows: a segment has 4 tiles at least, and their number grows with
-// the root of the length, since each starts by folding all before it.  Output
-// pass of 1 x 32768 x 4096 x 16 bf16 at 2048, 4096 and 8192 waves: 818, 632 and
-// 570 us; 2 x 1000 x 1536 x 16 fp32 in 11, 16, 21 and 32 segments: 23.4, 22,
-// 21.5 and 26 us; 2 x 301 x 320 x 8 fp32 in 5 and 10: 18 and 12 us.
+// length allows.  Output pass of 1 x 32768 x 4096 x 16 bf16 at 2048, 4096 and
+// 8192 waves: 818, 632 and 570 us.  What bounds their number is that each starts
+// by folding all before it, and that a second launch and pass are paid for: with
+// the device nearly empty a call takes about 5 + 1.2 tiles us in one piece and
+// 12.5 + 2.2 tiles / segments + 0.3 segments in several, so nothing is cut below
+// 16 tiles and the best number is 2.7 roots of the tiles; with some waves on
+// every SIMD fewer are better (2 x 1000 x 1536 x 16 fp32 in 11, 16, 21 and 32
+// segments: 23.4, 22, 21.5 and 26 us).
 ScanCut scan_cut(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
     const int64_t tiles = ceil_div(L, cls::kScanTile);
     const int64_t waves = batch * G * ceil_div(ch / G, cls::kScanCh) * cls::scan_waves(N);
-    int64_t nseg = waves >= 1024 ? 1 : ceil_div(8192, waves);
-    for (int64_t most : {int64_t(cls::kScanMaxSegs), tiles / 4, int64_t(1.75 * std::sqrt(double(tiles)))})
-        nseg = nseg < most ? nseg : most;
-    const int64_t len = ceil_div(tiles, nseg > 1 ? nseg : 1) * cls::kScanTile;
+    int64_t nseg = 1;
+    if (waves < 1024 && tiles >= 16) {
+        const double root = std::sqrt(double(tiles));
+        const int64_t empty = int64_t(2.7 * root) < 3072 / waves ? int64_t(2.7 * root) : 3072 / waves;
+        const int64_t full = int64_t(1.75 * root);
+        nseg = ceil_div(8192, waves);
+        for (int64_t most : {int64_t(cls::kScanMaxSegs), empty > full ? empty : full}) nseg = nseg < most ? nseg : most;
+    }
+    const int64_t len = ceil_div(tiles, nseg) * cls::kScanTile;
     return ScanCut{ceil_div(L, len), len};
 }
 

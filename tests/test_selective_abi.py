@@ -85,7 +85,7 @@ def test_structures_have_the_header_s_fields():
 
 
 def scan_in(**k):
-    a = dict(batch=2, seqlen=100, channels=64, dstate=16, ngroups=1, dtype=1, softplus=1, u=AT, dt=AT, z=AT, B=AT, C=AT,
+    a = dict(batch=2, seqlen=200, channels=64, dstate=16, ngroups=1, dtype=1, softplus=1, u=AT, dt=AT, z=AT, B=AT, C=AT,
              A=AT, D=AT, dt_bias=AT, h0=AT, seqlens=AT)
     a.update(k)
     return ScanInputs(**a)
@@ -122,7 +122,7 @@ def test_scan_refuses_other_pointers():
     assert lib.selective_scan_fwd(ref, AT + 1, AT, AT, AT, big, None) == -5
     assert lib.selective_scan_fwd(ref, AT, AT + 2, AT, AT, big, None) == -5
     assert lib.selective_scan_fwd(ref, AT, AT, AT + 4, AT, big, None) == -5
-    need = lib.selective_scan_workspace_size(2, 100, 64, 16, 1)
+    need = lib.selective_scan_workspace_size(2, 200, 64, 16, 1)
     assert need > 0  # 2 x 64 channels are cut into segments
     assert lib.selective_scan_fwd(ref, AT, AT, AT, AT, need - 1, None) == -6
     assert lib.selective_scan_fwd(ref, AT, AT, AT, None, big, None) == -6
@@ -134,7 +134,7 @@ def test_scan_refuses_other_pointers():
         g = ScanGrads(**{**full, k: None})
         assert lib.selective_scan_bwd(ref, ctypes.byref(g), AT, big, None) == -1, k
     g = ScanGrads(**full)
-    need = lib.selective_scan_bwd_workspace_size(2, 100, 64, 16, 1)
+    need = lib.selective_scan_bwd_workspace_size(2, 200, 64, 16, 1)
     assert lib.selective_scan_bwd(ref, ctypes.byref(g), AT, need - 1, None) == -6
     assert lib.selective_scan_bwd(ref, ctypes.byref(g), None, big, None) == -1
     g = ScanGrads(**full, dy_token=-4)
