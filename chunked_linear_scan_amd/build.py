@@ -54,7 +54,7 @@ def _compile_binding(obj):
     import torch
     from torch.utils import cpp_extension
     inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
-                                           os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include")]
+                                           os.path.join(cpp_extension.ROCM_HOME or "/opt/rocm", "include")]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", BINDING_SRC, "-o", obj,
            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
