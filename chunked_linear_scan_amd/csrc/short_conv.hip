@@ -4,10 +4,10 @@
 // A few operations per element read and written, so bound by memory: a thread
 // walks adjacent tokens of 4 or 8 channels with the last `width` inputs in
 // registers, reading each row once but for the width - 1 before its run.
-// 8 x 2048 x 1536 bf16: forward 24 us (101 MB: 19.5 us at copy rate), backward
+// 8 x 2048 x 1536 bf16: forward 23.5 us (101 MB: 19.5 us at copy rate), backward
 // 39.5 us (151 MB: 29 us; its recomputed convolution, silu' and four products
 // each for dx and the weights are some 22 us of vector instructions) and 5 us
-// for the weights' sums.  3 x 1021 x 1536: 8.5 us; one token of 64 x 5120: 3.8 us.
+// for the weights' sums.  3 x 1021 x 1536: 7.3 us; one token of 64 x 5120: 3.8 us.
 #include "selective.hpp"
 
 #include "launch_selective.hpp"
@@ -362,12 +362,17 @@ int launch(ConvParams p, hipStream_t s) {
     p.nvec = p.ch / V;
     const int64_t row = int64_t(p.batch) * p.nvec;
     if constexpr (WHAT == kFwd) {
-        // 16 tokens to a thread read 1.2 rows for one; 4 where that leaves the device without waves
-        p.run = row * ((p.L + 15) / 16) >= (int64_t(1) << 17) ? 16 : 4;
+        // Longer runs read fewer rows twice, shorter ones give the device more threads.  bf16, 16, 8 and 4 tokens:
+        // 8 x 2048 x 1536 23.5, 26, - us; 4 x 1000 x 2560 15.8, 12.3, 13.7; 3 x 1021 x 1536 -, 7.8, 7.3.
+        const auto threads = [&](int run) { return row * ((p.L + run - 1) / run); };
+        p.run = V > 4 || threads(16) >= (int64_t(1) << 18) ? 16 : threads(8) >= (int64_t(1) << 18) ? 8 : 4;
         p.chunks = (p.L + p.run - 1) / p.run;
         const dim3 grid = blocks_for(row * (p.chunks + (p.fin ? 1 : 0)));
         if (p.run == 16) hipLaunchKernelGGL((conv_fwd_kernel<E, V, W, 16>), grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((conv_fwd_kernel<E, V, W, 4>), grid, dim3(256), 0, s, p);
+        if constexpr (V <= 4) {
+            if (p.run == 8) hipLaunchKernelGGL((conv_fwd_kernel<E, V, W, 8>), grid, dim3(256), 0, s, p);
+            if (p.run == 4) hipLaunchKernelGGL((conv_fwd_kernel<E, V, W, 4>), grid, dim3(256), 0, s, p);
+        }
         return launched();
     } else if constexpr (WHAT == kStep) {
         hipLaunchKernelGGL((conv_step_kernel<E, V, W>), blocks_for(row), dim3(256), 0, s, p);
@@ -393,20 +398,25 @@ int launch_width(int64_t W, const ConvParams& p, hipStream_t s) {
                     : launch<WHAT, E, V, 4>(p, s);
 }
 
-// Whole vectors (16 bytes; 8 for 16-bit elements in the backward pass and the
-// step, whose registers and threads 4 channels suit better) where every row of
-// every tensor starts on one.
+// Whole vectors of 4 channels where every row of every tensor starts on one,
+// and of 8 for the largest forward calls of 16-bit elements (4 x 8192 x 5120
+// bf16: 144 us for 157; 8 x 2048 x 1536: 26.5 for 23.5).
 template <int WHAT, typename E>
 int launch_type(int64_t W, const ConvParams& p, hipStream_t s) {
-    constexpr int V = WHAT == kFwd ? 16 / int(sizeof(typename E::raw)) : 4;
-    uintptr_t at = 0;
+    constexpr int size = int(sizeof(typename E::raw));
+    uint64_t at = 0, params = 0;
     for (const void* q : {p.x, p.init, p.dy, p.dfin, static_cast<const void*>(p.y), static_cast<const void*>(p.fin),
-                          static_cast<const void*>(p.dx), static_cast<const void*>(p.dinit),
-                          static_cast<const void*>(p.w), static_cast<const void*>(p.bias)})
+                          static_cast<const void*>(p.dx), static_cast<const void*>(p.dinit)})
         at |= reinterpret_cast<uintptr_t>(q);
-    const bool whole = at % 16 == 0 && p.ch % V == 0 && p.x_b % V == 0 && p.x_t % V == 0 && p.dy_b % V == 0 &&
-                       p.dy_t % V == 0;
-    return whole ? launch_width<WHAT, E, V>(W, p, s) : launch_width<WHAT, E, 1>(W, p, s);
+    for (const void* q : {static_cast<const void*>(p.w), static_cast<const void*>(p.bias)})
+        params |= reinterpret_cast<uintptr_t>(q);
+    at |= uint64_t(p.ch | p.x_b | p.x_t | p.dy_b | p.dy_t) * size;
+    if (params % 16 != 0 || at % (4 * size) != 0) return launch_width<WHAT, E, 1>(W, p, s);
+    if constexpr (WHAT == kFwd && size == 2) {
+        if (at % 16 == 0 && int64_t(p.batch) * (p.ch / 8) * ((p.L + 15) / 16) >= (int64_t(1) << 19))
+            return launch_width<WHAT, E, 8>(W, p, s);
+    }
+    return launch_width<WHAT, E, 4>(W, p, s);
 }
 
 template <int WHAT>

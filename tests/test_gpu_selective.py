@@ -332,11 +332,26 @@ def test_conv(nb, L, ch, W, kind):
     check_conv(conv_case(30 + L, nb, L, ch, W, kind), label=f"{nb} {L} {ch} {W} {kind}")
 
 
-@pytest.mark.parametrize("nb,L,ch,W", [(4, 2050, 2048, 4), (1, 4097, 513, 3)])
-def test_conv_in_runs_of_16(nb, L, ch, W):
-    """Enough work for runs of 16 tokens forward, in whole vectors and channel by channel."""
+@pytest.mark.parametrize("nb,L,ch,W", [(4, 2050, 2048, 4), (1, 4097, 513, 3), (8, 2053, 2050, 4), (4, 2050, 1028, 2)])
+def test_conv_in_longer_runs(nb, L, ch, W):
+    """Enough work for runs of 8 and 16 tokens forward, in whole vectors and channel by channel."""
     print(f"[conv] {nb} {L} {ch} {W}", flush=True)
     check_conv(conv_case(35, nb, L, ch, W, "bf16", ragged=True), label=f"{nb} {L} {ch} {W}")
+
+
+def test_conv_in_vectors_of_eight():
+    """Enough 16-bit channels for vectors of 8: each token is that of its sequence alone, which runs in other vectors."""
+    g = torch.Generator(device="cuda").manual_seed(37)
+    nb, L, ch, W = 5, 8201, 1640, 4
+    assert nb * (ch // 8) * ((L + 15) // 16) >= 1 << 19 > (ch // 8) * ((L + 15) // 16)
+    x = torch.randn(nb, L, ch, generator=g, device="cuda").bfloat16()
+    w, b = torch.randn(ch, W, generator=g, device="cuda"), torch.randn(ch, generator=g, device="cuda")
+    start = torch.randn(nb, W - 1, ch, generator=g, device="cuda").bfloat16()
+    lens = torch.tensor([L, 0, 17, 5000, L - 1], dtype=torch.int32, device="cuda")
+    y, last = cls.short_conv(x, w, b, start, lens)
+    for i in range(nb):
+        y1, last1 = cls.short_conv(x[i:i + 1], w, b, start[i:i + 1], lens[i:i + 1])
+        assert torch.equal(y[i:i + 1], y1) and torch.equal(last[i:i + 1], last1), i
 
 
 def test_conv_gradients_in_long_runs():
