@@ -63,7 +63,8 @@ ScanCut scan_cut(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
     int64_t nseg = 1;
     if (waves < 1024 && tiles >= 16) {
         const double root = std::sqrt(double(tiles));
-        const int64_t empty = int64_t(2.7 * root) < 3072 / waves ? int64_t(2.7 * root) : 3072 / waves;
+        const int64_t three = 3 * 1024 / waves;  // segments that give each SIMD three waves
+        const int64_t empty = int64_t(2.7 * root) < three ? int64_t(2.7 * root) : three;
         const int64_t full = int64_t(1.75 * root);
         nseg = ceil_div(8192, waves);
         for (int64_t most : {int64_t(cls::kScanMaxSegs), empty > full ? empty : full}) nseg = nseg < most ? nseg : most;
