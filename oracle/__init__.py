@@ -18,6 +18,8 @@ chunked   a float64 mirror of the chunked (state-space duality) algebra, used to
           pin chunk-size invariance before any GPU code exists
 lookback  a float64 simulator of the decoupled look-back tile protocol under
           arbitrary tile completion orders, with deliberately broken variants
+selective the selective scan, its gradients, the short convolution and the 8-bit
+          state cache as token loops, with error scales
 compare   rel-L2 and first-mismatch reporting
 
 Pins: every function here is checked by ``tests/test_oracle_*.py`` against
