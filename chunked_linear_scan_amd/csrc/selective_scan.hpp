@@ -150,19 +150,22 @@ __device__ __forceinline__ f32x4 outer(float rows, float v, f32x4 c = f32x4{0.f,
 }
 
 // sum_k value(T, k) v[k].  The compiler does not fold a DPP operand into a
-// multiply-add, hence the instructions themselves; s_nop: a DPP operand may be
-// read no sooner than two wait states after a vector instruction wrote it.
-template <int T>
+// multiply-add, hence the instructions themselves, and it does not look into
+// them for the waits that their operands need: two wait states between a vector
+// instruction's write and a DPP operand, and five where v comes from a 4x4
+// matrix instruction (MATRIX).  s_nop N waits N + 1.
+template <int T, bool MATRIX = false>
 __device__ __forceinline__ float dot(const float* rows, const float (&v)[4]) {
     constexpr int I = (T & 3) * 4;
     float y;
-    asm("s_nop 1\n\t"
+    asm("s_nop %10\n\t"
         "v_mul_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
         : "=&v"(y)
-        : "v"(rows[T >> 2]), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "n"(I), "n"(I + 1), "n"(I + 2), "n"(I + 3));
+        : "v"(rows[T >> 2]), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "n"(I), "n"(I + 1), "n"(I + 2), "n"(I + 3),
+          "n"(MATRIX ? 5 : 1));
     return y;
 }
 

@@ -224,7 +224,7 @@ __global__ __launch_bounds__(NW * 64, scan_bwd_waves(NW, AGG)) void scan_bwd_ker
                             vB[k] = q[k] * d.y;
                             vC[k] = gy * hs[t][k];
                         }
-                        s_p[wave][0][t][lane] = dot<t>(qB, q);
+                        s_p[wave][0][t][lane] = dot<t, true>(qB, q);
                         s_p[wave][1][t][lane] = to_dt;
                         const float w0 = swap_add32(vB[0], vC[0]), w1 = swap_add32(vB[1], vC[1]);
                         const float w2 = swap_add32(vB[2], vC[2]), w3 = swap_add32(vB[3], vC[3]);
