@@ -268,6 +268,54 @@ def test_scan_on_a_side_stream_and_in_a_graph():
             assert all(torch.equal(a, b) for a, b in zip(got, want)), k
 
 
+def test_scan_from_two_threads_at_once():
+    """Two host threads, a stream each, over the same inputs: every call has a workspace of its own."""
+    import threading
+    c = on_gpu(scan_case(18, 2, 500, 80, 16, 1, kind="bf16", start=True))
+    args = [c[k] for k in SCAN_KEYS]
+
+    def step():
+        y, h, kept = cls.selective_scan(*args, want_checkpoints=True)
+        return [y, h, *cls.selective_scan_bwd(c["dy"], *args, checkpoints=kept).values()]
+
+    want = step()
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(10):
+                got = step()
+                s.synchronize()
+                bad.extend(i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not bad
+
+
+def test_outputs_given_by_the_caller():
+    """Every entry point with `out` writes there and returns it; another shape or type is refused."""
+    c = on_gpu(scan_case(19, 2, 30, 64, 16, 1, kind="bf16"))
+    args = [c[k] for k in SCAN_KEYS]
+    y, _ = cls.selective_scan(*args)
+    out = torch.empty_like(y)
+    got, _ = cls.selective_scan(*args, out=out)
+    assert got.data_ptr() == out.data_ptr() and torch.equal(out, y)
+    w = torch.randn(64, 4, device="cuda")
+    y, _ = cls.short_conv(c["u"], w)
+    got, _ = cls.short_conv(c["u"], w, out=out)
+    assert got.data_ptr() == out.data_ptr() and torch.equal(out, y)
+    with pytest.raises(ValueError):
+        cls.short_conv(c["u"], w, out=out[:, :5])
+    with pytest.raises(ValueError):
+        cls.short_conv(c["u"], w, out=torch.empty(2, 30, 128, dtype=torch.bfloat16, device="cuda")[..., :64])
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("nb,ch,N,G", [(1, 1, 1, 1), (3, 65, 16, 1), (2, 48, 5, 2), (5, 130, 20, 1), (2, 64, 64, 4),
                                        (70, 192, 16, 1), (2, 24, 3, 3),
