@@ -169,7 +169,13 @@ __device__ __forceinline__ float dot(const float* rows, const float (&v)[4]) {
     return y;
 }
 
-// Folds segment s's contribution into v: exp(A sum dt') v + its own, for the wave's states.
+// Folds segment s's contribution into v: exp(A sum dt') v + its own, for the
+// wave's states.  With decays above 1 the whole segment's decay may be infinite
+// in fp32 over a state that is zero or tiny, where the product is neither.  So
+// it is applied as three equal factors (A3: A log2(e) / 3) of 2^100 at most:
+// past that any state but zero overflows as the product does, and a zero stays
+// one.  Decays below 1 take the same way: a branch for the others cost the
+// gradients of 4 x 2048 x 1536 x 16 bf16 1-2 %, this 0.5 %.
 struct ScanFold {
     float sd, own[kScanK];
     __device__ __forceinline__ void load(const ScanParams& p, int s, int64_t b, int ch, int n0) {
@@ -179,11 +185,11 @@ struct ScanFold {
         for (int k = 0; k < kScanK; ++k) own[k] = n0 + k < p.N ? p.seg_h[(sb * p.N + n0 + k) * p.ch + ch] : 0.0f;
     }
     template <typename V>
-    __device__ __forceinline__ void apply(const float (&A2)[kScanK], V& v) const {
+    __device__ __forceinline__ void apply(const float (&A3)[kScanK], V& v) const {
 #pragma unroll
         for (int k = 0; k < kScanK; ++k) {
-            const float x = v[k];
-            v[k] = fmaf(fexp2(A2[k] * sd), x, own[k]);
+            const float f = fexp2(fminf(A3[k] * sd, 100.0f)), x = v[k];
+            v[k] = fmaf(f, f * (f * x), own[k]);
         }
     }
 };
@@ -196,6 +202,9 @@ constexpr int kFoldAtOnce = 4;
 template <typename V>
 __device__ __forceinline__ void scan_fold(const ScanParams& p, int from, int step, int n, int64_t b, int ch, int n0,
                                           const float (&A2)[kScanK], V& v) {
+    float A3[kScanK];
+#pragma unroll
+    for (int k = 0; k < kScanK; ++k) A3[k] = A2[k] * (1.0f / 3.0f);
     for (int i = 0; i < n; i += kFoldAtOnce) {
         ScanFold f[kFoldAtOnce];
 #pragma unroll
@@ -203,7 +212,7 @@ __device__ __forceinline__ void scan_fold(const ScanParams& p, int from, int ste
             if (i + j < n) f[j].load(p, from + step * (i + j), b, ch, n0);
 #pragma unroll
         for (int j = 0; j < kFoldAtOnce; ++j)
-            if (i + j < n) f[j].apply(A2, v);
+            if (i + j < n) f[j].apply(A3, v);
     }
 }
 

@@ -1,0 +1,78 @@
+"""GPU tests of the selective operators where the calls of test_gpu_selective.py do
+not go: decays above 1, sizes beyond the usual, rows on and off whole vectors, and
+how the functions stand beside autograd.  Oracle and tolerances are those of that
+file."""
+import numpy as np
+import pytest
+import torch
+
+import chunked_linear_scan_amd as cls
+from oracle import selective as osel
+from test_gpu_selective import (SCAN_KEYS, check_scan, close, conv_case, f64, on_gpu, oracle_args, scan_case)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# decays above 1
+# ---------------------------------------------------------------------------
+def scan_both_ways(c, label):
+    """Forward and backward of steps given as they are, without a gradient of the final state."""
+    d = on_gpu(c)
+    args = [d[k] for k in SCAN_KEYS]
+    y, h, kept = cls.selective_scan(*args, dt_softplus=False, want_checkpoints=True)
+    grads = cls.selective_scan_bwd(d["dy"], *args, dt_softplus=False, checkpoints=kept)
+    a = oracle_args(c)
+    ry, rh, ys, hs = osel.scan(**a, softplus=False)
+    close(y, ry, ys, label + " y")
+    close(h, rh, hs, label + " h")
+    G, S = osel.scan_grads(f64(c["dy"]), **a, softplus=False)
+    for k, v in grads.items():
+        close(v, G[k], S[k], f"{label} {k}")
+
+
+def growing_case(seed, L, N, sign):
+    """Decays exp(dt A) with A > 0 (sign 1), or with A < 0 and negative steps (sign -1)."""
+    c = scan_case(seed, 1, L, 8, N, 1, kind="f32", gate=False, bias=False, softplus=False)
+    c["A"] = sign * (0.5 + 0.5 * torch.rand(8, N, generator=torch.Generator().manual_seed(seed)))
+    c["dt"] = torch.full((1, L, 8), 0.01 * sign)
+    c["dy"] = c["dy"].contiguous()
+    return c
+
+
+@pytest.mark.parametrize("N", [4, 16])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("L", [120, 1024])  # in one piece, and in segments of some 40 tokens
+def test_scan_growth_of_a_zero_state(L, sign, N):
+    """A hundred steps whose decays multiply to infinity in 32 bits, over a state (or, backward, a gradient) that is
+    zero and stays it.  Even channels: at the start, where no input has come yet; odd ones: at the end, where no
+    gradient has."""
+    print(f"[scan] zero state, {L} tokens, sign {sign}, N={N}", flush=True)
+    c = growing_case(70, L, N, sign)
+    c["dt"][:, :100, ::2] = 6.0 * sign
+    c["u"][:, :100, ::2] = 0.0
+    c["dy"][:, :, ::2] = 0.0
+    c["dt"][:, L - 100:, 1::2] = 6.0 * sign
+    c["u"][:, :, 1::2] = 0.0
+    c["dy"][:, L - 100:, 1::2] = 0.0
+    scan_both_ways(c, f"zero state {L} {sign}")
+
+
+@pytest.mark.parametrize("N", [4, 16])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("L", [120, 1024])
+def test_scan_growth_of_a_tiny_state(L, sign, N):
+    """States of 1e-30 that grow by more than 32 bits hold, to values that they hold; gradients likewise."""
+    print(f"[scan] tiny state, {L} tokens, sign {sign}, N={N}", flush=True)
+    c = growing_case(71, L, N, sign)
+    g = torch.Generator().manual_seed(72)
+    c["A"] = torch.full((8, N), 1.0 * sign) + 0.02 * torch.rand(8, N, generator=g) * sign
+    c["h0"] = 1e-30 * torch.randn(1, 8, N, generator=g)
+    c["u"].zero_()
+    c["dt"].zero_()
+    grow = slice(0, 100) if L == 120 else slice(42, 78)  # within one segment of 40 to 79
+    c["dt"][:, grow] = (104.0 + torch.rand(1, 1, 8, generator=g)) / (grow.stop - grow.start) * sign
+    c["dy"] *= 1e-30
+    scan_both_ways(c, f"tiny state {L} {sign}")
+
+
