@@ -36,17 +36,6 @@ bool strides_ok(const int64_t* s, int n) {
     return true;
 }
 
-// SSD_OK or the status of sizes that the scan refuses.
-int scan_sizes(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
-    if (batch <= 0 || L <= 0 || ch <= 0 || N <= 0 || G <= 0 || ch % G != 0) return SSD_ERR_SHAPE;
-    if (batch > kMaxDim || L > kMaxTokens || ch > kMaxDim) return SSD_ERR_SHAPE;
-    if (N > cls::kScanMaxStates) return SSD_ERR_UNSUPPORTED;
-    const int64_t wgs = batch * G * ceil_div(ch / G, cls::kScanCh);
-    if (wgs * cls::kScanMaxSegs * cls::scan_waves(N) * 64 >= kMaxThreads) return SSD_ERR_SHAPE;
-    if (batch * L > (int64_t(1) << 40) / ch || batch * ch * (N + 2) >= kMaxThreads / 4) return SSD_ERR_SHAPE;
-    return SSD_OK;
-}
-
 // Where the channels and states alone give the device too few waves (below one
 // per SIMD), each sequence is cut into segments, to 8 waves per SIMD where its
 // length allows.  Output pass of 1 x 32768 x 4096 x 16 bf16 at 2048, 4096 and
@@ -71,6 +60,19 @@ ScanCut scan_cut(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
     }
     const int64_t len = ceil_div(tiles, nseg) * cls::kScanTile;
     return ScanCut{ceil_div(L, len), len};
+}
+
+// SSD_OK or the status of sizes that the scan refuses: indexes are 64 bits wide, but for a launch's threads.
+int scan_sizes(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
+    if (batch <= 0 || L <= 0 || ch <= 0 || N <= 0 || G <= 0 || ch % G != 0) return SSD_ERR_SHAPE;
+    if (batch > kMaxDim || L > kMaxTokens || ch > kMaxDim) return SSD_ERR_SHAPE;
+    if (N > cls::kScanMaxStates) return SSD_ERR_UNSUPPORTED;
+    if (batch * L > (int64_t(1) << 40) / ch) return SSD_ERR_SHAPE;
+    const int64_t wgs = batch * G * ceil_div(ch / G, cls::kScanCh) * scan_cut(batch, L, ch, N, G).nseg;
+    if (wgs * cls::scan_waves(N) * 64 >= kMaxThreads) return SSD_ERR_SHAPE;
+    // the last sums of the gradients: four threads to a value of dA, dD and ddt_bias, and 65536 workgroups
+    if (ch * (N + 2) > kMaxThreads / 4 - 65536 * 64 - 64) return SSD_ERR_SHAPE;
+    return SSD_OK;
 }
 
 struct ScanSpace { size_t seg_h, seg_dt, fwd, part_bc, part_a, bwd; };  // offsets, and the totals

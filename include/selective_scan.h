@@ -59,7 +59,12 @@ extern "C" {
  *              selective_scan_checkpoint_size bytes (NULL = not written): the
  *              state before every 8th token
  * dstate is 1..64 (SSD_ERR_UNSUPPORTED above), channels a multiple of
- * ngroups.  Decays above 1 (A > 0) are evaluated as they are.  An input that is
+ * ngroups.  SSD_ERR_SHAPE, too, for batch or channels above 2^24, seqlen above
+ * 2^30, batch * seqlen * channels above 2^40, channels * (dstate + 2) above
+ * 2^30 - 2^22 - 64, and where the launch would pass 2^32 - 1 threads: one for
+ * each four states, rounded up to a power of two, of each channel (a group's
+ * rounded up to 64), sequence and, for long sequences that leave the device
+ * nearly empty, segment.  Decays above 1 (A > 0) are evaluated as they are.  An input that is
  * not finite reaches its own channel's later outputs only (B and C: those of
  * their group), which it makes infinite or NaN.  Outputs must not alias inputs.
  */

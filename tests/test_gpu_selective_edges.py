@@ -76,3 +76,43 @@ def test_scan_growth_of_a_tiny_state(L, sign, N):
     scan_both_ways(c, f"tiny state {L} {sign}")
 
 
+# ---------------------------------------------------------------------------
+# large sizes
+# ---------------------------------------------------------------------------
+def test_scan_of_many_sequences():
+    """More sequences and channels than any cut of them; those picked equal the oracle."""
+    nb, ch, N = 4096, 5120, 16
+    some = [0, 1, 2047, 4095]
+    c = scan_case(73, len(some), 2, ch, N, 1, kind="bf16", start=True)
+    d = on_gpu(c)
+    full = {k: d[k] if d[k] is None or k in ("A", "D", "dt_bias") else
+            torch.zeros(nb, *d[k].shape[1:], dtype=d[k].dtype, device="cuda") for k in SCAN_KEYS}
+    for k, v in full.items():
+        if v is not None and v is not d[k]:
+            v[some] = d[k]
+    y, h = cls.selective_scan(*(full[k] for k in SCAN_KEYS))
+    ry, rh, ys, hs = osel.scan(**oracle_args(c))
+    close(y[some], ry, ys, "y")
+    close(h[some], rh, hs, "h")
+    y[some], h[some] = 0, 0
+    assert not y.any() and not h.any()
+
+
+def test_step_of_many_sequences():
+    """1024 sequences of 5120 channels and 64 states, 1.3 GB of them; those picked equal the oracle."""
+    nb, ch, N = 1024, 5120, 64
+    some = [0, 1, 511, 1023]
+    c = scan_case(74, len(some), 1, ch, N, 1, kind="bf16", start=True)
+    d = on_gpu(c)
+    spread = lambda v: torch.zeros(nb, *v.shape[1:], dtype=v.dtype, device="cuda").index_copy_(  # noqa: E731
+        0, torch.tensor(some, device="cuda"), v)
+    h = spread(d["h0"])
+    u, dt, z, B, C = (spread(d[k][:, 0]) for k in ("u", "dt", "z", "B", "C"))
+    y = cls.selective_scan_step(h, u, dt, d["A"], B, C, d["D"], z=z, dt_bias=d["dt_bias"])
+    ry, rh, ys, hs = osel.scan(**oracle_args(c))
+    close(y[some][:, None], ry, ys, "y")
+    close(h[some], rh, hs, "h")
+    y[some], h[some] = 0, 0
+    assert not y.any() and not h.any()
+
+

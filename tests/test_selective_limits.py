@@ -1,0 +1,37 @@
+"""CPU tests of the sizes that include/selective_scan.h names as its limits: those
+just inside are accepted, those just outside refused.  Nothing is launched: an
+accepted size is seen by the misaligned output that is refused after it."""
+import ctypes
+import os
+
+import pytest
+
+import chunked_linear_scan_amd as cls
+from test_selective_abi import AT, ScanGrads, library, scan_in
+
+pytestmark = pytest.mark.skipif(not os.path.exists(cls.LIB_PATH),
+                                reason="library not built (run __graft_entry__.build())")
+
+SHAPE, ALIGN = -2, -5
+
+
+# batch, seqlen, channels, states, groups
+SCAN_SIZES = [((1024, 1, 16384, 16, 1), ALIGN), ((4096, 2, 5120, 16, 1), ALIGN), ((64, 1, 1024, 64, 1024), ALIGN),
+              ((1024, 1, 5120, 64, 1), ALIGN),
+              (((1 << 18) - 1, 1, 4096, 16, 1), ALIGN), ((1 << 18, 1, 4096, 16, 1), SHAPE),   # 2^32 threads
+              (((1 << 20) - 1, 1, 1, 64, 1), ALIGN), (((1 << 22), 1, 1, 64, 1), SHAPE),
+              ((1, 1, 16205264, 64, 1), ALIGN), ((1, 1, 16205265, 64, 1), SHAPE),           # dA's sums
+              ((1, 1 << 30, 1024, 16, 1), ALIGN), ((1, 1 << 30, 1025, 16, 1), SHAPE),       # 2^40 values
+              ((1, (1 << 30) + 1, 1, 16, 1), SHAPE), (((1 << 24) + 1, 1, 1, 1, 1), SHAPE),
+              ((1, 1, (1 << 24) + 1, 1, 1), SHAPE)]
+
+
+@pytest.mark.parametrize("size,status", SCAN_SIZES)
+def test_scan_sizes(size, status):
+    lib = library()
+    s = scan_in(**dict(zip(("batch", "seqlen", "channels", "dstate", "ngroups"), size)))
+    assert lib.selective_scan_fwd(ctypes.byref(s), AT + 1, AT, AT, AT, 1 << 60, None) == status
+    g = ScanGrads(**{**{k: AT for k in ("dy", "checkpoints", "ddt", "dz", "dB", "dC", "dA")}, "du": AT + 1})
+    assert lib.selective_scan_bwd(ctypes.byref(s), ctypes.byref(g), AT, 1 << 60, None) == status
+    for f, args in ((lib.selective_scan_bwd_workspace_size, size), (lib.selective_scan_checkpoint_size, size[:4])):
+        assert (f(*args) > 0) == (status == ALIGN)
