@@ -14,6 +14,8 @@ struct ScanParams;
 
 int cls_selective_scan_fwd_launch(const cls::ScanParams& p, int dtype, hipStream_t stream);
 int cls_selective_scan_bwd_launch(const cls::ScanParams& p, int dtype, hipStream_t stream);
+// The workgroups of 256 that the step's launch has.
+int64_t cls_selective_scan_step_groups(const selective_scan_inputs& in);
 int cls_selective_scan_step_launch(const selective_scan_inputs& in, float* h, void* y, hipStream_t stream);
 
 // The most partial sums of weight gradients that short_conv_bwd adds up (rows of its workspace).

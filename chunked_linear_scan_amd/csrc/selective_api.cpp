@@ -62,11 +62,17 @@ ScanCut scan_cut(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
     return ScanCut{ceil_div(L, len), len};
 }
 
-// SSD_OK or the status of sizes that the scan refuses: indexes are 64 bits wide, but for a launch's threads.
-int scan_sizes(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
+// SSD_OK or the status of sizes that the scan, whole or one token, refuses.
+int scan_dims(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
     if (batch <= 0 || L <= 0 || ch <= 0 || N <= 0 || G <= 0 || ch % G != 0) return SSD_ERR_SHAPE;
     if (batch > kMaxDim || L > kMaxTokens || ch > kMaxDim) return SSD_ERR_SHAPE;
-    if (N > cls::kScanMaxStates) return SSD_ERR_UNSUPPORTED;
+    return N > cls::kScanMaxStates ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
+// Of whole sequences: indexes are 64 bits wide, but for a launch's threads.
+int scan_sizes(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
+    const int st = scan_dims(batch, L, ch, N, G);
+    if (st != SSD_OK) return st;
     if (batch * L > (int64_t(1) << 40) / ch) return SSD_ERR_SHAPE;
     const int64_t wgs = batch * G * ceil_div(ch / G, cls::kScanCh) * scan_cut(batch, L, ch, N, G).nseg;
     if (wgs * cls::scan_waves(N) * 64 >= kMaxThreads) return SSD_ERR_SHAPE;
@@ -89,12 +95,13 @@ ScanSpace scan_space(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G)
     return s;
 }
 
-// The checks of what the forward and the backward pass read.
-int scan_check(const selective_scan_inputs* in) {
+// The checks of what the forward and the backward pass, or one token (step), read.
+int scan_check(const selective_scan_inputs* in, bool step = false) {
     if (!in || !in->u || !in->dt || !in->B || !in->C || !in->A) return SSD_ERR_NULL;
     if (!dtype_ok(in->dtype)) return SSD_ERR_DTYPE;
-    const int st = scan_sizes(in->batch, in->seqlen, in->channels, in->dstate, in->ngroups);
+    const int st = (step ? scan_dims : scan_sizes)(in->batch, in->seqlen, in->channels, in->dstate, in->ngroups);
     if (st != SSD_OK) return st;
+    if (step && cls_selective_scan_step_groups(*in) * 256 >= kMaxThreads) return SSD_ERR_SHAPE;
     const int64_t strides[] = {in->u_batch, in->u_token, in->dt_batch, in->dt_token, in->z_batch, in->z_token,
                                in->B_batch, in->B_token, in->B_group, in->C_batch, in->C_token, in->C_group};
     if (!strides_ok(strides, 12)) return SSD_ERR_SHAPE;
@@ -239,10 +246,9 @@ int selective_scan_step(const selective_scan_inputs* in, float* h, void* y, void
     one.u_token = one.dt_token = one.z_token = one.B_token = one.C_token = 0;
     one.h0 = nullptr;
     one.seqlens = nullptr;
-    const int st = scan_check(&one);
+    const int st = scan_check(&one, true);
     if (st != SSD_OK) return st;
     if (!aligned(h, 16) || !aligned(y, elem_size(one.dtype))) return SSD_ERR_ALIGN;
-    if (one.batch * (one.channels + 16) >= kMaxThreads / 16) return SSD_ERR_SHAPE;  // 16 lanes to a channel, whole workgroups
     return launched(cls_selective_scan_step_launch(one, h, y, static_cast<hipStream_t>(stream)));
 }
 

@@ -160,42 +160,53 @@ __global__ __launch_bounds__(256) void scan_step_kernel(StepArgs s) {
     }
 }
 
+// Lanes that hold a channel's states, four each, and the workgroups side by side in the channels.
+inline int64_t step_lanes(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+inline int64_t step_blocks(const selective_scan_inputs& in) { return (in.channels * step_lanes(in.dstate) + 255) / 256; }
+
+// four sequences to a thread where that still leaves every CU a few workgroups
+inline int64_t step_fours(const selective_scan_inputs& in) { return step_blocks(in) * ((in.batch + 3) / 4); }
+inline bool step_in_fours(const selective_scan_inputs& in) { return step_lanes(in.dstate) >= 4 && step_fours(in) >= 1024; }
+
 template <typename E, int LS>
 int launch_lanes(StepArgs s, hipStream_t stream) {
     const selective_scan_inputs& in = s.in;
-    s.blocks = uint32_t((in.channels * LS + 255) / 256);
+    s.blocks = uint32_t(step_blocks(in));
     // whole vectors of four states where every row of A, B and C starts on one
     const uint64_t at = reinterpret_cast<uintptr_t>(in.B) | reinterpret_cast<uintptr_t>(in.C) |
                         uint64_t(in.B_batch | in.B_group | in.C_batch | in.C_group) * sizeof(typename E::raw);
     const bool wide = in.dstate % 4 == 0 && reinterpret_cast<uintptr_t>(in.A) % 16 == 0 &&
                       at % (4 * sizeof(typename E::raw)) == 0;
-    const int64_t four = s.blocks * ((in.batch + 3) / 4);
-    const dim3 one(uint32_t(s.blocks * in.batch));
+    const dim3 grid(uint32_t(cls_selective_scan_step_groups(in)));
     if constexpr (LS >= 4) {
-        // four sequences to a thread where that still leaves every CU a few workgroups
-        if (four >= 1024) {
-            if (wide) hipLaunchKernelGGL((scan_step_kernel<E, LS, 4, true>), dim3(uint32_t(four)), dim3(256), 0, stream, s);
-            else hipLaunchKernelGGL((scan_step_kernel<E, LS, 4, false>), dim3(uint32_t(four)), dim3(256), 0, stream, s);
+        if (step_in_fours(in)) {
+            if (wide) hipLaunchKernelGGL((scan_step_kernel<E, LS, 4, true>), grid, dim3(256), 0, stream, s);
+            else hipLaunchKernelGGL((scan_step_kernel<E, LS, 4, false>), grid, dim3(256), 0, stream, s);
             return hipGetLastError() == hipSuccess ? 0 : -7;
         }
     }
-    if (wide) hipLaunchKernelGGL((scan_step_kernel<E, LS, 1, true>), one, dim3(256), 0, stream, s);
-    else hipLaunchKernelGGL((scan_step_kernel<E, LS, 1, false>), one, dim3(256), 0, stream, s);
+    if (wide) hipLaunchKernelGGL((scan_step_kernel<E, LS, 1, true>), grid, dim3(256), 0, stream, s);
+    else hipLaunchKernelGGL((scan_step_kernel<E, LS, 1, false>), grid, dim3(256), 0, stream, s);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
 template <typename E>
 int launch_type(const StepArgs& s, hipStream_t stream) {
-    const int64_t lanes = (s.in.dstate + 3) / 4;
-    return lanes <= 1   ? launch_lanes<E, 1>(s, stream)
-           : lanes <= 2 ? launch_lanes<E, 2>(s, stream)
-           : lanes <= 4 ? launch_lanes<E, 4>(s, stream)
-           : lanes <= 8 ? launch_lanes<E, 8>(s, stream)
-                        : launch_lanes<E, 16>(s, stream);
+    switch (step_lanes(s.in.dstate)) {
+        case 1: return launch_lanes<E, 1>(s, stream);
+        case 2: return launch_lanes<E, 2>(s, stream);
+        case 4: return launch_lanes<E, 4>(s, stream);
+        case 8: return launch_lanes<E, 8>(s, stream);
+        default: return launch_lanes<E, 16>(s, stream);
+    }
 }
 
 }  // namespace
 }  // namespace cls
+
+int64_t cls_selective_scan_step_groups(const selective_scan_inputs& in) {
+    return cls::step_in_fours(in) ? cls::step_fours(in) : cls::step_blocks(in) * in.batch;
+}
 
 int cls_selective_scan_step_launch(const selective_scan_inputs& in, float* h, void* y, hipStream_t stream) {
     const cls::StepArgs s{in, h, y, 0};

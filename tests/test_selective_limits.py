@@ -35,3 +35,18 @@ def test_scan_sizes(size, status):
     assert lib.selective_scan_bwd(ctypes.byref(s), ctypes.byref(g), AT, 1 << 60, None) == status
     for f, args in ((lib.selective_scan_bwd_workspace_size, size), (lib.selective_scan_checkpoint_size, size[:4])):
         assert (f(*args) > 0) == (status == ALIGN)
+
+
+# batch, channels, states, groups
+STEP_SIZES = [((1024, 5120, 64, 1), ALIGN), ((64, 1024, 64, 1024), ALIGN), ((4096, 4096, 64, 4096), ALIGN),
+              ((1 << 20, 1 << 12, 4, 1), SHAPE), (((1 << 20) - 1, 1 << 12, 4, 1), ALIGN),   # a sequence to a thread
+              ((1 << 20, 1 << 12, 16, 1), SHAPE), (((1 << 20) - 4, 1 << 12, 16, 1), ALIGN),  # four
+              ((1 << 18, 1 << 12, 64, 1), SHAPE), (((1 << 18) - 4, 1 << 12, 64, 1), ALIGN),
+              ((1, (1 << 24) + 1, 4, 1), SHAPE), (((1 << 24) + 1, 1, 4, 1), SHAPE)]
+
+
+@pytest.mark.parametrize("size,status", STEP_SIZES)
+def test_step_sizes(size, status):
+    lib = library()
+    s = scan_in(**dict(zip(("batch", "channels", "dstate", "ngroups"), size)))
+    assert lib.selective_scan_step(ctypes.byref(s), AT, AT + 1, None) == status
