@@ -248,7 +248,8 @@ int selective_scan_step(const selective_scan_inputs* in, float* h, void* y, void
     one.seqlens = nullptr;
     const int st = scan_check(&one, true);
     if (st != SSD_OK) return st;
-    if (!aligned(h, 16) || !aligned(y, elem_size(one.dtype))) return SSD_ERR_ALIGN;
+    // whole vectors of states only where every row starts on one
+    if (!aligned(h, one.dstate % 4 == 0 ? 16 : 4) || !aligned(y, elem_size(one.dtype))) return SSD_ERR_ALIGN;
     return launched(cls_selective_scan_step_launch(one, h, y, static_cast<hipStream_t>(stream)));
 }
 

@@ -71,7 +71,8 @@ def selective_scan_bwd(dy, u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None
 def selective_scan_step(h, u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = True,
                         out: torch.Tensor | None = None):
     """One token of ``selective_scan`` for every sequence: updates the state h
-    [Bt, channels, N] (fp32) in place and returns y [Bt, channels].  u, dt and
+    [Bt, channels, N] (fp32; on 16 bytes where N is a multiple of 4, as torch
+    allocates and slices it) in place and returns y [Bt, channels].  u, dt and
     z [Bt, channels], B and C [Bt, groups, N]; the rest as there."""
     return _native().selective_scan_step(h, u, dt, A, B, C, D, z, dt_bias, dt_softplus, out)
 

@@ -133,11 +133,12 @@ int selective_scan_bwd(const selective_scan_inputs* in, const selective_scan_gra
 
 /*
  * One token of the same recurrence for every sequence: the state h
- * [batch, channels, dstate] (fp32, contiguous, 16-byte aligned) is updated in place.  `in`
- * is read with seqlen 1: its token strides, h0 and seqlens are not used.
- * y [batch, channels], contiguous.  Its launch has a thread for each four
- * states (rounded up to a power of two, four sequences sharing one where there
- * are many and dstate is above 8); SSD_ERR_SHAPE where they would pass 2^32 - 1.
+ * [batch, channels, dstate] (fp32, contiguous, 16-byte aligned where dstate is a
+ * multiple of 4) is updated in place.  `in` is read with seqlen 1: its token
+ * strides, h0 and seqlens are not used.  y [batch, channels], contiguous.  Its
+ * launch has a thread for each four states (rounded up to a power of two, four
+ * sequences sharing one where there are many and dstate is above 8);
+ * SSD_ERR_SHAPE where they would pass 2^32 - 1.
  */
 int selective_scan_step(const selective_scan_inputs* in, float* h, void* y, void* stream);
 

@@ -116,3 +116,23 @@ def test_step_of_many_sequences():
     assert not y.any() and not h.any()
 
 
+def test_step_on_states_sliced_from_more():
+    """States of sequences past the first, which with an odd number of values to a sequence start between vectors."""
+    c = scan_case(75, 4, 1, 5, 3, 1, kind="f32", start=True)
+    d = on_gpu(c)
+    h = d["h0"].clone()
+    part = h[1:]
+    assert part.is_contiguous() and part.data_ptr() % 16 != 0
+    one = lambda k: d[k][1:, 0]  # noqa: E731
+    y = cls.selective_scan_step(part, one("u"), one("dt"), d["A"], one("B"), one("C"), d["D"], z=one("z"),
+                                dt_bias=d["dt_bias"])
+    ry, rh, ys, hs = osel.scan(**oracle_args(c))
+    close(y[:, None], ry[1:], ys[1:], "y")
+    close(part, rh[1:], hs[1:], "h")
+    assert torch.equal(h[0], d["h0"][0])
+    off = torch.zeros(1 + 4 * 16, device="cuda")[1:].view(1, 4, 16)
+    z4, z16 = torch.zeros(1, 4, device="cuda"), torch.zeros(1, 1, 16, device="cuda")
+    with pytest.raises(cls.SSDError):  # rows of whole vectors, off them
+        cls.selective_scan_step(off, z4, z4, torch.zeros(4, 16, device="cuda"), z16, z16)
+
+

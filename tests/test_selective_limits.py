@@ -50,3 +50,10 @@ def test_step_sizes(size, status):
     lib = library()
     s = scan_in(**dict(zip(("batch", "channels", "dstate", "ngroups"), size)))
     assert lib.selective_scan_step(ctypes.byref(s), AT, AT + 1, None) == status
+
+
+@pytest.mark.parametrize("n,at", [(16, AT + 4), (16, AT + 8), (3, AT + 2)])
+def test_step_refuses_a_state_off_its_alignment(n, at):
+    """16 bytes where rows are whole vectors, else that of an element."""
+    s = scan_in(dstate=n)
+    assert library().selective_scan_step(ctypes.byref(s), at, AT, None) == ALIGN
