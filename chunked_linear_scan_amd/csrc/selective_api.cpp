@@ -134,14 +134,21 @@ ScanParams scan_params(const selective_scan_inputs& in) {
     return p;
 }
 
+// SSD_OK or the status of sizes that the convolution refuses.
+int conv_sizes(int64_t batch, int64_t L, int64_t ch, int64_t W) {
+    if (batch <= 0 || L <= 0 || ch <= 0 || W <= 0) return SSD_ERR_SHAPE;
+    if (batch > kMaxDim || L > kMaxTokens || ch > kMaxDim) return SSD_ERR_SHAPE;
+    if (W < 2 || W > 4) return SSD_ERR_UNSUPPORTED;
+    // a thread per channel and four tokens, and for the final state; workgroups of 256
+    if (batch * (ceil_div(L, 4) + 1) >= (kMaxThreads - 256) / (ch + 64)) return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
 int conv_check(const short_conv_inputs* in) {
     if (!in || !in->x || !in->weight) return SSD_ERR_NULL;
     if (!dtype_ok(in->dtype)) return SSD_ERR_DTYPE;
-    if (in->batch <= 0 || in->seqlen <= 0 || in->channels <= 0 || in->width <= 0) return SSD_ERR_SHAPE;
-    if (in->batch > kMaxDim || in->seqlen > kMaxTokens || in->channels > kMaxDim) return SSD_ERR_SHAPE;
-    if (in->width < 2 || in->width > 4) return SSD_ERR_UNSUPPORTED;
-    // a thread per channel and four tokens, and for the final state; workgroups of 256
-    if (in->batch * (ceil_div(in->seqlen, 4) + 1) >= (kMaxThreads - 256) / (in->channels + 64)) return SSD_ERR_SHAPE;
+    const int st = conv_sizes(in->batch, in->seqlen, in->channels, in->width);
+    if (st != SSD_OK) return st;
     const int64_t strides[] = {in->x_batch, in->x_token};
     if (!strides_ok(strides, 2)) return SSD_ERR_SHAPE;
     if (!aligned(in->x, elem_size(in->dtype)) || !aligned(in->initial_state, elem_size(in->dtype))) return SSD_ERR_ALIGN;
@@ -262,8 +269,7 @@ int short_conv_fwd(const short_conv_inputs* in, void* y, void* final_state, void
 }
 
 size_t short_conv_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t channels, int64_t width) {
-    if (batch <= 0 || seqlen <= 0 || channels <= 0 || width < 2 || width > 4) return 0;
-    if (batch > kMaxDim || seqlen > kMaxTokens || channels > kMaxDim) return 0;
+    if (conv_sizes(batch, seqlen, channels, width) != SSD_OK) return 0;
     return conv_space(batch, seqlen, channels, width);
 }
 

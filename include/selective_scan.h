@@ -154,6 +154,9 @@ int selective_scan_step(const selective_scan_inputs* in, float* h, void* y, void
  *   y            as x, contiguous
  *   final_state  [batch, width-1, channels]  dtype: the last width-1 inputs
  *                (NULL = not written); it may not alias initial_state
+ * SSD_ERR_SHAPE for batch or channels above 2^24, seqlen above 2^30, and where
+ * batch * (ceil(seqlen / 4) + 1) is not below floor((2^32 - 256) / (channels + 64)).
+ * Outputs must not alias inputs.
  */
 typedef struct {
     int64_t batch, seqlen, channels, width;
@@ -173,7 +176,8 @@ int short_conv_fwd(const short_conv_inputs* in, void* y, void* final_state, void
  * Its gradients: dy [batch, seqlen, channels] (strided) of y, dfinal of
  * final_state (NULL = 0).  Written: dx (contiguous), dweight
  * [channels, width] and dbias [channels] (fp32, NULL = not written),
- * dinitial as initial_state (NULL = not written).
+ * dinitial as initial_state (NULL = not written).  The workspace size is 0 for
+ * sizes that are refused.
  */
 size_t short_conv_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t channels, int64_t width);
 
@@ -201,7 +205,9 @@ int short_conv_step(const short_conv_inputs* in, void* state, void* y, void* str
  *   cache   [nslots, rows, dstate]  bytes, contiguous
  *   scales  [nslots, rows]          fp32, contiguous
  *   slots   [batch]                 int32, device memory: the slot of each state
- * dstate is 1..256.  Write: a state whose slot is outside 0..nslots-1 is not
+ * dstate is 1..256 (SSD_ERR_UNSUPPORTED above); SSD_ERR_SHAPE from
+ * batch * (rows + 256) = 2^26 or nslots = 2^31 on, and above
+ * nslots * rows * dstate = 2^46.  Write: a state whose slot is outside 0..nslots-1 is not
  * written; where a slot is named more than once the last state that names it
  * is kept; all other slots stay as they are.  Read: a slot outside 0..nslots-1
  * gives a state of zeros, the start of a sequence without a snapshot.

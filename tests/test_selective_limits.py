@@ -7,7 +7,7 @@ import os
 import pytest
 
 import chunked_linear_scan_amd as cls
-from test_selective_abi import AT, ScanGrads, library, scan_in
+from test_selective_abi import AT, ScanGrads, conv_in, library, scan_in
 
 pytestmark = pytest.mark.skipif(not os.path.exists(cls.LIB_PATH),
                                 reason="library not built (run __graft_entry__.build())")
@@ -57,3 +57,34 @@ def test_step_refuses_a_state_off_its_alignment(n, at):
     """16 bytes where rows are whole vectors, else that of an element."""
     s = scan_in(dstate=n)
     assert library().selective_scan_step(ctypes.byref(s), at, AT, None) == ALIGN
+
+
+# batch, seqlen, channels
+CONV_SIZES = [((1 << 24, 1 << 30, 1 << 24), SHAPE), ((1 << 20, 1 << 20, 1 << 20), SHAPE), ((64, 4096, 5120), ALIGN),
+              (((1 << 24) - 4, 1, 64), ALIGN), ((1 << 24, 1, 64), SHAPE), ((1, (1 << 24) - 12, 960), ALIGN),
+              ((1, (1 << 24) - 8, 960), SHAPE)]
+
+
+@pytest.mark.parametrize("size,status", CONV_SIZES)
+def test_conv_sizes(size, status):
+    lib = library()
+    s = conv_in(**dict(zip(("batch", "seqlen", "channels"), size)))
+    assert lib.short_conv_fwd(ctypes.byref(s), AT + 1, AT, None) == status
+    assert lib.short_conv_bwd(ctypes.byref(s), AT, 0, 0, None, AT + 1, AT, AT, AT, AT, 1 << 60, None) == status
+    for width in (2, 4):
+        assert (lib.short_conv_bwd_workspace_size(*size, width) > 0) == (status == ALIGN)
+    assert lib.short_conv_bwd_workspace_size(*size, 1) == 0 and lib.short_conv_bwd_workspace_size(*size, 5) == 0
+
+
+# batch, rows, states, slots
+CACHE_SIZES = [((1, (1 << 26) - 257, 1, 1), ALIGN), ((1, (1 << 26) - 256, 1, 1), SHAPE),
+               ((64, (1 << 20) - 257, 16, 64), ALIGN), ((64, (1 << 20) - 256, 16, 64), SHAPE),
+               ((1, 1 << 15, 1, (1 << 31) - 1), ALIGN), ((1, 1 << 15, 1, 1 << 31), SHAPE),
+               ((1, 1 << 16, 1, 1 << 30), ALIGN), ((1, (1 << 16) + 1, 1, 1 << 30), SHAPE)]
+
+
+@pytest.mark.parametrize("size,status", CACHE_SIZES)
+def test_cache_sizes(size, status):
+    lib = library()
+    assert lib.state_cache_write(AT + 2, AT, *size, 3, AT, AT, None) == status
+    assert lib.state_cache_read(AT, AT + 2, AT, *size, 3, AT, None) == status
