@@ -12,6 +12,8 @@
 #include <optional>
 #include <string>
 #include <tuple>
+#include <type_traits>
+#include <utility>
 #include <vector>
 
 #include "../../include/selective_scan.h"
@@ -89,6 +91,27 @@ void ok(int status, const char* what) {
     const py::object e = py::module_::import("chunked_linear_scan_amd").attr("SSDError");
     PyErr_SetObject(e.ptr(), e(status, what).ptr());
     throw py::error_already_set();
+}
+
+// Whether autograd follows one of the tensors now.
+template <typename... T>
+bool followed(const T&... tensors) {
+    const auto needs = [](const auto& t) {
+        if constexpr (std::is_same_v<std::decay_t<decltype(t)>, Maybe>) return t && t->requires_grad();
+        else return t.requires_grad();
+    };
+    return at::GradMode::is_enabled() && (needs(tensors) || ...);
+}
+
+// The outputs of a call on such tensors: the same values, through which a backward pass raises.
+std::vector<Tensor> unrecorded(const char* what, const std::vector<Tensor>& outputs) {
+    const py::object f = py::module_::import("chunked_linear_scan_amd.selective").attr("_unrecorded");
+    return f(what, outputs).cast<std::vector<Tensor>>();
+}
+std::pair<Tensor, Maybe> unrecorded(const char* what, const Tensor& output, const Maybe& state) {
+    if (!state) return {unrecorded(what, {output})[0], state};
+    const std::vector<Tensor> got = unrecorded(what, {output, *state});
+    return {got[0], got[1]};
 }
 
 // The launches' device is current for the scope's life.
@@ -174,6 +197,10 @@ std::tuple<Tensor, Maybe, Maybe> scan(const Tensor& u, const Tensor& dt, const T
     const size_t need = selective_scan_workspace_size(s.batch, s.seqlen, s.channels, s.dstate, s.ngroups);
     if (need) ws = bytes(need, u.device());
     ok(selective_scan_fwd(&s, ptr(y), ptr<float>(h), ptr(kept), ptr(ws), need, on.stream), "selective_scan");
+    if (followed(u, dt, A, B, C, D, z, dt_bias, h0)) {
+        const auto got = unrecorded("selective_scan", y, h);
+        return {got.first, got.second, kept};
+    }
     return {y, h, kept};
 }
 
@@ -220,6 +247,7 @@ Tensor scan_step(const Tensor& h, const Tensor& u, const Tensor& dt, const Tenso
     const On on(u.device());
     const Tensor y = output(out, u);
     ok(selective_scan_step(&s, ptr<float>(h), ptr(y), on.stream), "selective_scan_step");
+    if (followed(h, u, dt, A, B, C, D, z, dt_bias)) return unrecorded("selective_scan_step", {y})[0];
     return y;
 }
 
@@ -250,14 +278,15 @@ short_conv_inputs conv_inputs(const Tensor& x, const Tensor& weight, const Maybe
     return s;
 }
 
-std::tuple<Tensor, Maybe> conv(const Tensor& x, const Tensor& weight, const Maybe& bias, const Maybe& initial_state,
-                               const Maybe& seqlens, bool silu, bool final_state, const Maybe& out) {
+std::pair<Tensor, Maybe> conv(const Tensor& x, const Tensor& weight, const Maybe& bias, const Maybe& initial_state,
+                              const Maybe& seqlens, bool silu, bool final_state, const Maybe& out) {
     const short_conv_inputs s = conv_inputs(x, weight, bias, initial_state, seqlens, silu, false);
     const On on(x.device());
     const Tensor y = output(out, x);
     Maybe last;
     if (final_state) last = at::empty({s.batch, s.width > 0 ? s.width - 1 : 0, s.channels}, x.options());
     ok(short_conv_fwd(&s, ptr(y), ptr(last), on.stream), "short_conv");
+    if (followed(x, weight, bias, initial_state)) return unrecorded("short_conv", y, last);
     return {y, last};
 }
 
@@ -290,6 +319,7 @@ Tensor conv_step(const Tensor& state, const Tensor& x, const Tensor& weight, con
     const On on(x.device());
     const Tensor y = output(out, x);
     ok(short_conv_step(&s, ptr(state), ptr(y), on.stream), "short_conv_step");
+    if (followed(state, x, weight, bias)) return unrecorded("short_conv_step", {y})[0];
     return y;
 }
 

@@ -9,6 +9,11 @@ of the inputs' device.  Activations may be slices of wider rows (their last
 dimension adjacent); parameters and states are contiguous.  Each call has a
 workspace of its own from torch's allocator, so calls on several streams and
 captured graphs share none.
+
+Nothing is recorded for autograd: gradients come from ``selective_scan_bwd`` and
+``short_conv_bwd``.  Where a tensor that requires a gradient is passed while
+autograd records, a backward pass through the outputs raises (a state updated in
+place carries no such mark).
 """
 from __future__ import annotations
 
@@ -30,6 +35,28 @@ def _native():
                                "`python -c 'import __graft_entry__ as g; g.build()'`") from e
         _module = _selective_binding
     return _module
+
+
+class _Unrecorded(torch.autograd.Function):
+    """Outputs as they are, marked so that a backward pass through them raises.  The mark hangs on a tensor of its own:
+    it keeps no graph of the caller's alive."""
+
+    @staticmethod
+    def forward(ctx, what, mark, *outputs):
+        ctx.what = what
+        ctx.mark_dirty(*outputs)
+        return outputs
+
+    @staticmethod
+    def backward(ctx, *grads):
+        call = "selective_scan_bwd" if ctx.what.startswith("selective_scan") else "short_conv_bwd"
+        raise RuntimeError(f"{ctx.what} records no gradient: take those of its inputs from {call}, over whole sequences, "
+                           "or pass tensors that require none")
+
+
+def _unrecorded(what, outputs):
+    """Called by the binding where autograd follows one of a call's inputs."""
+    return list(_Unrecorded.apply(what, torch.empty(0, requires_grad=True), *(t.detach() for t in outputs)))
 
 
 # ---------------------------------------------------------------------------

@@ -136,3 +136,46 @@ def test_step_on_states_sliced_from_more():
         cls.selective_scan_step(off, z4, z4, torch.zeros(4, 16, device="cuda"), z16, z16)
 
 
+# ---------------------------------------------------------------------------
+# beside autograd
+# ---------------------------------------------------------------------------
+def layer_calls():
+    """name: (call, the tensors it takes) of every function with floating-point outputs of its own."""
+    c = on_gpu(scan_case(76, 2, 9, 16, 4, 1, kind="f32", start=True))
+    A, D, w, b = c["A"], c["D"], torch.randn(16, 4, device="cuda"), torch.randn(16, device="cuda")
+    state = torch.randn(2, 3, 16, device="cuda")
+    t = {k: c[k][:, 0].contiguous() for k in ("u", "dt", "z", "B", "C")}
+    return {
+        "selective_scan": (lambda u, dt, A, B, C, D, z, bias, h0: cls.selective_scan(
+            u, dt, A, B, C, D, z=z, dt_bias=bias, h0=h0),
+            [c["u"], c["dt"], A, c["B"], c["C"], D, c["z"], c["dt_bias"], c["h0"]]),
+        "selective_scan_step": (lambda u, dt, A, B, C, D, z, bias: (cls.selective_scan_step(
+            c["h0"].clone(), u, dt, A, B, C, D, z=z, dt_bias=bias),),
+            [t["u"], t["dt"], A, t["B"], t["C"], D, t["z"], c["dt_bias"]]),
+        "short_conv": (lambda x, w, b, s: cls.short_conv(x, w, b, s), [c["u"], w, b, state]),
+        "short_conv_step": (lambda x, w, b: (cls.short_conv_step(state.clone(), x, w, b),), [t["u"], w, b]),
+    }
+
+
+@pytest.mark.parametrize("name", ["selective_scan", "selective_scan_step", "short_conv", "short_conv_step"])
+def test_a_gradient_is_not_lost_in_silence(name):
+    """No function records a gradient: a backward pass that would need one raises, and says what to call."""
+    call, tensors = layer_calls()[name]
+    want = call(*tensors)
+    assert not any(v.requires_grad for v in want)
+    for i in range(len(tensors)):
+        leaves = [v.clone().requires_grad_() if j == i else v for j, v in enumerate(tensors)]
+        got = call(*leaves)
+        for g, w in zip(got, want):
+            assert g.requires_grad and torch.equal(g.detach(), w), (name, i)
+            with pytest.raises(RuntimeError, match=f"{name} records no gradient"):
+                g.sum().backward()
+        with torch.no_grad():
+            assert not any(v.requires_grad for v in call(*leaves))
+    # the gradient functions take what requires gradients, and give plain tensors
+    if name == "short_conv":
+        leaves = [v.clone().requires_grad_() for v in tensors]
+        grads = cls.short_conv_bwd(tensors[0], *leaves)
+        assert not any(v.requires_grad for v in grads.values())
+
+
