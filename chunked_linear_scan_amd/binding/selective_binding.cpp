@@ -121,6 +121,14 @@ struct On {
     explicit On(at::Device d) : guard(d), stream(c10::hip::getCurrentHIPStream(d.index()).stream()) {}
 };
 
+// Tells autograd that a tensor was written in place (one of inference mode counts no versions).
+void written(const Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(const Maybe& t) {
+    if (t) written(*t);
+}
+
 Tensor dense_like(const Tensor& t) { return at::empty(t.sizes(), t.options()); }
 
 Tensor output(const Maybe& out, const Tensor& like) {
@@ -197,6 +205,7 @@ std::tuple<Tensor, Maybe, Maybe> scan(const Tensor& u, const Tensor& dt, const T
     const size_t need = selective_scan_workspace_size(s.batch, s.seqlen, s.channels, s.dstate, s.ngroups);
     if (need) ws = bytes(need, u.device());
     ok(selective_scan_fwd(&s, ptr(y), ptr<float>(h), ptr(kept), ptr(ws), need, on.stream), "selective_scan");
+    written(out);
     if (followed(u, dt, A, B, C, D, z, dt_bias, h0)) {
         const auto got = unrecorded("selective_scan", y, h);
         return {got.first, got.second, kept};
@@ -247,6 +256,8 @@ Tensor scan_step(const Tensor& h, const Tensor& u, const Tensor& dt, const Tenso
     const On on(u.device());
     const Tensor y = output(out, u);
     ok(selective_scan_step(&s, ptr<float>(h), ptr(y), on.stream), "selective_scan_step");
+    written(h);
+    written(out);
     if (followed(h, u, dt, A, B, C, D, z, dt_bias)) return unrecorded("selective_scan_step", {y})[0];
     return y;
 }
@@ -286,6 +297,7 @@ std::pair<Tensor, Maybe> conv(const Tensor& x, const Tensor& weight, const Maybe
     Maybe last;
     if (final_state) last = at::empty({s.batch, s.width > 0 ? s.width - 1 : 0, s.channels}, x.options());
     ok(short_conv_fwd(&s, ptr(y), ptr(last), on.stream), "short_conv");
+    written(out);
     if (followed(x, weight, bias, initial_state)) return unrecorded("short_conv", y, last);
     return {y, last};
 }
@@ -319,6 +331,8 @@ Tensor conv_step(const Tensor& state, const Tensor& x, const Tensor& weight, con
     const On on(x.device());
     const Tensor y = output(out, x);
     ok(short_conv_step(&s, ptr(state), ptr(y), on.stream), "short_conv_step");
+    written(state);
+    written(out);
     if (followed(state, x, weight, bias)) return unrecorded("short_conv_step", {y})[0];
     return y;
 }
@@ -356,6 +370,8 @@ void cache_write(const Tensor& h, const Tensor& cache, const Tensor& scales, con
     ok(state_cache_write(ptr<float>(h), ptr<int32_t>(slots), a.batch, a.rows, a.dstate, a.nslots, a.format, ptr(cache),
                          ptr<float>(scales), on.stream),
        "state_cache_write");
+    written(cache);
+    written(scales);
 }
 
 Tensor cache_read(const Tensor& cache, const Tensor& scales, const Tensor& slots, const Maybe& out) {
@@ -366,6 +382,7 @@ Tensor cache_read(const Tensor& cache, const Tensor& scales, const Tensor& slots
     ok(state_cache_read(ptr(cache), ptr<float>(scales), ptr<int32_t>(slots), a.batch, a.rows, a.dstate, a.nslots,
                         a.format, ptr<float>(h), on.stream),
        "state_cache_read");
+    written(out);
     return h;
 }
 

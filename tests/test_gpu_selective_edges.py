@@ -179,3 +179,34 @@ def test_a_gradient_is_not_lost_in_silence(name):
         assert not any(v.requires_grad for v in grads.values())
 
 
+def test_writes_in_place_are_seen_by_autograd():
+    """States, caches and given outputs are written in place: a backward pass that still needs what they held raises."""
+    c = on_gpu(scan_case(77, 2, 9, 16, 4, 1, kind="f32", start=True))
+    t = {k: c[k][:, 0].contiguous() for k in ("u", "dt", "z", "B", "C")}
+    w, state = torch.randn(16, 4, device="cuda"), torch.randn(2, 3, 16, device="cuda")
+    cache, scales = torch.zeros(3, 16, 4, dtype=torch.int8, device="cuda"), torch.zeros(3, 16, device="cuda")
+    slots = torch.tensor([2, 0], dtype=torch.int32, device="cuda")
+    h, out, out1 = c["h0"].clone(), torch.empty(2, 9, 16, device="cuda"), torch.empty(2, 16, device="cuda")
+    back = torch.empty(2, 16, 4, device="cuda")
+    scan = [c[k] for k in ("u", "dt", "A", "B", "C")]
+    step = [t["u"], t["dt"], c["A"], t["B"], t["C"]]
+    for call, written in ((lambda: cls.selective_scan_step(h, *step, out=out1), (h, out1)),
+                          (lambda: cls.short_conv_step(state, t["u"], w, out=out1), (state, out1)),
+                          (lambda: cls.selective_scan(*scan, out=out), (out,)),
+                          (lambda: cls.short_conv(c["u"], w, out=out), (out,)),
+                          (lambda: cls.state_cache_write(h, cache, scales, slots), (cache, scales)),
+                          (lambda: cls.state_cache_read(cache, scales, slots, out=back), (back,))):
+        before = [v._version for v in written]
+        call()
+        assert [v._version for v in written] == [v + 1 for v in before]
+    x = torch.randn(2, 16, 4, device="cuda", requires_grad=True)
+    loss = (x * h).sum()
+    cls.selective_scan_step(h, *step)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():  # such tensors count no versions
+        inner = torch.zeros(2, 16, 4, device="cuda")
+    cls.selective_scan_step(inner, *step)
+    assert inner.any()
+
+
