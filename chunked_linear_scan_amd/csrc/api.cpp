@@ -109,13 +109,13 @@ const char* ssd_strerror(int status) {
     switch (status) {
         case SSD_OK: return "ok";
         case SSD_ERR_NULL: return "a required pointer is NULL";
-        case SSD_ERR_SHAPE: return "invalid shape (a size <= 0, too large, or heads % groups != 0)";
+        case SSD_ERR_SHAPE: return "invalid shape (a size or stride below its least or too large, or heads or channels not a multiple of the groups)";
         case SSD_ERR_DTYPE: return "an element type that the call does not take";
         case SSD_ERR_CHUNK: return "chunk must be 16, 32, 64, 128 or 256";
-        case SSD_ERR_ALIGN: return "a pointer is not 16-byte aligned";
+        case SSD_ERR_ALIGN: return "a pointer is not on the alignment that the call wants";
         case SSD_ERR_WORKSPACE: return "workspace is NULL or smaller than required";
         case SSD_ERR_HIP: return "a HIP kernel launch failed";
-        case SSD_ERR_UNSUPPORTED: return "head dim / state size not supported by this dtype's kernels";
+        case SSD_ERR_UNSUPPORTED: return "a head dim, state size or convolution width that the kernels of this element type do not take";
         default: return "unknown status";
     }
 }

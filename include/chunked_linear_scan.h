@@ -35,13 +35,13 @@ extern "C" {
 enum {
     SSD_OK = 0,
     SSD_ERR_NULL = -1,        /* a required pointer is NULL                      */
-    SSD_ERR_SHAPE = -2,       /* a size is <= 0, or heads % groups != 0          */
-    SSD_ERR_DTYPE = -3,       /* dtype is not SSD_F32 or SSD_BF16                */
+    SSD_ERR_SHAPE = -2,       /* a size <= 0 or too large, or not in groups      */
+    SSD_ERR_DTYPE = -3,       /* an element type that the call does not take     */
     SSD_ERR_CHUNK = -4,       /* chunk is not one of 16, 32, 64, 128, 256        */
-    SSD_ERR_ALIGN = -5,       /* a pointer is not 16-byte aligned                */
+    SSD_ERR_ALIGN = -5,       /* a pointer is not aligned as the call wants      */
     SSD_ERR_WORKSPACE = -6,   /* workspace NULL or smaller than required         */
     SSD_ERR_HIP = -7,         /* a HIP launch failed                             */
-    SSD_ERR_UNSUPPORTED = -8  /* head dim / state size outside the kernel's set  */
+    SSD_ERR_UNSUPPORTED = -8  /* head dim, state size or width outside the set   */
 };
 
 /* Element types of x, B, C and y (SSD_F32, SSD_BF16); dt, A, D and both

@@ -88,3 +88,9 @@ def test_cache_sizes(size, status):
     lib = library()
     assert lib.state_cache_write(AT + 2, AT, *size, 3, AT, AT, None) == status
     assert lib.state_cache_read(AT, AT + 2, AT, *size, 3, AT, None) == status
+
+
+@pytest.mark.parametrize("status,words", [(SHAPE, ("channels", "stride")), (ALIGN, ("alignment",)), (-8, ("width", "state"))])
+def test_error_texts_hold_for_every_call(status, words):
+    text = cls.strerror(status)
+    assert all(w in text for w in words) and "16" not in text
