@@ -88,14 +88,13 @@ def build(verbose: bool = True, jobs: int | None = None) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
         binding = ex.submit(_compile_binding, os.path.join(BUILD, "selective_binding.o"))
         objs = list(ex.map(_compile, srcs))
-        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    _link_binding(binding.result())  # last: the C library stands without torch's headers and g++
     if verbose:
         print(f"built {LIB} from {len(srcs)} sources, and {BINDING}", file=sys.stderr)
     return LIB
