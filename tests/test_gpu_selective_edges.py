@@ -210,3 +210,137 @@ def test_writes_in_place_are_seen_by_autograd():
     assert inner.any()
 
 
+def test_memory_that_runs_out_is_torch_s_error():
+    """An output larger than the device (inputs expanded over the batch), as torch reports it for its own."""
+    x = torch.zeros(1, 1 << 10, 1 << 10, device="cuda").expand(1 << 17, 1 << 10, 1 << 10)
+    B = torch.zeros(1, 1, 1, 4, device="cuda").expand(1 << 17, 1 << 10, 1, 4)
+    assert x.numel() * 4 > torch.cuda.get_device_properties(0).total_memory
+    with pytest.raises(torch.OutOfMemoryError):
+        cls.selective_scan(x, x, torch.zeros(1 << 10, 4, device="cuda"), B, B)
+    with pytest.raises(torch.OutOfMemoryError):
+        cls.short_conv(x, torch.zeros(1 << 10, 4, device="cuda"))
+
+
+# ---------------------------------------------------------------------------
+# rows on and off whole vectors
+# ---------------------------------------------------------------------------
+def step_case(seed, nb, ch, N, G, kind, first):
+    """One token whose B and C stand in one row behind `first` columns, as in a layer's projection."""
+    c = scan_case(seed, nb, 1, ch, N, G, kind=kind, start=True)
+    bc = torch.randn(nb, 1, first + 2 * G * N, generator=torch.Generator().manual_seed(seed)).to(c["u"].dtype)
+    c["B"] = bc[..., first:first + G * N].unflatten(-1, (G, N))
+    c["C"] = bc[..., first + G * N:].unflatten(-1, (G, N))
+    return c, bc
+
+
+# one and four sequences to a thread (1024 workgroups), whole and partial groups of four
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("nb,ch,N,G", [(2, 70, 4, 1), (3, 64, 8, 2), (1, 1536, 16, 1), (6, 33, 20, 3), (5, 24, 32, 1),
+                                       (3, 48, 64, 2), (301, 1200, 12, 1), (130, 2400, 16, 2), (99, 1504, 20, 1),
+                                       (67, 1928, 32, 4), (50, 1280, 64, 1), (29, 2320, 52, 1)])
+def test_step_in_whole_vectors(nb, ch, N, G, kind):
+    print(f"[scan step] {nb} {ch} {N} {G} {kind}", flush=True)
+    for first in (0, 48):
+        c, bc = step_case(80 + nb, nb, ch, N, G, kind, first)
+        d = on_gpu(c)
+        wide = bc.cuda()
+        d["B"] = wide[..., first:first + G * N].unflatten(-1, (G, N))
+        d["C"] = wide[..., first + G * N:].unflatten(-1, (G, N))
+        h = d["h0"].clone()
+        one = lambda k: d[k][:, 0]  # noqa: E731
+        size = 4 * d["B"].element_size()  # bytes of four states
+        for v in (one("B"), one("C")):
+            assert v.data_ptr() % size == 0 and all(s * v.element_size() % size == 0 for s in v.stride()[:2])
+        assert N % 4 == 0 and d["A"].data_ptr() % 16 == 0 and h.data_ptr() % 16 == 0
+        y = cls.selective_scan_step(h, one("u"), one("dt"), d["A"], one("B"), one("C"), d["D"], z=one("z"),
+                                    dt_bias=d["dt_bias"])
+        ry, rh, ys, hs = osel.scan(**oracle_args(c))
+        close(y[:, None], ry, ys, f"y {first}")
+        close(h, rh, hs, f"h {first}")
+
+
+def off_vectors(v):
+    """The same tensor one element past a whole vector, its strides unchanged."""
+    need = 1 + sum((n - 1) * s for n, s in zip(v.shape, v.stride()))
+    base = torch.empty(need + 1, dtype=v.dtype, device=v.device)
+    assert base.data_ptr() % 16 == 0
+    moved = base[1:].as_strided(v.shape, v.stride())
+    moved.copy_(v)
+    assert moved.data_ptr() % 8 == v.element_size()
+    return moved
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["x", "dy", "initial_state", "dfinal", "weight", "bias", "out", "none"])
+def test_conv_with_one_tensor_off_whole_vectors(name, kind):
+    """Strides that keep every row on a vector, from a first element that is not on one."""
+    print(f"[conv] {name} off {kind}", flush=True)
+    c = conv_case(81, 3, 70, 48, 4, kind)
+    c["x"], c["dy"] = c["x"].contiguous(), c["dy"].contiguous()
+    c["seqlens"] = torch.tensor([70, 0, 31], dtype=torch.int32)
+    d = on_gpu(c)
+    out = torch.empty_like(d["x"])
+    if name == "out":
+        out = off_vectors(out)
+    elif name != "none":
+        d[name] = off_vectors(d[name])
+    args = [d[k] for k in ("x", "weight", "bias", "initial_state", "seqlens")]
+    y, last = cls.short_conv(*args, out=out)
+    grads = cls.short_conv_bwd(d["dy"], *args, dfinal_state=d["dfinal"])
+    a = {k: f64(c[k]) for k in ("x", "weight", "bias", "initial_state")}
+    a["seqlens"] = c["seqlens"].numpy()
+    ry, rl, ys = osel.conv(**a)
+    close(y, ry, ys, "y")
+    assert np.array_equal(f64(last), rl)
+    G, S = osel.conv_grads(f64(c["dy"]), **a, dfinal=f64(c["dfinal"]))
+    for k, v in grads.items():
+        close(v, G[k], S[k], k)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["x", "state", "weight", "bias", "out", "none"])
+def test_conv_step_with_one_tensor_off_whole_vectors(name, kind):
+    print(f"[conv step] {name} off {kind}", flush=True)
+    c = conv_case(85, 3, 1, 48, 4, kind)
+    d = on_gpu(c)
+    t = dict(x=d["x"][:, 0].contiguous(), weight=d["weight"], bias=d["bias"], state=d["initial_state"].clone())
+    t["out"] = torch.empty_like(t["x"])
+    if name != "none":
+        t[name] = off_vectors(t[name])
+    y = cls.short_conv_step(t["state"], t["x"], t["weight"], t["bias"], out=t["out"])
+    ry, rl, ys = osel.conv(*(f64(c[k]) for k in ("x", "weight", "bias", "initial_state")))
+    close(y[:, None], ry, ys, "y")
+    assert np.array_equal(f64(t["state"]), rl)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_scan_with_every_tensor_off_whole_vectors(kind):
+    c = scan_case(82, 2, 70, 48, 16, 2, kind=kind, start=True)
+    d = on_gpu(c)
+    moved = {k: off_vectors(v) if torch.is_tensor(v) and v.is_floating_point() else v for k, v in d.items()}
+    runs = []
+    for a in (d, moved):
+        args = [a[k] for k in SCAN_KEYS]
+        y, h, kept = cls.selective_scan(*args, want_checkpoints=True)
+        runs.append([y, h, *cls.selective_scan_bwd(a["dy"], *args, checkpoints=kept, dh_final=a["dh"]).values()])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+# ---------------------------------------------------------------------------
+# segments
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("softplus", [True, False])
+@pytest.mark.parametrize("N,G", [(3, 1), (4, 2), (7, 3), (8, 1), (16, 2), (24, 2), (32, 1), (64, 2)])
+def test_scan_in_segments(N, G, softplus):
+    """Every number of waves to a workgroup, in segments, with groups and steps given as they are."""
+    print(f"[scan] segments N={N} G={G} softplus={softplus}", flush=True)
+    c = scan_case(83, 2, 333, 12, N, G, kind="f32", start=True, ragged=True, softplus=softplus)
+    c["seqlens"][0] = 333
+    check_scan(c, softplus=softplus, label=f"{N} {G} {softplus}")
+
+
+def test_scan_in_the_most_segments():
+    """8192 tokens of few channels: as many segments as there can be, and one sequence that ends in the first."""
+    c = scan_case(84, 2, 8192, 3, 4, 1, kind="f32", start=True)
+    c["seqlens"] = torch.tensor([8192, 5], dtype=torch.int32)
+    check_scan(c, label="most segments")
