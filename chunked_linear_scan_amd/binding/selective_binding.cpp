@@ -3,7 +3,7 @@
 // inputs' device.  It holds no computation and no state.  Native because a call
 // has up to a dozen tensors to check, which in Python takes longer than the
 // smallest kernels run: one decode token of a sequence took 10.5 us a call, and
-// takes 4.7 (3 of them the launch).
+// takes 4 to 5 (3 of them the launch).
 #include <torch/extension.h>
 
 #include <c10/core/DeviceGuard.h>

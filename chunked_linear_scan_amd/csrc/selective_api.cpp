@@ -45,7 +45,12 @@ bool strides_ok(const int64_t* s, int n) {
 // 12.5 + 2.2 tiles / segments + 0.3 segments in several, so nothing is cut below
 // 16 tiles and the best number is 2.7 roots of the tiles; with some waves on
 // every SIMD fewer are better (2 x 1000 x 1536 x 16 fp32 in 11, 16, 21 and 32
-// segments: 23.4, 22, 21.5 and 26 us).
+// segments: 23.4, 22, 21.5 and 26 us).  The border of one wave per SIMD is not
+// the best one: 8 x 2048 tokens of 1984 channels (cut) and of 2048 (whole) take
+// 254 and 318 us forward and 523 and 851 us for the gradients, of 4096 (whole,
+// two waves) 404 and 1048 us.  Nor is the most of 64 segments for long sequences
+// of few channels: 1 x 65536 x 64 x 16 takes 272 us, where more would be faster
+// by the formula above.
 ScanCut scan_cut(int64_t batch, int64_t L, int64_t ch, int64_t N, int64_t G) {
     const int64_t tiles = ceil_div(L, cls::kScanTile);
     const int64_t waves = batch * G * ceil_div(ch / G, cls::kScanCh) * cls::scan_waves(N);

@@ -24,7 +24,7 @@ constexpr int64_t kScanMaxTokenStride = int64_t(1) << 26;  // a tile's rows stay
 // Tokens per tile, and between checkpoints: the backward pass holds a tile's
 // states and decays in registers, and its partial sums in LDS.
 constexpr int kScanTile = 8;
-// waves of a workgroup at 4 states each
+// waves of a workgroup at 4 states each, up to a power of two (at 24 states two of 8 have none)
 inline __host__ __device__ constexpr int scan_waves(int64_t N) {
     return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16;
 }

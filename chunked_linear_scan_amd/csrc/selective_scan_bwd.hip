@@ -17,10 +17,15 @@
 // through partial results in the workspace: no atomics, the same bits every run.
 //
 // Bound by vector instructions: 16 per value (exp2 counting twice 17) and some
-// 170 per tile and wave for staging and finishing; busy 82 % of the time.
-// 4 x 2048 x 1536 x 16 bf16: 181-190 us, after 50 us for the segments' own
-// carries; then the sums, 8 us.  Its data at copy rate: 39 us.  16 tokens to a
-// tile measured 305 us where 8 took 252 (registers; LDS for the partial sums).
+// 170 per tile and wave for staging and finishing; busy 84 % of the time.  Its
+// waits are not hidden well: the state of a tile's checkpoint is loaded in the
+// tile that uses it, and its wait covers the next tile's loads, too.
+// 4 x 2048 x 1536 x 16 bf16: 188 us (185 at the fastest), after 50 us for the
+// segments' own carries; then the sums, 8 us.  Its data at copy rate: 39 us.
+// 16 tokens to a tile measured 305 us where 8 took 252 (registers; LDS for the
+// partial sums).  Above 32 states a workgroup's 16 waves leave 128 registers to
+// each, and 112 to 196 bytes a lane go to scratch memory in the loop:
+// 2 x 1024 x 1536 bf16 takes 527 us at 64 states and 156 at 24.
 #include "selective_scan.hpp"
 
 #include "launch_selective.hpp"

@@ -19,9 +19,10 @@
 // Where channels and sequences give too few waves, a first launch takes every
 // segment but the last from a zero state (16 cycles per value: no y); the
 // second folds what came before its segment, exp2(A sum dt') h + own, and runs
-// the outputs.  1 x 32768 x 4096 channels x 16 states, bf16: 375-395 us and
-// 543-575 us (VALU busy 88-90 % of the time at about 2.1 GHz); one pass over its
-// 1.1 GB at copy rate would be 209 us, its bare recurrence 562 us in both passes.
+// the outputs.  1 x 32768 x 4096 channels x 16 states, bf16: 916 us a call, in
+// kernels of 379 and 548 us at their fastest (medians of a profiled run 412 and
+// 602, at a lower clock; VALU busy 89-91 % of the time); one pass over its 1.1 GB
+// at copy rate would be 209 us, its bare recurrence 562 us in both passes.
 #include "selective_scan.hpp"
 
 #include "launch_selective.hpp"

@@ -4,10 +4,11 @@
 // A few operations per element read and written, so bound by memory: a thread
 // walks adjacent tokens of 4 or 8 channels with the last `width` inputs in
 // registers, reading each row once but for the width - 1 before its run.
-// 8 x 2048 x 1536 bf16: forward 23.5 us (101 MB: 19.5 us at copy rate), backward
-// 39.5 us (151 MB: 29 us; its recomputed convolution, silu' and four products
-// each for dx and the weights are some 22 us of vector instructions) and 5 us
-// for the weights' sums.  3 x 1021 x 1536: 7.3 us; one token of 64 x 5120: 3.8 us.
+// 8 x 2048 x 1536 bf16: forward 22.3 us (101 MB: 19.5 us at copy rate), backward
+// 39 us (151 MB: 29 us; its recomputed convolution, silu' and four products each
+// for dx and the weights are some 22 us of vector instructions, which the one
+// round of workgroups does not overlap with the loads wholly) and 4.7 us for the
+// weights' sums.  3 x 1021 x 1536: 7.0 us; one token of 64 x 5120: 3.6 us.
 #include "selective.hpp"
 
 #include "launch_selective.hpp"

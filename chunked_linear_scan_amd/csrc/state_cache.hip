@@ -190,8 +190,8 @@ int launch(CacheParams p, hipStream_t s) {
     if constexpr (READ) {
         hipLaunchKernelGGL((cache_read_kernel<FP8, WIDE, LS>), dim3(uint32_t(p.blocks * p.batch)), dim3(256), 0, s, p);
     } else if (blocks(4) * p.batch >= 1024) {
-        // four rows to a thread where that leaves every CU a few workgroups: 32 states of 5120 rows of 128 in 21-23 us
-        // for 26 us with one, 4 states of 1536 rows of 16 in 4.2 for 3.2
+        // four rows to a thread where that leaves every CU a few workgroups: 32 states of 5120 rows of 128 in 25.4 us
+        // for 28.6 us with one, 4 states of 1536 rows of 16 in 4.0 for 2.9
         p.blocks = blocks(4);
         hipLaunchKernelGGL((cache_write_kernel<FP8, WIDE, LS, 4>), dim3(uint32_t(p.blocks * p.batch)), dim3(256), 0, s, p);
     } else {

@@ -6,7 +6,8 @@ native module ``_selective_binding`` (``binding/selective_binding.cpp``):
 tensors are checked for device, dtype and shape, outputs and workspaces are
 allocated with torch, and the library's kernels run on torch's current stream
 of the inputs' device.  Activations may be slices of wider rows (their last
-dimension adjacent); parameters and states are contiguous.  Each call has a
+dimension adjacent); parameters and states are contiguous; outputs given as
+`out` must not overlap inputs.  Each call has a
 workspace of its own from torch's allocator, so calls on several streams and
 captured graphs share none.
 

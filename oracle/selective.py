@@ -6,9 +6,11 @@ roundoff u = 2^-24, what rounding can do to the fp32 evaluation of the same
 quantity: each elementary step contributes its own roundings and carries on
 those of its factors.  The counts are those of the kernels' formulas, taken
 generously: a step dt' = softplus(.) is within 8 u (exp2, log2, reciprocal of
-1 ulp each, their products), a decay exp(dt' A) within (4 + 12 |dt' A|) u (the
-exponent carries dt's error, its own two products and A's conversion), a
-factor silu or its derivative within 16 u of its largest term.
+1 ulp each, their products; the exponent's rounding, up to 1.5 |dt + dt_bias| u
+of a step in the tail, is left to the tests' factor of two, which holds it down
+to -8), a decay exp(dt' A) within (4 + 12 |dt' A|) u (the exponent carries dt's
+error, its own two products and A's conversion), a factor silu or its derivative
+within 16 u of its largest term.
 """
 from __future__ import annotations
 
