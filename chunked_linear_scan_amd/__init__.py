@@ -15,7 +15,9 @@ import threading
 
 import torch
 
-from . import selective
+from . import delta, selective
+from .delta import (gated_delta, gated_delta_bwd, gated_delta_step, gated_norm, gated_norm_bwd, residual_norm,
+                    residual_norm_bwd)
 from .selective import (selective_scan, selective_scan_bwd, selective_scan_step, short_conv, short_conv_bwd,
                         short_conv_step, state_cache_read, state_cache_write)
 

@@ -2,9 +2,10 @@
 
 Every HIP translation unit is compiled with hipcc for gfx950 only, with
 packed-fp32 instruction generation switched off, then linked into one
-shared library that exports the C ABI of ``include/chunked_linear_scan.h`` and
-``include/selective_scan.h``.  The native Python binding of the latter (host
-code only, on torch's C++ API) becomes ``_selective_binding.so`` beside it.
+shared library that exports the C ABI of ``include/chunked_linear_scan.h``,
+``include/selective_scan.h`` and ``include/gated_delta.h``.  The native Python
+binding of the latter two (host code only, on torch's C++ API) becomes
+``_selective_binding.so`` beside it.
 """
 from __future__ import annotations
 
@@ -21,7 +22,8 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libchunked_linear_scan.so")
 BINDING = os.path.join(HERE, "_selective_binding.so")
-BINDING_SRC = os.path.join(HERE, "binding", "selective_binding.cpp")
+BINDING_SRC = os.path.join(HERE, "binding")
+BINDING_UNITS = ("selective_binding", "delta_binding")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -50,12 +52,13 @@ def _compile(src):
 
 
 def _compile_binding(obj):
-    """Host code: g++ with torch's headers."""
+    """Host code: g++ with torch's headers.  The object is named after its source."""
     import torch
     from torch.utils import cpp_extension
     inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
                                            os.path.join(cpp_extension.ROCM_HOME or "/opt/rocm", "include")]
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", BINDING_SRC, "-o", obj,
+    src = os.path.join(BINDING_SRC, os.path.splitext(os.path.basename(obj))[0] + ".cpp")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", src, "-o", obj,
            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     for i in inc:
@@ -66,10 +69,10 @@ def _compile_binding(obj):
     return obj
 
 
-def _link_binding(obj):
+def _link_binding(objs):
     from torch.utils import cpp_extension
     tmp = BINDING + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + os.path.basename(LIB),
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, *objs, "-L" + HERE, "-l:" + os.path.basename(LIB),
            "-Wl,-rpath,$ORIGIN"]
     cmd += ["-L" + p for p in cpp_extension.library_paths()]
     cmd += ["-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", "-ltorch_python"]
@@ -86,7 +89,7 @@ def build(verbose: bool = True, jobs: int | None = None) -> str:
     srcs = sources()
     jobs = jobs or min(8, os.cpu_count() or 4)
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
-        binding = ex.submit(_compile_binding, os.path.join(BUILD, "selective_binding.o"))
+        binding = [ex.submit(_compile_binding, os.path.join(BUILD, unit + ".o")) for unit in BINDING_UNITS]
         objs = list(ex.map(_compile, srcs))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
@@ -94,7 +97,7 @@ def build(verbose: bool = True, jobs: int | None = None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding.result())  # last: the C library stands without torch's headers and g++
+    _link_binding([b.result() for b in binding])  # last: the C library stands without torch's headers and g++
     if verbose:
         print(f"built {LIB} from {len(srcs)} sources, and {BINDING}", file=sys.stderr)
     return LIB

@@ -1,0 +1,393 @@
+// Gradients of the gated delta rule, the part that takes all chunks at once: dq,
+// dk, dbeta and dg from the state S before each chunk and the gradient dS of the
+// one behind it, the corrections N and Z = (I + A)^-T dN.  With dP = dY N^T (j <= i),
+// M = Z N^T (j < i), pP_ij = scale D_ij dP_ij and pB_ij = -beta_i D_ij M_ij:
+//     dQ = scale e^gamma dY S^T + pP K
+//     dK = -beta e^gamma Z S^T + pB K  +  e^(gamma_C - gamma) N dS^T + pB^T K + pP^T Q
+//     dbeta_i = Z_i.V_i - e^gamma_i (S^T k_i).Z_i - sum_j D_ij k_i.k_j M_ij
+// (no division by beta, which may be zero).  g_t stands in every product between a token
+// before t and one from t on, so with F_ij = pP_ij q_i.k_j + pB_ij k_i.k_j
+//     dg_t = sum_{i >= t > j} F_ij + sum_{i >= t} read_i + sum_{j < t} write_j + e^gamma_C <S, dS>
+// where read and write are the state's parts of dQ.q + dK.k and of dK.k.  (Differences
+// q.dQ - k.dK of whole gradients would be shorter, but cancel and carry the operands'
+// rounding; sums of F are of the same numbers by rows and by columns.)
+// A wave has 16 tokens; products run transposed (tokens in the columns), so dQ and dK
+// leave as four adjacent values of a token, and the decays are factors of a lane.
+// What reaches dg and dbeta, fp32 outputs, takes computed operands in two parts;
+// pP and pB only reach dQ and dK and go in as one.
+#include <hip/hip_runtime.h>
+
+#include "delta.hpp"
+#include "device_once.hpp"
+#include "launch_delta.hpp"
+
+namespace cls {
+namespace {
+
+__device__ __forceinline__ float sum_groups(float v) {
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+
+// ROWS x 32 fp32 values of a matrix in memory, as parts of an operand in LDS.
+template <typename E, int ROWS, int THREADS>
+struct Tile32 {
+    static constexpr int N = ROWS * 8 / THREADS;
+    static_assert(ROWS * 8 % THREADS == 0, "");
+    f32x4 r[N];
+    __device__ __forceinline__ void load(const float* base, int64_t pitch, int rows, int col, int cols, bool vec) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int at = threadIdx.x + n * THREADS, row = at >> 3, c = col + 4 * (at & 7);
+            r[n] = row < rows ? load4<ElemF32>(reinterpret_cast<const uint32_t*>(base + row * pitch), c, cols, vec)
+                              : f32x4{0, 0, 0, 0};
+        }
+    }
+    __device__ __forceinline__ void store(typename E::raw* to, int pitch, int lo) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int at = threadIdx.x + n * THREADS;
+            put4<E>(to + (at >> 3) * pitch + 4 * (at & 7), lo, r[n]);
+        }
+    }
+    __device__ __forceinline__ float dot(const Tile32& o) const {
+        float v = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v = fmaf(r[n][e], o.r[n][e], v);
+        return v;
+    }
+};
+
+template <typename E>
+__device__ __forceinline__ Two<E> two_rows(const typename E::raw* p, int lo) {
+    Two<E> t;
+    t.hi = Mat<E>::rows(p);
+    if constexpr (Mat<E>::kSplit) t.lo = Mat<E>::rows(p + lo);
+    return t;
+}
+
+template <typename E, int DK>
+struct GradSize {
+    typedef Mat<E> M;
+    static constexpr int C = M::kChunk, KP = DK + M::kPad, SP = 32 + M::kPad, MP = ChunkMats<E>::kPitch;
+    static constexpr int kParts = ChunkMats<E>::kParts;
+    static constexpr int kTiles = kParts * (DK + C) * SP;  // a tile of S or dS, and of N
+    static constexpr int kPairs = 2 * C * MP;              // pB and pP, in the same place
+    static constexpr int kUnion = kTiles > kPairs ? kTiles : kPairs;
+    static constexpr size_t bytes = (2 * C * KP + kUnion) * sizeof(typename M::raw) + 9 * C * sizeof(float);
+};
+
+template <typename E, int DK>
+__global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaParams p) {
+    typedef Mat<E> M;
+    typedef typename M::raw raw;
+    typedef GradSize<E, DK> G;
+    constexpr int C = G::C, NT = C / 16, KT = DK / 16, THREADS = 64 * NT, KP = G::KP, SP = G::SP, MP = G::MP;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    raw* sK = reinterpret_cast<raw*>(lds);
+    raw* sQ = sK + C * KP;
+    raw* sS = sQ + C * KP;
+    raw* sN = sS + G::kParts * DK * SP;
+    raw* sB = sS;  // once the tiles are done with
+    raw* sP = sB + C * MP;
+    float* sG = reinterpret_cast<float*>(sS + G::kUnion);
+    float* sRow = sG + C;       // read_i + sum_j F_ij
+    float* sWrite = sRow + C;   // write_j
+    float* sCol = sWrite + C;   // [NT][C]: sums of F over a wave's tokens
+    float* sDot = sCol + NT * C;
+
+    const int h = blockIdx.x % p.H, c = blockIdx.x / p.H % p.nchunk, b = blockIdx.x / p.H / p.nchunk;
+    const int end = seq_end(p.seqlens, b, p.L), t0 = c * C;
+    const int rep = p.H / p.Hk, kh = h / rep, tid = threadIdx.x, w = tid >> 6, l16 = lane16(), g4 = group4();
+    const int i = 16 * w + l16, tok = t0 + i;  // this lane's token
+    const bool in = tok < end;
+    // rows of the outputs: of a token's head, or its part of a key head's sum
+    raw* dQ = static_cast<raw*>(p.dq) + ((int64_t(b) * p.L + tok) * p.Hk + kh) * p.dk;
+    raw* dK = static_cast<raw*>(p.dk_) + ((int64_t(b) * p.L + tok) * p.Hk + kh) * p.dk;
+    float* partQ = p.part_q + ((int64_t(b) * p.L + tok) * p.H + h) * p.dk;
+    float* partK = p.part_k + ((int64_t(b) * p.L + tok) * p.H + h) * p.dk;
+    const int64_t gat = (int64_t(b) * p.L + tok) * p.H + h;
+
+    const auto put_row = [&](raw* one, float* part, int d, const f32x4& v) {
+        if (tok >= p.L) return;
+        if (rep > 1) {
+            if (p.dk % 4 == 0) {
+                if (d < p.dk) *reinterpret_cast<f32x4*>(part + d) = v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (d + e < p.dk) part[d + e] = v[e];
+            }
+        } else if (p.dk % 4 == 0 && p.vec_out) {
+            if (d < p.dk) put4<E>(one + d, 0, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (d + e < p.dk) one[d + e] = E::put(v[e]);
+        }
+    };
+    if (t0 >= end) {  // padding
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+            put_row(dQ, partQ, 16 * t + 4 * g4, f32x4{0, 0, 0, 0});
+            put_row(dK, partK, 16 * t + 4 * g4, f32x4{0, 0, 0, 0});
+        }
+        if (g4 == 0 && tok < p.L) p.dg[gat] = p.dbeta[gat] = 0.0f;
+        return;
+    }
+
+    const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
+    const float* vecs = p.vecs + chunk * 3 * C;
+    const float start = vecs[i], after = vecs[C + i], beta = vecs[2 * C + i], fade = vecs[C - 1];
+    const float* S0 = p.states + chunk * p.dk * p.dv;
+    const float* dS = p.dstates + chunk * p.dk * p.dv;
+    const int64_t row = int64_t(p.H) * p.dv;
+    const float* N = p.fixes + ((int64_t(b) * p.L + t0) * p.H + h) * p.dv;
+    const uint32_t* Ni = reinterpret_cast<const uint32_t*>(N + i * row);
+    const uint32_t* Zi = reinterpret_cast<const uint32_t*>(p.z + ((int64_t(b) * p.L + tok) * p.H + h) * p.dv);
+    const raw* Yi = static_cast<const raw*>(p.dy) + b * p.sdy.batch + h * p.sdy.head + tok * p.sdy.token;
+    const raw* Vi = static_cast<const raw*>(p.v) + b * p.sv.batch + h * p.sv.head + tok * p.sv.token;
+    const int left = end - t0 < C ? end - t0 : C;  // tokens of the chunk
+    const bool v4 = p.dv % 4 == 0;                 // rows of states, N and Z are whole vectors
+    {
+        TileRegs<E, C, DK, THREADS> k, q;
+        k.load(static_cast<const raw*>(p.k) + b * p.sk.batch + kh * p.sk.head, p.sk.token, t0, end, p.dk, p.vec_k);
+        q.load(static_cast<const raw*>(p.q) + b * p.sq.batch + kh * p.sq.head, p.sq.token, t0, end, p.dk, p.vec_q);
+        if (tid < C) sG[tid] = t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f;
+        k.store(sK, KP);
+        q.store(sQ, KP);
+    }
+
+    // with the state before the chunk: X1 = S dY^T, X2 = S Z^T; with the corrections: dP^T and M^T
+    f32x4 X1[KT], X2[KT], dP[NT], Mz[NT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) X1[t] = X2[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) dP[t] = Mz[t] = f32x4{0, 0, 0, 0};
+    float zv = 0.0f;  // Z_i.V_i
+    Tile32<E, DK, THREADS> rs;
+    Tile32<E, C, THREADS> rn;
+    rs.load(S0, p.dv, p.dk, 0, p.dv, v4);
+    rn.load(N, row, left, 0, p.dv, v4);
+    for (int d0 = 0; d0 < p.dv; d0 += 32) {
+        __syncthreads();
+        rs.store(sS, SP, DK * SP);
+        rn.store(sN, SP, C * SP);
+        f32x4 z[2], y[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int col = d0 + 16 * u + 4 * g4;
+            z[u] = in ? load4<ElemF32>(Zi, col, p.dv, v4) : f32x4{0, 0, 0, 0};
+            y[u] = in ? load4<E>(Yi, col, p.dv, p.vec_dy) : f32x4{0, 0, 0, 0};
+            const f32x4 v = in ? load4<E>(Vi, col, p.dv, p.vec_v) : f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) zv = fmaf(z[u][e], v[e], zv);
+        }
+        __syncthreads();
+        if (d0 + 32 < p.dv) {
+            rs.load(S0, p.dv, p.dk, d0 + 32, p.dv, v4);
+            rn.load(N, row, left, d0 + 32, p.dv, v4);
+        }
+        const Two<E> zf = two<E>(z[0], z[1]);
+        const typename M::frag yf = M::cvt(y[0], y[1]);  // exact
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+            const Two<E> s = two_rows<E>(sS + (16 * t + l16) * SP, DK * SP);
+            X1[t] = mma2<E>(s, yf, X1[t]);
+            X2[t] = mma3<E>(s, zf, X2[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t > w) break;
+            const Two<E> nj = two_rows<E>(sN + (16 * t + l16) * SP, C * SP);
+            dP[t] = mma2<E>(nj, yf, dP[t]);
+            Mz[t] = mma3<E>(nj, zf, Mz[t]);
+        }
+    }
+    zv = sum_groups(zv);
+    const auto dot_row = [&](const raw* m, const f32x4 (&x)[KT]) {
+        float v = 0.0f;
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+            const f32x4 a = load4<E>(m + i * KP, 16 * t + 4 * g4, DK, true);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v = fmaf(a[r], x[t][r], v);
+        }
+        return sum_groups(v);
+    };
+    const float qx = p.scale * start * dot_row(sQ, X1), kx = start * dot_row(sK, X2);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+        X1[t] *= p.scale * start;
+        X2[t] *= -beta * start;
+    }
+
+    // with the gradient of the state behind it: + dS (e^(gamma_C - gamma) N)^T, and <S, dS>
+    float both = 0.0f;
+    {
+        Tile32<E, DK, THREADS> r0;
+        rs.load(dS, p.dv, p.dk, 0, p.dv, v4);
+        for (int d0 = 0; d0 < p.dv; d0 += 32) {
+            r0.load(S0, p.dv, p.dk, d0, p.dv, v4);
+            __syncthreads();
+            rs.store(sS, SP, DK * SP);
+            both += rs.dot(r0);
+            f32x4 x[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                x[u] = in ? load4<ElemF32>(Ni, d0 + 16 * u + 4 * g4, p.dv, v4) : f32x4{0, 0, 0, 0};
+                x[u] *= after;
+            }
+            __syncthreads();
+            if (d0 + 32 < p.dv) rs.load(dS, p.dv, p.dk, d0 + 32, p.dv, v4);
+            const Two<E> nf = two<E>(x[0], x[1]);
+#pragma unroll
+            for (int t = 0; t < KT; ++t) X2[t] = mma3<E>(two_rows<E>(sS + (16 * t + l16) * SP, DK * SP), nf, X2[t]);
+        }
+    }
+    const float write = dot_row(sK, X2) + beta * kx;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) both += __shfl_xor(both, d, 64);
+    if ((tid & 63) == 0) sDot[w] = both;
+
+    // pairs of tokens
+    f32x4 kk[NT], qk[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) kk[t] = qk[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int ks = 0; ks < DK / 32; ++ks) {
+        const typename M::frag ki = M::rows(sK + i * KP + 32 * ks), qi = M::rows(sQ + i * KP + 32 * ks);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t > w) break;
+            const typename M::frag kj = M::rows(sK + (16 * t + l16) * KP + 32 * ks);
+            kk[t] = M::mma(kj, ki, kk[t]);
+            qk[t] = M::mma(kj, qi, qk[t]);
+        }
+    }
+    float rows = 0.0f, db = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        if (t > w)
+            for (int r = 0; r < 4; ++r) kk[t][r] = 0.0f;
+    for_decays<NT>(sG, w, [&](int t, const f32x4& d) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int j = 16 * t + 4 * g4 + r;
+            const float m = j < i ? d[r] * Mz[t][r] : 0.0f;
+            dP[t][r] = j <= i ? p.scale * d[r] * dP[t][r] : 0.0f;
+            Mz[t][r] = -beta * m;
+            db = fmaf(m, kk[t][r], db);
+            const float f = j < i ? fmaf(dP[t][r], qk[t][r], Mz[t][r] * kk[t][r]) : 0.0f;
+            rows += f;
+            kk[t][r] = f;  // kk becomes F
+        }
+    });
+    rows = sum_groups(rows);
+    db = sum_groups(db);
+    // sums of F over the wave's tokens
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float v = kk[t][r];
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+            if (l16 == 0) sCol[w * C + 16 * t + 4 * g4 + r] = v;
+        }
+    if (g4 == 0) {
+        sRow[i] = rows + qx - beta * kx;
+        sWrite[i] = write;
+        if (tok < p.L) p.dbeta[gat] = in ? zv - kx - db : 0.0f;
+    }
+    __syncthreads();  // the tiles are read
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        put4<E>(sB + i * MP + 16 * t + 4 * g4, 0, Mz[t]);  // zeros for the tiles behind w
+        put4<E>(sP + i * MP + 16 * t + 4 * g4, 0, dP[t]);
+    }
+    __syncthreads();
+    if (tid < C) {  // dg of token tid
+        float v = fade * sDot[0];
+#pragma unroll
+        for (int k = 1; k < NT; ++k) v += fade * sDot[k];
+        for (int l = 0; l < C; ++l) {
+            float cols = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NT; ++k) cols += sCol[k * C + l];
+            v += l >= tid ? sRow[l] - cols : sWrite[l];
+        }
+        if (t0 + tid < p.L) p.dg[(int64_t(b) * p.L + t0 + tid) * p.H + h] = t0 + tid < end ? v : 0.0f;
+    }
+    // the pairs' parts: as the later token (operands from the lanes), as the earlier one (from LDS)
+    typename M::frag bi[NT / 2], pi[NT / 2], bj[NT / 2], pj[NT / 2];
+#pragma unroll
+    for (int s = 0; s < NT / 2; ++s) {
+        bi[s] = M::cvt(Mz[2 * s], Mz[2 * s + 1]);
+        pi[s] = M::cvt(dP[2 * s], dP[2 * s + 1]);
+        bj[s] = M::cols(sB + 32 * s * MP + 16 * w, MP);
+        pj[s] = M::cols(sP + 32 * s * MP + 16 * w, MP);
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+#pragma unroll
+        for (int s = 0; s < NT / 2; ++s) {
+            const typename M::frag kc = M::cols(sK + 32 * s * KP + 16 * t, KP);
+            const typename M::frag qc = M::cols(sQ + 32 * s * KP + 16 * t, KP);
+            X1[t] = M::mma(kc, pi[s], X1[t]);
+            X2[t] = M::mma(kc, bi[s], X2[t]);
+            X2[t] = M::mma(kc, bj[s], X2[t]);
+            X2[t] = M::mma(qc, pj[s], X2[t]);
+        }
+        if (!in) X1[t] = X2[t] = f32x4{0, 0, 0, 0};
+        put_row(dQ, partQ, 16 * t + 4 * g4, X1[t]);
+        put_row(dK, partK, 16 * t + 4 * g4, X2[t]);
+    }
+}
+
+// Sums over the heads of a key head.
+template <typename E>
+__global__ __launch_bounds__(256) void delta_heads_kernel(const float* part_q, const float* part_k, typename E::raw* dq,
+                                                          typename E::raw* dk, int64_t n, int dim, int rep) {
+    const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (at >= n) return;
+    const int64_t from = at / dim * rep * dim + at % dim;
+    float q = 0.0f, k = 0.0f;
+    for (int r = 0; r < rep; ++r) {
+        q += part_q[from + int64_t(r) * dim];
+        k += part_k[from + int64_t(r) * dim];
+    }
+    dq[at] = E::put(q);
+    dk[at] = E::put(k);
+}
+
+template <typename E, int DK>
+int launch(const DeltaParams& p, hipStream_t stream) {
+    constexpr size_t bytes = GradSize<E, DK>::bytes;
+    static DeviceOnce once;
+    const int st = run_once_per_device(once, [] {
+        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_grad_kernel<E, DK>),
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == hipSuccess ? 0 : -7;
+    });
+    if (st != 0) return st;
+    const unsigned wgs = unsigned(int64_t(p.batch) * p.nchunk * p.H);
+    delta_grad_kernel<E, DK><<<wgs, 4 * Mat<E>::kChunk, bytes, stream>>>(p);
+    if (hipGetLastError() != hipSuccess) return -7;
+    if (p.H == p.Hk) return 0;
+    typedef typename E::raw raw;
+    const int64_t n = int64_t(p.batch) * p.L * p.Hk * p.dk;
+    delta_heads_kernel<E><<<unsigned((n + 255) / 256), 256, 0, stream>>>(
+        p.part_q, p.part_k, static_cast<raw*>(p.dq), static_cast<raw*>(p.dk_), n, p.dk, p.H / p.Hk);
+    return hipGetLastError() == hipSuccess ? 0 : -7;
+}
+
+}  // namespace
+}  // namespace cls
+
+int cls_delta_grad_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream) {
+    return cls::by_type(dtype, p.dk, [&](auto e, auto dk) {
+        return cls::launch<decltype(e), decltype(dk)::value>(p, stream);
+    });
+}

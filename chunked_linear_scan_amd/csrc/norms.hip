@@ -1,0 +1,468 @@
+// The norms around a block: gated_norm behind a recurrence and residual_norm in
+// front of the next block, with their gradients.  All are bound by memory: a row
+// is read once, kept in registers between its sum of squares and its output, and
+// written once.  A row has 8 to 256 lanes by its length, 8 adjacent values (one or two
+// 16-byte vectors) to a lane at a time.  The gradients of weight and
+// scale are summed over the rows that a workgroup walks in its lanes, then over
+// the workgroups by a second launch in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "../../include/gated_delta.h"
+#include "launch_delta.hpp"
+#include "selective.hpp"
+
+namespace cls {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename E>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int left, bool vec, float (&v)[8]) {
+    const typename E::raw* p = static_cast<const typename E::raw*>(base) + at;
+    if (vec && left >= 8) {
+        if constexpr (sizeof(typename E::raw) == 4) {
+            const u32x4 a = ldg_b128(p), b = ldg_b128(p + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = as_float(a[e]);
+                v[4 + e] = as_float(b[e]);
+            }
+        } else {
+            const u32x4 a = ldg_b128(p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t w = a[e >> 1];
+                v[e] = E::get(typename E::raw(e & 1 ? w >> 16 : w));
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? E::get(p[e]) : 0.0f;
+}
+
+// Returns the values as they were kept.
+template <typename E>
+__device__ __forceinline__ void store8(void* base, int64_t at, int left, bool vec, const float (&v)[8]) {
+    typedef typename E::raw raw;
+    raw* p = static_cast<raw*>(base) + at;
+    if (vec && left >= 8) {
+        if constexpr (sizeof(raw) == 4) {
+            *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = uint32_t(E::put(v[2 * e])) | (uint32_t(E::put(v[2 * e + 1])) << 16);
+            *reinterpret_cast<u32x4*>(p) = w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < left) p[e] = E::put(v[e]);
+}
+
+// Sum over the LANES lanes of a row (all of a workgroup's threads for 256, whose calls meet at a barrier).
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, float* scratch) {
+#pragma unroll
+    for (int d = (LANES < 64 ? LANES : 64) / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+    if constexpr (LANES == kThreads) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = (scratch[0] + scratch[1]) + (scratch[2] + scratch[3]);
+    }
+    return v;
+}
+
+// Column sums of a workgroup's rows: one row of `parts`.
+template <int LANES, int NV>
+__device__ __forceinline__ void put_parts(const float (&sum)[NV][8], float* parts, int dim, float* scratch) {
+    constexpr int ROWS = kThreads / LANES;
+    const int lane = threadIdx.x % LANES;
+    if constexpr (ROWS == 1) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int col = (n * LANES + lane) * 8 + e;
+                if (col < dim) parts[int64_t(blockIdx.x) * dim + col] = sum[n][e];
+            }
+    } else {  // scratch: [kThreads][8]
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) scratch[threadIdx.x * 8 + e] = sum[n][e];
+            __syncthreads();
+            for (int col = threadIdx.x; col < LANES * 8; col += kThreads) {
+                float v = 0.0f;
+                for (int r = 0; r < ROWS; ++r) v += scratch[r * LANES * 8 + col];
+                const int at = n * LANES * 8 + col;
+                if (at < dim) parts[int64_t(blockIdx.x) * dim + at] = v;
+            }
+        }
+    }
+}
+
+struct GatedParams {
+    const void *x, *z, *dy;
+    const float* weight;
+    float* rstd;
+    void *y, *dx, *dz;
+    float* parts;
+    int64_t x_row, x_head, z_row, z_head, dy_row, dy_head;
+    int64_t total;  // rows * heads
+    int heads, dim, gate_first;
+    float eps;
+    uint8_t vec_x, vec_z, vec_dy, vec_out;
+};
+
+template <typename E, int LANES, int NV, bool BWD>
+__global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedParams p) {
+    constexpr int ROWS = kThreads / LANES;
+    __shared__ float scratch[BWD && ROWS > 1 ? kThreads * 8 : 4];
+    const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    const float inv = 1.0f / float(p.dim);
+    float w[NV][8], dw[NV][8];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int col = (n * LANES + lane) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[n][e] = col + e < p.dim ? (p.weight ? p.weight[col + e] : 1.0f) : 0.0f;
+            dw[n][e] = 0.0f;
+        }
+    }
+    // all of a workgroup's lanes take the same number of turns: sums may meet at a barrier
+    for (int64_t first = int64_t(blockIdx.x) * ROWS; first < p.total; first += int64_t(gridDim.x) * ROWS) {
+        const int64_t at = first + sub;
+        const bool on = at < p.total;
+        const int64_t row = on ? at / p.heads : 0, head = on ? at % p.heads : 0;
+        float x[NV][8], z[NV][8], dy[NV][8], u[NV][8];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
+            load8<E>(p.x, row * p.x_row + head * p.x_head + col, left, p.vec_x, x[n]);
+            load8<E>(p.z ? p.z : p.x, row * p.z_row + head * p.z_head + col, p.z ? left : 0, p.vec_z, z[n]);
+            if (BWD) load8<E>(p.dy, row * p.dy_row + head * p.dy_head + col, left, p.vec_dy, dy[n]);
+        }
+        float rstd = 0.0f, ss = 0.0f;
+        float gate[NV][8], sig[NV][8];
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sig[n][e] = p.z ? sigmoid(z[n][e]) : 1.0f;
+                gate[n][e] = p.z ? z[n][e] * sig[n][e] : 1.0f;
+                u[n][e] = p.gate_first ? x[n][e] * gate[n][e] : x[n][e];
+            }
+        if (BWD) {
+            rstd = on ? p.rstd[at] : 0.0f;
+        } else {
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(u[n][e], u[n][e], ss);
+            rstd = 1.0f / sqrtf(fmaf(row_sum<LANES>(ss, scratch), inv, p.eps));
+            if (p.rstd && on && lane == 0) p.rstd[at] = rstd;
+        }
+        const int64_t out = at * p.dim;
+        if (!BWD) {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    y[e] = u[n][e] * rstd * w[n][e];
+                    if (!p.gate_first) y[e] *= gate[n][e];
+                }
+                store8<E>(p.y, out + col, left, p.vec_out, y);
+            }
+            continue;
+        }
+        // the gradient of u: rstd (a - unit mean(a unit)), a that of unit = u rstd
+        float mean = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float dn = p.gate_first ? dy[n][e] : dy[n][e] * gate[n][e];
+                const float unit = u[n][e] * rstd;
+                dw[n][e] = fmaf(dn, unit, dw[n][e]);
+                mean = fmaf(dn * w[n][e], unit, mean);
+            }
+        mean = row_sum<LANES>(mean, scratch) * inv;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
+            float dx[8], dz[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float unit = u[n][e] * rstd, a = dy[n][e] * w[n][e];
+                const float slope = dsilu(z[n][e], sig[n][e]);
+                const float du = rstd * fmaf(-unit, mean, p.gate_first ? a : a * gate[n][e]);
+                dx[e] = p.gate_first ? du * gate[n][e] : du;
+                dz[e] = (p.gate_first ? du * x[n][e] : a * unit) * slope;
+            }
+            store8<E>(p.dx, out + col, left, p.vec_out, dx);
+            if (p.z) store8<E>(p.dz, out + col, left, p.vec_out, dz);
+        }
+    }
+    if (BWD && p.parts) put_parts<LANES, NV>(dw, p.parts, p.dim, scratch);
+}
+
+struct ResidualParams {
+    const void *x, *residual, *dy, *dr, *r_in;
+    const float *scale, *weight;
+    float* rstd;
+    void *y, *r, *dresidual, *dx;
+    float *parts_w, *parts_s;
+    int64_t x_row, residual_row, dy_row, dr_row, r_row, rows;
+    int dim;
+    float eps;
+    uint8_t vec_x, vec_res, vec_dy, vec_dr, vec_r, vec_out;
+};
+
+template <typename E, typename S, int LANES, int NV>
+__global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualParams p) {
+    constexpr int ROWS = kThreads / LANES;
+    __shared__ float scratch[4];
+    const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    const float inv = 1.0f / float(p.dim);
+    for (int64_t first = int64_t(blockIdx.x) * ROWS; first < p.rows; first += int64_t(gridDim.x) * ROWS) {
+        const int64_t row = first + sub;
+        const bool on = row < p.rows;
+        float r[NV][8];
+        float ss = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
+            float x[8];
+            load8<E>(p.x, row * p.x_row + col, left, p.vec_x, x);
+            if (p.residual) load8<S>(p.residual, row * p.residual_row + col, left, p.vec_res, r[n]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float s = p.scale ? (e < left ? p.scale[col + e] : 0.0f) : 1.0f;
+                const float v = p.residual ? fmaf(s, x[e], r[n][e]) : s * x[e];
+                r[n][e] = S::get(S::put(v));  // the norm is that of the stream as it is kept
+                ss = fmaf(r[n][e], r[n][e], ss);
+            }
+            store8<S>(p.r, row * p.dim + col, left, p.vec_out, r[n]);
+        }
+        const float rstd = 1.0f / sqrtf(fmaf(row_sum<LANES>(ss, scratch), inv, p.eps));
+        if (p.rstd && on && lane == 0) p.rstd[row] = rstd;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = r[n][e] * rstd * (p.weight && e < left ? p.weight[col + e] : 1.0f);
+            store8<E>(p.y, row * p.dim + col, left, p.vec_out, y);
+        }
+    }
+}
+
+template <typename E, typename S, int LANES, int NV>
+__global__ __launch_bounds__(kThreads) void residual_norm_bwd_kernel(ResidualParams p) {
+    constexpr int ROWS = kThreads / LANES;
+    __shared__ float scratch[ROWS > 1 ? kThreads * 8 : 4];
+    const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    const float inv = 1.0f / float(p.dim);
+    float w[NV][8], s[NV][8], dw[NV][8], ds[NV][8];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int col = (n * LANES + lane) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool in = col + e < p.dim;
+            w[n][e] = in ? (p.weight ? p.weight[col + e] : 1.0f) : 0.0f;
+            s[n][e] = in && p.scale ? p.scale[col + e] : 1.0f;
+            dw[n][e] = ds[n][e] = 0.0f;
+        }
+    }
+    for (int64_t first = int64_t(blockIdx.x) * ROWS; first < p.rows; first += int64_t(gridDim.x) * ROWS) {
+        const int64_t row = first + sub;
+        const bool on = row < p.rows;
+        const float rstd = on ? p.rstd[row] : 0.0f;
+        float dy[NV][8], unit[NV][8], dr[NV][8], x[NV][8];
+        float mean = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
+            load8<E>(p.dy, row * p.dy_row + col, left, p.vec_dy, dy[n]);
+            load8<S>(p.r_in, row * p.r_row + col, left, p.vec_r, unit[n]);
+            if (p.dr) load8<S>(p.dr, row * p.dr_row + col, left, p.vec_dr, dr[n]);
+            if (p.parts_s) load8<E>(p.x, row * p.x_row + col, left, p.vec_x, x[n]);
+        }
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                unit[n][e] *= rstd;
+                dw[n][e] = fmaf(dy[n][e], unit[n][e], dw[n][e]);
+                mean = fmaf(dy[n][e] * w[n][e], unit[n][e], mean);
+            }
+        mean = row_sum<LANES>(mean, scratch) * inv;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
+            float du[8], dx[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                du[e] = rstd * fmaf(-unit[n][e], mean, dy[n][e] * w[n][e]);
+                if (p.dr) du[e] += dr[n][e];
+                dx[e] = du[e] * s[n][e];
+                if (p.parts_s) ds[n][e] = fmaf(du[e], x[n][e], ds[n][e]);
+            }
+            store8<S>(p.dresidual, row * p.dim + col, left, p.vec_out, du);
+            if (p.dx) store8<E>(p.dx, row * p.dim + col, left, p.vec_out, dx);
+        }
+    }
+    if (p.parts_w) put_parts<LANES, NV>(dw, p.parts_w, p.dim, scratch);
+    if (p.parts_s) put_parts<LANES, NV>(ds, p.parts_s, p.dim, scratch);
+}
+
+// out[col] = sum of parts[0..n)[col]: 16 columns by 64 threads each, in a fixed order.
+__global__ __launch_bounds__(1024) void norm_sums_kernel(const float* parts, int n, int dim, float* out) {
+    __shared__ float s[64][17];
+    const int col = blockIdx.x * 16 + (threadIdx.x & 15), at = threadIdx.x >> 4;
+    float v = 0.0f;
+    if (col < dim)
+        for (int k = at; k < n; k += 64) v += parts[int64_t(k) * dim + col];
+    s[at][threadIdx.x & 15] = v;
+    __syncthreads();
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+        if (at < d) s[at][threadIdx.x & 15] += s[at + d][threadIdx.x & 15];
+        __syncthreads();
+    }
+    if (at == 0 && col < dim) out[col] = s[0][threadIdx.x & 15];
+}
+
+int sums(const float* parts, int n, int dim, float* out, hipStream_t stream) {
+    norm_sums_kernel<<<(dim + 15) / 16, 1024, 0, stream>>>(parts, n, dim, out);
+    return hipGetLastError() == hipSuccess ? 0 : -7;
+}
+
+int lanes_of(int64_t dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : dim <= 1024 ? 64 : 256; }
+
+// Calls f with the lanes of a row and the runs of 8 values that each has.
+template <typename F>
+int by_dim(int dim, F&& f) {
+    const auto of = [&](auto lanes, auto nv) { return f(lanes, nv); };
+    using std::integral_constant;
+    if (dim <= 64) return of(integral_constant<int, 8>(), integral_constant<int, 1>());
+    if (dim <= 128) return of(integral_constant<int, 16>(), integral_constant<int, 1>());
+    if (dim <= 512) return of(integral_constant<int, 64>(), integral_constant<int, 1>());
+    if (dim <= 1024) return of(integral_constant<int, 64>(), integral_constant<int, 2>());
+    if (dim <= 2048) return of(integral_constant<int, 256>(), integral_constant<int, 1>());
+    if (dim <= 4096) return of(integral_constant<int, 256>(), integral_constant<int, 2>());
+    if (dim <= 8192) return of(integral_constant<int, 256>(), integral_constant<int, 4>());
+    return of(integral_constant<int, 256>(), integral_constant<int, 8>());
+}
+
+template <typename F>
+int by_element(int dtype, F&& f) {
+    if (dtype == SSD_F32) return f(ElemF32());
+    return dtype == SSD_BF16 ? f(ElemBF16()) : f(ElemF16());
+}
+
+bool whole(const void* p, int64_t dim, int dtype, int64_t a, int64_t b) {
+    const int64_t ve = dtype == SSD_F32 ? 4 : 8;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && dim % 8 == 0 && a % ve == 0 && b % ve == 0;
+}
+
+unsigned groups(int64_t rows, int64_t dim, int64_t most) {
+    const int64_t per = kThreads / lanes_of(dim), n = (rows + per - 1) / per;
+    return unsigned(n < most ? n : most);
+}
+
+}  // namespace
+}  // namespace cls
+
+// Workgroups of the gradients' launch, each with a partial sum of the parameters' gradients: four to a compute unit.
+int64_t cls_norm_parts(int64_t rows, int64_t dim) { return cls::groups(rows, dim, 1024); }
+
+int cls_gated_norm_launch(const gated_norm_inputs& in, const void* dy, int64_t dy_row, int64_t dy_head, float* rstd,
+                          void* y, void* dx, void* dz, float* dweight, float* parts, hipStream_t stream) {
+    using namespace cls;
+    GatedParams p{};
+    p.x = in.x; p.z = in.z; p.dy = dy; p.weight = in.weight; p.rstd = rstd;
+    p.y = y; p.dx = dx; p.dz = dz; p.parts = dweight ? parts : nullptr;
+    p.x_row = in.x_row; p.x_head = in.x_head; p.z_row = in.z_row; p.z_head = in.z_head;
+    p.dy_row = dy_row; p.dy_head = dy_head;
+    p.total = in.rows * in.heads;
+    p.heads = int(in.heads); p.dim = int(in.dim); p.gate_first = in.gate_first; p.eps = in.eps;
+    p.vec_x = whole(in.x, in.dim, in.dtype, in.x_row, in.x_head);
+    p.vec_z = whole(in.z, in.dim, in.dtype, in.z_row, in.z_head);
+    p.vec_dy = whole(dy, in.dim, in.dtype, dy_row, dy_head);
+    p.vec_out = whole(dy ? dx : y, in.dim, in.dtype, 0, 0) && whole(dy ? dz : nullptr, in.dim, in.dtype, 0, 0);
+    const unsigned n = dy ? unsigned(cls_norm_parts(p.total, in.dim)) : groups(p.total, in.dim, int64_t(1) << 23);
+    const int st = by_element(in.dtype, [&](auto e) {
+        return by_dim(p.dim, [&](auto lanes, auto nv) {
+            typedef decltype(e) E;
+            constexpr int LANES = decltype(lanes)::value, NV = decltype(nv)::value;
+            if (dy) gated_norm_kernel<E, LANES, NV, true><<<n, kThreads, 0, stream>>>(p);
+            else gated_norm_kernel<E, LANES, NV, false><<<n, kThreads, 0, stream>>>(p);
+            return hipGetLastError() == hipSuccess ? 0 : -7;
+        });
+    });
+    return st == 0 && p.parts ? sums(parts, int(n), p.dim, dweight, stream) : st;
+}
+
+int cls_residual_norm_fwd_launch(const residual_norm_inputs& in, void* y, void* r, float* rstd, hipStream_t stream) {
+    using namespace cls;
+    ResidualParams p{};
+    p.x = in.x; p.residual = in.residual; p.scale = in.scale; p.weight = in.weight; p.rstd = rstd; p.y = y; p.r = r;
+    p.x_row = in.x_row; p.residual_row = in.residual_row; p.rows = in.rows; p.dim = int(in.dim); p.eps = in.eps;
+    p.vec_x = whole(in.x, in.dim, in.dtype, in.x_row, 0);
+    p.vec_res = whole(in.residual, in.dim, in.stream_dtype, in.residual_row, 0);
+    p.vec_out = whole(y, in.dim, in.dtype, 0, 0) && whole(r, in.dim, in.stream_dtype, 0, 0);
+    const unsigned n = groups(in.rows, in.dim, int64_t(1) << 23);
+    return by_element(in.dtype, [&](auto e) {
+        return by_dim(p.dim, [&](auto lanes, auto nv) {
+            typedef decltype(e) E;
+            constexpr int LANES = decltype(lanes)::value, NV = decltype(nv)::value;
+            if (in.stream_dtype == SSD_F32) residual_norm_kernel<E, ElemF32, LANES, NV><<<n, kThreads, 0, stream>>>(p);
+            else residual_norm_kernel<E, E, LANES, NV><<<n, kThreads, 0, stream>>>(p);
+            return hipGetLastError() == hipSuccess ? 0 : -7;
+        });
+    });
+}
+
+int cls_residual_norm_bwd_launch(const residual_norm_inputs& in, const residual_norm_grads& g, float* parts,
+                                 hipStream_t stream) {
+    using namespace cls;
+    ResidualParams p{};
+    p.x = in.x; p.scale = in.scale; p.weight = in.weight; p.x_row = in.x_row; p.rows = in.rows; p.dim = int(in.dim);
+    p.dy = g.dy; p.dr = g.dr; p.r_in = g.r; p.rstd = const_cast<float*>(g.rstd);
+    p.dy_row = g.dy_row; p.dr_row = g.dr_row; p.r_row = g.r_row;
+    p.dresidual = g.dresidual; p.dx = g.dx;
+    const int64_t n = cls_norm_parts(in.rows, in.dim);
+    p.parts_w = g.dweight ? parts : nullptr;
+    p.parts_s = g.dscale ? parts + n * in.dim : nullptr;
+    p.vec_x = whole(in.x, in.dim, in.dtype, in.x_row, 0);
+    p.vec_dy = whole(g.dy, in.dim, in.dtype, g.dy_row, 0);
+    p.vec_dr = whole(g.dr, in.dim, in.stream_dtype, g.dr_row, 0);
+    p.vec_r = whole(g.r, in.dim, in.stream_dtype, g.r_row, 0);
+    p.vec_out = whole(g.dresidual, in.dim, in.stream_dtype, 0, 0) && whole(g.dx, in.dim, in.dtype, 0, 0);
+    int st = by_element(in.dtype, [&](auto e) {
+        return by_dim(p.dim, [&](auto lanes, auto nv) {
+            typedef decltype(e) E;
+            constexpr int LANES = decltype(lanes)::value, NV = decltype(nv)::value;
+            if (in.stream_dtype == SSD_F32)
+                residual_norm_bwd_kernel<E, ElemF32, LANES, NV><<<unsigned(n), kThreads, 0, stream>>>(p);
+            else residual_norm_bwd_kernel<E, E, LANES, NV><<<unsigned(n), kThreads, 0, stream>>>(p);
+            return hipGetLastError() == hipSuccess ? 0 : -7;
+        });
+    });
+    if (st == 0 && g.dweight) st = sums(p.parts_w, int(n), p.dim, g.dweight, stream);
+    if (st == 0 && g.dscale) st = sums(p.parts_s, int(n), p.dim, g.dscale, stream);
+    return st;
+}

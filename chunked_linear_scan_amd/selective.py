@@ -50,7 +50,7 @@ class _Unrecorded(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        call = "selective_scan_bwd" if ctx.what.startswith("selective_scan") else "short_conv_bwd"
+        call = ctx.what.removesuffix("_step") + "_bwd"
         raise RuntimeError(f"{ctx.what} records no gradient: take those of its inputs from {call}, over whole sequences, "
                            "or pass tensors that require none")
 
