@@ -116,7 +116,7 @@ struct Mat<ElemF32> {
 };
 
 // A computed operand: with 16-bit elements x = hi + lo, hi the nearest number of
-// the type and lo that of what is left, which leaves 2^-18 (bf16) of x; in fp32 x.
+// the type and lo that of what is left, which leaves at most 2^-16 (bf16) of x; in fp32 x.
 template <typename E>
 struct Two {
     typename Mat<E>::frag hi, lo;
@@ -128,6 +128,14 @@ __device__ __forceinline__ Two<E> two(const f32x4& a, const f32x4& b) {
     Two<E> t;
     t.hi = M::cvt(a, b);
     if constexpr (M::kSplit) {
+        // what is left is that of these very bits: the compiler may otherwise round a product to hi a second time, in
+        // one step instead of two, and near a tie the two differ by a unit
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t bits = t.hi[w];
+            asm("" : "+v"(bits));
+            t.hi[w] = bits;
+        }
         f32x4 ra, rb;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -151,7 +159,7 @@ __device__ __forceinline__ f32x4 mma2(const Two<E>& a, const typename Mat<E>::fr
     if constexpr (Mat<E>::kSplit) c = Mat<E>::mma(a.lo, b, c);
     return Mat<E>::mma(a.hi, b, c);
 }
-// computed x computed: the product of the two small parts, 2^-18 of the whole, is left out
+// computed x computed: the product of the two small parts, at most 2^-16 of the whole (bf16), is left out
 template <typename E>
 __device__ __forceinline__ f32x4 mma3(const Two<E>& a, const Two<E>& b, f32x4 c) {
     if constexpr (Mat<E>::kSplit) {
@@ -174,7 +182,7 @@ struct DeltaParams {
     float *h_last, *dg, *dbeta, *dh0;
     float* states;   // [batch, chunks, heads, dk, dv]: the state before each chunk (NULL = not kept)
     float* fixes;    // [batch, L, heads, dv]: N, the corrections (NULL = not kept)
-    void* mats;      // per (batch, chunk, head): (I + A)^-1 and c D QK^T, in one part or two
+    void* mats;      // per (batch, chunk, head): (I + A)^-1 - I and D QK^T, in one part or two
     float* vecs;     // per (batch, chunk, head): e^gamma, e^(gamma_C - gamma), beta
     float* dstates;  // as states: the gradient of the state behind each chunk
     float* z;        // as fixes: (I + A)^-T dN

@@ -1,7 +1,7 @@
 // Gradients of the gated delta rule, the part that walks the chunks: from the
 // last to the first, a wave with 16 columns of dS, the gradient of the state, as
 // the forward walk has them of S.  Per chunk, dS being that of the state behind it,
-//     dN = e^(gamma_C - gamma) K dS + P^T dY,  Z = T^T dN,  dV = dR = beta Z,
+//     dN = e^(gamma_C - gamma) K dS + scale P^T dY,  Z = T^T dN,  dV = dR = beta Z,
 //     dS' = e^gamma_C dS + scale Q^T e^gamma dY - K^T e^gamma dR.
 // dS of every chunk and Z go to memory for the kernel that takes the chunks'
 // other gradients all at once (delta_grad.hip).
@@ -119,23 +119,24 @@ __global__ __launch_bounds__(kThreads) void delta_bwd_kernel(DeltaParams p) {
         for (int s = 0; s < NT / 2; ++s) df[s] = M::cvt(dy[2 * s], dy[2 * s + 1]);  // exact
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const f32x4 e = *reinterpret_cast<const f32x4*>(sV + C + 16 * t + 4 * g4);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) dN[t][r] *= e[r];
+            f32x4 later{0, 0, 0, 0};
 #pragma unroll
             for (int s = t / 2; s < NT / 2; ++s) {  // later tokens' outputs
                 Two<E> P;
                 P.hi = M::cols(sP + 32 * s * MP + 16 * t, MP);
                 if constexpr (M::kSplit) P.lo = M::cols(sP + C * MP + 32 * s * MP + 16 * t, MP);
-                dN[t] = mma2<E>(P, df[s], dN[t]);
+                later = mma2<E>(P, df[s], later);
             }
+            const f32x4 e = *reinterpret_cast<const f32x4*>(sV + C + 16 * t + 4 * g4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dN[t][r] = fmaf(dN[t][r], e[r], p.scale * later[r]);
         }
         Two<E> dn[NT / 2];
 #pragma unroll
         for (int s = 0; s < NT / 2; ++s) dn[s] = two<E>(dN[2 * s], dN[2 * s + 1]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            f32x4 Z{0, 0, 0, 0};
+            f32x4 Z = dN[t];
 #pragma unroll
             for (int s = t / 2; s < NT / 2; ++s) {
                 Two<E> T;

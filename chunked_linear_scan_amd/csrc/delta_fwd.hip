@@ -2,7 +2,7 @@
 // columns of the state S [dk, dv] in its registers and takes them through all
 // chunks of a sequence; columns do not meet, so waves only share what the
 // workgroup stages in LDS for them: the chunk's K, Q, T, P and factors.  Per chunk
-//     R = beta (V - e^gamma K S),  N = T R,  Y = scale e^gamma Q S + P N,
+//     R = beta (V - e^gamma K S),  N = T R,  Y = scale (e^gamma Q S + P N),
 //     S' = e^gamma_C S + K^T (e^(gamma_C - gamma) N)
 // where K S, T R and K^T N reach the state and take computed operands in two
 // parts, and Q S and P N only reach y and take them in one.
@@ -123,17 +123,17 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(DeltaParams p) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 R[t][r] = be[r] * fmaf(-e[r], ks[t][r], R[t][r]);
-                O[t][r] *= p.scale * e[r];
+                O[t][r] *= e[r];
             }
         }
-        // N = T R: tokens up to 32 (t / 2 + 1) reach tile t
+        // N = R + (T - I) R: tokens up to 32 (t / 2 + 1) reach tile t
         f32x4 N[NT];
         Two<E> rr[NT / 2];
 #pragma unroll
         for (int s = 0; s < NT / 2; ++s) rr[s] = two<E>(R[2 * s], R[2 * s + 1]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            N[t] = f32x4{0, 0, 0, 0};
+            N[t] = R[t];
 #pragma unroll
             for (int s = 0; s <= t / 2; ++s) {
                 Two<E> T;
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(DeltaParams p) {
                 for (int r = 0; r < 4; ++r) {
                     const int tok = t0 + 16 * t + 4 * g4 + r;
                     if (tok >= p.L) continue;
-                    Y[tok * row] = tok < end ? E::put(O[t][r]) : raw(0);
+                    Y[tok * row] = tok < end ? E::put(p.scale * O[t][r]) : raw(0);
                     if (p.fixes && tok < end) p.fixes[(int64_t(b) * p.L + tok) * row + int64_t(h) * p.dv + n] = N[t][r];
                 }
         }

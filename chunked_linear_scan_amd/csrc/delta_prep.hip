@@ -1,8 +1,11 @@
 // Gated delta rule: what a chunk of C tokens needs that no state enters, for all
 // chunks at once.  With D_ij = e^(g_{j+1} + .. + g_i) and A_ij = beta_i D_ij k_i.k_j
 // (j < i), the corrections N of a chunk solve (I + A) N = diag(beta) (V - e^gamma K S0);
-// here are T = (I + A)^-1, P_ij = scale D_ij q_i.k_j (j <= i) and the factors
-// e^gamma_i and e^(gamma_C - gamma_j) of reads and writes of the state.
+// here are T - I, T = (I + A)^-1, P_ij = D_ij q_i.k_j (j <= i) and the factors
+// e^gamma_i and e^(gamma_C - gamma_j) of reads and writes of the state.  The ones
+// of T's diagonal are left out so that what they multiply stays in fp32 (with two
+// bf16 numbers to an operand half of the states' error came from them), and the
+// scale, so that with fp16 fewer entries are subnormal.
 //
 // T by blocks: the 16x16 diagonal blocks by forward substitution (a column to a
 // lane, in registers), then T10 = -T11 A10 T00 for pairs of blocks and pairs of
@@ -94,7 +97,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
         for (int r = 0; r < 4; ++r) {
             const int j = 16 * t + 4 * g4 + r;
             a[r] = j < i ? beta * d[r] * kk[t][r] : 0.0f;
-            q[r] = j <= i ? p.scale * d[r] * qk[t][r] : 0.0f;
+            q[r] = j <= i ? d[r] * qk[t][r] : 0.0f;
         }
         *reinterpret_cast<f32x4*>(sA + i * AP + 16 * t + 4 * g4) = a;
         put4<E>(P + i * C + 16 * t + 4 * g4, p_parts > 1 ? ChunkMats<E>::kSize : 0, q);
@@ -154,7 +157,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
         if (C == 64 && row < 32 && col >= 32) continue;  // never read
         f32x4 v = *reinterpret_cast<const f32x4*>(sT + row * AP + col);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = col + r > row ? 0.0f : v[r];  // blocks above the diagonal were not written
+        for (int r = 0; r < 4; ++r) v[r] = col + r >= row ? 0.0f : v[r];  // less I; blocks above were not written
         put4<E>(mats + row * C + col, ChunkMats<E>::kSize, v);
     }
 }
