@@ -319,6 +319,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
             for (int k = 0; k < NT; ++k) cols += sCol[k * C + l];
             v += l >= tid ? sRow[l] - cols : sWrite[l];
         }
+        if (fexp(sG[tid]) == 0.0f) v = 0.0f;  // nothing passes: not the sums' roundings either
         if (t0 + tid < p.L) p.dg[(int64_t(b) * p.L + t0 + tid) * p.H + h] = t0 + tid < end ? v : 0.0f;
     }
     // the pairs' parts: as the later token (operands from the lanes), as the earlier one (from LDS)

@@ -52,8 +52,8 @@ extern "C" {
  * States, their updates and all sums are fp32; with 16-bit elements a computed
  * operand of a product that reaches a state or an fp32 gradient goes in as the
  * sum of two numbers of that type (bf16: 16 bits in all), one that only reaches
- * a 16-bit output as one.  With SSD_F16 states and values past 65504 become
- * infinite.  A value that is not finite reaches its head's outputs from the start of its
+ * a 16-bit output as one.  With SSD_F16 such operands have that type's range:
+ * past 65504 they are infinite, and they are held to 2^-25 at best.  A value that is not finite reaches its head's outputs from the start of its
  * chunk on.
  *
  * heads is a multiple of kheads; dk is 1..256 and dv 1..65536
@@ -97,6 +97,7 @@ int gated_delta_fwd(const gated_delta_inputs* in, void* y, float* h_final, void*
  *   dh_final  [batch, heads, dv, dk]       fp32 (NULL = 0)
  * Written, contiguous: dq, dk (as q; summed over the heads of a key head), dv
  * in dtype; dg, dbeta [batch, seqlen, heads] fp32; dh0 as h0 (NULL = not written).
+ * Where e^g is 0, dg is.
  */
 typedef struct {
     const void* dy;

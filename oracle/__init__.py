@@ -20,6 +20,8 @@ lookback  a float64 simulator of the decoupled look-back tile protocol under
           arbitrary tile completion orders, with deliberately broken variants
 selective the selective scan, its gradients, the short convolution and the 8-bit
           state cache as token loops, with error scales
+delta     the gated delta rule and its gradients as token loops, the chunk algebra
+          with error bounds, and the norms around a block
 compare   rel-L2 and first-mismatch reporting
 
 Pins: every function here is checked by ``tests/test_oracle_*.py`` against
