@@ -32,7 +32,6 @@ struct Mat16 {
     typedef u32x4 frag;
     static constexpr int kChunk = 64;
     static constexpr bool kSplit = true;  // computed operands are sums of two numbers
-    static constexpr int kPad = 8;        // elements behind each row in LDS
 
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         if constexpr (std::is_same_v<E, ElemBF16>) {
@@ -49,20 +48,6 @@ struct Mat16 {
         return frag{pack(a[0], a[1]), pack(a[2], a[3]), pack(b[0], b[1]), pack(b[2], b[3])};
     }
     static __device__ __forceinline__ float part(uint32_t w, int hi) { return E::get(raw(hi ? w >> 16 : w & 0xffffu)); }
-    // Four elements of a row from k on, and the four 16 further on.
-    static __device__ __forceinline__ frag rows(const raw* p) {
-        const u32x2 a = *reinterpret_cast<const u32x2*>(p + 4 * group4());
-        const u32x2 b = *reinterpret_cast<const u32x2*>(p + 16 + 4 * group4());
-        return frag{a[0], a[1], b[0], b[1]};
-    }
-    // The same of a column: depths run over the rows of a matrix in LDS from p on; p at the first of 16 columns.
-    static __device__ __forceinline__ frag cols(const raw* p, int pitch) {
-        typedef __attribute__((address_space(3))) s16x4* lp;
-        const raw* at = p + (4 * group4() + (lane16() >> 2)) * pitch + 4 * (lane16() & 3);
-        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at)));
-        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at + 16 * pitch)));
-        return frag{a[0], a[1], b[0], b[1]};
-    }
     static __device__ __forceinline__ float at(const frag& f, int j) { const uint32_t w = f[j >> 1]; return part(w, j & 1); }
 };
 
@@ -89,22 +74,7 @@ struct Mat<ElemF32> {
     struct frag { f32x4 a, b; };
     static constexpr int kChunk = 32;
     static constexpr bool kSplit = false;
-    static constexpr int kPad = 4;
     static __device__ __forceinline__ frag cvt(const f32x4& a, const f32x4& b) { return frag{a, b}; }
-    static __device__ __forceinline__ frag rows(const raw* p) {
-        return frag{*reinterpret_cast<const f32x4*>(p + 4 * group4()),
-                    *reinterpret_cast<const f32x4*>(p + 16 + 4 * group4())};
-    }
-    static __device__ __forceinline__ frag cols(const raw* p, int pitch) {
-        const raw* at = p + 4 * group4() * pitch + lane16();
-        frag f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            f.a[r] = as_float(at[r * pitch]);
-            f.b[r] = as_float(at[(16 + r) * pitch]);
-        }
-        return f;
-    }
     static __device__ __forceinline__ float at(const frag& f, int j) { return j < 4 ? f.a[j & 3] : f.b[j & 3]; }
     static __device__ __forceinline__ f32x4 mma(const frag& a, const frag& b, f32x4 c) {
 #pragma unroll
@@ -173,7 +143,10 @@ __device__ __forceinline__ f32x4 mma3(const Two<E>& a, const Two<E>& b, f32x4 c)
 // launch parameters and tiles
 // ---------------------------------------------------------------------------
 struct Strided3 { int64_t batch, token, head; };
+constexpr int64_t kDeltaMaxToken = int64_t(1) << 23;  // elements from a token to the next
 
+// q, k, v and dy are the caller's or, where those are off whole vectors (q and k) or have rows that overlap or lie
+// further apart than kDeltaMaxToken, copies.
 struct DeltaParams {
     const void *q, *k, *v, *dy;
     const float *g, *beta, *h0, *dh_last;
@@ -191,8 +164,8 @@ struct DeltaParams {
     int64_t g_batch, g_token, b_batch, b_token;
     int batch, L, Hk, H, dk, dv, nchunk;
     float scale;
-    uint8_t vec_q, vec_k, vec_v, vec_dy;  // rows of whole 16-byte vectors
-    uint8_t vec_out;                      // dq and dk start on 16 bytes
+    uint8_t vec_v, vec_dy;  // rows of whole 16-byte vectors, as those of q and k are here
+    uint8_t vec_out;        // dq and dk start on 16 bytes
 };
 
 // Matrices of a chunk in `mats`: T hi, T lo, P hi, P lo (16-bit), T, P (fp32).
@@ -202,50 +175,148 @@ struct ChunkMats {
     static constexpr int kSize = M::kChunk * M::kChunk;
     static constexpr int kParts = M::kSplit ? 2 : 1;
     static constexpr int kAll = 2 * kParts;
-    static constexpr int kPitch = M::kChunk + M::kPad;
 };
 
-// A 16-byte vector of a row: elements col.. of `dim` (zeros past it).
-template <typename E>
-__device__ __forceinline__ u32x4 load_vec(const typename E::raw* row, int col, int dim, bool vec) {
-    constexpr int VE = 16 / sizeof(typename E::raw);
-    if (vec) return col < dim ? ldg_b128(row + col) : u32x4{0, 0, 0, 0};
-    u32x4 v{0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-        if (col + e >= dim) continue;
-        const uint32_t w = row[col + e];
-        if constexpr (VE == 4) v[e] = w;
-        else v[e >> 1] |= w << (16 * (e & 1));
+// ---------------------------------------------------------------------------
+// matrices in LDS
+// ---------------------------------------------------------------------------
+// Rows of DIM elements without padding; the 16-byte pieces of a row are exchanged by
+// an exclusive or with a number of the row.  With 16-bit elements both reads of
+// operands (rows: 8 bytes of 16 rows; columns: transposing reads of 8 rows x 32 bytes)
+// and the 16-byte stores then touch every bank once.  (Padded rows gave the
+// columns' reads two-fold conflicts.)  fp32 rows are padded by 16 bytes instead.
+// An object holds a lane's offsets, which do not change from tile to tile.
+template <typename E, int DIM>
+struct LdsTile {
+    typedef Mat<E> M;
+    typedef typename M::raw raw;
+    static constexpr bool kSwap = M::kSplit;
+    static constexpr int kPitch = DIM + (kSwap ? 0 : 4);
+    static constexpr int VE = 16 / int(sizeof(raw));
+    static constexpr int kSpan = DIM < 128 ? DIM : 128;  // columns that the exchange covers
+    static constexpr int kRows = kSwap ? 2 * kSpan / 32 : 1, kCols = kSwap ? kSpan / 16 : 1;
+    uint32_t r[kRows], c[kCols];  // bytes
+
+    static __device__ __forceinline__ int swap(int row) {
+        const int x = kSpan == 64 ? (row >> 1) & 7 : row & 15;
+        return kSpan == 64 ? 2 * (x & 3) + (x >> 2) : 2 * (x & 7) + (x >> 3);
     }
+    // Element offset of a 16-byte piece (col a multiple of VE).
+    static __device__ __forceinline__ int piece(int row, int col) {
+        if constexpr (kSwap) return row * kPitch + ((col / VE) ^ swap(row)) * VE;
+        return row * kPitch + col;
+    }
+    // Of four elements (col a multiple of 4).
+    static __device__ __forceinline__ int quad(int row, int col) {
+        return piece(row, col / VE * VE) + col % VE;
+    }
+    __device__ __forceinline__ LdsTile() {
+        const int l16 = lane16(), g = group4();
+        if constexpr (kSwap) {
+#pragma unroll
+            for (int n = 0; n < kRows; ++n) r[n] = quad(l16, 16 * n + 4 * g) * sizeof(raw);
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) c[n] = quad(4 * g + (l16 >> 2), 16 * n + 4 * (l16 & 3)) * sizeof(raw);
+        } else {
+            r[0] = (l16 * kPitch + 4 * g) * sizeof(raw);
+            c[0] = (4 * g * kPitch + l16) * sizeof(raw);
+        }
+    }
+    // Operand of 16 rows from 16 t on, depths 32 s.. of them.
+    __device__ __forceinline__ typename M::frag rows(const raw* m, int t, int s) const {
+        const char* p = reinterpret_cast<const char*>(m + 16 * t * kPitch);
+        if constexpr (kSwap) {
+            p += 32 * s / kSpan * kSpan * sizeof(raw);
+            const u32x2 a = *reinterpret_cast<const u32x2*>(p + r[2 * s % kRows]);
+            const u32x2 b = *reinterpret_cast<const u32x2*>(p + r[2 * s % kRows + 1]);
+            return u32x4{a[0], a[1], b[0], b[1]};
+        } else {
+            p += r[0] + 32 * s * sizeof(raw);
+            return typename M::frag{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16 * sizeof(raw))};
+        }
+    }
+    // Operand of 16 columns from 16 t on, depths the rows 32 s..
+    __device__ __forceinline__ typename M::frag cols(const raw* m, int s, int t) const {
+        const char* p = reinterpret_cast<const char*>(m + 32 * s * kPitch);
+        if constexpr (kSwap) {
+            typedef __attribute__((address_space(3))) s16x4* lp;
+            p += 16 * t / kSpan * kSpan * sizeof(raw) + c[t % kCols];
+            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p)));
+            const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p + 16 * kPitch * sizeof(raw))));
+            return u32x4{a[0], a[1], b[0], b[1]};
+        } else {
+            const raw* at = reinterpret_cast<const raw*>(p + c[0]) + 16 * t;
+            typename M::frag f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f.a[k] = as_float(at[k * kPitch]);
+                f.b[k] = as_float(at[(16 + k) * kPitch]);
+            }
+            return f;
+        }
+    }
+};
+
+// Workgroup barrier for LDS traffic only: the wave's LDS operations are complete, then all waves meet.  Loads and
+// stores of memory stay in flight across it.
+__device__ __forceinline__ void lds_meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// matrices in memory: buffers of up to 2^31 bytes from a row on, where what lies outside reads as zeros and is not
+// written.  Strides are bounded by kDeltaMaxToken, so that the rows of a chunk lie within.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kOutside = 0x80000000u;
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer(const void* p, int64_t bytes = kOutside) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes < int64_t(kOutside) ? int(bytes) : int(kOutside),
+                                             0x00020000);
+}
+
+// A tile of ROWS tokens of a matrix with whole 16-byte vectors in its rows, padded to DIM columns, held by the
+// threads of a workgroup between memory and LDS.
+template <typename E, int ROWS, int DIM, int THREADS>
+struct TileRegs {
+    typedef typename E::raw raw;
+    static constexpr int VE = 16 / int(sizeof(raw)), PER_ROW = DIM / VE, STEP = THREADS / PER_ROW, N = ROWS / STEP;
+    static_assert(THREADS % PER_ROW == 0 && ROWS % STEP == 0, "");
+    u32x4 r[N];
+
+    // The offset of a thread's first vector, for rows `pitch` elements apart of `dim` columns.
+    static __device__ __forceinline__ uint32_t offset(int64_t pitch, int dim) {
+        const int row = threadIdx.x / PER_ROW, col = threadIdx.x % PER_ROW * VE;
+        return col < dim ? uint32_t((row * pitch + col) * sizeof(raw)) : kOutside;
+    }
+    __device__ __forceinline__ void load(Buffer b, uint32_t offset, int64_t pitch) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            r[n] = __builtin_amdgcn_raw_buffer_load_b128(b, int(offset + uint32_t(n * STEP * pitch * sizeof(raw))), 0, 0);
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(raw* lds) const {
+        const int row = threadIdx.x / PER_ROW, col = threadIdx.x % PER_ROW * VE;
+#pragma unroll
+        for (int n = 0; n < N; ++n) *reinterpret_cast<u32x4*>(lds + T::piece(row + n * STEP, col)) = r[n];
+    }
+};
+
+// The same value, computed on from where this stands: sums of it with a row's offset are made where they are used and
+// not kept in registers over the chunks (48 of them, which spilled).
+__device__ __forceinline__ uint32_t here(uint32_t v) {
+    asm volatile("" : "+v"(v));
     return v;
 }
 
-// A tile of ROWS tokens of a [.., dim] matrix, padded to DIM columns, held by the threads of a workgroup between
-// memory and LDS.
-template <typename E, int ROWS, int DIM, int THREADS>
-struct TileRegs {
-    static constexpr int VE = 16 / sizeof(typename E::raw);
-    static constexpr int PER_ROW = DIM / VE;
-    static constexpr int N = ROWS * PER_ROW / THREADS;
-    static_assert(ROWS * PER_ROW % THREADS == 0, "");
-    u32x4 r[N];
-
-    __device__ __forceinline__ void load(const typename E::raw* base, int64_t token, int t0, int end, int dim, bool vec) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int at = threadIdx.x + n * THREADS, row = at / PER_ROW, col = at % PER_ROW * VE;
-            r[n] = t0 + row < end ? load_vec<E>(base + (t0 + row) * token, col, dim, vec) : u32x4{0, 0, 0, 0};
-        }
-    }
-    __device__ __forceinline__ void store(typename E::raw* lds, int pitch) const {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int at = threadIdx.x + n * THREADS, row = at / PER_ROW, col = at % PER_ROW * VE;
-            *reinterpret_cast<u32x4*>(lds + row * pitch + col) = r[n];
-        }
-    }
-};
+// One element of a result tile's place.
+template <typename E>
+__device__ __forceinline__ typename E::raw load_one(Buffer b, uint32_t offset) {
+    if constexpr (sizeof(typename E::raw) == 4) return __builtin_amdgcn_raw_buffer_load_b32(b, int(offset), 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b16(b, int(offset), 0, 0);
+}
+template <typename E>
+__device__ __forceinline__ void store_one(Buffer b, uint32_t offset, float v) {
+    if constexpr (sizeof(typename E::raw) == 4) __builtin_amdgcn_raw_buffer_store_b32(as_uint(v), b, int(offset), 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(E::put(v), b, int(offset), 0, 0);
+}
 
 // Four values of a row: elements col.. of `dim` (zeros past it).
 template <typename E>

@@ -51,6 +51,7 @@ int delta_dims(const gated_delta_inputs& s) {
 int delta_sizes(const gated_delta_inputs& s) {
     const int st = delta_dims(s);
     if (st != SSD_OK) return st;
+    if (s.heads * s.dv > cls::kDeltaMaxToken || s.kheads * 256 > cls::kDeltaMaxToken) return SSD_ERR_SHAPE;
     const int64_t heads = s.batch * s.heads;
     if (heads * ceil_div(s.dv, 64) >= kMaxThreads / 256) return SSD_ERR_SHAPE;
     if (heads >= ceil_div(kMaxThreads / 256, ceil_div(s.seqlen, chunk_of(s.dtype)))) return SSD_ERR_SHAPE;
@@ -73,47 +74,73 @@ int delta_check(const gated_delta_inputs* in, bool step) {
     return aligned(in->seqlens, 4) ? SSD_OK : SSD_ERR_ALIGN;
 }
 
+// Whether the kernels read an activation's rows where they are: tokens apart by a row or more and no further than
+// their offsets reach, and (whole) rows of 16-byte vectors.  Others are copied into the workspace.
+bool in_place(const void* p, bool whole, int64_t L, int64_t dim, int dtype, int64_t batch, int64_t token, int64_t head) {
+    if (L > 1 && (token < dim || token > cls::kDeltaMaxToken)) return false;
+    return !whole || whole_vectors(p, dim, dtype, batch, L > 1 ? token : 0, head);
+}
+
+int64_t padded_keys(const gated_delta_inputs& s) {
+    const int64_t ve = 16 / int64_t(elem_size(s.dtype));
+    return ceil_div(s.dk, ve) * ve;
+}
+
 // Offsets in the workspaces and checkpoints, and their sizes.
 struct DeltaSpace {
-    size_t mats, vecs, fwd;            // both passes: matrices and factors of the chunks
-    size_t fixes, ckpt;                // checkpoints: states, then corrections
-    size_t dstates, z, part_q, part_k, bwd;  // backward
+    bool pack_q, pack_k, pack_v;
+    size_t mats, vecs, q, k, v, fwd;             // both passes: matrices and factors of the chunks, copies
+    size_t fixes, ckpt;                          // checkpoints: states, then corrections
+    size_t dstates, z, part_q, part_k, dy, bwd;  // backward
 };
 
 DeltaSpace delta_space(const gated_delta_inputs& s) {
-    const int64_t C = chunk_of(s.dtype), n = s.batch * s.heads * ceil_div(s.seqlen, C);
+    const int64_t C = chunk_of(s.dtype), n = s.batch * s.heads * ceil_div(s.seqlen, C), rows = s.batch * s.seqlen;
     const size_t mat = size_t(C * C) * elem_size(s.dtype) * (s.dtype == SSD_F32 ? 2 : 4);
+    const size_t keys = round_up(size_t(rows * s.kheads * padded_keys(s)) * elem_size(s.dtype), 256);
+    const size_t values = round_up(size_t(rows * s.heads * s.dv) * elem_size(s.dtype), 256);
     DeltaSpace d{};
+    d.pack_q = !in_place(s.q, true, s.seqlen, s.dk, s.dtype, s.q_batch, s.q_token, s.q_head);
+    d.pack_k = !in_place(s.k, true, s.seqlen, s.dk, s.dtype, s.k_batch, s.k_token, s.k_head);
+    d.pack_v = !in_place(s.v, false, s.seqlen, s.dv, s.dtype, s.v_batch, s.v_token, s.v_head);
     d.vecs = round_up(size_t(n) * mat, 256);
-    d.fwd = d.vecs + round_up(size_t(n) * 3 * C * 4, 256);
+    d.q = d.vecs + round_up(size_t(n) * 3 * C * 4, 256);
+    d.k = d.q + (d.pack_q ? keys : 0);
+    d.v = d.k + (d.pack_k ? keys : 0);
+    d.fwd = d.v + (d.pack_v ? values : 0);
     const size_t states = round_up(size_t(n) * s.dk * s.dv * 4, 256);
-    const size_t tokens = round_up(size_t(s.batch * s.seqlen * s.heads) * s.dv * 4, 256);
-    const size_t keys = s.heads > s.kheads ? round_up(size_t(s.batch * s.seqlen * s.heads) * s.dk * 4, 256) : 0;
+    const size_t tokens = round_up(size_t(rows * s.heads) * s.dv * 4, 256);
+    const size_t parts = s.heads > s.kheads ? round_up(size_t(rows * s.heads) * s.dk * 4, 256) : 0;
     d.fixes = states;
     d.ckpt = states + tokens;
     d.dstates = d.fwd;
     d.z = d.dstates + states;
     d.part_q = d.z + tokens;
-    d.part_k = d.part_q + keys;
-    d.bwd = d.part_k + keys;
+    d.part_k = d.part_q + parts;
+    d.dy = d.part_k + parts;
+    d.bwd = d.dy + values;
     return d;
 }
 
 DeltaParams delta_params(const gated_delta_inputs& in, void* workspace, void* checkpoints, const DeltaSpace& s) {
     DeltaParams p{};
-    p.q = in.q; p.k = in.k; p.v = in.v; p.g = in.g; p.beta = in.beta; p.h0 = in.h0; p.seqlens = in.seqlens;
-    p.sq = {in.q_batch, in.q_token, in.q_head};
-    p.sk = {in.k_batch, in.k_token, in.k_head};
-    p.sv = {in.v_batch, in.v_token, in.v_head};
+    p.g = in.g; p.beta = in.beta; p.h0 = in.h0; p.seqlens = in.seqlens;
     p.g_batch = in.g_batch; p.g_token = in.g_token; p.b_batch = in.beta_batch; p.b_token = in.beta_token;
     p.batch = int(in.batch); p.L = int(in.seqlen); p.Hk = int(in.kheads); p.H = int(in.heads);
     p.dk = int(in.dk); p.dv = int(in.dv);
     p.nchunk = int(ceil_div(in.seqlen, chunk_of(in.dtype)));
     p.scale = in.scale;
-    p.vec_q = whole_vectors(in.q, in.dk, in.dtype, in.q_batch, in.q_token, in.q_head);
-    p.vec_k = whole_vectors(in.k, in.dk, in.dtype, in.k_batch, in.k_token, in.k_head);
-    p.vec_v = whole_vectors(in.v, in.dv, in.dtype, in.v_batch, in.v_token, in.v_head);
     char* ws = static_cast<char*>(workspace);
+    const auto place = [&](const void* given, bool copied, size_t at, int64_t heads, int64_t dim, cls::Strided3 given_strides,
+                           const void*& to, cls::Strided3& strides) {
+        to = copied ? ws + at : given;
+        if (copied) strides = {in.seqlen * heads * dim, heads * dim, dim};
+        else strides = {given_strides.batch, in.seqlen > 1 ? given_strides.token : heads * dim, given_strides.head};
+    };
+    place(in.q, s.pack_q, s.q, in.kheads, padded_keys(in), {in.q_batch, in.q_token, in.q_head}, p.q, p.sq);
+    place(in.k, s.pack_k, s.k, in.kheads, padded_keys(in), {in.k_batch, in.k_token, in.k_head}, p.k, p.sk);
+    place(in.v, s.pack_v, s.v, in.heads, in.dv, {in.v_batch, in.v_token, in.v_head}, p.v, p.sv);
+    p.vec_v = whole_vectors(p.v, in.dv, in.dtype, p.sv.batch, p.sv.token, p.sv.head);
     p.mats = ws + s.mats;
     p.vecs = reinterpret_cast<float*>(ws + s.vecs);
     if (checkpoints) {
@@ -121,6 +148,23 @@ DeltaParams delta_params(const gated_delta_inputs& in, void* workspace, void* ch
         p.fixes = reinterpret_cast<float*>(static_cast<char*>(checkpoints) + s.fixes);
     }
     return p;
+}
+
+// The copies, where there are any.
+int delta_pack(const gated_delta_inputs& in, void* workspace, const DeltaSpace& s, hipStream_t stream) {
+    char* ws = static_cast<char*>(workspace);
+    const int64_t size = int64_t(elem_size(in.dtype)), dk = padded_keys(in);
+    int st = 0;
+    if (s.pack_q)
+        st = cls_delta_pack_launch(in.q, ws + s.q, size, in.batch, in.seqlen, in.kheads, in.dk, dk, in.q_batch, in.q_token,
+                                   in.q_head, stream);
+    if (st == 0 && s.pack_k)
+        st = cls_delta_pack_launch(in.k, ws + s.k, size, in.batch, in.seqlen, in.kheads, in.dk, dk, in.k_batch, in.k_token,
+                                   in.k_head, stream);
+    if (st == 0 && s.pack_v)
+        st = cls_delta_pack_launch(in.v, ws + s.v, size, in.batch, in.seqlen, in.heads, in.dv, in.dv, in.v_batch, in.v_token,
+                                   in.v_head, stream);
+    return st;
 }
 
 constexpr int64_t kMaxNormDim = 16384;
@@ -187,7 +231,8 @@ int gated_delta_fwd(const gated_delta_inputs* in, void* y, float* h_final, void*
     p.y = y;
     p.h_last = h_final;
     const hipStream_t hs = static_cast<hipStream_t>(stream);
-    int rc = cls_delta_prep_launch(p, in->dtype, false, hs);
+    int rc = delta_pack(*in, workspace, s, hs);
+    if (rc == 0) rc = cls_delta_prep_launch(p, in->dtype, false, hs);
     if (rc == 0) rc = cls_delta_fwd_launch(p, in->dtype, hs);
     return launched(rc);
 }
@@ -209,19 +254,26 @@ int gated_delta_bwd(const gated_delta_inputs* in, const gated_delta_grads* g, vo
     const DeltaSpace s = delta_space(*in);
     if (!workspace || workspace_bytes < s.bwd) return SSD_ERR_WORKSPACE;
     DeltaParams p = delta_params(*in, workspace, const_cast<void*>(g->checkpoints), s);
-    p.dy = g->dy;
-    p.sdy = {g->dy_batch, g->dy_token, g->dy_head};
-    p.vec_dy = whole_vectors(g->dy, in->dv, in->dtype, g->dy_batch, g->dy_token, g->dy_head);
+    char* ws = static_cast<char*>(workspace);
+    const bool pack_dy = !in_place(g->dy, false, in->seqlen, in->dv, in->dtype, g->dy_batch, g->dy_token, g->dy_head);
+    const int64_t row = in->heads * in->dv;
+    p.dy = pack_dy ? ws + s.dy : g->dy;
+    if (pack_dy) p.sdy = {in->seqlen * row, row, in->dv};
+    else p.sdy = {g->dy_batch, in->seqlen > 1 ? g->dy_token : row, g->dy_head};
+    p.vec_dy = whole_vectors(p.dy, in->dv, in->dtype, p.sdy.batch, p.sdy.token, p.sdy.head);
     p.vec_out = aligned(g->dq, 16) && aligned(g->dk, 16);
     p.dh_last = g->dh_final;
     p.dq = g->dq; p.dk_ = g->dk; p.dv_ = g->dv; p.dg = g->dg; p.dbeta = g->dbeta; p.dh0 = g->dh0;
-    char* ws = static_cast<char*>(workspace);
     p.dstates = reinterpret_cast<float*>(ws + s.dstates);
     p.z = reinterpret_cast<float*>(ws + s.z);
     p.part_q = reinterpret_cast<float*>(ws + s.part_q);
     p.part_k = reinterpret_cast<float*>(ws + s.part_k);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
-    int rc = cls_delta_prep_launch(p, in->dtype, true, hs);
+    int rc = delta_pack(*in, workspace, s, hs);
+    if (rc == 0 && pack_dy)
+        rc = cls_delta_pack_launch(g->dy, ws + s.dy, int64_t(elem_size(in->dtype)), in->batch, in->seqlen, in->heads, in->dv,
+                                   in->dv, g->dy_batch, g->dy_token, g->dy_head, hs);
+    if (rc == 0) rc = cls_delta_prep_launch(p, in->dtype, true, hs);
     if (rc == 0) rc = cls_delta_bwd_launch(p, in->dtype, hs);
     if (rc == 0) rc = cls_delta_grad_launch(p, in->dtype, hs);
     return launched(rc);

@@ -60,18 +60,32 @@ struct Tile32 {
     }
 };
 
+// Rows of 32 elements in LDS (a tile of S, dS or N), padded by 16 bytes: the operands' reads touch every bank once.
 template <typename E>
-__device__ __forceinline__ Two<E> two_rows(const typename E::raw* p, int lo) {
-    Two<E> t;
-    t.hi = Mat<E>::rows(p);
-    if constexpr (Mat<E>::kSplit) t.lo = Mat<E>::rows(p + lo);
-    return t;
-}
+struct Rows32 {
+    typedef typename E::raw raw;
+    static constexpr int kPitch = 32 + 16 / int(sizeof(raw));
+    static __device__ __forceinline__ typename Mat<E>::frag one(const raw* m, int t) {
+        const raw* p = m + (16 * t + lane16()) * kPitch + 4 * group4();
+        if constexpr (Mat<E>::kSplit) {
+            const u32x2 a = *reinterpret_cast<const u32x2*>(p), b = *reinterpret_cast<const u32x2*>(p + 16);
+            return u32x4{a[0], a[1], b[0], b[1]};
+        } else {
+            return typename Mat<E>::frag{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16)};
+        }
+    }
+    static __device__ __forceinline__ Two<E> two(const raw* m, int t, int lo) {
+        Two<E> x;
+        x.hi = one(m, t);
+        if constexpr (Mat<E>::kSplit) x.lo = one(m + lo, t);
+        return x;
+    }
+};
 
 template <typename E, int DK>
 struct GradSize {
     typedef Mat<E> M;
-    static constexpr int C = M::kChunk, KP = DK + M::kPad, SP = 32 + M::kPad, MP = ChunkMats<E>::kPitch;
+    static constexpr int C = M::kChunk, KP = LdsTile<E, DK>::kPitch, SP = Rows32<E>::kPitch, MP = LdsTile<E, C>::kPitch;
     static constexpr int kParts = ChunkMats<E>::kParts;
     static constexpr int kTiles = kParts * (DK + C) * SP;  // a tile of S or dS, and of N
     static constexpr int kPairs = 2 * C * MP;              // pB and pP, in the same place
@@ -151,13 +165,20 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     const raw* Vi = static_cast<const raw*>(p.v) + b * p.sv.batch + h * p.sv.head + tok * p.sv.token;
     const int left = end - t0 < C ? end - t0 : C;  // tokens of the chunk
     const bool v4 = p.dv % 4 == 0;                 // rows of states, N and Z are whole vectors
+    typedef LdsTile<E, DK> KTile;
+    typedef LdsTile<E, C> MTile;
+    const KTile kt;
+    const MTile mt;
     {
-        TileRegs<E, C, DK, THREADS> k, q;
-        k.load(static_cast<const raw*>(p.k) + b * p.sk.batch + kh * p.sk.head, p.sk.token, t0, end, p.dk, p.vec_k);
-        q.load(static_cast<const raw*>(p.q) + b * p.sq.batch + kh * p.sq.head, p.sq.token, t0, end, p.dk, p.vec_q);
+        typedef TileRegs<E, C, DK, THREADS> Regs;
+        Regs k, q;
+        const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + t0 * p.sk.token + kh * p.sk.head;
+        const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + t0 * p.sq.token + kh * p.sq.head;
+        k.load(buffer(K, left * p.sk.token * sizeof(raw)), Regs::offset(p.sk.token, p.dk), p.sk.token);
+        q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk), p.sq.token);
         if (tid < C) sG[tid] = t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f;
-        k.store(sK, KP);
-        q.store(sQ, KP);
+        k.template store<KTile>(sK);
+        q.template store<KTile>(sQ);
     }
 
     // with the state before the chunk: X1 = S dY^T, X2 = S Z^T; with the corrections: dP^T and M^T
@@ -194,14 +215,14 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
         const typename M::frag yf = M::cvt(y[0], y[1]);  // exact
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            const Two<E> s = two_rows<E>(sS + (16 * t + l16) * SP, DK * SP);
+            const Two<E> s = Rows32<E>::two(sS, t, DK * SP);
             X1[t] = mma2<E>(s, yf, X1[t]);
             X2[t] = mma3<E>(s, zf, X2[t]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (t > w) break;
-            const Two<E> nj = two_rows<E>(sN + (16 * t + l16) * SP, C * SP);
+            const Two<E> nj = Rows32<E>::two(sN, t, C * SP);
             dP[t] = mma2<E>(nj, yf, dP[t]);
             Mz[t] = mma3<E>(nj, zf, Mz[t]);
         }
@@ -211,7 +232,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
         float v = 0.0f;
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            const f32x4 a = load4<E>(m + i * KP, 16 * t + 4 * g4, DK, true);
+            const f32x4 a = load4<E>(m, KTile::quad(i, 16 * t + 4 * g4), 1 << 30, true);
 #pragma unroll
             for (int r = 0; r < 4; ++r) v = fmaf(a[r], x[t][r], v);
         }
@@ -244,7 +265,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
             if (d0 + 32 < p.dv) rs.load(dS, p.dv, p.dk, d0 + 32, p.dv, v4);
             const Two<E> nf = two<E>(x[0], x[1]);
 #pragma unroll
-            for (int t = 0; t < KT; ++t) X2[t] = mma3<E>(two_rows<E>(sS + (16 * t + l16) * SP, DK * SP), nf, X2[t]);
+            for (int t = 0; t < KT; ++t) X2[t] = mma3<E>(Rows32<E>::two(sS, t, DK * SP), nf, X2[t]);
         }
     }
     const float write = dot_row(sK, X2) + beta * kx;
@@ -258,11 +279,11 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     for (int t = 0; t < NT; ++t) kk[t] = qk[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int ks = 0; ks < DK / 32; ++ks) {
-        const typename M::frag ki = M::rows(sK + i * KP + 32 * ks), qi = M::rows(sQ + i * KP + 32 * ks);
+        const typename M::frag ki = kt.rows(sK, w, ks), qi = kt.rows(sQ, w, ks);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (t > w) break;
-            const typename M::frag kj = M::rows(sK + (16 * t + l16) * KP + 32 * ks);
+            const typename M::frag kj = kt.rows(sK, t, ks);
             kk[t] = M::mma(kj, ki, kk[t]);
             qk[t] = M::mma(kj, qi, qk[t]);
         }
@@ -305,8 +326,8 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     __syncthreads();  // the tiles are read
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        put4<E>(sB + i * MP + 16 * t + 4 * g4, 0, Mz[t]);  // zeros for the tiles behind w
-        put4<E>(sP + i * MP + 16 * t + 4 * g4, 0, dP[t]);
+        put4<E>(sB + MTile::quad(i, 16 * t + 4 * g4), 0, Mz[t]);  // zeros for the tiles behind w
+        put4<E>(sP + MTile::quad(i, 16 * t + 4 * g4), 0, dP[t]);
     }
     __syncthreads();
     if (tid < C) {  // dg of token tid
@@ -328,15 +349,14 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     for (int s = 0; s < NT / 2; ++s) {
         bi[s] = M::cvt(Mz[2 * s], Mz[2 * s + 1]);
         pi[s] = M::cvt(dP[2 * s], dP[2 * s + 1]);
-        bj[s] = M::cols(sB + 32 * s * MP + 16 * w, MP);
-        pj[s] = M::cols(sP + 32 * s * MP + 16 * w, MP);
+        bj[s] = mt.cols(sB, s, w);
+        pj[s] = mt.cols(sP, s, w);
     }
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
 #pragma unroll
         for (int s = 0; s < NT / 2; ++s) {
-            const typename M::frag kc = M::cols(sK + 32 * s * KP + 16 * t, KP);
-            const typename M::frag qc = M::cols(sQ + 32 * s * KP + 16 * t, KP);
+            const typename M::frag kc = kt.cols(sK, s, t), qc = kt.cols(sQ, s, t);
             X1[t] = M::mma(kc, pi[s], X1[t]);
             X2[t] = M::mma(kc, bi[s], X2[t]);
             X2[t] = M::mma(kc, bj[s], X2[t]);

@@ -42,9 +42,10 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
     typedef Mat<E> M;
     typedef typename M::raw raw;
     constexpr int C = M::kChunk, NT = C / 16, THREADS = 64 * NT;
-    constexpr int KP = DK + M::kPad, AP = C + 4;
-    __shared__ __attribute__((aligned(16))) raw sK[C * KP];
-    __shared__ __attribute__((aligned(16))) raw sQ[C * KP];
+    typedef LdsTile<E, DK> KT;
+    constexpr int AP = C + 4;
+    __shared__ __attribute__((aligned(16))) raw sK[C * KT::kPitch];
+    __shared__ __attribute__((aligned(16))) raw sQ[C * KT::kPitch];
     __shared__ __attribute__((aligned(16))) float sA[C * AP];
     __shared__ __attribute__((aligned(16))) float sT[C * AP];
     __shared__ __attribute__((aligned(16))) float sG[C];
@@ -54,28 +55,33 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
     if (t0 >= end) return;
     const int kh = h / (p.H / p.Hk), tid = threadIdx.x, w = tid >> 6, l16 = lane16(), g4 = group4();
     {
-        TileRegs<E, C, DK, THREADS> k, q;
-        k.load(static_cast<const raw*>(p.k) + b * p.sk.batch + kh * p.sk.head, p.sk.token, t0, end, p.dk, p.vec_k);
-        q.load(static_cast<const raw*>(p.q) + b * p.sq.batch + kh * p.sq.head, p.sq.token, t0, end, p.dk, p.vec_q);
+        typedef TileRegs<E, C, DK, THREADS> Regs;
+        Regs k, q;
+        const int left = end - t0;
+        const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + t0 * p.sk.token + kh * p.sk.head;
+        const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + t0 * p.sq.token + kh * p.sq.head;
+        k.load(buffer(K, left * p.sk.token * sizeof(raw)), Regs::offset(p.sk.token, p.dk), p.sk.token);
+        q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk), p.sq.token);
         if (tid < C) sG[tid] = t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f;
-        k.store(sK, KP);
-        q.store(sQ, KP);
+        k.template store<KT>(sK);
+        q.template store<KT>(sQ);
     }
     const int i = 16 * w + l16;  // this lane's token: the row of A and P
     const float beta = t0 + i < end ? p.beta[b * p.b_batch + int64_t(t0 + i) * p.b_token + h] : 0.0f;
     __syncthreads();
 
+    const KT kt;
     // products of keys, and of keys with queries, for tokens j = 16 t + 4 g4 + r before i
     f32x4 kk[NT], qk[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) kk[t] = qk[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int ks = 0; ks < DK / 32; ++ks) {
-        const typename M::frag ki = M::rows(sK + i * KP + 32 * ks), qi = M::rows(sQ + i * KP + 32 * ks);
+        const typename M::frag ki = kt.rows(sK, w, ks), qi = kt.rows(sQ, w, ks);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (t > w) break;
-            const typename M::frag kj = M::rows(sK + (16 * t + l16) * KP + 32 * ks);
+            const typename M::frag kj = kt.rows(sK, t, ks);
             kk[t] = M::mma(kj, ki, kk[t]);
             qk[t] = M::mma(kj, qi, qk[t]);
         }

@@ -79,7 +79,8 @@ def test_structures_have_the_header_s_fields(s):
 
 def delta_in(**k):
     a = dict(batch=2, seqlen=200, kheads=2, heads=4, dk=64, dv=48, dtype=1, scale=1.0, q=AT, k=AT, v=AT, g=AT, beta=AT,
-             h0=AT, seqlens=AT)
+             h0=AT, seqlens=AT, q_batch=200 * 128, q_token=128, q_head=64, k_batch=200 * 128, k_token=128, k_head=64,
+             v_batch=200 * 192, v_token=192, v_head=48, g_batch=800, g_token=4, beta_batch=800, beta_token=4)
     a.update(k)
     return DeltaInputs(**a)
 
@@ -147,7 +148,9 @@ LIMITS = [(dict(batch=1 << 20, seqlen=1, heads=8), ALIGN), (dict(batch=1 << 20, 
           (dict(batch=1, seqlen=(1 << 29) - 32, kheads=1, heads=1, dtype=0), ALIGN),
           (dict(batch=1, seqlen=1 << 29, kheads=1, heads=1, dtype=0), SHAPE),
           (dict(batch=1 << 14, seqlen=1, kheads=1, heads=1, dv=65536), SHAPE),
-          (dict(batch=(1 << 14) - 1, seqlen=1, kheads=1, heads=1, dv=65536), ALIGN)]
+          (dict(batch=(1 << 14) - 1, seqlen=1, kheads=1, heads=1, dv=65536), ALIGN),
+          (dict(batch=1, heads=128, dv=65536), ALIGN), (dict(batch=1, heads=130, dv=65536), SHAPE),  # 2^23 in a token's row
+          (dict(batch=1, kheads=1 << 15, heads=1 << 15), ALIGN), (dict(batch=1, kheads=(1 << 15) + 1, heads=(1 << 15) + 1), SHAPE)]
 
 
 @pytest.mark.parametrize("size,status", LIMITS)
@@ -178,11 +181,22 @@ def test_delta_sizes_add_up():
         chunks = 2 * 4 * -(-200 // C)
         fwd = up(chunks * mat) + up(chunks * 3 * C * 4)
         states, tokens = up(chunks * 64 * 48 * 4), up(2 * 200 * 4 * 48 * 4)
+        size = 4 if dtype == 0 else 2
+        keys, values = up(2 * 200 * 2 * 64 * size), up(2 * 200 * 4 * 48 * size)
         assert lib.gated_delta_workspace_size(ctypes.byref(s)) == fwd
         assert lib.gated_delta_checkpoint_size(ctypes.byref(s)) == states + tokens
-        assert lib.gated_delta_bwd_workspace_size(ctypes.byref(s)) == fwd + states + tokens + 2 * up(2 * 200 * 4 * 64 * 4)
+        assert lib.gated_delta_bwd_workspace_size(ctypes.byref(s)) == fwd + states + tokens + 2 * up(2 * 200 * 4 * 64 * 4) + values
+        # rows that the kernels cannot read in place are copied: those off whole vectors (q and k), and of other strides
+        for bad, more in ((dict(q=AT + 8), keys), (dict(k_head=63), keys), (dict(v=AT + 4), 0), (dict(v_token=47), values),
+                          (dict(v_token=(1 << 23) + 8), values), (dict(q_token=0, k_token=8), 2 * keys),
+                          (dict(seqlen=1, q_token=0, k_token=0, v_token=0), None)):
+            s = delta_in(dtype=dtype, **bad)
+            if more is None:
+                assert lib.gated_delta_workspace_size(ctypes.byref(s)) == up(8 * mat) + up(8 * 3 * C * 4)
+            else:
+                assert lib.gated_delta_workspace_size(ctypes.byref(s)) == fwd + more, bad
         s = delta_in(dtype=dtype, kheads=4)
-        assert lib.gated_delta_bwd_workspace_size(ctypes.byref(s)) == fwd + states + tokens
+        assert lib.gated_delta_bwd_workspace_size(ctypes.byref(s)) == fwd + states + tokens + values
 
 
 def norm_in(**k):
