@@ -180,41 +180,50 @@ struct ChunkMats {
 // ---------------------------------------------------------------------------
 // matrices in LDS
 // ---------------------------------------------------------------------------
-// Rows of DIM elements without padding; the 16-byte pieces of a row are exchanged by
-// an exclusive or with a number of the row.  With 16-bit elements both reads of
-// operands (rows: 8 bytes of 16 rows; columns: transposing reads of 8 rows x 32 bytes)
-// and the 16-byte stores then touch every bank once.  (Padded rows gave the
-// columns' reads two-fold conflicts.)  fp32 rows are padded by 16 bytes instead.
-// An object holds a lane's offsets, which do not change from tile to tile.
+// With 16-bit elements a row's quads of four elements lie in the operands' order: of each 32 elements piece
+// g (16 bytes) holds quads g and 4 + g, the depths of lane group g, so an operand of rows is one read.  Pieces are exchanged by an
+// exclusive or with a number of the row instead of padding: reads of 16 rows touch every bank once, transposing
+// reads of 16 columns (half a piece of 8 rows each) twice.  (With the quads in their natural order those are free of
+// conflicts, too, but an operand of rows is two reads, which the compiler joins across tiles and takes apart by moves.)
+// fp32 rows are padded by 16 bytes.  An object holds a lane's offsets, which do not change from tile to tile.
 template <typename E, int DIM>
 struct LdsTile {
     typedef Mat<E> M;
     typedef typename M::raw raw;
     static constexpr bool kSwap = M::kSplit;
     static constexpr int kPitch = DIM + (kSwap ? 0 : 4);
-    static constexpr int VE = 16 / int(sizeof(raw));
     static constexpr int kSpan = DIM < 128 ? DIM : 128;  // columns that the exchange covers
-    static constexpr int kRows = kSwap ? 2 * kSpan / 32 : 1, kCols = kSwap ? kSpan / 16 : 1;
+    static constexpr int kRows = kSwap ? kSpan / 32 : 1, kCols = kSwap ? kSpan / 16 : 1;
     uint32_t r[kRows], c[kCols];  // bytes
 
+    // A number of the row: 16 rows (pairs of rows, where two share the banks' width) differ, and four rows differ in
+    // the bits that pieces of one operand do not.
     static __device__ __forceinline__ int swap(int row) {
-        const int x = kSpan == 64 ? (row >> 1) & 7 : row & 15;
-        return kSpan == 64 ? 2 * (x & 3) + (x >> 2) : 2 * (x & 7) + (x >> 3);
+        if constexpr (kSpan == 64) return 4 * ((row >> 1) & 1) + ((row >> 2) & 3);
+        else return 4 * (row & 3) + ((row >> 2) & 3);
     }
-    // Element offset of a 16-byte piece (col a multiple of VE).
-    static __device__ __forceinline__ int piece(int row, int col) {
-        if constexpr (kSwap) return row * kPitch + ((col / VE) ^ swap(row)) * VE;
+    // Element offset of four elements (col a multiple of 4).
+    static __device__ __forceinline__ int quad(int row, int col) {
+        if constexpr (kSwap) {
+            const int piece = (col >> 5) * 4 + ((col >> 2) & 3);
+            return row * kPitch + (piece ^ swap(row)) * 8 + ((col >> 4) & 1) * 4;
+        }
         return row * kPitch + col;
     }
-    // Of four elements (col a multiple of 4).
-    static __device__ __forceinline__ int quad(int row, int col) {
-        return piece(row, col / VE * VE) + col % VE;
+    // A 16-byte vector of a row in memory.
+    static __device__ __forceinline__ void put(raw* m, int row, int col, const u32x4& v) {
+        if constexpr (kSwap) {
+            *reinterpret_cast<u32x2*>(m + quad(row, col)) = u32x2{v[0], v[1]};
+            *reinterpret_cast<u32x2*>(m + quad(row, col + 4)) = u32x2{v[2], v[3]};
+        } else {
+            *reinterpret_cast<u32x4*>(m + quad(row, col)) = v;
+        }
     }
     __device__ __forceinline__ LdsTile() {
         const int l16 = lane16(), g = group4();
         if constexpr (kSwap) {
 #pragma unroll
-            for (int n = 0; n < kRows; ++n) r[n] = quad(l16, 16 * n + 4 * g) * sizeof(raw);
+            for (int n = 0; n < kRows; ++n) r[n] = quad(l16, 32 * n + 4 * g) * sizeof(raw);
 #pragma unroll
             for (int n = 0; n < kCols; ++n) c[n] = quad(4 * g + (l16 >> 2), 16 * n + 4 * (l16 & 3)) * sizeof(raw);
         } else {
@@ -227,9 +236,7 @@ struct LdsTile {
         const char* p = reinterpret_cast<const char*>(m + 16 * t * kPitch);
         if constexpr (kSwap) {
             p += 32 * s / kSpan * kSpan * sizeof(raw);
-            const u32x2 a = *reinterpret_cast<const u32x2*>(p + r[2 * s % kRows]);
-            const u32x2 b = *reinterpret_cast<const u32x2*>(p + r[2 * s % kRows + 1]);
-            return u32x4{a[0], a[1], b[0], b[1]};
+            return *reinterpret_cast<const u32x4*>(p + r[s % kRows]);
         } else {
             p += r[0] + 32 * s * sizeof(raw);
             return typename M::frag{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16 * sizeof(raw))};
@@ -272,8 +279,8 @@ __device__ __forceinline__ Buffer buffer(const void* p, int64_t bytes = kOutside
                                              0x00020000);
 }
 
-// A tile of ROWS tokens of a matrix with whole 16-byte vectors in its rows, padded to DIM columns, held by the
-// threads of a workgroup between memory and LDS.
+// A tile of ROWS tokens of a matrix with whole 16-byte vectors in its rows, padded to DIM columns, held by THREADS
+// threads (the workgroup's or its last ones) between memory and LDS.
 template <typename E, int ROWS, int DIM, int THREADS>
 struct TileRegs {
     typedef typename E::raw raw;
@@ -283,7 +290,7 @@ struct TileRegs {
 
     // The offset of a thread's first vector, for rows `pitch` elements apart of `dim` columns.
     static __device__ __forceinline__ uint32_t offset(int64_t pitch, int dim) {
-        const int row = threadIdx.x / PER_ROW, col = threadIdx.x % PER_ROW * VE;
+        const int at = threadIdx.x % THREADS, row = at / PER_ROW, col = at % PER_ROW * VE;
         return col < dim ? uint32_t((row * pitch + col) * sizeof(raw)) : kOutside;
     }
     __device__ __forceinline__ void load(Buffer b, uint32_t offset, int64_t pitch) {
@@ -293,9 +300,9 @@ struct TileRegs {
     }
     template <typename T>
     __device__ __forceinline__ void store(raw* lds) const {
-        const int row = threadIdx.x / PER_ROW, col = threadIdx.x % PER_ROW * VE;
+        const int at = threadIdx.x % THREADS, row = at / PER_ROW, col = at % PER_ROW * VE;
 #pragma unroll
-        for (int n = 0; n < N; ++n) *reinterpret_cast<u32x4*>(lds + T::piece(row + n * STEP, col)) = r[n];
+        for (int n = 0; n < N; ++n) T::put(lds, row + n * STEP, col, r[n]);
     }
 };
 

@@ -1,294 +1,214 @@
 // Gated delta rule over whole sequences: the walk over the chunks.  A wave has 16
-// (or 32) columns of the state S [dk, dv] in its registers and takes them through all
-// chunks of a sequence; columns do not meet, so waves only share what the
-// workgroup stages in LDS for them: the chunk's K, Q, T - I, P and factors.  Per chunk
+// columns of the state S [dk, dv] in its registers and takes them through all
+// chunks of a sequence; columns do not meet, so waves only share what is
+// staged in LDS for them: the chunk's K, Q, T - I, P and factors.  Per chunk
 //     R = beta (V - e^gamma K S),  N = R + (T - I) R,  Y = scale (e^gamma Q S + P N),
 //     S' = e^gamma_C S + K^T (e^(gamma_C - gamma) N)
 // where K S, T R and K^T N reach the state and take computed operands in two
 // parts, and Q S and P N only reach y and take them in one.
 #include <hip/hip_runtime.h>
 
-#include "delta.hpp"
-#include "device_once.hpp"
+#include "delta_walk.hpp"
 #include "launch_delta.hpp"
 
 namespace cls {
 namespace {
 
-// COLS tiles of 16 columns to a wave, WAVES waves to a workgroup.
-template <typename E, int DK, int COLS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, DK == 256 ? 1 : 2) void delta_fwd_kernel(DeltaParams p) {
+template <typename E, int DK>
+__global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) {
     typedef Mat<E> M;
     typedef typename M::raw raw;
-    typedef ChunkMats<E> CM;
-    typedef LdsTile<E, DK> KTile;
-    typedef LdsTile<E, M::kChunk> MTile;
     typedef typename M::frag frag;
-    constexpr int C = M::kChunk, NT = C / 16, KT = DK / 16, THREADS = 64 * WAVES, WG = 16 * COLS * WAVES;
-    constexpr int NM = CM::kParts + 1, MS = C * MTile::kPitch;
+    constexpr int kParts = ChunkMats<E>::kParts, NM = kParts + 1;  // T - I in its parts, P
+    typedef WalkLds<E, DK, NM> Lds;
+    constexpr int C = M::kChunk, NT = C / 16, KT = DK / 16, KS = DK / 32;
     constexpr uint32_t SZ = sizeof(raw);
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    raw* sK = reinterpret_cast<raw*>(lds);
-    raw* sQ = sK + C * KTile::kPitch;
-    raw* sT = sQ + C * KTile::kPitch;  // T - I (its parts), P
-    raw* sP = sT + CM::kParts * MS;
-    float* sV = reinterpret_cast<float*>(sT + NM * MS);
 
-    const int nblk = (p.dv + WG - 1) / WG;
+    const int nblk = (p.dv + kWalkCols - 1) / kWalkCols;
     const int blk = blockIdx.x % nblk, h = blockIdx.x / nblk % p.H, b = blockIdx.x / nblk / p.H;
-    const int end = seq_end(p.seqlens, b, p.L), kh = h / (p.H / p.Hk);
-    const int tid = threadIdx.x, l16 = lane16(), g4 = group4();
-    const int n0 = blk * WG + (tid >> 6) * 16 * COLS + l16;  // the first of a lane's columns, the others 16 apart
-    const bool wave_on = n0 - l16 < p.dv;
-
-    const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + kh * p.sk.head;
-    const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + kh * p.sq.head;
+    const int end = seq_end(p.seqlens, b, p.L), chunks = (end + C - 1) / C;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave >= 4) {
+        walk_load<E, DK, NM>(p, lds, b, h, end, 0, 1, chunks);
+        return;
+    }
+    const int l16 = lane16(), g4 = group4();
+    const int n = blk * kWalkCols + wave * 16 + l16;  // the lane's column
+    const bool on = n < p.dv, wave_on = blk * kWalkCols + wave * 16 < p.dv;
     const raw* V = static_cast<const raw*>(p.v) + b * p.sv.batch + h * p.sv.head;
     const int64_t row = int64_t(p.H) * p.dv;  // of a token of y
     const int64_t out = int64_t(b) * p.L * row + int64_t(h) * p.dv;
     raw* Y = static_cast<raw*>(p.y) + out;
 
-    f32x4 S[COLS][KT];
-    bool on[COLS];
-#pragma unroll
-    for (int u = 0; u < COLS; ++u) {
-        const int n = n0 + 16 * u;
-        on[u] = n < p.dv;
-        const float* from = p.h0 + ((int64_t(b) * p.H + h) * p.dv + n) * p.dk;
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = 16 * t + 4 * g4 + r;
-                S[u][t][r] = p.h0 && on[u] && d < p.dk ? from[d] : 0.0f;
-            }
-    }
-
-    // offsets of a lane in a chunk: of its vectors of K, Q and the matrices, of its elements of V and Y
-    typedef TileRegs<E, C, DK, THREADS> KRegs;
-    typedef TileRegs<E, C, C, THREADS> MRegs;
-    const KTile kt;
-    const MTile mt;
-    const uint32_t ok = KRegs::offset(p.sk.token, p.dk), oq = KRegs::offset(p.sq.token, p.dk), om = MRegs::offset(C, C);
+    f32x4 S[KT];
+    load_state<KT>(S, p.h0, on, int64_t(b) * p.H + h, n, p);
+    const LdsTile<E, DK> kt;
+    const LdsTile<E, C> mt;
     const uint32_t vrow = uint32_t(p.sv.token) * SZ, yrow = uint32_t(row) * SZ;
-    uint32_t ov[COLS], oy[COLS];
-#pragma unroll
-    for (int u = 0; u < COLS; ++u) {
-        ov[u] = on[u] ? 4 * g4 * vrow + (n0 + 16 * u) * SZ : kOutside;
-        oy[u] = on[u] ? 4 * g4 * yrow + (n0 + 16 * u) * SZ : kOutside;
-    }
-    KRegs rk, rq;
-    MRegs rm[NM];
-    float rv = 0.0f;
-    raw v[COLS][NT][4];
-    const int chunks = (end + C - 1) / C;
+    const uint32_t ov = on ? 4 * g4 * vrow + n * SZ : kOutside, oy = on ? 4 * g4 * yrow + n * SZ : kOutside;
+    raw v[NT][4];
     const auto fetch = [&](int c) {
-        const int t0 = c * C, left = end - t0;
-        rk.load(buffer(K + t0 * p.sk.token, left * p.sk.token * SZ), ok, p.sk.token);
-        rq.load(buffer(Q + t0 * p.sq.token, left * p.sq.token * SZ), oq, p.sq.token);
-        const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
-        const raw* mats = static_cast<const raw*>(p.mats) + chunk * CM::kAll * CM::kSize;
+        const Buffer bv = buffer(V + c * C * p.sv.token, (end - c * C) * p.sv.token * SZ);
+        const uint32_t at = here(ov);
 #pragma unroll
-        for (int m = 0; m < NM; ++m) rm[m].load(buffer(mats + m * CM::kSize), om, C);
-        if (tid < 3 * C) rv = p.vecs[chunk * 3 * C + tid];
-        const Buffer bv = buffer(V + t0 * p.sv.token, left * p.sv.token * SZ);
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int u = 0; u < COLS; ++u) {
-            const uint32_t at = here(ov[u]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[u][t][r] = load_one<E>(bv, at + (16 * t + r) * vrow);
-        }
+            for (int r = 0; r < 4; ++r) v[t][r] = load_one<E>(bv, at + (16 * t + r) * vrow);
     };
     if (chunks > 0) fetch(0);
-    for (int c = 0; c < chunks; ++c) {
-        const int t0 = c * C;
-        lds_meet();  // the chunk before is read
-        rk.template store<KTile>(sK);
-        rq.template store<KTile>(sQ);
-#pragma unroll
-        for (int m = 0; m < NM; ++m) rm[m].template store<MTile>(sT + m * MS);
-        if (tid < 3 * C) sV[tid] = rv;
-        f32x4 R[COLS][NT];
-#pragma unroll
-        for (int u = 0; u < COLS; ++u)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) R[u][t][r] = E::get(v[u][t][r]);
-        lds_meet();
-        if (c + 1 < chunks) fetch(c + 1);
-        if (!wave_on) continue;
 
-        if (p.states) {
-            const Buffer bs = buffer(p.states + ((int64_t(b) * p.nchunk + c) * p.H + h) * p.dk * p.dv,
-                                     int64_t(p.dk) * p.dv * 4);
+    walk<Lds>(lds, chunks, [&](int c, const Lds& m) {
+        if (!wave_on) return;
+        const int t0 = c * C;
+        f32x4 R[NT];
 #pragma unroll
-            for (int u = 0; u < COLS; ++u) {
-                const uint32_t at = here(on[u] ? (4 * g4 * p.dv + n0 + 16 * u) * 4 : kOutside);
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) store_one<ElemF32>(bs, at + (16 * t + r) * p.dv * 4, S[u][t][r]);
-            }
-        }
-        f32x4 ks[COLS][NT], O[COLS][NT];
-#pragma unroll
-        for (int u = 0; u < COLS; ++u)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) ks[u][t] = O[u][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < DK / 32; ++s) {
-            Two<E> st[COLS];
-#pragma unroll
-            for (int u = 0; u < COLS; ++u) st[u] = two<E>(S[u][2 * s], S[u][2 * s + 1]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const frag k = kt.rows(sK, t, s), q = kt.rows(sQ, t, s);
-#pragma unroll
-                for (int u = 0; u < COLS; ++u) {
-                    ks[u][t] = mma2<E>(k, st[u], ks[u][t]);
-                    O[u][t] = M::mma(q, st[u].hi, O[u][t]);
-                }
-            }
-        }
+            for (int r = 0; r < 4; ++r) R[t][r] = E::get(v[t][r]);
+        if (c + 1 < chunks) fetch(c + 1);
+        if (p.states)
+            keep_state<KT>(S, p.states, (int64_t(b) * p.nchunk + c) * p.H + h, on ? (4 * g4 * p.dv + n) * 4 : kOutside, p);
+
+        // K S and Q S; the operands of a step are read while the one before is multiplied
+        f32x4 ks[NT], O[NT];
+        frag k[2][NT], q[2][NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const f32x4 e = *reinterpret_cast<const f32x4*>(sV + 16 * t + 4 * g4);
-            const f32x4 be = *reinterpret_cast<const f32x4*>(sV + 2 * C + 16 * t + 4 * g4);
-#pragma unroll
-            for (int u = 0; u < COLS; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    R[u][t][r] = be[r] * fmaf(-e[r], ks[u][t][r], R[u][t][r]);
-                    O[u][t][r] *= e[r];
-                }
+            ks[t] = O[t] = f32x4{0, 0, 0, 0};
+            k[0][t] = kt.rows(m.k, t, 0);
+            q[0][t] = kt.rows(m.q, t, 0);
         }
-        // N = R + (T - I) R: tokens up to 32 (t / 2 + 1) reach tile t
-        f32x4 N[COLS][NT];
-        {
-            Two<E> rr[COLS][NT / 2];
+        Two<E> T[NT][NT / 2];
 #pragma unroll
-            for (int u = 0; u < COLS; ++u)
+        for (int s = 0; s < KS; ++s) {
+            if (s + 1 < KS) {
 #pragma unroll
-                for (int s = 0; s < NT / 2; ++s) rr[u][s] = two<E>(R[u][2 * s], R[u][2 * s + 1]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int u = 0; u < COLS; ++u) N[u][t] = R[u][t];
-#pragma unroll
-                for (int s = 0; s <= t / 2; ++s) {
-                    Two<E> T;
-                    T.hi = mt.rows(sT, t, s);
-                    if constexpr (M::kSplit) T.lo = mt.rows(sT + MS, t, s);
-#pragma unroll
-                    for (int u = 0; u < COLS; ++u) N[u][t] = mma3<E>(T, rr[u][s], N[u][t]);
+                for (int t = 0; t < NT; ++t) {
+                    k[(s + 1) & 1][t] = kt.rows(m.k, t, s + 1);
+                    q[(s + 1) & 1][t] = kt.rows(m.q, t, s + 1);
                 }
-            }
-        }
-        const int64_t at = out + t0 * row;
-        const Buffer by = buffer(Y + t0 * row, int64_t(p.L - t0) * row * SZ);
-        {
-            frag nf[COLS][NT / 2];
-#pragma unroll
-            for (int u = 0; u < COLS; ++u)
-#pragma unroll
-                for (int s = 0; s < NT / 2; ++s) nf[u][s] = M::cvt(N[u][2 * s], N[u][2 * s + 1]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int s = 0; s <= t / 2; ++s) {
-                    const frag P = mt.rows(sP, t, s);
-#pragma unroll
-                    for (int u = 0; u < COLS; ++u) O[u][t] = M::mma(P, nf[u][s], O[u][t]);
-                }
-            }
-        }
-        if (t0 + C > end)  // padding within the chunk
-#pragma unroll
-            for (int u = 0; u < COLS; ++u)
+            } else {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (t0 + 16 * t + 4 * g4 + r >= end) O[u][t][r] = 0.0f;
-#pragma unroll
-        for (int u = 0; u < COLS; ++u) {
-            const uint32_t to = here(oy[u]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) store_one<E>(by, to + (16 * t + r) * yrow, p.scale * O[u][t][r]);
-        }
-        if (p.fixes) {
-            const Buffer bf = buffer(p.fixes + at, int64_t(p.L - t0) * row * 4);
-#pragma unroll
-            for (int u = 0; u < COLS; ++u) {
-                const uint32_t of = here(on[u] ? (4 * g4 * uint32_t(row) + n0 + 16 * u) * 4 : kOutside);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) store_one<ElemF32>(bf, of + (16 * t + r) * uint32_t(row) * 4, N[u][t][r]);
+                    for (int u = 0; u <= t / 2; ++u) {
+                        T[t][u].hi = mt.rows(m.m, t, u);
+                        if constexpr (M::kSplit) T[t][u].lo = mt.rows(m.m + Lds::MS, t, u);
+                    }
             }
+            __builtin_amdgcn_sched_barrier(0);
+            const Two<E> st = two<E>(S[2 * s], S[2 * s + 1]);
+            if constexpr (M::kSplit) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) ks[t] = M::mma(k[s & 1][t], st.lo, ks[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) ks[t] = M::mma(k[s & 1][t], st.hi, ks[t]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) O[t] = M::mma(q[s & 1][t], st.hi, O[t]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const f32x4 e = *reinterpret_cast<const f32x4*>(sV + C + 16 * t + 4 * g4);
-#pragma unroll
-            for (int u = 0; u < COLS; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) N[u][t][r] *= e[r];
-        }
-        const float fade = sV[C - 1];
-        Two<E> nn[COLS][NT / 2];
-#pragma unroll
-        for (int u = 0; u < COLS; ++u)
-#pragma unroll
-            for (int s = 0; s < NT / 2; ++s) nn[u][s] = two<E>(N[u][2 * s], N[u][2 * s + 1]);
-#pragma unroll
-        for (int t = 0; t < KT; ++t) {
-#pragma unroll
-            for (int u = 0; u < COLS; ++u) S[u][t] *= fade;
-#pragma unroll
-            for (int s = 0; s < NT / 2; ++s) {
-                const frag k = kt.cols(sK, s, t);
-#pragma unroll
-                for (int u = 0; u < COLS; ++u) S[u][t] = mma2<E>(k, nn[u][s], S[u][t]);
-            }
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < COLS; ++u) {
-        if (!on[u]) continue;
-        for (int tok = chunks * C + g4; tok < p.L; tok += 4) Y[tok * row + n0 + 16 * u] = raw(0);
-        if (!p.h_last) continue;
-        float* to = p.h_last + ((int64_t(b) * p.H + h) * p.dv + n0 + 16 * u) * p.dk;
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
+            const f32x4 e = *reinterpret_cast<const f32x4*>(m.v + 16 * t + 4 * g4);
+            const f32x4 be = *reinterpret_cast<const f32x4*>(m.v + 2 * C + 16 * t + 4 * g4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int d = 16 * t + 4 * g4 + r;
-                if (d < p.dk) to[d] = S[u][t][r];
+                R[t][r] = be[r] * fmaf(-e[r], ks[t][r], R[t][r]);
+                O[t][r] *= e[r];
             }
-    }
+        }
+        // N = R + (T - I) R: tokens up to 32 (t / 2 + 1) reach tile t
+        frag P[NT][NT / 2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int s = 0; s <= t / 2; ++s) P[t][s] = mt.rows(m.m + kParts * Lds::MS, t, s);
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 N[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) N[t] = R[t];
+#pragma unroll
+        for (int s = 0; s < NT / 2; ++s) {
+            const Two<E> rr = two<E>(R[2 * s], R[2 * s + 1]);
+            if constexpr (M::kSplit) {
+#pragma unroll
+                for (int t = 2 * s; t < NT; ++t) N[t] = M::mma(T[t][s].lo, rr.hi, N[t]);
+#pragma unroll
+                for (int t = 2 * s; t < NT; ++t) N[t] = M::mma(T[t][s].hi, rr.lo, N[t]);
+            }
+#pragma unroll
+            for (int t = 2 * s; t < NT; ++t) N[t] = M::mma(T[t][s].hi, rr.hi, N[t]);
+        }
+        // the state, and beside it y
+        frag kc[2][NT / 2];
+#pragma unroll
+        for (int s = 0; s < NT / 2; ++s) kc[0][s] = kt.cols(m.k, s, 0);
+        f32x4 En[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) En[t] = N[t] * *reinterpret_cast<const f32x4*>(m.v + C + 16 * t + 4 * g4);
+        const float fade = m.v[C - 1];
+        __builtin_amdgcn_sched_barrier(0);
+        Two<E> nn[NT / 2];
+        frag nf[NT / 2];
+#pragma unroll
+        for (int s = 0; s < NT / 2; ++s) {
+            nn[s] = two<E>(En[2 * s], En[2 * s + 1]);
+            nf[s] = M::cvt(N[2 * s], N[2 * s + 1]);
+        }
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+            if (t + 1 < KT) {
+#pragma unroll
+                for (int s = 0; s < NT / 2; ++s) kc[(t + 1) & 1][s] = kt.cols(m.k, s, t + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            S[t] *= fade;
+#pragma unroll
+            for (int s = 0; s < NT / 2; ++s) S[t] = mma2<E>(kc[t & 1][s], nn[s], S[t]);
+            if (t < NT) {
+#pragma unroll
+                for (int s = 0; s <= t / 2; ++s) O[t] = M::mma(P[t][s], nf[s], O[t]);
+            }
+        }
+        const Buffer by = buffer(Y + t0 * row, int64_t(p.L - t0) * row * SZ);
+        const uint32_t to = here(oy);
+        if (t0 + C > end) {  // padding within the chunk
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (t0 + 16 * t + 4 * g4 + r >= end) O[t][r] = 0.0f;
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) store_one<E>(by, to + (16 * t + r) * yrow, p.scale * O[t][r]);
+        if (p.fixes) {
+            const Buffer bf = buffer(p.fixes + out + t0 * row, int64_t(p.L - t0) * row * 4);
+            const uint32_t of = here(on ? (4 * g4 * uint32_t(row) + n) * 4 : kOutside);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) store_one<ElemF32>(bf, of + (16 * t + r) * uint32_t(row) * 4, N[t][r]);
+        }
+    });
+    if (!on) return;
+    for (int tok = chunks * C + g4; tok < p.L; tok += 4) Y[tok * row + n] = raw(0);
+    if (p.h_last) store_state<KT>(S, p.h_last, int64_t(b) * p.H + h, n, p);
 }
 
-template <typename E, int DK, int COLS, int WAVES>
+template <typename E, int DK>
 int launch(const DeltaParams& p, hipStream_t stream) {
-    typedef Mat<E> M;
-    typedef ChunkMats<E> CM;
-    constexpr size_t bytes = (2 * M::kChunk * LdsTile<E, DK>::kPitch + (CM::kParts + 1) * M::kChunk * LdsTile<E, M::kChunk>::kPitch) *
-                                 sizeof(typename M::raw) + 3 * M::kChunk * sizeof(float);
+    constexpr int bytes = WalkLds<E, DK, ChunkMats<E>::kParts + 1>::kBytes;
     static DeviceOnce once;
     const int st = run_once_per_device(once, [] {
-        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_fwd_kernel<E, DK, COLS, WAVES>),
-                                   hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == hipSuccess ? 0 : -7;
+        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_fwd_kernel<E, DK>),
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess ? 0 : -7;
     });
     if (st != 0) return st;
-    constexpr int WG = 16 * COLS * WAVES;
-    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + WG - 1) / WG));
-    delta_fwd_kernel<E, DK, COLS, WAVES><<<wgs, 64 * WAVES, bytes, stream>>>(p);
+    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + kWalkCols - 1) / kWalkCols));
+    delta_fwd_kernel<E, DK><<<wgs, kWalkThreads, bytes, stream>>>(p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
@@ -297,6 +217,6 @@ int launch(const DeltaParams& p, hipStream_t stream) {
 
 int cls_delta_fwd_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream) {
     return cls::by_type(dtype, p.dk, [&](auto e, auto dk) {
-        return cls::launch<decltype(e), decltype(dk)::value, 1, 4>(p, stream);
+        return cls::launch<decltype(e), decltype(dk)::value>(p, stream);
     });
 }
