@@ -153,10 +153,10 @@ struct DeltaParams {
     const int32_t* seqlens;
     void *y, *dq, *dk_, *dv_;
     float *h_last, *dg, *dbeta, *dh0;
-    float* states;   // [batch, chunks, heads, dk, dv]: the state before each chunk (NULL = not kept)
-    float* fixes;    // [batch, L, heads, dv]: N, the corrections (NULL = not kept)
-    void* mats;      // per (batch, chunk, head): (I + A)^-1 - I and D QK^T, in one part or two
-    float* vecs;     // per (batch, chunk, head): e^gamma, e^(gamma_C - gamma), beta
+    float* states;   // [batch, chunks, heads, dv, dk]: the state before each chunk (NULL = not kept)
+    float* fixes;    // [batch, chunks, heads, dv, chunk]: N, the corrections (NULL = not kept)
+    void* mats;      // per (batch, chunk, head): (I + A)^-1 - I and D QK^T (forward: times scale), in one part or two
+    float* vecs;     // per (batch, chunk, head): kVecs factors of each token
     float* dstates;  // as states: the gradient of the state behind each chunk
     float* z;        // as fixes: (I + A)^-T dN
     float *part_q, *part_k;  // [batch, L, heads, dk], where key heads are shared
@@ -165,7 +165,8 @@ struct DeltaParams {
     int batch, L, Hk, H, dk, dv, nchunk;
     float scale;
     uint8_t vec_v, vec_dy;  // rows of whole 16-byte vectors, as those of q and k are here
-    uint8_t vec_out;        // dq and dk start on 16 bytes
+    uint8_t vec_out;        // y or dv has rows of whole 16-byte vectors
+    uint8_t vec_dqk;        // dq and dk start on 16 bytes
 };
 
 // Matrices of a chunk in `mats`: T hi, T lo, P hi, P lo (16-bit), T, P (fp32).
@@ -176,6 +177,9 @@ struct ChunkMats {
     static constexpr int kParts = M::kSplit ? 2 : 1;
     static constexpr int kAll = 2 * kParts;
 };
+
+// Factors of a token in `vecs`, each for all of a chunk's: scale e^gamma, e^(gamma_C - gamma), beta, beta e^gamma, e^gamma.
+enum { kRead, kWrite, kBeta, kBetaStart, kStart, kVecs };
 
 // ---------------------------------------------------------------------------
 // matrices in LDS
@@ -196,11 +200,11 @@ struct LdsTile {
     static constexpr int kRows = kSwap ? kSpan / 32 : 1, kCols = kSwap ? kSpan / 16 : 1;
     uint32_t r[kRows], c[kCols];  // bytes
 
-    // A number of the row: 16 rows (pairs of rows, where two share the banks' width) differ, and four rows differ in
-    // the bits that pieces of one operand do not.
+    // A number of the row: its upper bits differ among four rows, its lower two among every fourth, in an order that
+    // keeps the 16 lanes which a 16-byte read serves at a time apart (0-3, 12-15 and 20-27 of 32, so rows of two lane groups).
     static __device__ __forceinline__ int swap(int row) {
-        if constexpr (kSpan == 64) return 4 * ((row >> 1) & 1) + ((row >> 2) & 3);
-        else return 4 * (row & 3) + ((row >> 2) & 3);
+        const int x = (row >> 2) & 3, low = (((x ^ (x >> 1)) & 1) << 1) + (x >> 1);
+        return 4 * (kSpan == 64 ? (row >> 1) & 1 : row & 3) + low;
     }
     // Element offset of four elements (col a multiple of 4).
     static __device__ __forceinline__ int quad(int row, int col) {
@@ -213,8 +217,11 @@ struct LdsTile {
     // A 16-byte vector of a row in memory.
     static __device__ __forceinline__ void put(raw* m, int row, int col, const u32x4& v) {
         if constexpr (kSwap) {
-            *reinterpret_cast<u32x2*>(m + quad(row, col)) = u32x2{v[0], v[1]};
-            *reinterpret_cast<u32x2*>(m + quad(row, col + 4)) = u32x2{v[2], v[3]};
+            // the rows that share banks start with different halves
+            const bool odd = kSpan == 64 ? row & 2 : row & 1;
+            const u32x2 a{v[0], v[1]}, b{v[2], v[3]};
+            *reinterpret_cast<u32x2*>(m + quad(row, col + (odd ? 4 : 0))) = odd ? b : a;
+            *reinterpret_cast<u32x2*>(m + quad(row, col + (odd ? 0 : 4))) = odd ? a : b;
         } else {
             *reinterpret_cast<u32x4*>(m + quad(row, col)) = v;
         }
@@ -305,13 +312,6 @@ struct TileRegs {
         for (int n = 0; n < N; ++n) T::put(lds, row + n * STEP, col, r[n]);
     }
 };
-
-// The same value, computed on from where this stands: sums of it with a row's offset are made where they are used and
-// not kept in registers over the chunks (48 of them, which spilled).
-__device__ __forceinline__ uint32_t here(uint32_t v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
 
 // One element of a result tile's place.
 template <typename E>

@@ -104,12 +104,12 @@ DeltaSpace delta_space(const gated_delta_inputs& s) {
     d.pack_k = !in_place(s.k, true, s.seqlen, s.dk, s.dtype, s.k_batch, s.k_token, s.k_head);
     d.pack_v = !in_place(s.v, false, s.seqlen, s.dv, s.dtype, s.v_batch, s.v_token, s.v_head);
     d.vecs = round_up(size_t(n) * mat, 256);
-    d.q = d.vecs + round_up(size_t(n) * 3 * C * 4, 256);
+    d.q = d.vecs + round_up(size_t(n) * cls::kVecs * C * 4, 256);
     d.k = d.q + (d.pack_q ? keys : 0);
     d.v = d.k + (d.pack_k ? keys : 0);
     d.fwd = d.v + (d.pack_v ? values : 0);
     const size_t states = round_up(size_t(n) * s.dk * s.dv * 4, 256);
-    const size_t tokens = round_up(size_t(rows * s.heads) * s.dv * 4, 256);
+    const size_t tokens = round_up(size_t(n) * s.dv * C * 4, 256);
     const size_t parts = s.heads > s.kheads ? round_up(size_t(rows * s.heads) * s.dk * 4, 256) : 0;
     d.fixes = states;
     d.ckpt = states + tokens;
@@ -229,6 +229,7 @@ int gated_delta_fwd(const gated_delta_inputs* in, void* y, float* h_final, void*
     if (!workspace || workspace_bytes < s.fwd) return SSD_ERR_WORKSPACE;
     DeltaParams p = delta_params(*in, workspace, checkpoints, s);
     p.y = y;
+    p.vec_out = whole_vectors(y, in->dv, in->dtype);
     p.h_last = h_final;
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     int rc = delta_pack(*in, workspace, s, hs);
@@ -261,7 +262,8 @@ int gated_delta_bwd(const gated_delta_inputs* in, const gated_delta_grads* g, vo
     if (pack_dy) p.sdy = {in->seqlen * row, row, in->dv};
     else p.sdy = {g->dy_batch, in->seqlen > 1 ? g->dy_token : row, g->dy_head};
     p.vec_dy = whole_vectors(p.dy, in->dv, in->dtype, p.sdy.batch, p.sdy.token, p.sdy.head);
-    p.vec_out = aligned(g->dq, 16) && aligned(g->dk, 16);
+    p.vec_out = whole_vectors(g->dv, in->dv, in->dtype);
+    p.vec_dqk = aligned(g->dq, 16) && aligned(g->dk, 16);
     p.dh_last = g->dh_final;
     p.dq = g->dq; p.dk_ = g->dk; p.dv_ = g->dv; p.dg = g->dg; p.dbeta = g->dbeta; p.dh0 = g->dh0;
     p.dstates = reinterpret_cast<float*>(ws + s.dstates);

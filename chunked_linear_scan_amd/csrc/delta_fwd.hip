@@ -18,12 +18,10 @@ namespace {
 template <typename E, int DK, bool KEEP>
 __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) {
     typedef Mat<E> M;
-    typedef typename M::raw raw;
     typedef typename M::frag frag;
     constexpr int kParts = ChunkMats<E>::kParts, NM = kParts + 1;  // T - I in its parts, P
     typedef WalkLds<E, DK, NM> Lds;
     constexpr int C = M::kChunk, NT = C / 16, KT = DK / 16, KS = DK / 32;
-    constexpr uint32_t SZ = sizeof(raw);
     extern __shared__ __attribute__((aligned(16))) char lds[];
 
     const int nblk = (p.dv + kWalkCols - 1) / kWalkCols;
@@ -31,55 +29,30 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
     const int end = seq_end(p.seqlens, b, p.L), chunks = (end + C - 1) / C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= 4) {
-        walk_load<E, DK, NM>(p, lds, b, h, end, 0, 1, chunks);
+        const WalkColumns w{p.v, p.sv, p.y, bool(p.vec_v), bool(p.vec_out)};
+        walk_load<E, DK, NM>(p, w, lds, b, h, blk * kWalkCols, end, 0, 1, chunks);
         return;
     }
     const int l16 = lane16(), g4 = group4();
     const int n = blk * kWalkCols + wave * 16 + l16;  // the lane's column
-    const bool on = n < p.dv, wave_on = blk * kWalkCols + wave * 16 < p.dv;
-    const raw* V = static_cast<const raw*>(p.v) + b * p.sv.batch + h * p.sv.head;
-    const int64_t row = int64_t(p.H) * p.dv;  // of a token of y
-    const int64_t out = int64_t(b) * p.L * row + int64_t(h) * p.dv;
-    raw* Y = static_cast<raw*>(p.y) + out;
+    const bool wave_on = blk * kWalkCols + wave * 16 < p.dv;
 
     f32x4 S[KT];
     load_state<KT>(S, p.h0, int64_t(b) * p.H + h, n, p);
-    const LdsTile<E, DK> kt;
-    const LdsTile<E, C> mt;
-    const uint32_t vrow = uint32_t(p.sv.token) * SZ, yrow = uint32_t(row) * SZ;
-    const uint32_t ov = on ? 4 * g4 * vrow + n * SZ : kOutside, oy = on ? 4 * g4 * yrow + n * SZ : kOutside;
-    raw v[NT][4];
-    f32x4 R[NT];  // V of the chunk to come
-    const auto fetch = [&](int c) {
-        const Buffer bv = buffer(V + c * C * p.sv.token, (end - c * C) * p.sv.token * SZ);
-        const uint32_t at = here(ov);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[t][r] = load_one<E>(bv, at + (16 * t + r) * vrow);
-    };
-    // Loads are waited for where nothing was stored after them: the counter that a wave waits on counts both in turn.
-    const auto arrived = [&] {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) R[t][r] = E::get(v[t][r]);
-    };
-    if (chunks > 0) {
-        fetch(0);
-        arrived();
-    }
+    const typename Lds::KTile kt;
+    const typename Lds::MTile mt;
+    const typename Lds::XTile xt;
+    const int oy = 4 * g4 * Lds::YP + wave * 16 + l16;
 
     walk<Lds>(lds, chunks, [&](int c, const Lds& m) {
         if (!wave_on) return;
-        const int t0 = c * C;
-        if constexpr (KEEP)
-            keep_state<KT>(S, p.states, (int64_t(b) * p.nchunk + c) * p.H + h, on ? (4 * g4 * p.dv + n) * 4 : kOutside, p);
-        fetch(c + 1 < chunks ? c + 1 : c);
+        const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
+        const auto factors = [&](int which, int t) { return *reinterpret_cast<const f32x4*>(m.v + which * C + 16 * t + 4 * g4); };
+        if constexpr (KEEP) store_state<KT>(S, p.states, chunk, n, p);
 
         // K S and Q S; the operands of a step are read, and S is taken apart, while the one before is multiplied
-        f32x4 ks[NT], O[NT], e[NT], be[NT];
-        frag k[2][NT], q[2][NT];
+        f32x4 ks[NT], O[NT], R[NT], a[NT], e[NT];
+        frag k[2][NT], q[2][NT], v[NT / 2];
         Two<E> T[NT][NT / 2], st[2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -87,6 +60,10 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
             k[0][t] = kt.rows(m.k, t, 0);
             q[0][t] = kt.rows(m.q, t, 0);
         }
+#pragma unroll
+        for (int s = 0; s < NT / 2; ++s) v[s] = xt.cols(m.x, s, wave);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) a[t] = factors(kBeta, t);
         st[0] = two<E>(S[0], S[1]);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -100,8 +77,8 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
             } else {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    e[t] = *reinterpret_cast<const f32x4*>(m.v + 16 * t + 4 * g4);
-                    be[t] = *reinterpret_cast<const f32x4*>(m.v + 2 * C + 16 * t + 4 * g4);
+                    a[t] = factors(kBetaStart, t);
+                    e[t] = factors(kRead, t);
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -113,6 +90,12 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
             }
             fence();
             if (s + 1 < KS) st[at ^ 1] = two<E>(S[2 * s + 2], S[2 * s + 3]);
+            if (s == 0) {  // beta V
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) R[t][r] = a[t][r] * M::at(v[t / 2], 4 * (t & 1) + r);
+            }
             if constexpr (M::kSplit) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) ks[t] = M::mma(k[at][t], st[at].lo, ks[t]);
@@ -123,14 +106,14 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
 #pragma unroll
             for (int t = 0; t < NT; ++t) O[t] = M::mma(q[at][t], st[at].hi, O[t]);
             if (s + 1 < KS) {
-                interleave<3 * NT, 3>();
+                interleave<3 * NT, 4>();
                 fence();
             }
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) R[t][r] = be[t][r] * fmaf(-e[t][r], ks[t][r], R[t][r]);
+            for (int r = 0; r < 4; ++r) R[t][r] = fmaf(-a[t][r], ks[t][r], R[t][r]);
         // N = R + (T - I) R: tokens up to 32 (t / 2 + 1) reach tile t
         frag P[NT][NT / 2];
         f32x4 N[NT];
@@ -145,9 +128,9 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
         for (int t = 0; t < NT; ++t) {
             N[t] = R[t];
             O[t] *= e[t];
-            e[t] = *reinterpret_cast<const f32x4*>(m.v + C + 16 * t + 4 * g4);  // of the writes, from here on
+            e[t] = factors(kWrite, t);
         }
-        const float fade = m.v[C - 1];
+        const float fade = m.v[kStart * C + C - 1];
         frag kc[2][NT / 2];
 #pragma unroll
         for (int s = 0; s < NT / 2; ++s) kc[0][s] = kt.cols(m.k, s, 0);
@@ -175,17 +158,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
         }
         nn[NT / 2 - 1] = two<E>(N[NT - 2] * e[NT - 2], N[NT - 1] * e[NT - 1]);
         nf[NT / 2 - 1] = M::cvt(N[NT - 2], N[NT - 1]);
-        arrived();
         // the state, and beside it y
-        const Buffer by = buffer(Y + t0 * row, int64_t(p.L - t0) * row * SZ);
-        const uint32_t to = here(oy);
-        const auto put = [&](int t) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float y = t0 + C > end && t0 + 16 * t + 4 * g4 + r >= end ? 0.0f : p.scale * O[t][r];  // padding
-                store_one<E>(by, to + (16 * t + r) * yrow, y);
-            }
-        };
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
             if (t + 1 < KT) {
@@ -200,22 +173,14 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
             }
 #pragma unroll
             for (int s = 0; s < NT / 2; ++s) S[t] = mma2<E>(kc[t & 1][s], nn[s], S[t]);
-            if (t >= NT && t < 2 * NT) put(t - NT);
+            if (t >= NT && t < 2 * NT) put_column<E, Lds::YP>(m.y + oy, t - NT, O[t - NT]);
         }
 #pragma unroll
-        for (int t = KT >= 2 * NT ? NT : 0; t < NT; ++t) put(t);
-        if constexpr (KEEP) {
-            const Buffer bf = buffer(p.fixes + out + t0 * row, int64_t(p.L - t0) * row * 4);
-            const uint32_t of = here(on ? (4 * g4 * uint32_t(row) + n) * 4 : kOutside);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) store_one<ElemF32>(bf, of + (16 * t + r) * uint32_t(row) * 4, N[t][r]);
-        }
+        for (int t = KT >= 2 * NT ? NT : 0; t < NT; ++t) put_column<E, Lds::YP>(m.y + oy, t, O[t]);
+        if constexpr (KEEP) store_tokens<C>(N, p.fixes, chunk, n, p);
+        settle(S[KT - 1]);
     });
     if (p.h_last) store_state<KT>(S, p.h_last, int64_t(b) * p.H + h, n, p);
-    if (on)
-        for (int tok = chunks * C + g4; tok < p.L; tok += 4) Y[tok * row + n] = raw(0);
 }
 
 template <typename E, int DK, bool KEEP>

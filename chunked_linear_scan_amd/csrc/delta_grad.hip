@@ -29,26 +29,39 @@ __device__ __forceinline__ float sum_groups(float v) {
     return v + __shfl_xor(v, 32, 64);
 }
 
-// ROWS x 32 fp32 values of a matrix in memory, as parts of an operand in LDS.
-template <typename E, int ROWS, int THREADS>
+// 32 rows (of dv) of a matrix [dv, cols] of fp32 values, padded to COLS columns, held by the workgroup's threads between
+// memory and LDS, where they are an operand's parts.
+template <typename E, int COLS, int THREADS>
 struct Tile32 {
-    static constexpr int N = ROWS * 8 / THREADS;
-    static_assert(ROWS * 8 % THREADS == 0, "");
+    typedef LdsTile<E, COLS> Lds;
+    static constexpr int PER_ROW = COLS / 4, STEP = THREADS / PER_ROW, N = 32 / STEP;
+    static_assert(THREADS % PER_ROW == 0 && 32 % STEP == 0, "");
+    static constexpr int kPart = 32 * Lds::kPitch;
     f32x4 r[N];
-    __device__ __forceinline__ void load(const float* base, int64_t pitch, int rows, int col, int cols, bool vec) {
+    __device__ __forceinline__ void load(const float* m, int64_t dv, int row0, int cols) {
+        const Buffer b = buffer(m, dv * cols * 4);
+        const int col = threadIdx.x % PER_ROW * 4;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int at = threadIdx.x + n * THREADS, row = at >> 3, c = col + 4 * (at & 7);
-            r[n] = row < rows ? load4<ElemF32>(reinterpret_cast<const uint32_t*>(base + row * pitch), c, cols, vec)
-                              : f32x4{0, 0, 0, 0};
+            const int row = row0 + int(threadIdx.x) / PER_ROW + n * STEP;
+            const uint32_t at = uint32_t(row * cols + col) * 4;
+            if (cols % 4 == 0) {
+                r[n] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, int(col < cols ? at : kOutside), 0, 0));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[n][e] = as_float(load_one<ElemF32>(b, col + e < cols ? at + 4 * e : kOutside));
+            }
         }
     }
-    __device__ __forceinline__ void store(typename E::raw* to, int pitch, int lo) const {
+    __device__ __forceinline__ void store(typename E::raw* to) const {
+        const int col = threadIdx.x % PER_ROW * 4;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int at = threadIdx.x + n * THREADS;
-            put4<E>(to + (at >> 3) * pitch + 4 * (at & 7), lo, r[n]);
-        }
+        for (int n = 0; n < N; ++n) put4<E>(to + Lds::quad(int(threadIdx.x) / PER_ROW + n * STEP, col), kPart, r[n]);
+    }
+    // times a factor of each column
+    __device__ __forceinline__ void scale(const f32x4& f) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) r[n] *= f;
     }
     __device__ __forceinline__ float dot(const Tile32& o) const {
         float v = 0.0f;
@@ -60,35 +73,22 @@ struct Tile32 {
     }
 };
 
-// Rows of 32 elements in LDS (a tile of S, dS or N), padded by 16 bytes: the operands' reads touch every bank once.
-template <typename E>
-struct Rows32 {
-    typedef typename E::raw raw;
-    static constexpr int kPitch = 32 + 16 / int(sizeof(raw));
-    static __device__ __forceinline__ typename Mat<E>::frag one(const raw* m, int t) {
-        const raw* p = m + (16 * t + lane16()) * kPitch + 4 * group4();
-        if constexpr (Mat<E>::kSplit) {
-            const u32x2 a = *reinterpret_cast<const u32x2*>(p), b = *reinterpret_cast<const u32x2*>(p + 16);
-            return u32x4{a[0], a[1], b[0], b[1]};
-        } else {
-            return typename Mat<E>::frag{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16)};
-        }
-    }
-    static __device__ __forceinline__ Two<E> two(const raw* m, int t, int lo) {
-        Two<E> x;
-        x.hi = one(m, t);
-        if constexpr (Mat<E>::kSplit) x.lo = one(m + lo, t);
-        return x;
-    }
-};
+// 16 columns of such a tile as an operand.
+template <typename E, typename T>
+__device__ __forceinline__ Two<E> two_cols(const T& tile, const typename E::raw* m, int t) {
+    Two<E> x;
+    x.hi = tile.cols(m, 0, t);
+    if constexpr (Mat<E>::kSplit) x.lo = tile.cols(m + 32 * T::kPitch, 0, t);
+    return x;
+}
 
 template <typename E, int DK>
 struct GradSize {
     typedef Mat<E> M;
-    static constexpr int C = M::kChunk, KP = LdsTile<E, DK>::kPitch, SP = Rows32<E>::kPitch, MP = LdsTile<E, C>::kPitch;
+    static constexpr int C = M::kChunk, KP = LdsTile<E, DK>::kPitch, MP = LdsTile<E, C>::kPitch;
     static constexpr int kParts = ChunkMats<E>::kParts;
-    static constexpr int kTiles = kParts * (DK + C) * SP;  // a tile of S or dS, and of N
-    static constexpr int kPairs = 2 * C * MP;              // pB and pP, in the same place
+    static constexpr int kTiles = kParts * 32 * (KP + 2 * MP);  // tiles of S or dS, of N and of Z
+    static constexpr int kPairs = 2 * C * MP;                   // pB and pP, in the same place
     static constexpr int kUnion = kTiles > kPairs ? kTiles : kPairs;
     static constexpr size_t bytes = (2 * C * KP + kUnion) * sizeof(typename M::raw) + 9 * C * sizeof(float);
 };
@@ -98,12 +98,13 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     typedef Mat<E> M;
     typedef typename M::raw raw;
     typedef GradSize<E, DK> G;
-    constexpr int C = G::C, NT = C / 16, KT = DK / 16, THREADS = 64 * NT, KP = G::KP, SP = G::SP, MP = G::MP;
+    constexpr int C = G::C, NT = C / 16, KT = DK / 16, THREADS = 64 * NT, KP = G::KP, MP = G::MP;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     raw* sK = reinterpret_cast<raw*>(lds);
     raw* sQ = sK + C * KP;
     raw* sS = sQ + C * KP;
-    raw* sN = sS + G::kParts * DK * SP;
+    raw* sN = sS + G::kParts * 32 * KP;
+    raw* sZ = sN + G::kParts * 32 * MP;
     raw* sB = sS;  // once the tiles are done with
     raw* sP = sB + C * MP;
     float* sG = reinterpret_cast<float*>(sS + G::kUnion);
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
                 for (int e = 0; e < 4; ++e)
                     if (d + e < p.dk) part[d + e] = v[e];
             }
-        } else if (p.dk % 4 == 0 && p.vec_out) {
+        } else if (p.dk % 4 == 0 && p.vec_dqk) {
             if (d < p.dk) put4<E>(one + d, 0, v);
         } else {
 #pragma unroll
@@ -153,18 +154,15 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     }
 
     const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
-    const float* vecs = p.vecs + chunk * 3 * C;
-    const float start = vecs[i], after = vecs[C + i], beta = vecs[2 * C + i], fade = vecs[C - 1];
+    const float* vecs = p.vecs + chunk * kVecs * C;
+    const float start = vecs[kStart * C + i], beta = vecs[kBeta * C + i], fade = vecs[kStart * C + C - 1];
     const float* S0 = p.states + chunk * p.dk * p.dv;
     const float* dS = p.dstates + chunk * p.dk * p.dv;
-    const int64_t row = int64_t(p.H) * p.dv;
-    const float* N = p.fixes + ((int64_t(b) * p.L + t0) * p.H + h) * p.dv;
-    const uint32_t* Ni = reinterpret_cast<const uint32_t*>(N + i * row);
-    const uint32_t* Zi = reinterpret_cast<const uint32_t*>(p.z + ((int64_t(b) * p.L + tok) * p.H + h) * p.dv);
+    const float* N = p.fixes + chunk * p.dv * C;
+    const float* Z = p.z + chunk * p.dv * C;
     const raw* Yi = static_cast<const raw*>(p.dy) + b * p.sdy.batch + h * p.sdy.head + tok * p.sdy.token;
     const raw* Vi = static_cast<const raw*>(p.v) + b * p.sv.batch + h * p.sv.head + tok * p.sv.token;
     const int left = end - t0 < C ? end - t0 : C;  // tokens of the chunk
-    const bool v4 = p.dv % 4 == 0;                 // rows of states, N and Z are whole vectors
     typedef LdsTile<E, DK> KTile;
     typedef LdsTile<E, C> MTile;
     const KTile kt;
@@ -188,41 +186,49 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
 #pragma unroll
     for (int t = 0; t < NT; ++t) dP[t] = Mz[t] = f32x4{0, 0, 0, 0};
     float zv = 0.0f;  // Z_i.V_i
-    Tile32<E, DK, THREADS> rs;
-    Tile32<E, C, THREADS> rn;
-    rs.load(S0, p.dv, p.dk, 0, p.dv, v4);
-    rn.load(N, row, left, 0, p.dv, v4);
+    typedef Tile32<E, DK, THREADS> STile;
+    typedef Tile32<E, C, THREADS> NTile;
+    STile rs;
+    NTile rn, rz;
+    rs.load(S0, p.dv, 0, p.dk);
+    rn.load(N, p.dv, 0, C);
+    rz.load(Z, p.dv, 0, C);
     for (int d0 = 0; d0 < p.dv; d0 += 32) {
         __syncthreads();
-        rs.store(sS, SP, DK * SP);
-        rn.store(sN, SP, C * SP);
-        f32x4 z[2], y[2];
+        rs.store(sS);
+        rn.store(sN);
+        rz.store(sZ);
+        f32x4 y[2], v[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int col = d0 + 16 * u + 4 * g4;
-            z[u] = in ? load4<ElemF32>(Zi, col, p.dv, v4) : f32x4{0, 0, 0, 0};
             y[u] = in ? load4<E>(Yi, col, p.dv, p.vec_dy) : f32x4{0, 0, 0, 0};
-            const f32x4 v = in ? load4<E>(Vi, col, p.dv, p.vec_v) : f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) zv = fmaf(z[u][e], v[e], zv);
+            v[u] = in ? load4<E>(Vi, col, p.dv, p.vec_v) : f32x4{0, 0, 0, 0};
         }
         __syncthreads();
         if (d0 + 32 < p.dv) {
-            rs.load(S0, p.dv, p.dk, d0 + 32, p.dv, v4);
-            rn.load(N, row, left, d0 + 32, p.dv, v4);
+            rs.load(S0, p.dv, d0 + 32, p.dk);
+            rn.load(N, p.dv, d0 + 32, C);
+            rz.load(Z, p.dv, d0 + 32, C);
         }
-        const Two<E> zf = two<E>(z[0], z[1]);
+        const Two<E> zf = two_cols<E>(mt, sZ, w);
         const typename M::frag yf = M::cvt(y[0], y[1]);  // exact
 #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float z = M::at(zf.hi, e);
+            if constexpr (M::kSplit) z += M::at(zf.lo, e);
+            zv = fmaf(z, v[e >> 2][e & 3], zv);
+        }
+#pragma unroll
         for (int t = 0; t < KT; ++t) {
-            const Two<E> s = Rows32<E>::two(sS, t, DK * SP);
+            const Two<E> s = two_cols<E>(kt, sS, t);
             X1[t] = mma2<E>(s, yf, X1[t]);
             X2[t] = mma3<E>(s, zf, X2[t]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (t > w) break;
-            const Two<E> nj = Rows32<E>::two(sN, t, C * SP);
+            const Two<E> nj = two_cols<E>(mt, sN, t);
             dP[t] = mma2<E>(nj, yf, dP[t]);
             Mz[t] = mma3<E>(nj, zf, Mz[t]);
         }
@@ -248,24 +254,25 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     // with the gradient of the state behind it: + dS (e^(gamma_C - gamma) N)^T, and <S, dS>
     float both = 0.0f;
     {
-        Tile32<E, DK, THREADS> r0;
-        rs.load(dS, p.dv, p.dk, 0, p.dv, v4);
+        STile r0;
+        const f32x4 after = *reinterpret_cast<const f32x4*>(vecs + kWrite * C + threadIdx.x % NTile::PER_ROW * 4);
+        rs.load(dS, p.dv, 0, p.dk);
+        rn.load(N, p.dv, 0, C);
         for (int d0 = 0; d0 < p.dv; d0 += 32) {
-            r0.load(S0, p.dv, p.dk, d0, p.dv, v4);
+            r0.load(S0, p.dv, d0, p.dk);
             __syncthreads();
-            rs.store(sS, SP, DK * SP);
+            rs.store(sS);
+            rn.scale(after);
+            rn.store(sN);
             both += rs.dot(r0);
-            f32x4 x[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                x[u] = in ? load4<ElemF32>(Ni, d0 + 16 * u + 4 * g4, p.dv, v4) : f32x4{0, 0, 0, 0};
-                x[u] *= after;
-            }
             __syncthreads();
-            if (d0 + 32 < p.dv) rs.load(dS, p.dv, p.dk, d0 + 32, p.dv, v4);
-            const Two<E> nf = two<E>(x[0], x[1]);
+            if (d0 + 32 < p.dv) {
+                rs.load(dS, p.dv, d0 + 32, p.dk);
+                rn.load(N, p.dv, d0 + 32, C);
+            }
+            const Two<E> nf = two_cols<E>(mt, sN, w);
 #pragma unroll
-            for (int t = 0; t < KT; ++t) X2[t] = mma3<E>(Rows32<E>::two(sS, t, DK * SP), nf, X2[t]);
+            for (int t = 0; t < KT; ++t) X2[t] = mma3<E>(two_cols<E>(kt, sS, t), nf, X2[t]);
         }
     }
     const float write = dot_row(sK, X2) + beta * kx;

@@ -4,8 +4,9 @@
 // here are T - I, T = (I + A)^-1, P_ij = D_ij q_i.k_j (j <= i) and the factors
 // e^gamma_i and e^(gamma_C - gamma_j) of reads and writes of the state.  The ones
 // of T's diagonal are left out so that what they multiply stays in fp32 (with two
-// bf16 numbers to an operand half of the states' error came from them), and the
-// scale, so that with fp16 fewer entries are subnormal.
+// bf16 numbers to an operand half of the states' error came from them).  For the
+// forward pass P is multiplied by the scale; for the backward pass, which takes it
+// in two parts, it is not, so that with fp16 fewer entries are subnormal.
 //
 // T by blocks: the 16x16 diagonal blocks by forward substitution (a column to a
 // lane, in registers), then T10 = -T11 A10 T00 for pairs of blocks and pairs of
@@ -97,24 +98,28 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
             if (part < p_parts)
                 put4<E>(P + part * ChunkMats<E>::kSize + i * C + 16 * (w + 1) + 4 * g4, 0, f32x4{0, 0, 0, 0});
     }
+    const float scale = p_parts > 1 ? 1.0f : p.scale;
     const float sum = for_decays<NT>(sG, w, [&](int t, const f32x4& d) {
         f32x4 a, q;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int j = 16 * t + 4 * g4 + r;
             a[r] = j < i ? beta * d[r] * kk[t][r] : 0.0f;
-            q[r] = j <= i ? d[r] * qk[t][r] : 0.0f;
+            q[r] = j <= i ? scale * d[r] * qk[t][r] : 0.0f;
         }
         *reinterpret_cast<f32x4*>(sA + i * AP + 16 * t + 4 * g4) = a;
         put4<E>(P + i * C + 16 * t + 4 * g4, p_parts > 1 ? ChunkMats<E>::kSize : 0, q);
     });
     if (g4 == 0) {
-        float* vecs = p.vecs + chunk * 3 * C;
-        vecs[i] = fexp(sum);
+        float* vecs = p.vecs + chunk * kVecs * C;
         float after = 0.0f;
         for (int l = i + 1; l < C; ++l) after += sG[l];
-        vecs[C + i] = fexp(after);
-        vecs[2 * C + i] = beta;
+        const float start = fexp(sum);
+        vecs[kRead * C + i] = p.scale * start;
+        vecs[kWrite * C + i] = fexp(after);
+        vecs[kBeta * C + i] = beta;
+        vecs[kBetaStart * C + i] = beta * start;
+        vecs[kStart * C + i] = start;
     }
     __syncthreads();
 

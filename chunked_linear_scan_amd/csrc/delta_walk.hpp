@@ -1,9 +1,10 @@
 // What the forward and the backward walk over the chunks share: a workgroup of
 // four waves that compute, 16 columns of a state each, and four that load.  The
 // computing waves' work on a chunk is one long chain of products, so what
-// bounds a walk is that chain's latency: the loading waves keep the loads and
-// stores into LDS (56 registers and 60 instructions a chunk) out of it, and the registers that this
-// frees hold the next operands while a product runs.
+// bounds a walk is that chain's latency: the loading waves keep the traffic with memory
+// (but for kept states) out of it, and the registers that this
+// frees hold the next operands while a product runs.  V (or dY) comes and y (or
+// dV) leaves through LDS as whole rows, too.
 #pragma once
 
 #include "delta.hpp"
@@ -26,28 +27,53 @@ __device__ __forceinline__ void interleave() {
 }
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// LDS of a walk: K, Q, NM matrices of a chunk and its factors, twice where that fits.
+// Lets the last product's result be written: the compiler's copies of it at a loop's end (v_mov_b64) were seen two
+// instructions behind the product, without the wait for its last two registers.
+__device__ __forceinline__ void settle(f32x4& x) {
+    float a = x[0], b = x[1], c = x[2], d = x[3];
+    asm volatile("s_nop 15" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+    x = f32x4{a, b, c, d};
+}
+
+// LDS of a walk: K, Q, NM matrices of a chunk, 64 columns of V and its factors, and 64 of y; twice where that fits.
 template <typename E, int DK, int NM>
 struct WalkLds {
     typedef typename Mat<E>::raw raw;
+    typedef LdsTile<E, DK> KTile;
+    typedef LdsTile<E, Mat<E>::kChunk> MTile;
+    typedef LdsTile<E, kWalkCols> XTile;
     static constexpr int C = Mat<E>::kChunk;
-    static constexpr int KS = C * LdsTile<E, DK>::kPitch, MS = C * LdsTile<E, C>::kPitch;
-    static constexpr int kBuffer = int((2 * KS + NM * MS) * sizeof(raw) + 3 * C * sizeof(float));
-    static constexpr bool kTwice = 2 * kBuffer <= 160 * 1024;
-    static constexpr int kBytes = kTwice ? 2 * kBuffer : kBuffer;
-    raw *k, *q, *m;
-    float* v;  // e^gamma, e^(gamma_C - gamma), beta
+    static constexpr int KS = C * KTile::kPitch, MS = C * MTile::kPitch, XS = C * XTile::kPitch;
+    static constexpr int YP = kWalkCols + 16 / int(sizeof(raw));  // pitch of y: four rows touch every bank once
+    static constexpr int kBuffer = int((2 * KS + NM * MS + XS) * sizeof(raw) + kVecs * C * sizeof(float));
+    static constexpr int kOut = C * YP * int(sizeof(raw));
+    static constexpr bool kTwice = 2 * (kBuffer + kOut) <= 160 * 1024;
+    static constexpr int kBytes = (kTwice ? 2 : 1) * (kBuffer + kOut);
+    raw *k, *q, *m, *x, *y;
+    float* v;
     __device__ __forceinline__ WalkLds(char* lds, int at) {
-        k = reinterpret_cast<raw*>(lds + (kTwice ? (at & 1) * kBuffer : 0));
+        const int one = kTwice ? at & 1 : 0;
+        k = reinterpret_cast<raw*>(lds + one * kBuffer);
         q = k + KS;
         m = q + KS;
-        v = reinterpret_cast<float*>(m + NM * MS);
+        x = m + NM * MS;
+        v = reinterpret_cast<float*>(x + XS);
+        y = reinterpret_cast<raw*>(lds + (kTwice ? 2 : 1) * kBuffer + one * kOut);
     }
+};
+
+// 64 columns of V or dY in, of y or dV out.
+struct WalkColumns {
+    const void* x;
+    Strided3 sx;
+    void* y;
+    bool vec_x, vec_y;
 };
 
 // The loading waves' part: chunks first, first + step, .. (n of them).
 template <typename E, int DK, int NM>
-__device__ __forceinline__ void walk_load(const DeltaParams& p, char* lds, int b, int h, int end, int first, int step, int n) {
+__device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumns& w, char* lds, int b, int h, int col0, int end,
+                                          int first, int step, int n) {
     typedef Mat<E> M;
     typedef typename M::raw raw;
     typedef ChunkMats<E> CM;
@@ -56,16 +82,23 @@ __device__ __forceinline__ void walk_load(const DeltaParams& p, char* lds, int b
     constexpr int64_t SZ = sizeof(raw);
     typedef TileRegs<E, C, DK, THREADS> KRegs;
     typedef TileRegs<E, C, C, THREADS> MRegs;
+    typedef TileRegs<E, C, kWalkCols, THREADS> XRegs;
     const int kh = h / (p.H / p.Hk), tid = threadIdx.x % THREADS;
     const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + kh * p.sk.head;
     const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + kh * p.sq.head;
+    const raw* X = static_cast<const raw*>(w.x) + b * w.sx.batch + h * w.sx.head + col0;
+    const int cols = p.dv - col0 < kWalkCols ? p.dv - col0 : kWalkCols;
     const uint32_t ok = KRegs::offset(p.sk.token, p.dk), oq = KRegs::offset(p.sq.token, p.dk), om = MRegs::offset(C, C);
-    // two chunks in flight: a chunk takes less time than a load from memory
+    const uint32_t ox = XRegs::offset(w.sx.token, cols);
+    // Two chunks in flight: a chunk may take less time than a load from memory.  (One where LDS holds one: dk above 128,
+    // whose chunks are longer and whose vectors would be twice as many.)
+    constexpr int SETS = Lds::kTwice ? 2 : 1;
     struct Set {
         KRegs k, q;
         MRegs m[NM];
-        float v;
-    } set[2];
+        XRegs x;
+        u32x4 v;
+    } set[SETS];
     const auto fetch = [&](Set& r, int i) {
         const int c = first + i * step, t0 = c * C, left = end - t0;
         r.k.load(buffer(K + t0 * p.sk.token, left * p.sk.token * SZ), ok, p.sk.token);
@@ -74,54 +107,98 @@ __device__ __forceinline__ void walk_load(const DeltaParams& p, char* lds, int b
         const raw* mats = static_cast<const raw*>(p.mats) + chunk * CM::kAll * CM::kSize;
 #pragma unroll
         for (int m = 0; m < NM; ++m) r.m[m].load(buffer(mats + m * CM::kSize), om, C);
-        r.v = p.vecs[chunk * 3 * C + (tid < 3 * C ? tid : 0)];
+        const Buffer bx = buffer(X + t0 * w.sx.token, left * w.sx.token * SZ - col0 * SZ);
+        if (w.vec_x) {
+            r.x.load(bx, ox, w.sx.token);
+        } else {
+#pragma unroll
+            for (int v = 0; v < XRegs::N; ++v) {
+                const int at = tid + v * THREADS, row = at / XRegs::PER_ROW, col = at % XRegs::PER_ROW * XRegs::VE;
+                r.x.r[v] = u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < XRegs::VE; ++e) {
+                    const uint32_t one = load_one<E>(bx, col + e < cols ? uint32_t((row * w.sx.token + col + e) * SZ) : kOutside);
+                    if constexpr (SZ == 4) r.x.r[v][e] = one;
+                    else r.x.r[v][e >> 1] |= one << (16 * (e & 1));
+                }
+            }
+        }
+        r.v = ldg_b128(p.vecs + chunk * kVecs * C + 4 * (tid < kVecs * C / 4 ? tid : 0));
     };
     const auto put = [&](const Set& r, int i) {
         const Lds to(lds, i);
-        r.k.template store<LdsTile<E, DK>>(to.k);
-        r.q.template store<LdsTile<E, DK>>(to.q);
+        r.k.template store<typename Lds::KTile>(to.k);
+        r.q.template store<typename Lds::KTile>(to.q);
 #pragma unroll
-        for (int m = 0; m < NM; ++m) r.m[m].template store<LdsTile<E, C>>(to.m + m * Lds::MS);
-        if (tid < 3 * C) to.v[tid] = r.v;
+        for (int m = 0; m < NM; ++m) r.m[m].template store<typename Lds::MTile>(to.m + m * Lds::MS);
+        r.x.template store<typename Lds::XTile>(to.x);
+        if (tid < kVecs * C / 4) *reinterpret_cast<u32x4*>(to.v + 4 * tid) = r.v;
+    };
+    const int64_t row = int64_t(p.H) * p.dv;  // of a token of y
+    raw* Y = static_cast<raw*>(w.y) + int64_t(b) * p.L * row + int64_t(h) * p.dv + col0;
+    const auto out = [&](int i) {
+        const Lds from(lds, i);
+        const int t0 = (first + i * step) * C;
+        const Buffer by = buffer(Y + t0 * row, int64_t(p.L - t0) * row * SZ - (int64_t(h) * p.dv + col0) * SZ);
+#pragma unroll
+        for (int v = 0; v < XRegs::N; ++v) {
+            const int at = tid + v * THREADS, r = at / XRegs::PER_ROW, col = at % XRegs::PER_ROW * XRegs::VE;
+            u32x4 x = *reinterpret_cast<const u32x4*>(from.y + r * Lds::YP + col);
+            if (t0 + r >= end) x = u32x4{0, 0, 0, 0};  // padding
+            const uint32_t to = uint32_t((r * row + col) * SZ);
+            if (w.vec_y) {
+                __builtin_amdgcn_raw_buffer_store_b128(x, by, int(col < cols ? to : kOutside), 0, 0);
+            } else {
+#pragma unroll
+                for (int e = 0; e < XRegs::VE; ++e) {
+                    const uint32_t word = x[SZ == 4 ? e : e >> 1], at2 = col + e < cols ? to + uint32_t(e * SZ) : kOutside;
+                    if constexpr (SZ == 4) __builtin_amdgcn_raw_buffer_store_b32(word, by, int(at2), 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b16(uint16_t(word >> (16 * (e & 1))), by, int(at2), 0, 0);
+                }
+            }
+        }
     };
     const auto last = [&](int i) { return i < n ? i : n - 1; };  // past the end: loaded again, not used
-    if (n == 0) {
-        if (Lds::kTwice) lds_meet();
-        return;
-    }
-    fetch(set[0], 0);
-    fetch(set[1], last(1));
-    if constexpr (Lds::kTwice) {
-        put(set[0], 0);
-        fetch(set[0], last(2));
-        lds_meet();
-        for (int i = 0; i < n; i += 2) {
-            if (i + 1 < n) put(set[1], i + 1);
-            fetch(set[1], last(i + 3));
+    if (n > 0) {
+        fetch(set[0], 0);
+        if constexpr (Lds::kTwice) {
+            // while chunk i is computed: y of the one before leaves, the one behind it comes
+            fetch(set[1], last(1));
+            put(set[0], 0);
+            fetch(set[0], last(2));
             lds_meet();
-            if (i + 1 == n) break;
-            if (i + 2 < n) put(set[0], i + 2);
-            fetch(set[0], last(i + 4));
+            for (int i = 0; i < n; i += 2) {
+                if (i > 0) out(i - 1);
+                if (i + 1 < n) put(set[1], i + 1);
+                fetch(set[1], last(i + 3));
+                lds_meet();
+                if (i + 1 == n) break;
+                out(i);
+                if (i + 2 < n) put(set[0], i + 2);
+                fetch(set[0], last(i + 4));
+                lds_meet();
+            }
+        } else {
+            for (int i = 0; i < n; ++i) {
+                lds_meet();
+                if (i > 0) out(i - 1);
+                put(set[0], i);
+                lds_meet();
+                fetch(set[0], last(i + 1));
+            }
             lds_meet();
         }
-    } else {
-        for (int i = 0; i < n; i += 2) {
-            lds_meet();
-            put(set[0], i);
-            lds_meet();
-            if (i + 1 == n) break;
-            fetch(set[0], last(i + 2));
-            lds_meet();
-            put(set[1], i + 1);
-            lds_meet();
-            fetch(set[1], last(i + 3));
-        }
+        out(n - 1);
     }
+    // whole chunks of padding
+    const int64_t t1 = (end + C - 1) / C * C;
+    for (int64_t at = tid; at < (p.L - t1) * cols; at += THREADS) Y[(t1 + at / cols) * row + at % cols] = raw(0);
 }
 
 // The computing waves' part: f(i, lds) for every chunk that the loading waves bring.
 template <typename Lds, typename F>
 __device__ __forceinline__ void walk(char* lds, int n, F&& f) {
+    if (n == 0) return;
     if constexpr (Lds::kTwice) {
         lds_meet();
         for (int i = 0; i < n; ++i) {
@@ -134,11 +211,12 @@ __device__ __forceinline__ void walk(char* lds, int n, F&& f) {
             lds_meet();
             f(i, Lds(lds, i));
         }
+        lds_meet();
     }
 }
 
 // A lane's part of a state [dv, dk] in memory: column n, rows 4 (l/16) + r of each tile; `of` is the state's place
-// among those of all sequences and heads.
+// among those of all sequences and heads (and chunks).
 template <int KT>
 __device__ __forceinline__ void load_state(f32x4 (&S)[KT], const float* from, int64_t of, int n, const DeltaParams& p) {
 #pragma unroll
@@ -183,15 +261,30 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[KT], float* to, int
         }
     }
 }
-// The same as a chunk's [dk, dv] for the kernel of the gradients.
-template <int KT>
-__device__ __forceinline__ void keep_state(const f32x4 (&S)[KT], float* states, int64_t chunk, uint32_t offset, const DeltaParams& p) {
-    const Buffer b = buffer(states + chunk * p.dk * p.dv, int64_t(p.dk) * p.dv * 4);
-    const uint32_t at = here(offset);
+// A column's values of the chunk's tokens: [dv, C].
+template <int C>
+__device__ __forceinline__ void store_tokens(const f32x4 (&x)[C / 16], float* to, int64_t chunk, int n, const DeltaParams& p) {
+    const Buffer b = buffer(to + chunk * p.dv * C, int64_t(p.dv) * C * 4);
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int t = 0; t < C / 16; ++t)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x[t]), b,
+                                               int(n < p.dv ? uint32_t(n * C + 16 * t + 4 * group4()) * 4 : kOutside), 0, 0);
+}
+
+// A result tile's rows to a column of y in LDS.
+template <typename E, int YP>
+__device__ __forceinline__ void put_column(typename E::raw* y, int t, const f32x4& v) {
+    typename E::raw* to = y + 16 * t * YP;
+    if constexpr (Mat<E>::kSplit) {
+        const uint32_t a = Mat<E>::pack(v[0], v[1]), b = Mat<E>::pack(v[2], v[3]);
+        to[0] = uint16_t(a);
+        to[YP] = uint16_t(a >> 16);
+        to[2 * YP] = uint16_t(b);
+        to[3 * YP] = uint16_t(b >> 16);
+    } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) store_one<ElemF32>(b, at + uint32_t((16 * t + r) * p.dv) * 4, S[t][r]);
+        for (int r = 0; r < 4; ++r) to[r * YP] = E::put(v[r]);
+    }
 }
 
 }  // namespace cls

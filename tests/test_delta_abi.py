@@ -179,8 +179,8 @@ def test_delta_sizes_add_up():
     for dtype, C, mat in ((1, 64, 4 * 64 * 64 * 2), (0, 32, 2 * 32 * 32 * 4)):
         s = delta_in(dtype=dtype)
         chunks = 2 * 4 * -(-200 // C)
-        fwd = up(chunks * mat) + up(chunks * 3 * C * 4)
-        states, tokens = up(chunks * 64 * 48 * 4), up(2 * 200 * 4 * 48 * 4)
+        fwd = up(chunks * mat) + up(chunks * 5 * C * 4)
+        states, tokens = up(chunks * 64 * 48 * 4), up(chunks * C * 48 * 4)
         size = 4 if dtype == 0 else 2
         keys, values = up(2 * 200 * 2 * 64 * size), up(2 * 200 * 4 * 48 * size)
         assert lib.gated_delta_workspace_size(ctypes.byref(s)) == fwd
@@ -192,7 +192,7 @@ def test_delta_sizes_add_up():
                           (dict(seqlen=1, q_token=0, k_token=0, v_token=0), None)):
             s = delta_in(dtype=dtype, **bad)
             if more is None:
-                assert lib.gated_delta_workspace_size(ctypes.byref(s)) == up(8 * mat) + up(8 * 3 * C * 4)
+                assert lib.gated_delta_workspace_size(ctypes.byref(s)) == up(8 * mat) + up(8 * 5 * C * 4)
             else:
                 assert lib.gated_delta_workspace_size(ctypes.byref(s)) == fwd + more, bad
         s = delta_in(dtype=dtype, kheads=4)
