@@ -287,7 +287,7 @@ __device__ __forceinline__ Buffer buffer(const void* p, int64_t bytes = kOutside
 }
 
 // A tile of ROWS tokens of a matrix with whole 16-byte vectors in its rows, padded to DIM columns, held by THREADS
-// threads (the workgroup's or its last ones) between memory and LDS.
+// threads between memory and LDS.
 template <typename E, int ROWS, int DIM, int THREADS>
 struct TileRegs {
     typedef typename E::raw raw;
@@ -296,18 +296,21 @@ struct TileRegs {
     u32x4 r[N];
 
     // The offset of a thread's first vector, for rows `pitch` elements apart of `dim` columns.
-    static __device__ __forceinline__ uint32_t offset(int64_t pitch, int dim) {
-        const int at = threadIdx.x % THREADS, row = at / PER_ROW, col = at % PER_ROW * VE;
+    static __device__ __forceinline__ uint32_t offset(int64_t pitch, int dim, int tid) {
+        const int row = tid / PER_ROW, col = tid % PER_ROW * VE;
         return col < dim ? uint32_t((row * pitch + col) * sizeof(raw)) : kOutside;
     }
-    __device__ __forceinline__ void load(Buffer b, uint32_t offset, int64_t pitch) {
+    __device__ __forceinline__ void load(Buffer b, uint32_t offset, int64_t pitch) { load(b, offset, pitch, offset); }
+    // `first`: the offset for rows before 32.
+    __device__ __forceinline__ void load(Buffer b, uint32_t offset, int64_t pitch, uint32_t first) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            r[n] = __builtin_amdgcn_raw_buffer_load_b128(b, int(offset + uint32_t(n * STEP * pitch * sizeof(raw))), 0, 0);
+            r[n] = __builtin_amdgcn_raw_buffer_load_b128(
+                b, int((n * STEP < 32 ? first : offset) + uint32_t(n * STEP * pitch * sizeof(raw))), 0, 0);
     }
     template <typename T>
-    __device__ __forceinline__ void store(raw* lds) const {
-        const int at = threadIdx.x % THREADS, row = at / PER_ROW, col = at % PER_ROW * VE;
+    __device__ __forceinline__ void store(raw* lds, int tid) const {
+        const int row = tid / PER_ROW, col = tid % PER_ROW * VE;
 #pragma unroll
         for (int n = 0; n < N; ++n) T::put(lds, row + n * STEP, col, r[n]);
     }

@@ -13,27 +13,28 @@
 namespace cls {
 namespace {
 
-template <typename E, int DK>
-__global__ __launch_bounds__(kWalkThreads) void delta_bwd_kernel(DeltaParams p) {
+template <typename E, int DK, int WAVES>
+__global__ __launch_bounds__(64 * (WAVES + 4), 2) void delta_bwd_kernel(DeltaParams p) {
     typedef Mat<E> M;
     typedef typename M::frag frag;
     constexpr int kParts = ChunkMats<E>::kParts, NM = ChunkMats<E>::kAll;  // T - I, P, in their parts
-    typedef WalkLds<E, DK, NM> Lds;
+    typedef WalkLds<E, DK, NM, WAVES> Lds;
     constexpr int C = M::kChunk, NT = C / 16, KT = DK / 16, KS = DK / 32;
+    constexpr bool AHEAD = DK <= 128;  // operands are read a step before their products: registers for it
     extern __shared__ __attribute__((aligned(16))) char lds[];
 
-    const int nblk = (p.dv + kWalkCols - 1) / kWalkCols;
+    const int nblk = (p.dv + Lds::kCols - 1) / Lds::kCols;
     const int blk = blockIdx.x % nblk, h = blockIdx.x / nblk % p.H, b = blockIdx.x / nblk / p.H;
     const int end = seq_end(p.seqlens, b, p.L), chunks = (end + C - 1) / C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave >= 4) {
+    if (wave >= WAVES) {
         const WalkColumns w{p.dy, p.sdy, p.dv_, bool(p.vec_dy), bool(p.vec_out)};
-        walk_load<E, DK, NM>(p, w, lds, b, h, blk * kWalkCols, end, chunks - 1, -1, chunks);
+        walk_load<E, DK, NM, WAVES>(p, w, lds, b, h, blk * Lds::kCols, end, chunks - 1, -1, chunks);
         return;
     }
     const int l16 = lane16(), g4 = group4();
-    const int n = blk * kWalkCols + wave * 16 + l16;  // the lane's column
-    const bool wave_on = blk * kWalkCols + wave * 16 < p.dv;
+    const int n = blk * Lds::kCols + wave * 16 + l16;  // the lane's column
+    const bool wave_on = blk * Lds::kCols + wave * 16 < p.dv;
 
     f32x4 S[KT];
     load_state<KT>(S, p.dh_last, int64_t(b) * p.H + h, n, p);
@@ -55,17 +56,17 @@ __global__ __launch_bounds__(kWalkThreads) void delta_bwd_kernel(DeltaParams p) 
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             dN[t] = later[t] = f32x4{0, 0, 0, 0};
-            k[0][t] = kt.rows(m.k, t, 0);
+            if (AHEAD) k[0][t] = kt.rows(m.k, t, 0);
         }
 #pragma unroll
         for (int s = 0; s < NT / 2; ++s) y[s] = xt.cols(m.x, s, wave);
         st[0] = two<E>(S[0], S[1]);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const int at = s & 1;
-            if (s + 1 < KS) {
+            const int at = AHEAD ? s & 1 : 0, at1 = AHEAD ? at ^ 1 : 0;
+            if (!AHEAD || s + 1 < KS) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) k[at ^ 1][t] = kt.rows(m.k, t, s + 1);
+                for (int t = 0; t < NT; ++t) k[at1][t] = kt.rows(m.k, t, AHEAD ? s + 1 : s);
             }
             if (s < NT / 2) {  // P of outputs 32 s.., which reach the tiles up to theirs
 #pragma unroll
@@ -75,12 +76,20 @@ __global__ __launch_bounds__(kWalkThreads) void delta_bwd_kernel(DeltaParams p) 
                 }
             }
             fence();
-            if (s + 1 < KS) st[at ^ 1] = two<E>(S[2 * s + 2], S[2 * s + 3]);
+            if (s + 1 < KS) st[(s + 1) & 1] = two<E>(S[2 * s + 2], S[2 * s + 3]);
+            if constexpr (M::kSplit) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) dN[t] = mma2<E>(k[at][t], st[at], dN[t]);
+                for (int t = 0; t < NT; ++t) dN[t] = M::mma(k[at][t], st[s & 1].lo, dN[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) dN[t] = M::mma(k[at][t], st[s & 1].hi, dN[t]);
             if (s > 0 && s <= NT / 2) {
 #pragma unroll
-                for (int t = 0; t <= 2 * s - 1; ++t) later[t] = mma2<E>(P[t][s - 1], y[s - 1], later[t]);
+                for (int t = 0; t <= 2 * s - 1; ++t) later[t] = M::mma(P[t][s - 1].hi, y[s - 1], later[t]);
+                if constexpr (M::kSplit) {
+#pragma unroll
+                    for (int t = 0; t <= 2 * s - 1; ++t) later[t] = M::mma(P[t][s - 1].lo, y[s - 1], later[t]);
+                }
             }
             interleave<2 * NT, 4>();
             fence();
@@ -142,49 +151,63 @@ __global__ __launch_bounds__(kWalkThreads) void delta_bwd_kernel(DeltaParams p) 
             fence();
         }
         const float fade = m.v[kStart * C + C - 1];
-        frag kc[2][NT / 2], qc[2][NT / 2];
+        frag kc[2][2][NT / 2], qc[2][2][NT / 2];
+        const auto next = [&](int at, int t) {
 #pragma unroll
-        for (int s = 0; s < NT / 2; ++s) {
-            qc[0][s] = kt.cols(m.q, s, 0);
-            kc[0][s] = kt.cols(m.k, s, 0);
-        }
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int s = 0; s < NT / 2; ++s) {
+                    qc[at][u][s] = kt.cols(m.q, s, t + u);
+                    kc[at][u][s] = kt.cols(m.k, s, t + u);
+                }
+        };
+        if (AHEAD) next(0, 0);
 #pragma unroll
         for (int s = 0; s < NT / 2; ++s) a[s] = two<E>(-(bs[2 * s] * Z[2 * s]), -(bs[2 * s + 1] * Z[2 * s + 1]));
         store_tokens<C>(Z, p.z, chunk, n, p);
+        // two tiles in turn: a product waits for the one before it on its tile
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            if (t + 1 < KT) {
-#pragma unroll
-                for (int s = 0; s < NT / 2; ++s) {
-                    qc[(t + 1) & 1][s] = kt.cols(m.q, s, t + 1);
-                    kc[(t + 1) & 1][s] = kt.cols(m.k, s, t + 1);
-                }
-            }
+        for (int t = 0; t < KT; t += 2) {
+            const int at = AHEAD ? t / 2 & 1 : 0;
+            if (!AHEAD) next(0, t);
+            else if (t + 2 < KT) next(at ^ 1, t + 2);
             fence();
-            S[t] *= fade;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) S[t + u] *= fade;
 #pragma unroll
             for (int s = 0; s < NT / 2; ++s) {
-                S[t] = mma2<E>(qc[t & 1][s], q[s], S[t]);
-                S[t] = mma2<E>(kc[t & 1][s], a[s], S[t]);
+                if constexpr (M::kSplit) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) S[t + u] = M::mma(qc[at][u][s], q[s].lo, S[t + u]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) S[t + u] = M::mma(kc[at][u][s], a[s].lo, S[t + u]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) S[t + u] = M::mma(qc[at][u][s], q[s].hi, S[t + u]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) S[t + u] = M::mma(kc[at][u][s], a[s].hi, S[t + u]);
             }
-            if (t < NT) put_column<E, Lds::YP>(m.y + oy, t, be[t] * Z[t]);
+            if (t < NT) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) put_column<E, Lds::YP>(m.y + oy, t + u, be[t + u] * Z[t + u]);
+            }
         }
         settle(S[KT - 1]);
     });
     if (p.dh0) store_state<KT>(S, p.dh0, int64_t(b) * p.H + h, n, p);
 }
 
-template <typename E, int DK>
+template <typename E, int DK, int WAVES>
 int launch(const DeltaParams& p, hipStream_t stream) {
-    constexpr int bytes = WalkLds<E, DK, ChunkMats<E>::kAll>::kBytes;
+    typedef WalkLds<E, DK, ChunkMats<E>::kAll, WAVES> Lds;
     static DeviceOnce once;
     const int st = run_once_per_device(once, [] {
-        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_bwd_kernel<E, DK>),
-                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess ? 0 : -7;
+        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_bwd_kernel<E, DK, WAVES>),
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, Lds::kBytes) == hipSuccess ? 0 : -7;
     });
     if (st != 0) return st;
-    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + kWalkCols - 1) / kWalkCols));
-    delta_bwd_kernel<E, DK><<<wgs, kWalkThreads, bytes, stream>>>(p);
+    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + Lds::kCols - 1) / Lds::kCols));
+    delta_bwd_kernel<E, DK, WAVES><<<wgs, Lds::kThreads, Lds::kBytes, stream>>>(p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
@@ -193,6 +216,8 @@ int launch(const DeltaParams& p, hipStream_t stream) {
 
 int cls_delta_bwd_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream) {
     return cls::by_type(dtype, p.dk, [&](auto e, auto dk) {
-        return cls::launch<decltype(e), decltype(dk)::value>(p, stream);
+        typedef decltype(e) E;
+        constexpr int DK = decltype(dk)::value;
+        return cls::walk_waves(p) == 2 ? cls::launch<E, DK, 2>(p, stream) : cls::launch<E, DK, 4>(p, stream);
     });
 }

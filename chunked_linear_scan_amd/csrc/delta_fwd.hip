@@ -15,27 +15,28 @@ namespace cls {
 namespace {
 
 // KEEP: with the states and corrections that the gradients need.
-template <typename E, int DK, bool KEEP>
-__global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) {
+template <typename E, int DK, int WAVES, bool KEEP>
+__global__ __launch_bounds__(64 * (WAVES + 4), 2) void delta_fwd_kernel(DeltaParams p) {
     typedef Mat<E> M;
     typedef typename M::frag frag;
     constexpr int kParts = ChunkMats<E>::kParts, NM = kParts + 1;  // T - I in its parts, P
-    typedef WalkLds<E, DK, NM> Lds;
+    typedef WalkLds<E, DK, NM, WAVES> Lds;
     constexpr int C = M::kChunk, NT = C / 16, KT = DK / 16, KS = DK / 32;
+    constexpr bool AHEAD = DK <= 128;  // operands are read a step before their products: registers for it
     extern __shared__ __attribute__((aligned(16))) char lds[];
 
-    const int nblk = (p.dv + kWalkCols - 1) / kWalkCols;
+    const int nblk = (p.dv + Lds::kCols - 1) / Lds::kCols;
     const int blk = blockIdx.x % nblk, h = blockIdx.x / nblk % p.H, b = blockIdx.x / nblk / p.H;
     const int end = seq_end(p.seqlens, b, p.L), chunks = (end + C - 1) / C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave >= 4) {
+    if (wave >= WAVES) {
         const WalkColumns w{p.v, p.sv, p.y, bool(p.vec_v), bool(p.vec_out)};
-        walk_load<E, DK, NM>(p, w, lds, b, h, blk * kWalkCols, end, 0, 1, chunks);
+        walk_load<E, DK, NM, WAVES>(p, w, lds, b, h, blk * Lds::kCols, end, 0, 1, chunks);
         return;
     }
     const int l16 = lane16(), g4 = group4();
-    const int n = blk * kWalkCols + wave * 16 + l16;  // the lane's column
-    const bool wave_on = blk * kWalkCols + wave * 16 < p.dv;
+    const int n = blk * Lds::kCols + wave * 16 + l16;  // the lane's column
+    const bool wave_on = blk * Lds::kCols + wave * 16 < p.dv;
 
     f32x4 S[KT];
     load_state<KT>(S, p.h0, int64_t(b) * p.H + h, n, p);
@@ -57,6 +58,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             ks[t] = O[t] = f32x4{0, 0, 0, 0};
+            if (!AHEAD) continue;
             k[0][t] = kt.rows(m.k, t, 0);
             q[0][t] = kt.rows(m.q, t, 0);
         }
@@ -67,14 +69,15 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
         st[0] = two<E>(S[0], S[1]);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const int at = s & 1;
-            if (s + 1 < KS) {
+            const int at = AHEAD ? s & 1 : 0, at1 = AHEAD ? at ^ 1 : 0;
+            if (!AHEAD || s + 1 < KS) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    k[at ^ 1][t] = kt.rows(m.k, t, s + 1);
-                    q[at ^ 1][t] = kt.rows(m.q, t, s + 1);
+                    k[at1][t] = kt.rows(m.k, t, AHEAD ? s + 1 : s);
+                    q[at1][t] = kt.rows(m.q, t, AHEAD ? s + 1 : s);
                 }
-            } else {
+            }
+            if (s + 1 == KS) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     a[t] = factors(kBetaStart, t);
@@ -89,7 +92,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
                     }
             }
             fence();
-            if (s + 1 < KS) st[at ^ 1] = two<E>(S[2 * s + 2], S[2 * s + 3]);
+            if (s + 1 < KS) st[(s + 1) & 1] = two<E>(S[2 * s + 2], S[2 * s + 3]);
             if (s == 0) {  // beta V
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -98,13 +101,13 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
             }
             if constexpr (M::kSplit) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) ks[t] = M::mma(k[at][t], st[at].lo, ks[t]);
+                for (int t = 0; t < NT; ++t) ks[t] = M::mma(k[at][t], st[s & 1].lo, ks[t]);
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) ks[t] = M::mma(k[at][t], st[at].hi, ks[t]);
+            for (int t = 0; t < NT; ++t) ks[t] = M::mma(k[at][t], st[s & 1].hi, ks[t]);
             if (s + 1 == KS) fence();
 #pragma unroll
-            for (int t = 0; t < NT; ++t) O[t] = M::mma(q[at][t], st[at].hi, O[t]);
+            for (int t = 0; t < NT; ++t) O[t] = M::mma(q[at][t], st[s & 1].hi, O[t]);
             if (s + 1 < KS) {
                 interleave<3 * NT, 4>();
                 fence();
@@ -131,9 +134,13 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
             e[t] = factors(kWrite, t);
         }
         const float fade = m.v[kStart * C + C - 1];
-        frag kc[2][NT / 2];
+        frag kc[2][2][NT / 2];
 #pragma unroll
-        for (int s = 0; s < NT / 2; ++s) kc[0][s] = kt.cols(m.k, s, 0);
+        for (int s = 0; s < NT / 2; ++s) {
+            if (!AHEAD) continue;
+            kc[0][0][s] = kt.cols(m.k, s, 0);
+            kc[0][1][s] = kt.cols(m.k, s, 1);
+        }
         Two<E> nn[NT / 2];
         frag nf[NT / 2];
 #pragma unroll
@@ -158,22 +165,37 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
         }
         nn[NT / 2 - 1] = two<E>(N[NT - 2] * e[NT - 2], N[NT - 1] * e[NT - 1]);
         nf[NT / 2 - 1] = M::cvt(N[NT - 2], N[NT - 1]);
-        // the state, and beside it y
+        // the state, two tiles in turn (a product waits for the one before it on its tile), and beside it y
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            if (t + 1 < KT) {
+        for (int t = 0; t < KT; t += 2) {
+            const int at = AHEAD ? t / 2 & 1 : 0, at1 = AHEAD ? at ^ 1 : 0;
+            if (!AHEAD || t + 2 < KT) {
 #pragma unroll
-                for (int s = 0; s < NT / 2; ++s) kc[(t + 1) & 1][s] = kt.cols(m.k, s, t + 1);
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int s = 0; s < NT / 2; ++s) kc[at1][u][s] = kt.cols(m.k, s, t + (AHEAD ? 2 : 0) + u);
             }
             fence();
-            S[t] *= fade;
-            if (t < NT) {
 #pragma unroll
-                for (int s = 0; s <= t / 2; ++s) O[t] = M::mma(P[t][s], nf[s], O[t]);
+            for (int u = 0; u < 2; ++u) S[t + u] *= fade;
+#pragma unroll
+            for (int s = 0; s < NT / 2; ++s) {
+                if constexpr (M::kSplit) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) S[t + u] = M::mma(kc[at][u][s], nn[s].lo, S[t + u]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) S[t + u] = M::mma(kc[at][u][s], nn[s].hi, S[t + u]);
+                if (t < NT) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (s <= (t + u) / 2) O[t + u] = M::mma(P[t + u][s], nf[s], O[t + u]);
+                }
             }
+            if (t >= NT && t < 2 * NT) {
 #pragma unroll
-            for (int s = 0; s < NT / 2; ++s) S[t] = mma2<E>(kc[t & 1][s], nn[s], S[t]);
-            if (t >= NT && t < 2 * NT) put_column<E, Lds::YP>(m.y + oy, t - NT, O[t - NT]);
+                for (int u = 0; u < 2; ++u) put_column<E, Lds::YP>(m.y + oy, t + u - NT, O[t + u - NT]);
+            }
         }
 #pragma unroll
         for (int t = KT >= 2 * NT ? NT : 0; t < NT; ++t) put_column<E, Lds::YP>(m.y + oy, t, O[t]);
@@ -183,17 +205,17 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
     if (p.h_last) store_state<KT>(S, p.h_last, int64_t(b) * p.H + h, n, p);
 }
 
-template <typename E, int DK, bool KEEP>
+template <typename E, int DK, int WAVES, bool KEEP>
 int launch(const DeltaParams& p, hipStream_t stream) {
-    constexpr int bytes = WalkLds<E, DK, ChunkMats<E>::kParts + 1>::kBytes;
+    typedef WalkLds<E, DK, ChunkMats<E>::kParts + 1, WAVES> Lds;
     static DeviceOnce once;
     const int st = run_once_per_device(once, [] {
-        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_fwd_kernel<E, DK, KEEP>),
-                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess ? 0 : -7;
+        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_fwd_kernel<E, DK, WAVES, KEEP>),
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, Lds::kBytes) == hipSuccess ? 0 : -7;
     });
     if (st != 0) return st;
-    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + kWalkCols - 1) / kWalkCols));
-    delta_fwd_kernel<E, DK, KEEP><<<wgs, kWalkThreads, bytes, stream>>>(p);
+    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + Lds::kCols - 1) / Lds::kCols));
+    delta_fwd_kernel<E, DK, WAVES, KEEP><<<wgs, Lds::kThreads, Lds::kBytes, stream>>>(p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
@@ -204,6 +226,8 @@ int cls_delta_fwd_launch(const cls::DeltaParams& p, int dtype, hipStream_t strea
     return cls::by_type(dtype, p.dk, [&](auto e, auto dk) {
         typedef decltype(e) E;
         constexpr int DK = decltype(dk)::value;
-        return p.states ? cls::launch<E, DK, true>(p, stream) : cls::launch<E, DK, false>(p, stream);
+        if (cls::walk_waves(p) == 2)
+            return p.states ? cls::launch<E, DK, 2, true>(p, stream) : cls::launch<E, DK, 2, false>(p, stream);
+        return p.states ? cls::launch<E, DK, 4, true>(p, stream) : cls::launch<E, DK, 4, false>(p, stream);
     });
 }

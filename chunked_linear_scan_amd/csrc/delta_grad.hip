@@ -172,11 +172,11 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
         Regs k, q;
         const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + t0 * p.sk.token + kh * p.sk.head;
         const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + t0 * p.sq.token + kh * p.sq.head;
-        k.load(buffer(K, left * p.sk.token * sizeof(raw)), Regs::offset(p.sk.token, p.dk), p.sk.token);
-        q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk), p.sq.token);
+        k.load(buffer(K, left * p.sk.token * sizeof(raw)), Regs::offset(p.sk.token, p.dk, tid), p.sk.token);
+        q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk, tid), p.sq.token);
         if (tid < C) sG[tid] = t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f;
-        k.template store<KTile>(sK);
-        q.template store<KTile>(sQ);
+        k.template store<KTile>(sK, tid);
+        q.template store<KTile>(sQ, tid);
     }
 
     // with the state before the chunk: X1 = S dY^T, X2 = S Z^T; with the corrections: dP^T and M^T

@@ -61,11 +61,11 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
         const int left = end - t0;
         const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + t0 * p.sk.token + kh * p.sk.head;
         const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + t0 * p.sq.token + kh * p.sq.head;
-        k.load(buffer(K, left * p.sk.token * sizeof(raw)), Regs::offset(p.sk.token, p.dk), p.sk.token);
-        q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk), p.sq.token);
+        k.load(buffer(K, left * p.sk.token * sizeof(raw)), Regs::offset(p.sk.token, p.dk, tid), p.sk.token);
+        q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk, tid), p.sq.token);
         if (tid < C) sG[tid] = t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f;
-        k.template store<KT>(sK);
-        q.template store<KT>(sQ);
+        k.template store<KT>(sK, tid);
+        q.template store<KT>(sQ, tid);
     }
     const int i = 16 * w + l16;  // this lane's token: the row of A and P
     const float beta = t0 + i < end ? p.beta[b * p.b_batch + int64_t(t0 + i) * p.b_token + h] : 0.0f;

@@ -1,5 +1,5 @@
 // What the forward and the backward walk over the chunks share: a workgroup of
-// four waves that compute, 16 columns of a state each, and four that load.  The
+// two or four waves that compute, 16 columns of a state each, and four that load.  The
 // computing waves' work on a chunk is one long chain of products, so what
 // bounds a walk is that chain's latency: the loading waves keep the traffic with memory
 // (but for kept states) out of it, and the registers that this
@@ -12,8 +12,12 @@
 
 namespace cls {
 
-constexpr int kWalkCols = 64;      // columns to a workgroup
-constexpr int kWalkThreads = 512;  // computing waves, then loading waves
+// The computing waves of a workgroup: what bounds four is LDS, from which each reads the chunk's matrices for itself
+// (3200 cycles a chunk of 128-element keys, of which the products take 1700), so while a compute unit is free for every
+// 32 columns there are two.
+inline int walk_waves(const DeltaParams& p) {
+    return int64_t(p.batch) * p.H * ((p.dv + 31) / 32) <= 256 ? 2 : 4;
+}
 
 // Asks for N matrix instructions with V vector ones behind each, of those between two scheduling barriers: left to
 // itself the compiler issues products in blocks, during which the vector unit waits, and the other way round.
@@ -35,16 +39,17 @@ __device__ __forceinline__ void settle(f32x4& x) {
     x = f32x4{a, b, c, d};
 }
 
-// LDS of a walk: K, Q, NM matrices of a chunk, 64 columns of V and its factors, and 64 of y; twice where that fits.
-template <typename E, int DK, int NM>
+// LDS of a walk: K, Q, NM matrices of a chunk, its columns of V and its factors, and those of y; twice where that fits.
+template <typename E, int DK, int NM, int WAVES>
 struct WalkLds {
     typedef typename Mat<E>::raw raw;
     typedef LdsTile<E, DK> KTile;
     typedef LdsTile<E, Mat<E>::kChunk> MTile;
-    typedef LdsTile<E, kWalkCols> XTile;
-    static constexpr int C = Mat<E>::kChunk;
+    typedef LdsTile<E, 64> XTile;  // whose second half two waves do not use
+    static constexpr int C = Mat<E>::kChunk, kCols = 16 * WAVES;
+    static constexpr int kThreads = 64 * (WAVES + 4);  // computing waves, then loading waves
     static constexpr int KS = C * KTile::kPitch, MS = C * MTile::kPitch, XS = C * XTile::kPitch;
-    static constexpr int YP = kWalkCols + 16 / int(sizeof(raw));  // pitch of y: four rows touch every bank once
+    static constexpr int YP = 64 + 16 / int(sizeof(raw));  // pitch of y: four rows touch every bank once
     static constexpr int kBuffer = int((2 * KS + NM * MS + XS) * sizeof(raw) + kVecs * C * sizeof(float));
     static constexpr int kOut = C * YP * int(sizeof(raw));
     static constexpr bool kTwice = 2 * (kBuffer + kOut) <= 160 * 1024;
@@ -62,7 +67,7 @@ struct WalkLds {
     }
 };
 
-// 64 columns of V or dY in, of y or dV out.
+// Columns of V or dY in, of y or dV out.
 struct WalkColumns {
     const void* x;
     Strided3 sx;
@@ -71,25 +76,26 @@ struct WalkColumns {
 };
 
 // The loading waves' part: chunks first, first + step, .. (n of them).
-template <typename E, int DK, int NM>
+template <typename E, int DK, int NM, int WAVES>
 __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumns& w, char* lds, int b, int h, int col0, int end,
                                           int first, int step, int n) {
     typedef Mat<E> M;
     typedef typename M::raw raw;
     typedef ChunkMats<E> CM;
-    typedef WalkLds<E, DK, NM> Lds;
+    typedef WalkLds<E, DK, NM, WAVES> Lds;
     constexpr int C = M::kChunk, THREADS = 256;
     constexpr int64_t SZ = sizeof(raw);
     typedef TileRegs<E, C, DK, THREADS> KRegs;
     typedef TileRegs<E, C, C, THREADS> MRegs;
-    typedef TileRegs<E, C, kWalkCols, THREADS> XRegs;
-    const int kh = h / (p.H / p.Hk), tid = threadIdx.x % THREADS;
+    typedef TileRegs<E, C, 64, THREADS> XRegs;
+    const int kh = h / (p.H / p.Hk), tid = (threadIdx.x - 64 * WAVES) % THREADS;
     const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + kh * p.sk.head;
     const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + kh * p.sq.head;
     const raw* X = static_cast<const raw*>(w.x) + b * w.sx.batch + h * w.sx.head + col0;
-    const int cols = p.dv - col0 < kWalkCols ? p.dv - col0 : kWalkCols;
-    const uint32_t ok = KRegs::offset(p.sk.token, p.dk), oq = KRegs::offset(p.sq.token, p.dk), om = MRegs::offset(C, C);
-    const uint32_t ox = XRegs::offset(w.sx.token, cols);
+    const int cols = p.dv - col0 < Lds::kCols ? p.dv - col0 : Lds::kCols;
+    const uint32_t ok = KRegs::offset(p.sk.token, p.dk, tid), oq = KRegs::offset(p.sq.token, p.dk, tid);
+    const uint32_t ox = XRegs::offset(w.sx.token, cols, tid), om = MRegs::offset(C, C, tid);
+    const uint32_t om0 = MRegs::offset(C, 32, tid);  // of the first 32 rows only 32 columns are there
     // Two chunks in flight: a chunk may take less time than a load from memory.  (One where LDS holds one: dk above 128,
     // whose chunks are longer and whose vectors would be twice as many.)
     constexpr int SETS = Lds::kTwice ? 2 : 1;
@@ -106,7 +112,7 @@ __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumn
         const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
         const raw* mats = static_cast<const raw*>(p.mats) + chunk * CM::kAll * CM::kSize;
 #pragma unroll
-        for (int m = 0; m < NM; ++m) r.m[m].load(buffer(mats + m * CM::kSize), om, C);
+        for (int m = 0; m < NM; ++m) r.m[m].load(buffer(mats + m * CM::kSize), om, C, om0);
         const Buffer bx = buffer(X + t0 * w.sx.token, left * w.sx.token * SZ - col0 * SZ);
         if (w.vec_x) {
             r.x.load(bx, ox, w.sx.token);
@@ -127,11 +133,11 @@ __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumn
     };
     const auto put = [&](const Set& r, int i) {
         const Lds to(lds, i);
-        r.k.template store<typename Lds::KTile>(to.k);
-        r.q.template store<typename Lds::KTile>(to.q);
+        r.k.template store<typename Lds::KTile>(to.k, tid);
+        r.q.template store<typename Lds::KTile>(to.q, tid);
 #pragma unroll
-        for (int m = 0; m < NM; ++m) r.m[m].template store<typename Lds::MTile>(to.m + m * Lds::MS);
-        r.x.template store<typename Lds::XTile>(to.x);
+        for (int m = 0; m < NM; ++m) r.m[m].template store<typename Lds::MTile>(to.m + m * Lds::MS, tid);
+        r.x.template store<typename Lds::XTile>(to.x, tid);
         if (tid < kVecs * C / 4) *reinterpret_cast<u32x4*>(to.v + 4 * tid) = r.v;
     };
     const int64_t row = int64_t(p.H) * p.dv;  // of a token of y
