@@ -364,37 +364,103 @@ __device__ __forceinline__ void put4(typename E::raw* p, int lo, const f32x4& v)
     }
 }
 
-// Decays between the tokens of a chunk, from its logarithms g (in LDS): calls f(t, d) for the tiles t = w..0 of
-// 16 tokens, where d[r] = e^(g_{j+1} + .. + g_i) for the lane's token i = 16 w + l%16 and j = 16 t + 4 (l/16) + r
-// (of t = w only where j <= i is d of use).  All are exponentials of sums of g between the two tokens, never of
-// differences of running sums: terms of one sign, so nothing cancels, and g = -infinity gives exactly 0.
-// Returns the sum of g up to i.
-template <int NT, typename F>
-__device__ __forceinline__ float for_decays(const float* sG, int w, F&& f) {
-    const int l16 = lane16(), g4 = group4();
-    float pre = 0.0f, mid = 0.0f;  // of i's own tile up to i; of the tiles between j's and i's
-#pragma unroll
-    for (int l = 0; l < 16; ++l) pre += l <= l16 ? sG[16 * w + l] : 0.0f;
-#pragma unroll
-    for (int t = NT - 1; t >= 0; --t) {
-        if (t > w) continue;
-        f32x4 s{0, 0, 0, 0};
-        float whole = 0.0f;
-#pragma unroll
-        for (int l = 0; l < 16; ++l) {
-            const float gl = sG[16 * t + l];
-            whole += gl;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s[r] += l > 4 * g4 + r && (t < w || l <= l16) ? gl : 0.0f;
-        }
-        f32x4 d;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) d[r] = fexp(t < w ? s[r] + mid + pre : s[r]);
-        f(t, d);
-        if (t < w) mid += whole;
-    }
-    return mid + pre;
+// Sums over 16 adjacent lanes (a row of the data-parallel primitives): inclusive from the row's start, and of those
+// behind a lane.
+template <int CTRL>
+__device__ __forceinline__ float row_move(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
+__device__ __forceinline__ float row_prefix(float v) {
+    v += row_move<0x111>(v);
+    v += row_move<0x112>(v);
+    v += row_move<0x114>(v);
+    return v + row_move<0x118>(v);
+}
+__device__ __forceinline__ float row_behind(float v) {
+    v = row_move<0x101>(v);
+    v += row_move<0x101>(v);
+    v += row_move<0x102>(v);
+    v += row_move<0x104>(v);
+    return v + row_move<0x108>(v);
+}
+// The sum of the row, in all of its lanes.
+__device__ __forceinline__ float row_total(float v) {
+    v += row_move<0x121>(v);
+    v += row_move<0x122>(v);
+    v += row_move<0x124>(v);
+    return v + row_move<0x128>(v);
+}
+
+// Decays between the tokens of a chunk, all exponentials of sums of g between the two tokens, never of differences
+// of running sums: terms of one sign, so nothing cancels, and g = -infinity gives exactly 0.  In LDS: g, and of each
+// token the sum of its tile of 16 up to it, that of its tile behind it, and the tiles' sums.
+template <int C>
+struct Decays {
+    static constexpr int NT = C / 16, kFloats = 3 * C + 16;
+    // By the first C threads.
+    static __device__ __forceinline__ void put(float* s, float g) {
+        const int i = threadIdx.x;
+        const float to = row_prefix(g);
+        s[i] = g;
+        s[C + i] = to;
+        s[2 * C + i] = row_behind(g);
+        if ((i & 15) == 15) s[3 * C + (i >> 4)] = to;
+    }
+    // Calls f(t, d) for the tiles t = w..0, where d[r] = e^(g_{j+1} + .. + g_i) for the lane's token i = 16 w + l%16 and
+    // j = 16 t + 4 (l/16) + r (of t = w only where j <= i is d of use).
+    template <typename F>
+    static __device__ __forceinline__ void each(const float* s, int w, F&& f) {
+        const int l16 = lane16(), g4 = group4();
+        const float pre = s[C + 16 * w + l16];
+        {
+            f32x4 g[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) g[q] = *reinterpret_cast<const f32x4*>(s + 16 * w + 4 * q);
+            float base = 0.0f;  // of the tokens behind the lane's four
+            f32x4 own = g[0];
+#pragma unroll
+            for (int q = 1; q < 4; ++q) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    base += q > g4 && 4 * q + r <= l16 ? g[q][r] : 0.0f;
+                    own[r] = q == g4 ? g[q][r] : own[r];
+                }
+            }
+            f32x4 x;
+            x[3] = base;
+#pragma unroll
+            for (int r = 2; r >= 0; --r) x[r] = x[r + 1] + (4 * g4 + r + 1 <= l16 ? own[r + 1] : 0.0f);
+            f32x4 d;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d[r] = fexp(x[r]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (t == w) f(t, d);
+        }
+        float mid = pre;  // and of the tiles between
+#pragma unroll
+        for (int t = NT - 2; t >= 0; --t) {
+            if (t >= w) continue;
+            const f32x4 behind = *reinterpret_cast<const f32x4*>(s + 2 * C + 16 * t + 4 * g4);
+            f32x4 d;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d[r] = fexp(behind[r] + mid);
+            f(t, d);
+            mid += s[3 * C + t];
+        }
+    }
+    // e^ of the sum up to the lane's token, and of that behind it.
+    static __device__ __forceinline__ float start(const float* s, int w) {
+        float v = s[C + 16 * w + lane16()];
+        for (int t = 0; t < w; ++t) v += s[3 * C + t];
+        return fexp(v);
+    }
+    static __device__ __forceinline__ float behind(const float* s, int w) {
+        float v = s[2 * C + 16 * w + lane16()];
+        for (int t = w + 1; t < NT; ++t) v += s[3 * C + t];
+        return fexp(v);
+    }
+};
 
 // Calls f with the element type and the padded size of a key (its place in LDS and registers).
 template <typename F>

@@ -90,11 +90,11 @@ struct GradSize {
     static constexpr int kTiles = kParts * 32 * (KP + 2 * MP);  // tiles of S or dS, of N and of Z
     static constexpr int kPairs = 2 * C * MP;                   // pB and pP, in the same place
     static constexpr int kUnion = kTiles > kPairs ? kTiles : kPairs;
-    static constexpr size_t bytes = (2 * C * KP + kUnion) * sizeof(typename M::raw) + 9 * C * sizeof(float);
+    static constexpr size_t bytes = (2 * C * KP + kUnion) * sizeof(typename M::raw) + (Decays<C>::kFloats + (2 + C / 16) * C + C / 16) * sizeof(float);
 };
 
 template <typename E, int DK>
-__global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaParams p) {
+__global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_grad_kernel(DeltaParams p) {
     typedef Mat<E> M;
     typedef typename M::raw raw;
     typedef GradSize<E, DK> G;
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     raw* sB = sS;  // once the tiles are done with
     raw* sP = sB + C * MP;
     float* sG = reinterpret_cast<float*>(sS + G::kUnion);
-    float* sRow = sG + C;       // read_i + sum_j F_ij
+    float* sRow = sG + Decays<C>::kFloats;  // read_i + sum_j F_ij
     float* sWrite = sRow + C;   // write_j
     float* sCol = sWrite + C;   // [NT][C]: sums of F over a wave's tokens
     float* sDot = sCol + NT * C;
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
         const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + t0 * p.sq.token + kh * p.sq.head;
         k.load(buffer(K, left * p.sk.token * sizeof(raw)), Regs::offset(p.sk.token, p.dk, tid), p.sk.token);
         q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk, tid), p.sq.token);
-        if (tid < C) sG[tid] = t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f;
+        if (tid < C) Decays<C>::put(sG, t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f);
         k.template store<KTile>(sK, tid);
         q.template store<KTile>(sQ, tid);
     }
@@ -193,23 +193,28 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     rs.load(S0, p.dv, 0, p.dk);
     rn.load(N, p.dv, 0, C);
     rz.load(Z, p.dv, 0, C);
-    for (int d0 = 0; d0 < p.dv; d0 += 32) {
-        __syncthreads();
-        rs.store(sS);
-        rn.store(sN);
-        rz.store(sZ);
-        f32x4 y[2], v[2];
+    f32x4 y1[2], v1[2];  // of dY and V, of the columns to come
+    const auto ahead = [&](int d0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int col = d0 + 16 * u + 4 * g4;
-            y[u] = in ? load4<E>(Yi, col, p.dv, p.vec_dy) : f32x4{0, 0, 0, 0};
-            v[u] = in ? load4<E>(Vi, col, p.dv, p.vec_v) : f32x4{0, 0, 0, 0};
+            y1[u] = in ? load4<E>(Yi, col, p.dv, p.vec_dy) : f32x4{0, 0, 0, 0};
+            v1[u] = in ? load4<E>(Vi, col, p.dv, p.vec_v) : f32x4{0, 0, 0, 0};
         }
-        __syncthreads();
+    };
+    ahead(0);
+    for (int d0 = 0; d0 < p.dv; d0 += 32) {
+        lds_meet();
+        rs.store(sS);
+        rn.store(sN);
+        rz.store(sZ);
+        const f32x4 y[2] = {y1[0], y1[1]}, v[2] = {v1[0], v1[1]};
+        lds_meet();
         if (d0 + 32 < p.dv) {
             rs.load(S0, p.dv, d0 + 32, p.dk);
             rn.load(N, p.dv, d0 + 32, C);
             rz.load(Z, p.dv, d0 + 32, C);
+            ahead(d0 + 32);
         }
         const Two<E> zf = two_cols<E>(mt, sZ, w);
         const typename M::frag yf = M::cvt(y[0], y[1]);  // exact
@@ -257,17 +262,18 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
         STile r0;
         const f32x4 after = *reinterpret_cast<const f32x4*>(vecs + kWrite * C + threadIdx.x % NTile::PER_ROW * 4);
         rs.load(dS, p.dv, 0, p.dk);
+        r0.load(S0, p.dv, 0, p.dk);
         rn.load(N, p.dv, 0, C);
         for (int d0 = 0; d0 < p.dv; d0 += 32) {
-            r0.load(S0, p.dv, d0, p.dk);
-            __syncthreads();
+            lds_meet();
             rs.store(sS);
             rn.scale(after);
             rn.store(sN);
             both += rs.dot(r0);
-            __syncthreads();
+            lds_meet();
             if (d0 + 32 < p.dv) {
                 rs.load(dS, p.dv, d0 + 32, p.dk);
+                r0.load(S0, p.dv, d0 + 32, p.dk);
                 rn.load(N, p.dv, d0 + 32, C);
             }
             const Two<E> nf = two_cols<E>(mt, sN, w);
@@ -300,7 +306,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     for (int t = 0; t < NT; ++t)
         if (t > w)
             for (int r = 0; r < 4; ++r) kk[t][r] = 0.0f;
-    for_decays<NT>(sG, w, [&](int t, const f32x4& d) {
+    Decays<C>::each(sG, w, [&](int t, const f32x4& d) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int j = 16 * t + 4 * g4 + r;
@@ -320,9 +326,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            float v = kk[t][r];
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+            const float v = row_total(kk[t][r]);
             if (l16 == 0) sCol[w * C + 16 * t + 4 * g4 + r] = v;
         }
     if (g4 == 0) {
@@ -337,18 +341,30 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_grad_kernel(DeltaPar
         put4<E>(sP + MTile::quad(i, 16 * t + 4 * g4), 0, dP[t]);
     }
     __syncthreads();
-    if (tid < C) {  // dg of token tid
-        float v = fade * sDot[0];
+    if (tid < 64) {  // dg of token tid, by the first wave
+        float both = 0.0f, row = 0.0f, put = 0.0f;
 #pragma unroll
-        for (int k = 1; k < NT; ++k) v += fade * sDot[k];
-        for (int l = 0; l < C; ++l) {
-            float cols = 0.0f;
+        for (int k = 0; k < NT; ++k) both += fade * sDot[k];
+        if (tid < C) {
+            row = sRow[tid];
+            put = sWrite[tid];
 #pragma unroll
-            for (int k = 0; k < NT; ++k) cols += sCol[k * C + l];
-            v += l >= tid ? sRow[l] - cols : sWrite[l];
+            for (int k = 0; k < NT; ++k) row -= sCol[k * C + tid];
         }
-        if (fexp(sG[tid]) == 0.0f) v = 0.0f;  // nothing passes: not the sums' roundings either
-        if (t0 + tid < p.L) p.dg[(int64_t(b) * p.L + t0 + tid) * p.H + h] = t0 + tid < end ? v : 0.0f;
+        // from tid on, and before tid: sums over 16 lanes, then over their rows
+        float from = row + row_behind(row), before = row_prefix(row_move<0x111>(put));  // of those before it
+        const float rows16 = row_total(row), puts16 = row_total(put);
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+            const float a = __shfl(rows16, 16 * k, 64), c = __shfl(puts16, 16 * k, 64);
+            from += k > tid >> 4 ? a : 0.0f;
+            before += k < tid >> 4 ? c : 0.0f;
+        }
+        float v = both + from + before;
+        if (tid < C && t0 + tid < p.L) {
+            if (fexp(sG[tid]) == 0.0f) v = 0.0f;  // nothing passes: not the sums' roundings either
+            p.dg[(int64_t(b) * p.L + t0 + tid) * p.H + h] = t0 + tid < end ? v : 0.0f;
+        }
     }
     // the pairs' parts: as the later token (operands from the lanes), as the earlier one (from LDS)
     typename M::frag bi[NT / 2], pi[NT / 2], bj[NT / 2], pj[NT / 2];

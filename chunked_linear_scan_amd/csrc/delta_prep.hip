@@ -45,11 +45,14 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
     constexpr int C = M::kChunk, NT = C / 16, THREADS = 64 * NT;
     typedef LdsTile<E, DK> KT;
     constexpr int AP = C + 4;
-    __shared__ __attribute__((aligned(16))) raw sK[C * KT::kPitch];
-    __shared__ __attribute__((aligned(16))) raw sQ[C * KT::kPitch];
-    __shared__ __attribute__((aligned(16))) float sA[C * AP];
-    __shared__ __attribute__((aligned(16))) float sT[C * AP];
-    __shared__ __attribute__((aligned(16))) float sG[C];
+    // K and Q, and once their products are taken A and T in the same place
+    constexpr size_t kKeys = 2 * C * KT::kPitch * sizeof(raw), kTri = 2 * C * AP * sizeof(float);
+    __shared__ __attribute__((aligned(16))) char lds[kKeys > kTri ? kKeys : kTri];
+    __shared__ __attribute__((aligned(16))) float sG[Decays<C>::kFloats];
+    raw* sK = reinterpret_cast<raw*>(lds);
+    raw* sQ = sK + C * KT::kPitch;
+    float* sA = reinterpret_cast<float*>(lds);
+    float* sT = sA + C * AP;
 
     const int h = blockIdx.x % p.H, c = blockIdx.x / p.H % p.nchunk, b = blockIdx.x / p.H / p.nchunk;
     const int end = seq_end(p.seqlens, b, p.L), t0 = c * C;
@@ -63,7 +66,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
         const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + t0 * p.sq.token + kh * p.sq.head;
         k.load(buffer(K, left * p.sk.token * sizeof(raw)), Regs::offset(p.sk.token, p.dk, tid), p.sk.token);
         q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk, tid), p.sq.token);
-        if (tid < C) sG[tid] = t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f;
+        if (tid < C) Decays<C>::put(sG, t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f);
         k.template store<KT>(sK, tid);
         q.template store<KT>(sQ, tid);
     }
@@ -88,7 +91,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
         }
     }
 
-    // decays: sums of g from j + 1 to i
+    __syncthreads();
     const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
     raw* mats = static_cast<raw*>(p.mats) + chunk * ChunkMats<E>::kAll * ChunkMats<E>::kSize;
     raw* P = mats + ChunkMats<E>::kParts * ChunkMats<E>::kSize;
@@ -99,7 +102,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
                 put4<E>(P + part * ChunkMats<E>::kSize + i * C + 16 * (w + 1) + 4 * g4, 0, f32x4{0, 0, 0, 0});
     }
     const float scale = p_parts > 1 ? 1.0f : p.scale;
-    const float sum = for_decays<NT>(sG, w, [&](int t, const f32x4& d) {
+    Decays<C>::each(sG, w, [&](int t, const f32x4& d) {
         f32x4 a, q;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -112,11 +115,9 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
     });
     if (g4 == 0) {
         float* vecs = p.vecs + chunk * kVecs * C;
-        float after = 0.0f;
-        for (int l = i + 1; l < C; ++l) after += sG[l];
-        const float start = fexp(sum);
+        const float start = Decays<C>::start(sG, w);
         vecs[kRead * C + i] = p.scale * start;
-        vecs[kWrite * C + i] = fexp(after);
+        vecs[kWrite * C + i] = Decays<C>::behind(sG, w);
         vecs[kBeta * C + i] = beta;
         vecs[kBetaStart * C + i] = beta * start;
         vecs[kStart * C + i] = start;
