@@ -462,6 +462,15 @@ struct Decays {
     }
 };
 
+// A workgroup's unit (of n) and its place in it (of `per`): workgroups go to the eight dies in turn, so those of a
+// unit, which read the same rows, are eight apart and share a die's L2.
+struct UnitPart { int unit, part; };
+__device__ __forceinline__ UnitPart unit_part(int n, int per) {
+    const int group = blockIdx.x / (8 * per), r = blockIdx.x % (8 * per);
+    const int units = n - 8 * group < 8 ? n - 8 * group : 8;
+    return {8 * group + r % units, r / units};
+}
+
 // Calls f with the element type and the padded size of a key (its place in LDS and registers).
 template <typename F>
 int by_type(int dtype, int dk, F&& f) {

@@ -24,7 +24,9 @@ __global__ __launch_bounds__(64 * (WAVES + 4), 2) void delta_bwd_kernel(DeltaPar
     extern __shared__ __attribute__((aligned(16))) char lds[];
 
     const int nblk = (p.dv + Lds::kCols - 1) / Lds::kCols;
-    const int blk = blockIdx.x % nblk, h = blockIdx.x / nblk % p.H, b = blockIdx.x / nblk / p.H;
+    const int rep = p.H / p.Hk;
+    const UnitPart u = unit_part(p.batch * p.Hk, rep * nblk);
+    const int blk = u.part % nblk, h = u.unit % p.Hk * rep + u.part / nblk, b = u.unit / p.Hk;
     const int end = seq_end(p.seqlens, b, p.L), chunks = (end + C - 1) / C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= WAVES) {

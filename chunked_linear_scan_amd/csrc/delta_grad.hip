@@ -113,9 +113,11 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_g
     float* sCol = sWrite + C;   // [NT][C]: sums of F over a wave's tokens
     float* sDot = sCol + NT * C;
 
-    const int h = blockIdx.x % p.H, c = blockIdx.x / p.H % p.nchunk, b = blockIdx.x / p.H / p.nchunk;
+    const int rep = p.H / p.Hk;
+    const UnitPart u = unit_part(p.batch * p.nchunk * p.Hk, rep);
+    const int kh = u.unit % p.Hk, h = kh * rep + u.part, c = u.unit / p.Hk % p.nchunk, b = u.unit / p.Hk / p.nchunk;
     const int end = seq_end(p.seqlens, b, p.L), t0 = c * C;
-    const int rep = p.H / p.Hk, kh = h / rep, tid = threadIdx.x, w = tid >> 6, l16 = lane16(), g4 = group4();
+    const int tid = threadIdx.x, w = tid >> 6, l16 = lane16(), g4 = group4();
     const int i = 16 * w + l16, tok = t0 + i;  // this lane's token
     const bool in = tok < end;
     // rows of the outputs: of a token's head, or its part of a key head's sum

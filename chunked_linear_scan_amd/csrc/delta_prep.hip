@@ -54,10 +54,12 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
     float* sA = reinterpret_cast<float*>(lds);
     float* sT = sA + C * AP;
 
-    const int h = blockIdx.x % p.H, c = blockIdx.x / p.H % p.nchunk, b = blockIdx.x / p.H / p.nchunk;
+    const int rep = p.H / p.Hk;
+    const UnitPart u = unit_part(p.batch * p.nchunk * p.Hk, rep);
+    const int kh = u.unit % p.Hk, h = kh * rep + u.part, c = u.unit / p.Hk % p.nchunk, b = u.unit / p.Hk / p.nchunk;
     const int end = seq_end(p.seqlens, b, p.L), t0 = c * C;
     if (t0 >= end) return;
-    const int kh = h / (p.H / p.Hk), tid = threadIdx.x, w = tid >> 6, l16 = lane16(), g4 = group4();
+    const int tid = threadIdx.x, w = tid >> 6, l16 = lane16(), g4 = group4();
     {
         typedef TileRegs<E, C, DK, THREADS> Regs;
         Regs k, q;
