@@ -145,8 +145,8 @@ __device__ __forceinline__ f32x4 mma3(const Two<E>& a, const Two<E>& b, f32x4 c)
 struct Strided3 { int64_t batch, token, head; };
 constexpr int64_t kDeltaMaxToken = int64_t(1) << 23;  // elements from a token to the next
 
-// q, k, v and dy are the caller's or, where those are off whole vectors (q and k) or have rows that overlap or lie
-// further apart than kDeltaMaxToken, copies.
+// q, k, v and dy have rows of whole 16-byte vectors: the caller's or, where those are off whole vectors or have rows that
+// overlap or lie further apart than kDeltaMaxToken, copies with zeros behind a row's end.
 struct DeltaParams {
     const void *q, *k, *v, *dy;
     const float *g, *beta, *h0, *dh_last;
@@ -164,9 +164,8 @@ struct DeltaParams {
     int64_t g_batch, g_token, b_batch, b_token;
     int batch, L, Hk, H, dk, dv, nchunk;
     float scale;
-    uint8_t vec_v, vec_dy;  // rows of whole 16-byte vectors, as those of q and k are here
-    uint8_t vec_out;        // y or dv has rows of whole 16-byte vectors
-    uint8_t vec_dqk;        // dq and dk start on 16 bytes
+    uint8_t vec_out;  // y or dv has rows of whole 16-byte vectors
+    uint8_t vec_dqk;  // dq and dk start on 16 bytes
 };
 
 // Matrices of a chunk in `mats`: T hi, T lo, P hi, P lo (16-bit), T, P (fp32).
@@ -204,7 +203,7 @@ struct LdsTile {
     // keeps the 16 lanes which a 16-byte read serves at a time apart (0-3, 12-15 and 20-27 of 32, so rows of two lane groups).
     static __device__ __forceinline__ int swap(int row) {
         const int x = (row >> 2) & 3, low = (((x ^ (x >> 1)) & 1) << 1) + (x >> 1);
-        return 4 * (kSpan == 64 ? (row >> 1) & 1 : row & 3) + low;
+        return kSpan == 32 ? low : 4 * (kSpan == 64 ? (row >> 1) & 1 : row & 3) + low;
     }
     // Element offset of four elements (col a multiple of 4).
     static __device__ __forceinline__ int quad(int row, int col) {
@@ -218,7 +217,7 @@ struct LdsTile {
     static __device__ __forceinline__ void put(raw* m, int row, int col, const u32x4& v) {
         if constexpr (kSwap) {
             // the rows that share banks start with different halves
-            const bool odd = kSpan == 64 ? row & 2 : row & 1;
+            const bool odd = kSpan == 32 ? row & 4 : kSpan == 64 ? row & 2 : row & 1;
             const u32x2 a{v[0], v[1]}, b{v[2], v[3]};
             *reinterpret_cast<u32x2*>(m + quad(row, col + (odd ? 4 : 0))) = odd ? b : a;
             *reinterpret_cast<u32x2*>(m + quad(row, col + (odd ? 0 : 4))) = odd ? a : b;
@@ -226,16 +225,18 @@ struct LdsTile {
             *reinterpret_cast<u32x4*>(m + quad(row, col)) = v;
         }
     }
-    __device__ __forceinline__ LdsTile() {
+    // Steps and tiles count from column `first` on, a multiple of 32 (of kSpan where that is less than what is used;
+    // of 16 for the tile that starts there).
+    __device__ __forceinline__ explicit LdsTile(int first = 0) {
         const int l16 = lane16(), g = group4();
         if constexpr (kSwap) {
 #pragma unroll
-            for (int n = 0; n < kRows; ++n) r[n] = quad(l16, 32 * n + 4 * g) * sizeof(raw);
+            for (int n = 0; n < kRows; ++n) r[n] = quad(l16, (first + 32 * n) % DIM + 4 * g) * sizeof(raw);
 #pragma unroll
-            for (int n = 0; n < kCols; ++n) c[n] = quad(4 * g + (l16 >> 2), 16 * n + 4 * (l16 & 3)) * sizeof(raw);
+            for (int n = 0; n < kCols; ++n) c[n] = quad(4 * g + (l16 >> 2), (first + 16 * n) % DIM + 4 * (l16 & 3)) * sizeof(raw);
         } else {
-            r[0] = (l16 * kPitch + 4 * g) * sizeof(raw);
-            c[0] = (4 * g * kPitch + l16) * sizeof(raw);
+            r[0] = (l16 * kPitch + first + 4 * g) * sizeof(raw);
+            c[0] = (4 * g * kPitch + first + l16) * sizeof(raw);
         }
     }
     // Operand of 16 rows from 16 t on, depths 32 s.. of them.

@@ -40,6 +40,12 @@ uint8_t whole_vectors(const void* p, int64_t dim, int dtype, S... strides) {
     return aligned(p, 16) && dim % ve == 0 && ((strides % ve == 0) && ...);
 }
 
+// A copied row's length.
+int64_t padded(int64_t dim, int dtype) {
+    const int64_t ve = 16 / int64_t(elem_size(dtype));
+    return ceil_div(dim, ve) * ve;
+}
+
 // SSD_OK or the status of sizes that are refused.
 int delta_dims(const gated_delta_inputs& s) {
     if (!dtype_ok(s.dtype)) return SSD_ERR_DTYPE;
@@ -51,9 +57,9 @@ int delta_dims(const gated_delta_inputs& s) {
 int delta_sizes(const gated_delta_inputs& s) {
     const int st = delta_dims(s);
     if (st != SSD_OK) return st;
-    if (s.heads * s.dv > cls::kDeltaMaxToken || s.kheads * 256 > cls::kDeltaMaxToken) return SSD_ERR_SHAPE;
+    if (s.heads * padded(s.dv, s.dtype) > cls::kDeltaMaxToken || s.kheads * 256 > cls::kDeltaMaxToken) return SSD_ERR_SHAPE;
     const int64_t heads = s.batch * s.heads;
-    if (heads * ceil_div(s.dv, 64) >= kMaxThreads / 256) return SSD_ERR_SHAPE;
+    if (heads * ceil_div(s.dv, 32) >= kMaxThreads / 512) return SSD_ERR_SHAPE;
     if (heads >= ceil_div(kMaxThreads / 256, ceil_div(s.seqlen, chunk_of(s.dtype)))) return SSD_ERR_SHAPE;
     return SSD_OK;
 }
@@ -75,15 +81,10 @@ int delta_check(const gated_delta_inputs* in, bool step) {
 }
 
 // Whether the kernels read an activation's rows where they are: tokens apart by a row or more and no further than
-// their offsets reach, and (whole) rows of 16-byte vectors.  Others are copied into the workspace.
-bool in_place(const void* p, bool whole, int64_t L, int64_t dim, int dtype, int64_t batch, int64_t token, int64_t head) {
+// their offsets reach, in whole 16-byte vectors.  Others are copied into the workspace.
+bool in_place(const void* p, int64_t L, int64_t dim, int dtype, int64_t batch, int64_t token, int64_t head) {
     if (L > 1 && (token < dim || token > cls::kDeltaMaxToken)) return false;
-    return !whole || whole_vectors(p, dim, dtype, batch, L > 1 ? token : 0, head);
-}
-
-int64_t padded_keys(const gated_delta_inputs& s) {
-    const int64_t ve = 16 / int64_t(elem_size(s.dtype));
-    return ceil_div(s.dk, ve) * ve;
+    return whole_vectors(p, dim, dtype, batch, L > 1 ? token : 0, head);
 }
 
 // Offsets in the workspaces and checkpoints, and their sizes.
@@ -97,12 +98,12 @@ struct DeltaSpace {
 DeltaSpace delta_space(const gated_delta_inputs& s) {
     const int64_t C = chunk_of(s.dtype), n = s.batch * s.heads * ceil_div(s.seqlen, C), rows = s.batch * s.seqlen;
     const size_t mat = size_t(C * C) * elem_size(s.dtype) * (s.dtype == SSD_F32 ? 2 : 4);
-    const size_t keys = round_up(size_t(rows * s.kheads * padded_keys(s)) * elem_size(s.dtype), 256);
-    const size_t values = round_up(size_t(rows * s.heads * s.dv) * elem_size(s.dtype), 256);
+    const size_t keys = round_up(size_t(rows * s.kheads * padded(s.dk, s.dtype)) * elem_size(s.dtype), 256);
+    const size_t values = round_up(size_t(rows * s.heads * padded(s.dv, s.dtype)) * elem_size(s.dtype), 256);
     DeltaSpace d{};
-    d.pack_q = !in_place(s.q, true, s.seqlen, s.dk, s.dtype, s.q_batch, s.q_token, s.q_head);
-    d.pack_k = !in_place(s.k, true, s.seqlen, s.dk, s.dtype, s.k_batch, s.k_token, s.k_head);
-    d.pack_v = !in_place(s.v, false, s.seqlen, s.dv, s.dtype, s.v_batch, s.v_token, s.v_head);
+    d.pack_q = !in_place(s.q, s.seqlen, s.dk, s.dtype, s.q_batch, s.q_token, s.q_head);
+    d.pack_k = !in_place(s.k, s.seqlen, s.dk, s.dtype, s.k_batch, s.k_token, s.k_head);
+    d.pack_v = !in_place(s.v, s.seqlen, s.dv, s.dtype, s.v_batch, s.v_token, s.v_head);
     d.vecs = round_up(size_t(n) * mat, 256);
     d.q = d.vecs + round_up(size_t(n) * cls::kVecs * C * 4, 256);
     d.k = d.q + (d.pack_q ? keys : 0);
@@ -137,10 +138,9 @@ DeltaParams delta_params(const gated_delta_inputs& in, void* workspace, void* ch
         if (copied) strides = {in.seqlen * heads * dim, heads * dim, dim};
         else strides = {given_strides.batch, in.seqlen > 1 ? given_strides.token : heads * dim, given_strides.head};
     };
-    place(in.q, s.pack_q, s.q, in.kheads, padded_keys(in), {in.q_batch, in.q_token, in.q_head}, p.q, p.sq);
-    place(in.k, s.pack_k, s.k, in.kheads, padded_keys(in), {in.k_batch, in.k_token, in.k_head}, p.k, p.sk);
-    place(in.v, s.pack_v, s.v, in.heads, in.dv, {in.v_batch, in.v_token, in.v_head}, p.v, p.sv);
-    p.vec_v = whole_vectors(p.v, in.dv, in.dtype, p.sv.batch, p.sv.token, p.sv.head);
+    place(in.q, s.pack_q, s.q, in.kheads, padded(in.dk, in.dtype), {in.q_batch, in.q_token, in.q_head}, p.q, p.sq);
+    place(in.k, s.pack_k, s.k, in.kheads, padded(in.dk, in.dtype), {in.k_batch, in.k_token, in.k_head}, p.k, p.sk);
+    place(in.v, s.pack_v, s.v, in.heads, padded(in.dv, in.dtype), {in.v_batch, in.v_token, in.v_head}, p.v, p.sv);
     p.mats = ws + s.mats;
     p.vecs = reinterpret_cast<float*>(ws + s.vecs);
     if (checkpoints) {
@@ -153,7 +153,7 @@ DeltaParams delta_params(const gated_delta_inputs& in, void* workspace, void* ch
 // The copies, where there are any.
 int delta_pack(const gated_delta_inputs& in, void* workspace, const DeltaSpace& s, hipStream_t stream) {
     char* ws = static_cast<char*>(workspace);
-    const int64_t size = int64_t(elem_size(in.dtype)), dk = padded_keys(in);
+    const int64_t size = int64_t(elem_size(in.dtype)), dk = padded(in.dk, in.dtype);
     int st = 0;
     if (s.pack_q)
         st = cls_delta_pack_launch(in.q, ws + s.q, size, in.batch, in.seqlen, in.kheads, in.dk, dk, in.q_batch, in.q_token,
@@ -162,7 +162,7 @@ int delta_pack(const gated_delta_inputs& in, void* workspace, const DeltaSpace& 
         st = cls_delta_pack_launch(in.k, ws + s.k, size, in.batch, in.seqlen, in.kheads, in.dk, dk, in.k_batch, in.k_token,
                                    in.k_head, stream);
     if (st == 0 && s.pack_v)
-        st = cls_delta_pack_launch(in.v, ws + s.v, size, in.batch, in.seqlen, in.heads, in.dv, in.dv, in.v_batch, in.v_token,
+        st = cls_delta_pack_launch(in.v, ws + s.v, size, in.batch, in.seqlen, in.heads, in.dv, padded(in.dv, in.dtype), in.v_batch, in.v_token,
                                    in.v_head, stream);
     return st;
 }
@@ -256,12 +256,11 @@ int gated_delta_bwd(const gated_delta_inputs* in, const gated_delta_grads* g, vo
     if (!workspace || workspace_bytes < s.bwd) return SSD_ERR_WORKSPACE;
     DeltaParams p = delta_params(*in, workspace, const_cast<void*>(g->checkpoints), s);
     char* ws = static_cast<char*>(workspace);
-    const bool pack_dy = !in_place(g->dy, false, in->seqlen, in->dv, in->dtype, g->dy_batch, g->dy_token, g->dy_head);
-    const int64_t row = in->heads * in->dv;
+    const bool pack_dy = !in_place(g->dy, in->seqlen, in->dv, in->dtype, g->dy_batch, g->dy_token, g->dy_head);
+    const int64_t dv = padded(in->dv, in->dtype), row = in->heads * dv;
     p.dy = pack_dy ? ws + s.dy : g->dy;
-    if (pack_dy) p.sdy = {in->seqlen * row, row, in->dv};
+    if (pack_dy) p.sdy = {in->seqlen * row, row, dv};
     else p.sdy = {g->dy_batch, in->seqlen > 1 ? g->dy_token : row, g->dy_head};
-    p.vec_dy = whole_vectors(p.dy, in->dv, in->dtype, p.sdy.batch, p.sdy.token, p.sdy.head);
     p.vec_out = whole_vectors(g->dv, in->dv, in->dtype);
     p.vec_dqk = aligned(g->dq, 16) && aligned(g->dk, 16);
     p.dh_last = g->dh_final;
@@ -274,7 +273,7 @@ int gated_delta_bwd(const gated_delta_inputs* in, const gated_delta_grads* g, vo
     int rc = delta_pack(*in, workspace, s, hs);
     if (rc == 0 && pack_dy)
         rc = cls_delta_pack_launch(g->dy, ws + s.dy, int64_t(elem_size(in->dtype)), in->batch, in->seqlen, in->heads, in->dv,
-                                   in->dv, g->dy_batch, g->dy_token, g->dy_head, hs);
+                                   dv, g->dy_batch, g->dy_token, g->dy_head, hs);
     if (rc == 0) rc = cls_delta_prep_launch(p, in->dtype, true, hs);
     if (rc == 0) rc = cls_delta_bwd_launch(p, in->dtype, hs);
     if (rc == 0) rc = cls_delta_grad_launch(p, in->dtype, hs);

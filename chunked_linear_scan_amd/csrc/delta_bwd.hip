@@ -13,203 +13,252 @@
 namespace cls {
 namespace {
 
-template <typename E, int DK, int WAVES>
-__global__ __launch_bounds__(64 * (WAVES + 4), 2) void delta_bwd_kernel(DeltaParams p) {
+template <typename E, int DK>
+__global__ __launch_bounds__(kWalkThreads) void delta_bwd_kernel(DeltaParams p) {
     typedef Mat<E> M;
+    typedef HalfOps<E> Op;
     typedef typename M::frag frag;
+    typedef typename Op::op op;
+    constexpr bool kSplit = M::kSplit;
     constexpr int kParts = ChunkMats<E>::kParts, NM = ChunkMats<E>::kAll;  // T - I, P, in their parts
-    typedef WalkLds<E, DK, NM, WAVES> Lds;
-    constexpr int C = M::kChunk, NT = C / 16, KT = DK / 16, KS = DK / 32;
-    constexpr bool AHEAD = DK <= 128;  // operands are read a step before their products: registers for it
+    typedef WalkLds<E, DK, NM> Lds;
+    constexpr int C = M::kChunk, NT = C / 16, OT = Op::OT;  // tiles of a chunk's tokens, of a half's
+    constexpr int KT = DK / 32, KS = DK / 64;               // of a wave's half of the keys' elements: tiles, steps
     extern __shared__ __attribute__((aligned(16))) char lds[];
 
-    const int nblk = (p.dv + Lds::kCols - 1) / Lds::kCols;
+    const int nblk = (p.dv + kWalkCols - 1) / kWalkCols;
     const int rep = p.H / p.Hk;
     const UnitPart u = unit_part(p.batch * p.Hk, rep * nblk);
     const int blk = u.part % nblk, h = u.unit % p.Hk * rep + u.part / nblk, b = u.unit / p.Hk;
     const int end = seq_end(p.seqlens, b, p.L), chunks = (end + C - 1) / C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave >= WAVES) {
-        const WalkColumns w{p.dy, p.sdy, p.dv_, bool(p.vec_dy), bool(p.vec_out)};
-        walk_load<E, DK, NM, WAVES>(p, w, lds, b, h, blk * Lds::kCols, end, chunks - 1, -1, chunks);
+    if (wave >= 4) {
+        const WalkColumns w{p.dy, p.sdy, p.dv_, bool(p.vec_out)};
+        walk_load<E, DK, NM>(p, w, lds, b, h, blk * kWalkCols, end, chunks - 1, -1, chunks);
         return;
     }
+    const int a = wave & 1, tile = wave >> 1;  // the wave's half, its tile of the columns
     const int l16 = lane16(), g4 = group4();
-    const int n = blk * Lds::kCols + wave * 16 + l16;  // the lane's column
-    const bool wave_on = blk * Lds::kCols + wave * 16 < p.dv;
+    const int n = blk * kWalkCols + tile * 16 + l16;  // the lane's column
 
     f32x4 S[KT];
-    load_state<KT>(S, p.dh_last, int64_t(b) * p.H + h, n, p);
-    const typename Lds::KTile kt;
-    const typename Lds::MTile mt;
-    const typename Lds::XTile xt;
-    const int oy = 4 * g4 * Lds::YP + wave * 16 + l16;
+    load_state<KT>(S, p.dh_last, int64_t(b) * p.H + h, n, a * (DK / 2), p);
+    const typename Lds::KTile kt(a * (DK / 2));
+    const typename Lds::MTile mt, xt(16 * tile);
+    const Exchange ex(lds, wave, Lds::kSlots);
+    const int oy = (C / 2 * a + 4 * g4) * Lds::YP + tile * 16 + l16;
+    constexpr int HALF = C / 2 * Lds::KTile::kPitch;  // of K
 
     walk<Lds>(lds, chunks, [&](int i, const Lds& m) {
-        if (!wave_on) return;
         const int64_t chunk = (int64_t(b) * p.nchunk + chunks - 1 - i) * p.H + h;
-        const auto factors = [&](int which, int t) { return *reinterpret_cast<const f32x4*>(m.v + which * C + 16 * t + 4 * g4); };
-        store_state<KT>(S, p.dstates, chunk, n, p);
-
-        // K dS, and beside it P^T dY
-        f32x4 dN[NT], later[NT], e[NT];
-        frag k[2][NT], y[NT / 2];
-        Two<E> st[2], P[NT][NT / 2];
+        const auto factors = [&](int which, int j) {
+            return *reinterpret_cast<const f32x4*>(m.v + which * C + C / 2 * a + 16 * j + 4 * g4);
+        };
+        const auto* ko = m.k + a * HALF;
+        const auto* kx = m.k + (1 - a) * HALF;
+        const auto read = [&](frag (&k)[NT], int s) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            dN[t] = later[t] = f32x4{0, 0, 0, 0};
-            if (AHEAD) k[0][t] = kt.rows(m.k, t, 0);
+            for (int j = 0; j < OT; ++j) {
+                k[OT + j] = kt.rows(kx, j, s);
+                k[j] = kt.rows(ko, j, s);
+            }
+        };
+
+        // the wave's share of K dS, tiles of its own tokens and of the other half's, and beside it P^T dY of its own
+        f32x4 kd[NT], later[OT], e[OT], rd[OT], be[OT], bs[OT];
+        frag k[2][NT];
+        Two<E> st[2];
+        read(k[0], 0);
+        const op yo = Op::tokens(xt, m.x, a, 0), yx = Op::tokens(xt, m.x, 1, 0);  // of dY: own tokens, the second half's
+        op Ph[OT], Pl[OT], Th[OT], Tl[OT], Xh[OT], Xl[OT];
+#pragma unroll
+        for (int j = 0; j < OT; ++j) {
+            Ph[j] = Op::cols(mt, m.m + kParts * Lds::MS, Lds::M1, a, a, j);
+            if constexpr (kSplit) Pl[j] = Op::cols(mt, m.m + (kParts + 1) * Lds::MS, Lds::M1, a, a, j);
+            later[j] = f32x4{0, 0, 0, 0};
+            rd[j] = factors(kRead, j);
         }
 #pragma unroll
-        for (int s = 0; s < NT / 2; ++s) y[s] = xt.cols(m.x, s, wave);
+        for (int t = 0; t < NT; ++t) kd[t] = f32x4{0, 0, 0, 0};
         st[0] = two<E>(S[0], S[1]);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const int at = AHEAD ? s & 1 : 0, at1 = AHEAD ? at ^ 1 : 0;
-            if (!AHEAD || s + 1 < KS) {
+            if (s + 1 < KS) {
+                read(k[(s + 1) & 1], s + 1);
+            } else {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) k[at1][t] = kt.rows(m.k, t, AHEAD ? s + 1 : s);
-            }
-            if (s < NT / 2) {  // P of outputs 32 s.., which reach the tiles up to theirs
-#pragma unroll
-                for (int t = 0; t <= 2 * s + 1; ++t) {
-                    P[t][s].hi = mt.cols(m.m + kParts * Lds::MS, s, t);
-                    if constexpr (M::kSplit) P[t][s].lo = mt.cols(m.m + (kParts + 1) * Lds::MS, s, t);
+                for (int j = 0; j < OT; ++j) {
+                    e[j] = factors(kWrite, j);
+                    Th[j] = Op::cols(mt, m.m, Lds::M1, a, a, j);
+                    if constexpr (kSplit) Tl[j] = Op::cols(mt, m.m + Lds::MS, Lds::M1, a, a, j);
                 }
             }
             fence();
             if (s + 1 < KS) st[(s + 1) & 1] = two<E>(S[2 * s + 2], S[2 * s + 3]);
-            if constexpr (M::kSplit) {
+            if constexpr (kSplit) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) dN[t] = M::mma(k[at][t], st[s & 1].lo, dN[t]);
+                for (int t = NT - 1; t >= 0; --t) kd[t] = M::mma(k[s & 1][t], st[s & 1].lo, kd[t]);
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) dN[t] = M::mma(k[at][t], st[s & 1].hi, dN[t]);
-            if (s > 0 && s <= NT / 2) {
+            for (int t = NT - 1; t >= 0; --t) kd[t] = M::mma(k[s & 1][t], st[s & 1].hi, kd[t]);
+            if (s == 0) {
+                if constexpr (kSplit) {
 #pragma unroll
-                for (int t = 0; t <= 2 * s - 1; ++t) later[t] = M::mma(P[t][s - 1].hi, y[s - 1], later[t]);
-                if constexpr (M::kSplit) {
-#pragma unroll
-                    for (int t = 0; t <= 2 * s - 1; ++t) later[t] = M::mma(P[t][s - 1].lo, y[s - 1], later[t]);
+                    for (int j = 0; j < OT; ++j) later[j] = Op::mma(Pl[j], yo, later[j]);
                 }
+#pragma unroll
+                for (int j = 0; j < OT; ++j) later[j] = Op::mma(Ph[j], yo, later[j]);
+                // what dY adds to dS: e^gamma dY of its own tokens
+#pragma unroll
+                for (int j = 0; j < OT; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) rd[j][r] *= Op::at(yo, j, r);
             }
-            interleave<2 * NT, 4>();
+            interleave<2 * NT, 5>();
             fence();
         }
-        // the operands of the rest
-        Two<E> T[NT][NT / 2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            e[t] = factors(kWrite, t);
+        for (int j = 0; j < OT; ++j) ex.put(j, kd[OT + j]);
+        if (a == 0) {  // outputs of the second half
 #pragma unroll
-            for (int s = t / 2; s < NT / 2; ++s) {
-                T[t][s].hi = mt.cols(m.m, s, t);
-                if constexpr (M::kSplit) T[t][s].lo = mt.cols(m.m + Lds::MS, s, t);
+            for (int j = 0; j < OT; ++j) {
+                Ph[j] = Op::cols(mt, m.m + kParts * Lds::MS, Lds::M1, 0, 1, j);
+                later[j] = Op::mma(Ph[j], yx, later[j]);
+                if constexpr (kSplit) {
+                    Pl[j] = Op::cols(mt, m.m + (kParts + 1) * Lds::MS, Lds::M1, 0, 1, j);
+                    later[j] = Op::mma(Pl[j], yx, later[j]);
+                }
             }
+        }
+        const auto qq = Op::two(rd);
+        lds_meet();  // 1: both halves' shares
+        f32x4 x[OT], dN[OT], Z[OT];
+#pragma unroll
+        for (int j = 0; j < OT; ++j) ex.get(j, x[j]);
+#pragma unroll
+        for (int j = 0; j < OT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dN[j][r] = fmaf(kd[j][r] + x[j][r], e[j][r], p.scale * later[j][r]);
+        // Z = dN + (T - I)^T dN: the second half's tokens reach the first's
+        const auto dn = Op::two(dN);
+        if (a) {
+            ex.put(4, dn.hi);
+            if constexpr (kSplit) ex.put(5, dn.lo);
+        }
+#pragma unroll
+        for (int j = 0; j < OT; ++j) Z[j] = dN[j];
+        if constexpr (kSplit) {
+#pragma unroll
+            for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Tl[j], dn.hi, Z[j]);
+#pragma unroll
+            for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Th[j], dn.lo, Z[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Th[j], dn.hi, Z[j]);
+#pragma unroll
+        for (int j = 0; j < OT; ++j) {
+            be[j] = factors(kBeta, j);
+            bs[j] = factors(kBetaStart, j);
+            if (a) continue;
+            Xh[j] = Op::cols(mt, m.m, Lds::M1, 0, 1, j);
+            if constexpr (kSplit) Xl[j] = Op::cols(mt, m.m + Lds::MS, Lds::M1, 0, 1, j);
+        }
+        op kc[2][2], qc[2][2];
+        const auto next = [&](int at, int half, int t) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                qc[at][y] = Op::tokens(kt, m.q, half, t + y);
+                kc[at][y] = Op::tokens(kt, m.k, half, t + y);
+            }
+        };
+        next(0, a, 0);
+        const float fade = m.v[kStart * C + C - 1];
+        lds_meet();  // 2: the second half's dN
+        if (a == 0) {
+            auto xx = dn;
+            ex.get(4, xx.hi);
+            if constexpr (kSplit) {
+                ex.get(5, xx.lo);
+#pragma unroll
+                for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Xl[j], xx.hi, Z[j]);
+#pragma unroll
+                for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Xh[j], xx.lo, Z[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Xh[j], xx.hi, Z[j]);
+        }
+        f32x4 w[OT];
+#pragma unroll
+        for (int j = 0; j < OT; ++j) w[j] = -(bs[j] * Z[j]);
+        const auto aa = Op::two(w);
+        ex.put(0, aa.hi);
+        ex.put(1, qq.hi);
+        if constexpr (kSplit) {
+            ex.put(2, aa.lo);
+            ex.put(3, qq.lo);
         }
         fence();
-        if constexpr (KS <= NT / 2) {
+        store_state<KT>(S, p.dstates, chunk, n, a * (DK / 2), p);
+        store_tokens<C>(Z, p.z, chunk, n, a, p);
+        // the state's gradient, by the half's own tokens, then by the others; two tiles in turn, as a product waits for
+        // the one before it on its tile
+        const auto add = [&](int half, const auto& ka, const auto& qy, bool more) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) later[t] = mma2<E>(P[t][NT / 2 - 1], y[NT / 2 - 1], later[t]);
-        }
+            for (int t = 0; t < KT; t += 2) {
+                const int at = t / 2 & 1;
+                if (t + 2 < KT) next(at ^ 1, half, t + 2);
+                else if (more) next(at ^ 1, 1 - half, 0);
+                fence();
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+                for (int y = 0; y < 2; ++y)
+                    if (more) S[t + y] *= fade;
+                if constexpr (kSplit) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dN[t][r] = fmaf(dN[t][r], e[t][r], p.scale * later[t][r]);
-        // Z = dN + (T - I)^T dN, from the last tokens: 32 s.. reach the tiles up to theirs
-        f32x4 Z[NT];
+                    for (int y = 0; y < 2; ++y) S[t + y] = Op::mma(qc[at][y], qy.lo, S[t + y]);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) Z[t] = dN[t];
-        Two<E> dn = two<E>(dN[NT - 2], dN[NT - 1]);
-        // beside it what dY adds to dS
-        Two<E> q[NT / 2], a[NT / 2];
-        f32x4 be[NT], bs[NT];
-#pragma unroll
-        for (int s = NT / 2 - 1; s >= 0; --s) {
-            be[2 * s] = factors(kBeta, 2 * s);
-            be[2 * s + 1] = factors(kBeta, 2 * s + 1);
-            bs[2 * s] = factors(kBetaStart, 2 * s);
-            bs[2 * s + 1] = factors(kBetaStart, 2 * s + 1);
-            f32x4 r0 = factors(kRead, 2 * s), r1 = factors(kRead, 2 * s + 1);
-            fence();
-            Two<E> next;
-            if (s > 0) next = two<E>(dN[2 * s - 2], dN[2 * s - 1]);
-            if constexpr (M::kSplit) {
-#pragma unroll
-                for (int t = 0; t <= 2 * s + 1; ++t) Z[t] = M::mma(T[t][s].lo, dn.hi, Z[t]);
-#pragma unroll
-                for (int t = 0; t <= 2 * s + 1; ++t) Z[t] = M::mma(T[t][s].hi, dn.lo, Z[t]);
-            }
-#pragma unroll
-            for (int t = 0; t <= 2 * s + 1; ++t) Z[t] = M::mma(T[t][s].hi, dn.hi, Z[t]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                r0[r] *= M::at(y[s], r);
-                r1[r] *= M::at(y[s], 4 + r);
-            }
-            q[s] = two<E>(r0, r1);
-            dn = next;
-            interleave<3 * (NT - 2), 6>();
-            fence();
-        }
-        const float fade = m.v[kStart * C + C - 1];
-        frag kc[2][2][NT / 2], qc[2][2][NT / 2];
-        const auto next = [&](int at, int t) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int s = 0; s < NT / 2; ++s) {
-                    qc[at][u][s] = kt.cols(m.q, s, t + u);
-                    kc[at][u][s] = kt.cols(m.k, s, t + u);
+                    for (int y = 0; y < 2; ++y) S[t + y] = Op::mma(kc[at][y], ka.lo, S[t + y]);
                 }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) S[t + y] = Op::mma(qc[at][y], qy.hi, S[t + y]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) S[t + y] = Op::mma(kc[at][y], ka.hi, S[t + y]);
+            }
         };
-        if (AHEAD) next(0, 0);
+        add(a, aa, qq, true);
+        if constexpr (KT / 2 % 2 == 1) {  // the other half's first tiles are where the last ones were not
 #pragma unroll
-        for (int s = 0; s < NT / 2; ++s) a[s] = two<E>(-(bs[2 * s] * Z[2 * s]), -(bs[2 * s + 1] * Z[2 * s + 1]));
-        store_tokens<C>(Z, p.z, chunk, n, p);
-        // two tiles in turn: a product waits for the one before it on its tile
-#pragma unroll
-        for (int t = 0; t < KT; t += 2) {
-            const int at = AHEAD ? t / 2 & 1 : 0;
-            if (!AHEAD) next(0, t);
-            else if (t + 2 < KT) next(at ^ 1, t + 2);
-            fence();
-#pragma unroll
-            for (int u = 0; u < 2; ++u) S[t + u] *= fade;
-#pragma unroll
-            for (int s = 0; s < NT / 2; ++s) {
-                if constexpr (M::kSplit) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) S[t + u] = M::mma(qc[at][u][s], q[s].lo, S[t + u]);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) S[t + u] = M::mma(kc[at][u][s], a[s].lo, S[t + u]);
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) S[t + u] = M::mma(qc[at][u][s], q[s].hi, S[t + u]);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) S[t + u] = M::mma(kc[at][u][s], a[s].hi, S[t + u]);
-            }
-            if (t < NT) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) put_column<E, Lds::YP>(m.y + oy, t + u, be[t + u] * Z[t + u]);
+            for (int y = 0; y < 2; ++y) {
+                kc[0][y] = kc[1][y];
+                qc[0][y] = qc[1][y];
             }
         }
+        lds_meet();  // 3: what the other half's tokens add
+        auto xa = aa, xq = qq;
+        ex.get(0, xa.hi);
+        ex.get(1, xq.hi);
+        if constexpr (kSplit) {
+            ex.get(2, xa.lo);
+            ex.get(3, xq.lo);
+        }
+        add(1 - a, xa, xq, false);
+#pragma unroll
+        for (int j = 0; j < OT; ++j) put_column<E, Lds::YP>(m.y + oy, j, be[j] * Z[j]);
         settle(S[KT - 1]);
     });
-    if (p.dh0) store_state<KT>(S, p.dh0, int64_t(b) * p.H + h, n, p);
+    if (p.dh0) store_state<KT>(S, p.dh0, int64_t(b) * p.H + h, n, a * (DK / 2), p);
 }
 
-template <typename E, int DK, int WAVES>
+template <typename E, int DK>
 int launch(const DeltaParams& p, hipStream_t stream) {
-    typedef WalkLds<E, DK, ChunkMats<E>::kAll, WAVES> Lds;
+    typedef WalkLds<E, DK, ChunkMats<E>::kAll> Lds;
     static DeviceOnce once;
     const int st = run_once_per_device(once, [] {
-        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_bwd_kernel<E, DK, WAVES>),
+        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_bwd_kernel<E, DK>),
                                    hipFuncAttributeMaxDynamicSharedMemorySize, Lds::kBytes) == hipSuccess ? 0 : -7;
     });
     if (st != 0) return st;
-    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + Lds::kCols - 1) / Lds::kCols));
-    delta_bwd_kernel<E, DK, WAVES><<<wgs, Lds::kThreads, Lds::kBytes, stream>>>(p);
+    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + kWalkCols - 1) / kWalkCols));
+    delta_bwd_kernel<E, DK><<<wgs, kWalkThreads, Lds::kBytes, stream>>>(p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
@@ -218,8 +267,6 @@ int launch(const DeltaParams& p, hipStream_t stream) {
 
 int cls_delta_bwd_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream) {
     return cls::by_type(dtype, p.dk, [&](auto e, auto dk) {
-        typedef decltype(e) E;
-        constexpr int DK = decltype(dk)::value;
-        return cls::walk_waves(p) == 2 ? cls::launch<E, DK, 2>(p, stream) : cls::launch<E, DK, 4>(p, stream);
+        return cls::launch<decltype(e), decltype(dk)::value>(p, stream);
     });
 }

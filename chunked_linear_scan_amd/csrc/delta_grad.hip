@@ -200,8 +200,8 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_g
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int col = d0 + 16 * u + 4 * g4;
-            y1[u] = in ? load4<E>(Yi, col, p.dv, p.vec_dy) : f32x4{0, 0, 0, 0};
-            v1[u] = in ? load4<E>(Vi, col, p.dv, p.vec_v) : f32x4{0, 0, 0, 0};
+            y1[u] = in ? load4<E>(Yi, col, p.dv, true) : f32x4{0, 0, 0, 0};
+            v1[u] = in ? load4<E>(Vi, col, p.dv, true) : f32x4{0, 0, 0, 0};
         }
     };
     ahead(0);

@@ -1,23 +1,23 @@
-// What the forward and the backward walk over the chunks share: a workgroup of
-// two or four waves that compute, 16 columns of a state each, and four that load.  The
-// computing waves' work on a chunk is one long chain of products, so what
-// bounds a walk is that chain's latency: the loading waves keep the traffic with memory
-// (but for kept states) out of it, and the registers that this
-// frees hold the next operands while a product runs.  V (or dY) comes and y (or
-// dV) leaves through LDS as whole rows, too.
+// What the forward and the backward walk over the chunks share.  A chunk's work
+// on a column of the state is one long chain of products, and of vector instructions on
+// their results, of which a wave issues one in 8.5 cycles: that chain's
+// latency bounds a walk, not any unit's rate.  So
+//   - two waves have 16 columns of a state between them, each the rows of one half of the
+//     keys' elements and the tokens of one half of a chunk.  Products with the state are sums of two halves, which the
+//     waves exchange through LDS, as they do what the other half's tokens add to the state: four
+//     meetings a chunk, and half the instructions between them;
+//   - four more waves load, and store what is not kept for the gradients, two chunks ahead;
+//   - operands are read from LDS a step before their products, and products are
+//     interleaved with vector instructions.
+// A workgroup has 32 columns: four computing waves, one to a SIMD, and four that load.  A chunk of 64 tokens and keys of
+// 128 takes 1.7 us, 1.5 of them the computing waves'.  (One wave to 16 columns: 1.95 us with two computing waves to a workgroup,
+// 2.3 with four, where their reads of LDS took 3200 cycles of the 5500.)
 #pragma once
 
 #include "delta.hpp"
 #include "device_once.hpp"
 
 namespace cls {
-
-// The computing waves of a workgroup: what bounds four is LDS, from which each reads the chunk's matrices for itself
-// (3200 cycles a chunk of 128-element keys, of which the products take 1700), so while a compute unit is free for every
-// 32 columns there are two.
-inline int walk_waves(const DeltaParams& p) {
-    return int64_t(p.batch) * p.H * ((p.dv + 31) / 32) <= 256 ? 2 : 4;
-}
 
 // Asks for N matrix instructions with V vector ones behind each, of those between two scheduling barriers: left to
 // itself the compiler issues products in blocks, during which the vector unit waits, and the other way round.
@@ -39,105 +39,197 @@ __device__ __forceinline__ void settle(f32x4& x) {
     x = f32x4{a, b, c, d};
 }
 
-// LDS of a walk: K, Q, NM matrices of a chunk, its columns of V and its factors, and those of y; twice where that fits.
-template <typename E, int DK, int NM, int WAVES>
+constexpr int kWalkCols = 32;      // columns to a workgroup
+constexpr int kWalkThreads = 512;  // computing waves (16 (w / 2).. of the columns, half w % 2), then loading waves
+
+// LDS of a walk: K, Q, NM triangular matrices of a chunk (32 columns of all rows, then the others of the last 32), its
+// columns of V and its factors; those of y; what waves exchange.  The first two twice where that fits.
+template <typename E, int DK, int NM>
 struct WalkLds {
     typedef typename Mat<E>::raw raw;
     typedef LdsTile<E, DK> KTile;
-    typedef LdsTile<E, Mat<E>::kChunk> MTile;
-    typedef LdsTile<E, 64> XTile;  // whose second half two waves do not use
-    static constexpr int C = Mat<E>::kChunk, kCols = 16 * WAVES;
-    static constexpr int kThreads = 64 * (WAVES + 4);  // computing waves, then loading waves
-    static constexpr int KS = C * KTile::kPitch, MS = C * MTile::kPitch, XS = C * XTile::kPitch;
-    static constexpr int YP = 64 + 16 / int(sizeof(raw));  // pitch of y: four rows touch every bank once
-    static constexpr int kBuffer = int((2 * KS + NM * MS + XS) * sizeof(raw) + kVecs * C * sizeof(float));
+    typedef LdsTile<E, 32> MTile;  // of a block of 32 columns, and of V
+    static constexpr int C = Mat<E>::kChunk;
+    static constexpr int KS = C * KTile::kPitch, M1 = C * MTile::kPitch, MS = M1 + (C - 32) * MTile::kPitch;
+    static constexpr int YP = kWalkCols + 16 / int(sizeof(raw));  // pitch of y
+    static constexpr int kBuffer = int((2 * KS + NM * MS + M1) * sizeof(raw) + kVecs * C * sizeof(float));
     static constexpr int kOut = C * YP * int(sizeof(raw));
-    static constexpr bool kTwice = 2 * (kBuffer + kOut) <= 160 * 1024;
-    static constexpr int kBytes = (kTwice ? 2 : 1) * (kBuffer + kOut);
+    static constexpr int kSlots = 6, kExchange = 4 * kSlots * 1024;
+    static constexpr bool kTwice = 2 * (kBuffer + kOut) + kExchange <= 160 * 1024;
+    static constexpr int kBytes = (kTwice ? 2 : 1) * (kBuffer + kOut) + kExchange;
     raw *k, *q, *m, *x, *y;
     float* v;
     __device__ __forceinline__ WalkLds(char* lds, int at) {
         const int one = kTwice ? at & 1 : 0;
-        k = reinterpret_cast<raw*>(lds + one * kBuffer);
+        k = reinterpret_cast<raw*>(lds + kExchange + one * kBuffer);
         q = k + KS;
         m = q + KS;
         x = m + NM * MS;
-        v = reinterpret_cast<float*>(x + XS);
-        y = reinterpret_cast<raw*>(lds + (kTwice ? 2 : 1) * kBuffer + one * kOut);
+        v = reinterpret_cast<float*>(x + M1);
+        y = reinterpret_cast<raw*>(lds + kExchange + (kTwice ? 2 : 1) * kBuffer + one * kOut);
     }
 };
 
+// ---------------------------------------------------------------------------
+// operands whose depths are half a chunk's tokens: two tiles with 16-bit elements, one (half an operand) in fp32
+// ---------------------------------------------------------------------------
+template <typename E>
+struct HalfOps {
+    typedef Mat<E> M;
+    typedef typename M::raw raw;
+    typedef typename M::frag op;
+    static constexpr int OT = M::kChunk / 32;  // tiles of half a chunk's tokens
+    static __device__ __forceinline__ op cvt(const f32x4 (&x)[OT]) { return M::cvt(x[0], x[1]); }
+    static __device__ __forceinline__ float at(const op& x, int t, int r) { return M::at(x, 4 * t + r); }
+    static __device__ __forceinline__ f32x4 mma(const op& a, const op& b, f32x4 c) { return M::mma(a, b, c); }
+    static __device__ __forceinline__ Two<E> two(const f32x4 (&x)[OT]) { return cls::two<E>(x[0], x[1]); }
+    // Of a chunk's triangular matrix the rows of tile j of half h against the depths of half hd (h >= hd).
+    template <typename T>
+    static __device__ __forceinline__ op rows(const T& t, const raw* m, int m1, int h, int hd, int j) {
+        return t.rows(m + (hd ? m1 : 32 * h * T::kPitch), j, 0);
+    }
+    // Its columns of tile j of half h against the depths of half hd (h <= hd).
+    template <typename T>
+    static __device__ __forceinline__ op cols(const T& t, const raw* m, int m1, int h, int hd, int j) {
+        return t.cols(m + (h ? m1 : 32 * hd * T::kPitch), 0, j);
+    }
+    // Columns of tile j of a matrix whose rows are tokens, depths those of half hd.
+    template <typename T>
+    static __device__ __forceinline__ op tokens(const T& t, const raw* m, int hd, int j) {
+        return t.cols(m + 32 * hd * T::kPitch, 0, j);
+    }
+};
+
+template <>
+struct HalfOps<ElemF32> {
+    typedef Mat<ElemF32> M;
+    typedef uint32_t raw;
+    typedef f32x4 op;
+    static constexpr int OT = 1;
+    static __device__ __forceinline__ op cvt(const f32x4 (&x)[1]) { return x[0]; }
+    static __device__ __forceinline__ float at(const op& x, int, int r) { return x[r]; }
+    static __device__ __forceinline__ f32x4 mma(const op& a, const op& b, f32x4 c) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
+        return c;
+    }
+    struct One { op hi, lo; };
+    static __device__ __forceinline__ One two(const f32x4 (&x)[1]) { return {x[0], x[0]}; }
+    template <typename T>
+    static __device__ __forceinline__ op rows(const T&, const raw* m, int, int h, int hd, int) {
+        return *reinterpret_cast<const f32x4*>(m + (16 * h + lane16()) * T::kPitch + 16 * hd + 4 * group4());
+    }
+    template <typename T>
+    static __device__ __forceinline__ op cols(const T& t, const raw* m, int, int h, int hd, int) {
+        return tokens(t, m, hd, h);
+    }
+    template <typename T>
+    static __device__ __forceinline__ op tokens(const T& t, const raw* m, int hd, int j) {
+        const raw* at = reinterpret_cast<const raw*>(reinterpret_cast<const char*>(m + 16 * hd * T::kPitch) + t.c[0]) + 16 * j;
+        op x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = as_float(at[k * T::kPitch]);
+        return x;
+    }
+};
+
+// A wave's place for what its partner reads: slots of 16 bytes to a lane.
+struct Exchange {
+    char *mine, *other;
+    __device__ __forceinline__ Exchange(char* lds, int wave, int slots) {
+        const int lane = 16 * (threadIdx.x & 63);
+        mine = lds + wave * slots * 1024 + lane;
+        other = lds + (wave ^ 1) * slots * 1024 + lane;
+    }
+    template <typename T>
+    __device__ __forceinline__ void put(int slot, const T& x) const {
+        static_assert(sizeof(T) == 16, "");
+        *reinterpret_cast<u32x4*>(mine + slot * 1024) = __builtin_bit_cast(u32x4, x);
+    }
+    template <typename T>
+    __device__ __forceinline__ void get(int slot, T& x) const {
+        static_assert(sizeof(T) == 16, "");
+        x = __builtin_bit_cast(T, *reinterpret_cast<const u32x4*>(other + slot * 1024));
+    }
+};
+
+// ---------------------------------------------------------------------------
+// the loading waves
+// ---------------------------------------------------------------------------
 // Columns of V or dY in, of y or dV out.
 struct WalkColumns {
     const void* x;
     Strided3 sx;
     void* y;
-    bool vec_x, vec_y;
+    bool vec_y;
 };
 
-// The loading waves' part: chunks first, first + step, .. (n of them).
-template <typename E, int DK, int NM, int WAVES>
+// Chunks first, first + step, .. (n of them).
+template <typename E, int DK, int NM>
 __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumns& w, char* lds, int b, int h, int col0, int end,
                                           int first, int step, int n) {
     typedef Mat<E> M;
     typedef typename M::raw raw;
     typedef ChunkMats<E> CM;
-    typedef WalkLds<E, DK, NM, WAVES> Lds;
+    typedef WalkLds<E, DK, NM> Lds;
     constexpr int C = M::kChunk, THREADS = 256;
     constexpr int64_t SZ = sizeof(raw);
     typedef TileRegs<E, C, DK, THREADS> KRegs;
-    typedef TileRegs<E, C, C, THREADS> MRegs;
-    typedef TileRegs<E, C, 64, THREADS> XRegs;
-    const int kh = h / (p.H / p.Hk), tid = (threadIdx.x - 64 * WAVES) % THREADS;
+    typedef TileRegs<E, C, 32, THREADS> XRegs;  // 32 columns: of a matrix, of V, of y
+    static_assert(XRegs::N == 1, "");
+    constexpr int LOW = (C - 32) * XRegs::PER_ROW;  // threads with a vector of the last 32 columns
+    const int kh = h / (p.H / p.Hk), tid = threadIdx.x % THREADS;
     const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + kh * p.sk.head;
     const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + kh * p.sq.head;
     const raw* X = static_cast<const raw*>(w.x) + b * w.sx.batch + h * w.sx.head + col0;
-    const int cols = p.dv - col0 < Lds::kCols ? p.dv - col0 : Lds::kCols;
+    const int cols = p.dv - col0 < kWalkCols ? p.dv - col0 : kWalkCols;
+    const int xrow = tid / XRegs::PER_ROW, xcol = tid % XRegs::PER_ROW * XRegs::VE;  // a thread's vector of 32 columns
     const uint32_t ok = KRegs::offset(p.sk.token, p.dk, tid), oq = KRegs::offset(p.sq.token, p.dk, tid);
-    const uint32_t ox = XRegs::offset(w.sx.token, cols, tid), om = MRegs::offset(C, C, tid);
-    const uint32_t om0 = MRegs::offset(C, 32, tid);  // of the first 32 rows only 32 columns are there
-    // Two chunks in flight: a chunk may take less time than a load from memory.  (One where LDS holds one: dk above 128,
-    // whose chunks are longer and whose vectors would be twice as many.)
+    // two chunks in flight, where LDS has two: a chunk may take less time than a load from memory
     constexpr int SETS = Lds::kTwice ? 2 : 1;
     struct Set {
         KRegs k, q;
-        MRegs m[NM];
-        XRegs x;
-        u32x4 v;
+        u32x4 m[NM], low[NM], x, v;
     } set[SETS];
-    const auto fetch = [&](Set& r, int i) {
-        const int c = first + i * step, t0 = c * C, left = end - t0;
-        r.k.load(buffer(K + t0 * p.sk.token, left * p.sk.token * SZ), ok, p.sk.token);
-        r.q.load(buffer(Q + t0 * p.sq.token, left * p.sq.token * SZ), oq, p.sq.token);
-        const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
-        const raw* mats = static_cast<const raw*>(p.mats) + chunk * CM::kAll * CM::kSize;
-#pragma unroll
-        for (int m = 0; m < NM; ++m) r.m[m].load(buffer(mats + m * CM::kSize), om, C, om0);
-        const Buffer bx = buffer(X + t0 * w.sx.token, left * w.sx.token * SZ - col0 * SZ);
-        if (w.vec_x) {
-            r.x.load(bx, ox, w.sx.token);
-        } else {
-#pragma unroll
-            for (int v = 0; v < XRegs::N; ++v) {
-                const int at = tid + v * THREADS, row = at / XRegs::PER_ROW, col = at % XRegs::PER_ROW * XRegs::VE;
-                r.x.r[v] = u32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int e = 0; e < XRegs::VE; ++e) {
-                    const uint32_t one = load_one<E>(bx, col + e < cols ? uint32_t((row * w.sx.token + col + e) * SZ) : kOutside);
-                    if constexpr (SZ == 4) r.x.r[v][e] = one;
-                    else r.x.r[v][e >> 1] |= one << (16 * (e & 1));
-                }
-            }
-        }
-        r.v = ldg_b128(p.vecs + chunk * kVecs * C + 4 * (tid < kVecs * C / 4 ? tid : 0));
+    const auto fetch_keys = [&](KRegs& r, const raw* from, const Strided3& s, uint32_t at, int i) {
+        const int t0 = (first + i * step) * C;
+        r.load(buffer(from + t0 * s.token, (end - t0) * s.token * SZ), at, s.token);
+        fence();
     };
-    const auto put = [&](const Set& r, int i) {
-        const Lds to(lds, i);
-        r.k.template store<typename Lds::KTile>(to.k, tid);
-        r.q.template store<typename Lds::KTile>(to.q, tid);
+    const auto fetch_k = [&](Set& r, int i) { fetch_keys(r.k, K, p.sk, ok, i); };
+    const auto fetch_q = [&](Set& r, int i) { fetch_keys(r.q, Q, p.sq, oq, i); };
+    const auto fetch_rest = [&](Set& r, int i) {
+        const int c = first + i * step, t0 = c * C, left = end - t0;
+        const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
+        // A wait counts the loads behind the one that it is for.  So none is under a branch, or the other set's would be
+        // waited for, too.
+        const Buffer bm = buffer(static_cast<const raw*>(p.mats) + chunk * CM::kAll * CM::kSize);
 #pragma unroll
-        for (int m = 0; m < NM; ++m) r.m[m].template store<typename Lds::MTile>(to.m + m * Lds::MS, tid);
-        r.x.template store<typename Lds::XTile>(to.x, tid);
+        for (int m = 0; m < NM; ++m) {
+            const uint32_t at = uint32_t((m * CM::kSize + xrow * C + xcol) * SZ);
+            r.m[m] = __builtin_amdgcn_raw_buffer_load_b128(bm, int(at), 0, 0);
+            if constexpr (LOW > 0)
+                r.low[m] = __builtin_amdgcn_raw_buffer_load_b128(bm, int(tid < LOW ? at + uint32_t((32 * C + 32) * SZ) : kOutside), 0, 0);
+        }
+        const Buffer bx = buffer(X + t0 * w.sx.token, left * w.sx.token * SZ - col0 * SZ);
+        r.x = __builtin_amdgcn_raw_buffer_load_b128(
+            bx, int(xcol < cols ? uint32_t((xrow * w.sx.token + xcol) * SZ) : kOutside), 0, 0);
+        r.v = ldg_b128(p.vecs + chunk * kVecs * C + 4 * (tid < kVecs * C / 4 ? tid : 0));
+        fence();
+    };
+    const auto fetch = [&](Set& r, int i) {
+        fetch_k(r, i);
+        fetch_q(r, i);
+        fetch_rest(r, i);
+    };
+    const auto put_keys = [&](const KRegs& r, raw* to) { r.template store<typename Lds::KTile>(to, tid); };
+    const auto put_rest = [&](const Set& r, const Lds& to) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            Lds::MTile::put(to.m + m * Lds::MS, xrow, xcol, r.m[m]);
+            if (LOW > 0 && tid < LOW) Lds::MTile::put(to.m + m * Lds::MS + Lds::M1, xrow, xcol, r.low[m]);
+        }
+        Lds::MTile::put(to.x, xrow, xcol, r.x);
         if (tid < kVecs * C / 4) *reinterpret_cast<u32x4*>(to.v + 4 * tid) = r.v;
     };
     const int64_t row = int64_t(p.H) * p.dv;  // of a token of y
@@ -146,21 +238,17 @@ __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumn
         const Lds from(lds, i);
         const int t0 = (first + i * step) * C;
         const Buffer by = buffer(Y + t0 * row, int64_t(p.L - t0) * row * SZ - (int64_t(h) * p.dv + col0) * SZ);
+        u32x4 x = *reinterpret_cast<const u32x4*>(from.y + xrow * Lds::YP + xcol);
+        if (t0 + xrow >= end) x = u32x4{0, 0, 0, 0};  // padding
+        const uint32_t to = uint32_t((xrow * row + xcol) * SZ);
+        if (w.vec_y) {
+            __builtin_amdgcn_raw_buffer_store_b128(x, by, int(xcol < cols ? to : kOutside), 0, 0);
+        } else {
 #pragma unroll
-        for (int v = 0; v < XRegs::N; ++v) {
-            const int at = tid + v * THREADS, r = at / XRegs::PER_ROW, col = at % XRegs::PER_ROW * XRegs::VE;
-            u32x4 x = *reinterpret_cast<const u32x4*>(from.y + r * Lds::YP + col);
-            if (t0 + r >= end) x = u32x4{0, 0, 0, 0};  // padding
-            const uint32_t to = uint32_t((r * row + col) * SZ);
-            if (w.vec_y) {
-                __builtin_amdgcn_raw_buffer_store_b128(x, by, int(col < cols ? to : kOutside), 0, 0);
-            } else {
-#pragma unroll
-                for (int e = 0; e < XRegs::VE; ++e) {
-                    const uint32_t word = x[SZ == 4 ? e : e >> 1], at2 = col + e < cols ? to + uint32_t(e * SZ) : kOutside;
-                    if constexpr (SZ == 4) __builtin_amdgcn_raw_buffer_store_b32(word, by, int(at2), 0, 0);
-                    else __builtin_amdgcn_raw_buffer_store_b16(uint16_t(word >> (16 * (e & 1))), by, int(at2), 0, 0);
-                }
+            for (int e = 0; e < XRegs::VE; ++e) {
+                const uint32_t word = x[SZ == 4 ? e : e >> 1], at = xcol + e < cols ? to + uint32_t(e * SZ) : kOutside;
+                if constexpr (SZ == 4) __builtin_amdgcn_raw_buffer_store_b32(word, by, int(at), 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b16(uint16_t(word >> (16 * (e & 1))), by, int(at), 0, 0);
             }
         }
     };
@@ -168,29 +256,49 @@ __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumn
     if (n > 0) {
         fetch(set[0], 0);
         if constexpr (Lds::kTwice) {
-            // while chunk i is computed: y of the one before leaves, the one behind it comes
+            const Lds lds0(lds, 0);
             fetch(set[1], last(1));
-            put(set[0], 0);
+            put_keys(set[0].k, lds0.k);
+            put_keys(set[0].q, lds0.q);
+            put_rest(set[0], lds0);
             fetch(set[0], last(2));
             lds_meet();
-            for (int i = 0; i < n; i += 2) {
+            // While chunk i is computed the one behind it comes and y of the one before leaves, in pieces between the
+            // computing waves' meetings.  A piece's registers are loaded again at once (1 x 32768 x 32 heads of 128: 891 us;
+            // all loads behind the last piece: 1150).  Behind the last chunk there is one more that nobody reads.
+            const auto turn = [&](Set& r, int i) {
+                const Lds to(lds, i + 1);
+                put_keys(r.k, to.k);
+                fetch_k(r, last(i + 3));
+                lds_meet();
+                put_keys(r.q, to.q);
+                fetch_q(r, last(i + 3));
+                lds_meet();
+                put_rest(r, to);
+                fetch_rest(r, last(i + 3));
+                lds_meet();
                 if (i > 0) out(i - 1);
-                if (i + 1 < n) put(set[1], i + 1);
-                fetch(set[1], last(i + 3));
                 lds_meet();
-                if (i + 1 == n) break;
-                out(i);
-                if (i + 2 < n) put(set[0], i + 2);
-                fetch(set[0], last(i + 4));
-                lds_meet();
+            };
+            int i = 0;
+            for (; i + 1 < n; i += 2) {  // no way from one set's turn to the same set's, for the waits' sake
+                turn(set[1], i);
+                turn(set[0], i + 1);
             }
+            if (i < n) turn(set[1], i);
         } else {
+            const Lds to(lds, 0);
             for (int i = 0; i < n; ++i) {
                 lds_meet();
                 if (i > 0) out(i - 1);
-                put(set[0], i);
+                put_keys(set[0].k, to.k);
+                put_keys(set[0].q, to.q);
+                put_rest(set[0], to);
                 lds_meet();
                 fetch(set[0], last(i + 1));
+                lds_meet();
+                lds_meet();
+                lds_meet();
             }
             lds_meet();
         }
@@ -201,7 +309,7 @@ __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumn
     for (int64_t at = tid; at < (p.L - t1) * cols; at += THREADS) Y[(t1 + at / cols) * row + at % cols] = raw(0);
 }
 
-// The computing waves' part: f(i, lds) for every chunk that the loading waves bring.
+// The computing waves' part: f(i, lds) for every chunk that the loading waves bring, which meets three times.
 template <typename Lds, typename F>
 __device__ __forceinline__ void walk(char* lds, int n, F&& f) {
     if (n == 0) return;
@@ -221,17 +329,20 @@ __device__ __forceinline__ void walk(char* lds, int n, F&& f) {
     }
 }
 
-// A lane's part of a state [dv, dk] in memory: column n, rows 4 (l/16) + r of each tile; `of` is the state's place
-// among those of all sequences and heads (and chunks).
+// ---------------------------------------------------------------------------
+// states in memory
+// ---------------------------------------------------------------------------
+// A lane's part of a state [dv, dk]: column n, keys' elements first + 16 t + 4 (l/16) + r; `of` is the state's place among
+// those of all sequences and heads (and chunks).
 template <int KT>
-__device__ __forceinline__ void load_state(f32x4 (&S)[KT], const float* from, int64_t of, int n, const DeltaParams& p) {
+__device__ __forceinline__ void load_state(f32x4 (&S)[KT], const float* from, int64_t of, int n, int first, const DeltaParams& p) {
 #pragma unroll
     for (int t = 0; t < KT; ++t) S[t] = f32x4{0, 0, 0, 0};
     if (from) {
         const Buffer b = buffer(from + of * p.dv * p.dk, int64_t(p.dv) * p.dk * 4);
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            const int d = 16 * t + 4 * group4();
+            const int d = first + 16 * t + 4 * group4();
             const uint32_t at = uint32_t(n * p.dk + d) * 4;
             if (p.dk % 4 == 0) {
                 S[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, int(d < p.dk && n < p.dv ? at : kOutside), 0, 0));
@@ -253,11 +364,11 @@ __device__ __forceinline__ void load_state(f32x4 (&S)[KT], const float* from, in
         }
 }
 template <int KT>
-__device__ __forceinline__ void store_state(const f32x4 (&S)[KT], float* to, int64_t of, int n, const DeltaParams& p) {
+__device__ __forceinline__ void store_state(const f32x4 (&S)[KT], float* to, int64_t of, int n, int first, const DeltaParams& p) {
     const Buffer b = buffer(to + of * p.dv * p.dk, int64_t(p.dv) * p.dk * 4);
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-        const int d = 16 * t + 4 * group4();
+        const int d = first + 16 * t + 4 * group4();
         const uint32_t at = uint32_t(n * p.dk + d) * 4;
         if (p.dk % 4 == 0) {
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[t]), b, int(d < p.dk && n < p.dv ? at : kOutside), 0, 0);
@@ -267,14 +378,14 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[KT], float* to, int
         }
     }
 }
-// A column's values of the chunk's tokens: [dv, C].
+// A column's values of half h of the chunk's tokens: [dv, C].
 template <int C>
-__device__ __forceinline__ void store_tokens(const f32x4 (&x)[C / 16], float* to, int64_t chunk, int n, const DeltaParams& p) {
+__device__ __forceinline__ void store_tokens(const f32x4 (&x)[C / 32], float* to, int64_t chunk, int n, int h, const DeltaParams& p) {
     const Buffer b = buffer(to + chunk * p.dv * C, int64_t(p.dv) * C * 4);
 #pragma unroll
-    for (int t = 0; t < C / 16; ++t)
+    for (int t = 0; t < C / 32; ++t)
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x[t]), b,
-                                               int(n < p.dv ? uint32_t(n * C + 16 * t + 4 * group4()) * 4 : kOutside), 0, 0);
+                                               int(n < p.dv ? uint32_t(n * C + C / 2 * h + 16 * t + 4 * group4()) * 4 : kOutside), 0, 0);
 }
 
 // A result tile's rows to a column of y in LDS.

@@ -58,8 +58,9 @@ extern "C" {
  *
  * heads is a multiple of kheads; dk is 1..256 and dv 1..65536
  * (SSD_ERR_UNSUPPORTED above).  SSD_ERR_SHAPE, too, for batch or heads above
- * 2^20, seqlen above 2^30, heads * dv or kheads * 256 above 2^23, strides above 2^40, and where a launch would have 2^32 threads or more
- * (256 for each 64 of dv, head and sequence; 256 for each chunk, head and
+ * 2^20, seqlen above 2^30, heads * dv (dv to whole vectors) or
+ * kheads * 256 above 2^23, strides above 2^40, and where a launch would have 2^32 threads or more
+ * (512 for each 32 of dv, head and sequence; 256 for each chunk, head and
  * sequence; with gradients and heads > kheads one for each element of q).
  */
 typedef struct {
@@ -83,8 +84,8 @@ int64_t gated_delta_chunk(int dtype);
 
 /* Bytes of workspace for a forward or a backward call, and of the checkpoints
  * (0 for sizes that are refused).  They depend on the strides and pointers of q,
- * k and v, too: rows of q and k that are not whole 16-byte vectors, and tokens less than
- * a row or more than 2^23 elements apart, are copied into the workspace first. */
+ * k and v, too: rows that are not whole 16-byte vectors, and tokens less than a
+ * row or more than 2^23 elements apart, are copied into the workspace first. */
 size_t gated_delta_workspace_size(const gated_delta_inputs* in);
 size_t gated_delta_bwd_workspace_size(const gated_delta_inputs* in);
 size_t gated_delta_checkpoint_size(const gated_delta_inputs* in);

@@ -143,12 +143,12 @@ def test_delta_refuses_other_pointers():
 
 
 # a misaligned output is what is refused after the sizes
-LIMITS = [(dict(batch=1 << 20, seqlen=1, heads=8), ALIGN), (dict(batch=1 << 20, seqlen=64, heads=16), SHAPE),
+LIMITS = [(dict(batch=1 << 20, seqlen=1, heads=6), SHAPE), (dict(batch=1 << 20, seqlen=1, kheads=1, heads=3), ALIGN), (dict(batch=1 << 20, seqlen=64, heads=16), SHAPE),
           (dict(batch=1, seqlen=1 << 30, kheads=1, heads=1), SHAPE), (dict(batch=1, seqlen=(1 << 30) - 64, kheads=1, heads=1), ALIGN),
           (dict(batch=1, seqlen=(1 << 29) - 32, kheads=1, heads=1, dtype=0), ALIGN),
           (dict(batch=1, seqlen=1 << 29, kheads=1, heads=1, dtype=0), SHAPE),
-          (dict(batch=1 << 14, seqlen=1, kheads=1, heads=1, dv=65536), SHAPE),
-          (dict(batch=(1 << 14) - 1, seqlen=1, kheads=1, heads=1, dv=65536), ALIGN),
+          (dict(batch=1 << 12, seqlen=1, kheads=1, heads=1, dv=65536), SHAPE),
+          (dict(batch=(1 << 12) - 1, seqlen=1, kheads=1, heads=1, dv=65536), ALIGN),
           (dict(batch=1, heads=128, dv=65536), ALIGN), (dict(batch=1, heads=130, dv=65536), SHAPE),  # 2^23 in a token's row
           (dict(batch=1, kheads=1 << 15, heads=1 << 15), ALIGN), (dict(batch=1, kheads=(1 << 15) + 1, heads=(1 << 15) + 1), SHAPE)]
 
@@ -187,7 +187,7 @@ def test_delta_sizes_add_up():
         assert lib.gated_delta_checkpoint_size(ctypes.byref(s)) == states + tokens
         assert lib.gated_delta_bwd_workspace_size(ctypes.byref(s)) == fwd + states + tokens + 2 * up(2 * 200 * 4 * 64 * 4) + values
         # rows that the kernels cannot read in place are copied: those off whole vectors (q and k), and of other strides
-        for bad, more in ((dict(q=AT + 8), keys), (dict(k_head=63), keys), (dict(v=AT + 4), 0), (dict(v_token=47), values),
+        for bad, more in ((dict(q=AT + 8), keys), (dict(k_head=63), keys), (dict(v=AT + 4), values), (dict(v_token=47), values),
                           (dict(v_token=(1 << 23) + 8), values), (dict(q_token=0, k_token=8), 2 * keys),
                           (dict(seqlen=1, q_token=0, k_token=0, v_token=0), None)):
             s = delta_in(dtype=dtype, **bad)
