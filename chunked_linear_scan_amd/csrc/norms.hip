@@ -43,7 +43,6 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int left, bo
     for (int e = 0; e < 8; ++e) v[e] = e < left ? E::get(p[e]) : 0.0f;
 }
 
-// Returns the values as they were kept.
 template <typename E>
 __device__ __forceinline__ void store8(void* base, int64_t at, int left, bool vec, const float (&v)[8]) {
     typedef typename E::raw raw;
@@ -63,6 +62,21 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int left, bool ve
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (e < left) p[e] = E::put(v[e]);
+}
+
+// A lane's part of a row's factors, `fill` where there are none.
+template <int LANES, int NV>
+__device__ __forceinline__ void load_row(const float* p, int dim, bool vec, float fill, float (&v)[NV][8]) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int col = (n * LANES + threadIdx.x % LANES) * 8;
+        if (p) {
+            load8<ElemF32>(p, col, dim - col, vec, v[n]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[n][e] = fill;
+        }
+    }
 }
 
 // Sum over the LANES lanes of a row (all of a workgroup's threads for 256, whose calls meet at a barrier).
@@ -119,7 +133,7 @@ struct GatedParams {
     int64_t total;  // rows * heads
     int heads, dim, gate_first;
     float eps;
-    uint8_t vec_x, vec_z, vec_dy, vec_out;
+    uint8_t vec_x, vec_z, vec_dy, vec_out, vec_w;
 };
 
 template <typename E, int LANES, int NV, bool BWD>
@@ -128,21 +142,19 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedParams p) {
     __shared__ float scratch[BWD && ROWS > 1 ? kThreads * 8 : 4];
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv = 1.0f / float(p.dim);
-    float w[NV][8], dw[NV][8];
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int col = (n * LANES + lane) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[n][e] = col + e < p.dim ? (p.weight ? p.weight[col + e] : 1.0f) : 0.0f;
-            dw[n][e] = 0.0f;
-        }
-    }
+    float w[NV][8], dw[NV][8] = {};
+    load_row<LANES, NV>(p.weight, p.dim, p.vec_w, 1.0f, w);
+    // rows are counted with their heads: one division, then steps
+    const int64_t step = int64_t(gridDim.x) * ROWS;
+    int64_t at = int64_t(blockIdx.x) * ROWS + sub, row = at / p.heads, head = at % p.heads;
+    const int64_t rows = step / p.heads, heads = step % p.heads;
     // all of a workgroup's lanes take the same number of turns: sums may meet at a barrier
-    for (int64_t first = int64_t(blockIdx.x) * ROWS; first < p.total; first += int64_t(gridDim.x) * ROWS) {
-        const int64_t at = first + sub;
+    for (; at - sub < p.total; at += step, row += rows, head += heads) {
+        if (head >= p.heads) {
+            head -= p.heads;
+            ++row;
+        }
         const bool on = at < p.total;
-        const int64_t row = on ? at / p.heads : 0, head = on ? at % p.heads : 0;
         float x[NV][8], z[NV][8], dy[NV][8], u[NV][8];
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
@@ -226,7 +238,7 @@ struct ResidualParams {
     int64_t x_row, residual_row, dy_row, dr_row, r_row, rows;
     int dim;
     float eps;
-    uint8_t vec_x, vec_res, vec_dy, vec_dr, vec_r, vec_out;
+    uint8_t vec_x, vec_res, vec_dy, vec_dr, vec_r, vec_out, vec_w;  // vec_w: scale and weight
 };
 
 template <typename E, typename S, int LANES, int NV>
@@ -235,21 +247,26 @@ __global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualParams 
     __shared__ float scratch[4];
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv = 1.0f / float(p.dim);
+    float w[NV][8], s[NV][8];
+    load_row<LANES, NV>(p.weight, p.dim, p.vec_w, 1.0f, w);
+    load_row<LANES, NV>(p.scale, p.dim, p.vec_w, 1.0f, s);
     for (int64_t first = int64_t(blockIdx.x) * ROWS; first < p.rows; first += int64_t(gridDim.x) * ROWS) {
         const int64_t row = first + sub;
         const bool on = row < p.rows;
-        float r[NV][8];
+        float r[NV][8], x[NV][8];
         float ss = 0.0f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
-            float x[8];
-            load8<E>(p.x, row * p.x_row + col, left, p.vec_x, x);
+            load8<E>(p.x, row * p.x_row + col, left, p.vec_x, x[n]);
             if (p.residual) load8<S>(p.residual, row * p.residual_row + col, left, p.vec_res, r[n]);
+        }
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float s = p.scale ? (e < left ? p.scale[col + e] : 0.0f) : 1.0f;
-                const float v = p.residual ? fmaf(s, x[e], r[n][e]) : s * x[e];
+                const float v = p.residual ? fmaf(s[n][e], x[n][e], r[n][e]) : s[n][e] * x[n][e];
                 r[n][e] = S::get(S::put(v));  // the norm is that of the stream as it is kept
                 ss = fmaf(r[n][e], r[n][e], ss);
             }
@@ -262,7 +279,7 @@ __global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualParams 
             const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = r[n][e] * rstd * (p.weight && e < left ? p.weight[col + e] : 1.0f);
+            for (int e = 0; e < 8; ++e) y[e] = r[n][e] * rstd * w[n][e];
             store8<E>(p.y, row * p.dim + col, left, p.vec_out, y);
         }
     }
@@ -274,18 +291,9 @@ __global__ __launch_bounds__(kThreads) void residual_norm_bwd_kernel(ResidualPar
     __shared__ float scratch[ROWS > 1 ? kThreads * 8 : 4];
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv = 1.0f / float(p.dim);
-    float w[NV][8], s[NV][8], dw[NV][8], ds[NV][8];
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int col = (n * LANES + lane) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const bool in = col + e < p.dim;
-            w[n][e] = in ? (p.weight ? p.weight[col + e] : 1.0f) : 0.0f;
-            s[n][e] = in && p.scale ? p.scale[col + e] : 1.0f;
-            dw[n][e] = ds[n][e] = 0.0f;
-        }
-    }
+    float w[NV][8], s[NV][8], dw[NV][8] = {}, ds[NV][8] = {};
+    load_row<LANES, NV>(p.weight, p.dim, p.vec_w, 1.0f, w);
+    load_row<LANES, NV>(p.scale, p.dim, p.vec_w, 1.0f, s);
     for (int64_t first = int64_t(blockIdx.x) * ROWS; first < p.rows; first += int64_t(gridDim.x) * ROWS) {
         const int64_t row = first + sub;
         const bool on = row < p.rows;
@@ -328,13 +336,27 @@ __global__ __launch_bounds__(kThreads) void residual_norm_bwd_kernel(ResidualPar
     if (p.parts_s) put_parts<LANES, NV>(ds, p.parts_s, p.dim, scratch);
 }
 
-// out[col] = sum of parts[0..n)[col]: 16 columns by 64 threads each, in a fixed order.
-__global__ __launch_bounds__(1024) void norm_sums_kernel(const float* parts, int n, int dim, float* out) {
+// out[col] = sum of parts[0..n)[col], for one or two: 16 columns by 64 threads each, in a fixed order.
+struct SumsParams {
+    const float* parts[2];
+    float* out[2];
+    int n, dim;
+};
+__global__ __launch_bounds__(1024) void norm_sums_kernel(SumsParams p) {
     __shared__ float s[64][17];
     const int col = blockIdx.x * 16 + (threadIdx.x & 15), at = threadIdx.x >> 4;
+    const float* parts = blockIdx.y ? p.parts[1] : p.parts[0];
     float v = 0.0f;
-    if (col < dim)
-        for (int k = at; k < n; k += 64) v += parts[int64_t(k) * dim + col];
+    if (col < p.dim) {
+        constexpr int U = 8;  // loads in flight
+        for (int k = at; k < p.n; k += 64 * U) {
+            float x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = k + 64 * u < p.n ? parts[int64_t(k + 64 * u) * p.dim + col] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) v += x[u];
+        }
+    }
     s[at][threadIdx.x & 15] = v;
     __syncthreads();
 #pragma unroll
@@ -342,11 +364,11 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float* parts, int
         if (at < d) s[at][threadIdx.x & 15] += s[at + d][threadIdx.x & 15];
         __syncthreads();
     }
-    if (at == 0 && col < dim) out[col] = s[0][threadIdx.x & 15];
+    if (at == 0 && col < p.dim) (blockIdx.y ? p.out[1] : p.out[0])[col] = s[0][threadIdx.x & 15];
 }
 
-int sums(const float* parts, int n, int dim, float* out, hipStream_t stream) {
-    norm_sums_kernel<<<(dim + 15) / 16, 1024, 0, stream>>>(parts, n, dim, out);
+int sums(const SumsParams& p, hipStream_t stream) {
+    norm_sums_kernel<<<dim3((p.dim + 15) / 16, p.out[1] ? 2 : 1), 1024, 0, stream>>>(p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
@@ -378,6 +400,8 @@ bool whole(const void* p, int64_t dim, int dtype, int64_t a, int64_t b) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && dim % 8 == 0 && a % ve == 0 && b % ve == 0;
 }
 
+constexpr int64_t kForward = 2048;
+
 unsigned groups(int64_t rows, int64_t dim, int64_t most) {
     const int64_t per = kThreads / lanes_of(dim), n = (rows + per - 1) / per;
     return unsigned(n < most ? n : most);
@@ -400,10 +424,11 @@ int cls_gated_norm_launch(const gated_norm_inputs& in, const void* dy, int64_t d
     p.total = in.rows * in.heads;
     p.heads = int(in.heads); p.dim = int(in.dim); p.gate_first = in.gate_first; p.eps = in.eps;
     p.vec_x = whole(in.x, in.dim, in.dtype, in.x_row, in.x_head);
+    p.vec_w = whole(in.weight, in.dim, SSD_F32, 0, 0);
     p.vec_z = whole(in.z, in.dim, in.dtype, in.z_row, in.z_head);
     p.vec_dy = whole(dy, in.dim, in.dtype, dy_row, dy_head);
     p.vec_out = whole(dy ? dx : y, in.dim, in.dtype, 0, 0) && whole(dy ? dz : nullptr, in.dim, in.dtype, 0, 0);
-    const unsigned n = dy ? unsigned(cls_norm_parts(p.total, in.dim)) : groups(p.total, in.dim, int64_t(1) << 23);
+    const unsigned n = dy ? unsigned(cls_norm_parts(p.total, in.dim)) : groups(p.total, in.dim, kForward);
     const int st = by_element(in.dtype, [&](auto e) {
         return by_dim(p.dim, [&](auto lanes, auto nv) {
             typedef decltype(e) E;
@@ -413,7 +438,7 @@ int cls_gated_norm_launch(const gated_norm_inputs& in, const void* dy, int64_t d
             return hipGetLastError() == hipSuccess ? 0 : -7;
         });
     });
-    return st == 0 && p.parts ? sums(parts, int(n), p.dim, dweight, stream) : st;
+    return st == 0 && p.parts ? sums({{parts, nullptr}, {dweight, nullptr}, int(n), p.dim}, stream) : st;
 }
 
 int cls_residual_norm_fwd_launch(const residual_norm_inputs& in, void* y, void* r, float* rstd, hipStream_t stream) {
@@ -422,9 +447,10 @@ int cls_residual_norm_fwd_launch(const residual_norm_inputs& in, void* y, void* 
     p.x = in.x; p.residual = in.residual; p.scale = in.scale; p.weight = in.weight; p.rstd = rstd; p.y = y; p.r = r;
     p.x_row = in.x_row; p.residual_row = in.residual_row; p.rows = in.rows; p.dim = int(in.dim); p.eps = in.eps;
     p.vec_x = whole(in.x, in.dim, in.dtype, in.x_row, 0);
+    p.vec_w = whole(in.weight, in.dim, SSD_F32, 0, 0) && whole(in.scale, in.dim, SSD_F32, 0, 0);
     p.vec_res = whole(in.residual, in.dim, in.stream_dtype, in.residual_row, 0);
     p.vec_out = whole(y, in.dim, in.dtype, 0, 0) && whole(r, in.dim, in.stream_dtype, 0, 0);
-    const unsigned n = groups(in.rows, in.dim, int64_t(1) << 23);
+    const unsigned n = groups(in.rows, in.dim, kForward);
     return by_element(in.dtype, [&](auto e) {
         return by_dim(p.dim, [&](auto lanes, auto nv) {
             typedef decltype(e) E;
@@ -448,11 +474,12 @@ int cls_residual_norm_bwd_launch(const residual_norm_inputs& in, const residual_
     p.parts_w = g.dweight ? parts : nullptr;
     p.parts_s = g.dscale ? parts + n * in.dim : nullptr;
     p.vec_x = whole(in.x, in.dim, in.dtype, in.x_row, 0);
+    p.vec_w = whole(in.weight, in.dim, SSD_F32, 0, 0) && whole(in.scale, in.dim, SSD_F32, 0, 0);
     p.vec_dy = whole(g.dy, in.dim, in.dtype, g.dy_row, 0);
     p.vec_dr = whole(g.dr, in.dim, in.stream_dtype, g.dr_row, 0);
     p.vec_r = whole(g.r, in.dim, in.stream_dtype, g.r_row, 0);
     p.vec_out = whole(g.dresidual, in.dim, in.stream_dtype, 0, 0) && whole(g.dx, in.dim, in.dtype, 0, 0);
-    int st = by_element(in.dtype, [&](auto e) {
+    const int st = by_element(in.dtype, [&](auto e) {
         return by_dim(p.dim, [&](auto lanes, auto nv) {
             typedef decltype(e) E;
             constexpr int LANES = decltype(lanes)::value, NV = decltype(nv)::value;
@@ -462,7 +489,7 @@ int cls_residual_norm_bwd_launch(const residual_norm_inputs& in, const residual_
             return hipGetLastError() == hipSuccess ? 0 : -7;
         });
     });
-    if (st == 0 && g.dweight) st = sums(p.parts_w, int(n), p.dim, g.dweight, stream);
-    if (st == 0 && g.dscale) st = sums(p.parts_s, int(n), p.dim, g.dscale, stream);
-    return st;
+    if (st != 0 || (!g.dweight && !g.dscale)) return st;
+    if (!g.dweight) return sums({{p.parts_s, nullptr}, {g.dscale, nullptr}, int(n), p.dim}, stream);
+    return sums({{p.parts_w, p.parts_s}, {g.dweight, g.dscale}, int(n), p.dim}, stream);
 }
