@@ -1,10 +1,19 @@
 // The norms around a block: gated_norm behind a recurrence and residual_norm in
-// front of the next block, with their gradients.  All are bound by memory: a row
-// is read once, kept in registers between its sum of squares and its output, and
-// written once.  A row has 8 to 256 lanes by its length, 8 adjacent values (one or two
-// 16-byte vectors) to a lane at a time.  The gradients of weight and
-// scale are summed over the rows that a workgroup walks in its lanes, then over
-// the workgroups by a second launch in a fixed order.
+// front of the next block, with their gradients:
+//     y = unit(x) w silu(z)  or  unit(x silu(z)) w;   r = residual + s x, y = unit(r) w,
+//     unit(u) = u / sqrt(mean(u^2) + eps),  du = rstd (a - unit mean(a unit)), a the gradient of unit.
+// All are bound by memory: a row is read once, kept in registers between its sum
+// and its output, and written once.  8 adjacent values (one or two 16-byte vectors)
+// to a lane at a time; a row has 8 to 1024 lanes, as few as it needs in one run for the
+// gradients, which keep several arrays of a row (8192 x 4096 in 256 lanes of two runs: 174 us, in 512 of one: 86), and two
+// or three runs otherwise, where barriers and the lanes behind a row's end cost more (1021 x 5120 in 1024 lanes of one run: 17 us,
+// in 256 of three: 10).  Workgroups walk over rows, so that w and s are read once (16384 x 4096: 102 us, 5.3 TB/s; one row to a
+// workgroup: 165).  The gradients of w and s are summed over the rows that a workgroup walks in its lanes, then over the
+// workgroups by a second launch in a fixed order.
+//
+//     bf16             forward          gradients           their sums over workgroups
+//     131072 x 128     19.4 us  5.2 TB/s  30.7 us  5.5 TB/s   4.7 us    gated_norm
+//     8192 x 2048      34.1 us  5.9 TB/s  58.2 us  5.2 TB/s   7.0 us    residual_norm, the stream in fp32
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -16,7 +25,8 @@
 namespace cls {
 namespace {
 
-constexpr int kThreads = 256;
+// A workgroup has as many rows as fit 256 lanes, or one.
+constexpr int threads_of(int lanes) { return lanes > 256 ? lanes : 256; }
 
 template <typename E>
 __device__ __forceinline__ void load8(const void* base, int64_t at, int left, bool vec, float (&v)[8]) {
@@ -64,6 +74,16 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int left, bool ve
         if (e < left) p[e] = E::put(v[e]);
 }
 
+// Where a lane has several runs of a row its gradients do not keep them all: they are read one at a time, and again, from
+// the cache, when the row's sum is there (gated_norm of 2048 x 16384: 157 us; all kept, and spilled: 286).
+template <int NV>
+__device__ __forceinline__ void again() {
+    if constexpr (NV > 1) {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 // A lane's part of a row's factors, `fill` where there are none.
 template <int LANES, int NV>
 __device__ __forceinline__ void load_row(const float* p, int dim, bool vec, float fill, float (&v)[NV][8]) {
@@ -79,16 +99,23 @@ __device__ __forceinline__ void load_row(const float* p, int dim, bool vec, floa
     }
 }
 
-// Sum over the LANES lanes of a row (all of a workgroup's threads for 256, whose calls meet at a barrier).
+// Sum over the LANES lanes of a row.  Where those are of more than one wave all of a workgroup's waves meet, once: calls
+// use the two halves of scratch (kSums floats) in turn.
 template <int LANES>
-__device__ __forceinline__ float row_sum(float v, float* scratch) {
+constexpr int kSums = LANES > 64 ? 2 * threads_of(LANES) / 64 : 1;
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, float* scratch, int& turn) {
 #pragma unroll
     for (int d = (LANES < 64 ? LANES : 64) / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-    if constexpr (LANES == kThreads) {
+    if constexpr (LANES > 64) {
+        constexpr int W = LANES / 64;
+        float* s = scratch + (turn ^= threads_of(LANES) / 64);
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) s[wave] = v;
         __syncthreads();
-        if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = (scratch[0] + scratch[1]) + (scratch[2] + scratch[3]);
+        v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) v += s[wave / W * W + k];
     }
     return v;
 }
@@ -96,7 +123,7 @@ __device__ __forceinline__ float row_sum(float v, float* scratch) {
 // Column sums of a workgroup's rows: one row of `parts`.
 template <int LANES, int NV>
 __device__ __forceinline__ void put_parts(const float (&sum)[NV][8], float* parts, int dim, float* scratch) {
-    constexpr int ROWS = kThreads / LANES;
+    constexpr int THREADS = threads_of(LANES), ROWS = THREADS / LANES;
     const int lane = threadIdx.x % LANES;
     if constexpr (ROWS == 1) {
 #pragma unroll
@@ -106,14 +133,14 @@ __device__ __forceinline__ void put_parts(const float (&sum)[NV][8], float* part
                 const int col = (n * LANES + lane) * 8 + e;
                 if (col < dim) parts[int64_t(blockIdx.x) * dim + col] = sum[n][e];
             }
-    } else {  // scratch: [kThreads][8]
+    } else {  // scratch: [THREADS][8]
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < 8; ++e) scratch[threadIdx.x * 8 + e] = sum[n][e];
             __syncthreads();
-            for (int col = threadIdx.x; col < LANES * 8; col += kThreads) {
+            for (int col = threadIdx.x; col < LANES * 8; col += THREADS) {
                 float v = 0.0f;
                 for (int r = 0; r < ROWS; ++r) v += scratch[r * LANES * 8 + col];
                 const int at = n * LANES * 8 + col;
@@ -137,11 +164,12 @@ struct GatedParams {
 };
 
 template <typename E, int LANES, int NV, bool BWD>
-__global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedParams p) {
-    constexpr int ROWS = kThreads / LANES;
-    __shared__ float scratch[BWD && ROWS > 1 ? kThreads * 8 : 4];
+__global__ __launch_bounds__(threads_of(LANES)) void gated_norm_kernel(GatedParams p) {
+    constexpr int THREADS = threads_of(LANES), ROWS = THREADS / LANES;
+    __shared__ float scratch[BWD && ROWS > 1 ? THREADS * 8 : kSums<LANES>];
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv = 1.0f / float(p.dim);
+    int turn = 0;
     float w[NV][8], dw[NV][8] = {};
     load_row<LANES, NV>(p.weight, p.dim, p.vec_w, 1.0f, w);
     // rows are counted with their heads: one division, then steps
@@ -155,32 +183,30 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedParams p) {
             ++row;
         }
         const bool on = at < p.total;
-        float x[NV][8], z[NV][8], dy[NV][8], u[NV][8];
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
+        float x[NV][8], z[NV][8], dy[NV][8], u[NV][8], gate[NV][8], sig[NV][8];
+        const auto read = [&](int n) {
             const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
             load8<E>(p.x, row * p.x_row + head * p.x_head + col, left, p.vec_x, x[n]);
             load8<E>(p.z ? p.z : p.x, row * p.z_row + head * p.z_head + col, p.z ? left : 0, p.vec_z, z[n]);
             if (BWD) load8<E>(p.dy, row * p.dy_row + head * p.dy_head + col, left, p.vec_dy, dy[n]);
-        }
-        float rstd = 0.0f, ss = 0.0f;
-        float gate[NV][8], sig[NV][8];
-#pragma unroll
-        for (int n = 0; n < NV; ++n)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 sig[n][e] = p.z ? sigmoid(z[n][e]) : 1.0f;
                 gate[n][e] = p.z ? z[n][e] * sig[n][e] : 1.0f;
                 u[n][e] = p.gate_first ? x[n][e] * gate[n][e] : x[n][e];
             }
+        };
+        float rstd = 0.0f, ss = 0.0f;
         if (BWD) {
             rstd = on ? p.rstd[at] : 0.0f;
         } else {
 #pragma unroll
+            for (int n = 0; n < NV; ++n) read(n);
+#pragma unroll
             for (int n = 0; n < NV; ++n)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss = fmaf(u[n][e], u[n][e], ss);
-            rstd = 1.0f / sqrtf(fmaf(row_sum<LANES>(ss, scratch), inv, p.eps));
+            rstd = 1.0f / sqrtf(fmaf(row_sum<LANES>(ss, scratch, turn), inv, p.eps));
             if (p.rstd && on && lane == 0) p.rstd[at] = rstd;
         }
         const int64_t out = at * p.dim;
@@ -201,7 +227,8 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedParams p) {
         // the gradient of u: rstd (a - unit mean(a unit)), a that of unit = u rstd
         float mean = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
+        for (int n = 0; n < NV; ++n) {
+            read(n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float dn = p.gate_first ? dy[n][e] : dy[n][e] * gate[n][e];
@@ -209,11 +236,14 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedParams p) {
                 dw[n][e] = fmaf(dn, unit, dw[n][e]);
                 mean = fmaf(dn * w[n][e], unit, mean);
             }
-        mean = row_sum<LANES>(mean, scratch) * inv;
+            again<NV>();
+        }
+        mean = row_sum<LANES>(mean, scratch, turn) * inv;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
             float dx[8], dz[8];
+            if (NV > 1) read(n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float unit = u[n][e] * rstd, a = dy[n][e] * w[n][e];
@@ -224,6 +254,7 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedParams p) {
             }
             store8<E>(p.dx, out + col, left, p.vec_out, dx);
             if (p.z) store8<E>(p.dz, out + col, left, p.vec_out, dz);
+            again<NV>();
         }
     }
     if (BWD && p.parts) put_parts<LANES, NV>(dw, p.parts, p.dim, scratch);
@@ -242,11 +273,12 @@ struct ResidualParams {
 };
 
 template <typename E, typename S, int LANES, int NV>
-__global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualParams p) {
-    constexpr int ROWS = kThreads / LANES;
-    __shared__ float scratch[4];
+__global__ __launch_bounds__(threads_of(LANES)) void residual_norm_kernel(ResidualParams p) {
+    constexpr int THREADS = threads_of(LANES), ROWS = THREADS / LANES;
+    __shared__ float scratch[kSums<LANES>];
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv = 1.0f / float(p.dim);
+    int turn = 0;
     float w[NV][8], s[NV][8];
     load_row<LANES, NV>(p.weight, p.dim, p.vec_w, 1.0f, w);
     load_row<LANES, NV>(p.scale, p.dim, p.vec_w, 1.0f, s);
@@ -272,7 +304,7 @@ __global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualParams 
             }
             store8<S>(p.r, row * p.dim + col, left, p.vec_out, r[n]);
         }
-        const float rstd = 1.0f / sqrtf(fmaf(row_sum<LANES>(ss, scratch), inv, p.eps));
+        const float rstd = 1.0f / sqrtf(fmaf(row_sum<LANES>(ss, scratch, turn), inv, p.eps));
         if (p.rstd && on && lane == 0) p.rstd[row] = rstd;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
@@ -286,11 +318,12 @@ __global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualParams 
 }
 
 template <typename E, typename S, int LANES, int NV>
-__global__ __launch_bounds__(kThreads) void residual_norm_bwd_kernel(ResidualParams p) {
-    constexpr int ROWS = kThreads / LANES;
-    __shared__ float scratch[ROWS > 1 ? kThreads * 8 : 4];
+__global__ __launch_bounds__(threads_of(LANES)) void residual_norm_bwd_kernel(ResidualParams p) {
+    constexpr int THREADS = threads_of(LANES), ROWS = THREADS / LANES;
+    __shared__ float scratch[ROWS > 1 ? THREADS * 8 : kSums<LANES>];
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv = 1.0f / float(p.dim);
+    int turn = 0;
     float w[NV][8], s[NV][8], dw[NV][8] = {}, ds[NV][8] = {};
     load_row<LANES, NV>(p.weight, p.dim, p.vec_w, 1.0f, w);
     load_row<LANES, NV>(p.scale, p.dim, p.vec_w, 1.0f, s);
@@ -300,36 +333,43 @@ __global__ __launch_bounds__(kThreads) void residual_norm_bwd_kernel(ResidualPar
         const float rstd = on ? p.rstd[row] : 0.0f;
         float dy[NV][8], unit[NV][8], dr[NV][8], x[NV][8];
         float mean = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
+        const auto read = [&](int n, bool all) {
             const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
             load8<E>(p.dy, row * p.dy_row + col, left, p.vec_dy, dy[n]);
             load8<S>(p.r_in, row * p.r_row + col, left, p.vec_r, unit[n]);
-            if (p.dr) load8<S>(p.dr, row * p.dr_row + col, left, p.vec_dr, dr[n]);
-            if (p.parts_s) load8<E>(p.x, row * p.x_row + col, left, p.vec_x, x[n]);
-        }
+            if (all) {
+                load8<S>(p.dr ? p.dr : p.r_in, row * p.dr_row + col, p.dr ? left : 0, p.vec_dr, dr[n]);
+                load8<E>(p.parts_s ? p.x : p.dy, row * p.x_row + col, p.parts_s ? left : 0, p.vec_x, x[n]);
+            }
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
+            for (int e = 0; e < 8; ++e) unit[n][e] *= rstd;
+        };
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            read(n, NV == 1);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                unit[n][e] *= rstd;
                 dw[n][e] = fmaf(dy[n][e], unit[n][e], dw[n][e]);
                 mean = fmaf(dy[n][e] * w[n][e], unit[n][e], mean);
             }
-        mean = row_sum<LANES>(mean, scratch) * inv;
+            again<NV>();
+        }
+        mean = row_sum<LANES>(mean, scratch, turn) * inv;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int col = (n * LANES + lane) * 8, left = on ? p.dim - col : 0;
             float du[8], dx[8];
+            if (NV > 1) read(n, true);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 du[e] = rstd * fmaf(-unit[n][e], mean, dy[n][e] * w[n][e]);
-                if (p.dr) du[e] += dr[n][e];
+                du[e] += dr[n][e];
                 dx[e] = du[e] * s[n][e];
-                if (p.parts_s) ds[n][e] = fmaf(du[e], x[n][e], ds[n][e]);
+                ds[n][e] = fmaf(du[e], x[n][e], ds[n][e]);
             }
             store8<S>(p.dresidual, row * p.dim + col, left, p.vec_out, du);
             if (p.dx) store8<E>(p.dx, row * p.dim + col, left, p.vec_out, dx);
+            again<NV>();
         }
     }
     if (p.parts_w) put_parts<LANES, NV>(dw, p.parts_w, p.dim, scratch);
@@ -372,21 +412,28 @@ int sums(const SumsParams& p, hipStream_t stream) {
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
-int lanes_of(int64_t dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : dim <= 1024 ? 64 : 256; }
-
-// Calls f with the lanes of a row and the runs of 8 values that each has.
-template <typename F>
-int by_dim(int dim, F&& f) {
+// Calls f with the lanes of a row and the runs of 8 values that each has.  The gradients keep several arrays of a row, so
+// theirs are of one run.
+template <bool BWD, typename F>
+auto by_dim(int dim, F&& f) {
     const auto of = [&](auto lanes, auto nv) { return f(lanes, nv); };
     using std::integral_constant;
     if (dim <= 64) return of(integral_constant<int, 8>(), integral_constant<int, 1>());
     if (dim <= 128) return of(integral_constant<int, 16>(), integral_constant<int, 1>());
     if (dim <= 512) return of(integral_constant<int, 64>(), integral_constant<int, 1>());
-    if (dim <= 1024) return of(integral_constant<int, 64>(), integral_constant<int, 2>());
-    if (dim <= 2048) return of(integral_constant<int, 256>(), integral_constant<int, 1>());
-    if (dim <= 4096) return of(integral_constant<int, 256>(), integral_constant<int, 2>());
-    if (dim <= 8192) return of(integral_constant<int, 256>(), integral_constant<int, 4>());
-    return of(integral_constant<int, 256>(), integral_constant<int, 8>());
+    if constexpr (BWD) {
+        if (dim <= 1024) return of(integral_constant<int, 128>(), integral_constant<int, 1>());
+        if (dim <= 2048) return of(integral_constant<int, 256>(), integral_constant<int, 1>());
+        if (dim <= 4096) return of(integral_constant<int, 512>(), integral_constant<int, 1>());
+        if (dim <= 8192) return of(integral_constant<int, 1024>(), integral_constant<int, 1>());
+    } else {
+        if (dim <= 1024) return of(integral_constant<int, 64>(), integral_constant<int, 2>());
+        if (dim <= 2048) return of(integral_constant<int, 256>(), integral_constant<int, 1>());
+        if (dim <= 4096) return of(integral_constant<int, 256>(), integral_constant<int, 2>());
+        if (dim <= 6144) return of(integral_constant<int, 256>(), integral_constant<int, 3>());
+        if (dim <= 8192) return of(integral_constant<int, 512>(), integral_constant<int, 2>());
+    }
+    return of(integral_constant<int, 1024>(), integral_constant<int, 2>());
 }
 
 template <typename F>
@@ -400,18 +447,22 @@ bool whole(const void* p, int64_t dim, int dtype, int64_t a, int64_t b) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && dim % 8 == 0 && a % ve == 0 && b % ve == 0;
 }
 
-constexpr int64_t kForward = 2048;
-
-unsigned groups(int64_t rows, int64_t dim, int64_t most) {
-    const int64_t per = kThreads / lanes_of(dim), n = (rows + per - 1) / per;
-    return unsigned(n < most ? n : most);
+// Workgroups of a launch: as many rows as a compute unit's lanes have, or half of them for the gradients, whose partial sums
+// are one to a workgroup.
+template <bool BWD>
+unsigned groups(int64_t rows, int64_t dim) {
+    return by_dim<BWD>(int(dim), [&](auto lanes, auto) {
+        constexpr int THREADS = threads_of(decltype(lanes)::value);
+        const int64_t per = THREADS / lanes, n = (rows + per - 1) / per, most = 256 * (BWD ? 1024 : 2048) / THREADS;
+        return unsigned(n < most ? n : most);
+    });
 }
 
 }  // namespace
 }  // namespace cls
 
-// Workgroups of the gradients' launch, each with a partial sum of the parameters' gradients: four to a compute unit.
-int64_t cls_norm_parts(int64_t rows, int64_t dim) { return cls::groups(rows, dim, 1024); }
+// Workgroups of the gradients' launch, each with a partial sum of the parameters' gradients.
+int64_t cls_norm_parts(int64_t rows, int64_t dim) { return cls::groups<true>(rows, dim); }
 
 int cls_gated_norm_launch(const gated_norm_inputs& in, const void* dy, int64_t dy_row, int64_t dy_head, float* rstd,
                           void* y, void* dx, void* dz, float* dweight, float* parts, hipStream_t stream) {
@@ -428,15 +479,17 @@ int cls_gated_norm_launch(const gated_norm_inputs& in, const void* dy, int64_t d
     p.vec_z = whole(in.z, in.dim, in.dtype, in.z_row, in.z_head);
     p.vec_dy = whole(dy, in.dim, in.dtype, dy_row, dy_head);
     p.vec_out = whole(dy ? dx : y, in.dim, in.dtype, 0, 0) && whole(dy ? dz : nullptr, in.dim, in.dtype, 0, 0);
-    const unsigned n = dy ? unsigned(cls_norm_parts(p.total, in.dim)) : groups(p.total, in.dim, kForward);
+    const unsigned n = dy ? groups<true>(p.total, in.dim) : groups<false>(p.total, in.dim);
     const int st = by_element(in.dtype, [&](auto e) {
-        return by_dim(p.dim, [&](auto lanes, auto nv) {
-            typedef decltype(e) E;
-            constexpr int LANES = decltype(lanes)::value, NV = decltype(nv)::value;
-            if (dy) gated_norm_kernel<E, LANES, NV, true><<<n, kThreads, 0, stream>>>(p);
-            else gated_norm_kernel<E, LANES, NV, false><<<n, kThreads, 0, stream>>>(p);
-            return hipGetLastError() == hipSuccess ? 0 : -7;
-        });
+        const auto launch = [&](auto bwd) {
+            return by_dim<decltype(bwd)::value>(p.dim, [&](auto lanes, auto nv) {
+                constexpr int LANES = decltype(lanes)::value;
+                gated_norm_kernel<decltype(e), LANES, decltype(nv)::value, decltype(bwd)::value>
+                    <<<n, threads_of(LANES), 0, stream>>>(p);
+                return hipGetLastError() == hipSuccess ? 0 : -7;
+            });
+        };
+        return dy ? launch(std::true_type()) : launch(std::false_type());
     });
     return st == 0 && p.parts ? sums({{parts, nullptr}, {dweight, nullptr}, int(n), p.dim}, stream) : st;
 }
@@ -450,13 +503,13 @@ int cls_residual_norm_fwd_launch(const residual_norm_inputs& in, void* y, void* 
     p.vec_w = whole(in.weight, in.dim, SSD_F32, 0, 0) && whole(in.scale, in.dim, SSD_F32, 0, 0);
     p.vec_res = whole(in.residual, in.dim, in.stream_dtype, in.residual_row, 0);
     p.vec_out = whole(y, in.dim, in.dtype, 0, 0) && whole(r, in.dim, in.stream_dtype, 0, 0);
-    const unsigned n = groups(in.rows, in.dim, kForward);
+    const unsigned n = groups<false>(in.rows, in.dim);
     return by_element(in.dtype, [&](auto e) {
-        return by_dim(p.dim, [&](auto lanes, auto nv) {
+        return by_dim<false>(p.dim, [&](auto lanes, auto nv) {
             typedef decltype(e) E;
             constexpr int LANES = decltype(lanes)::value, NV = decltype(nv)::value;
-            if (in.stream_dtype == SSD_F32) residual_norm_kernel<E, ElemF32, LANES, NV><<<n, kThreads, 0, stream>>>(p);
-            else residual_norm_kernel<E, E, LANES, NV><<<n, kThreads, 0, stream>>>(p);
+            if (in.stream_dtype == SSD_F32) residual_norm_kernel<E, ElemF32, LANES, NV><<<n, threads_of(LANES), 0, stream>>>(p);
+            else residual_norm_kernel<E, E, LANES, NV><<<n, threads_of(LANES), 0, stream>>>(p);
             return hipGetLastError() == hipSuccess ? 0 : -7;
         });
     });
@@ -480,12 +533,12 @@ int cls_residual_norm_bwd_launch(const residual_norm_inputs& in, const residual_
     p.vec_r = whole(g.r, in.dim, in.stream_dtype, g.r_row, 0);
     p.vec_out = whole(g.dresidual, in.dim, in.stream_dtype, 0, 0) && whole(g.dx, in.dim, in.dtype, 0, 0);
     const int st = by_element(in.dtype, [&](auto e) {
-        return by_dim(p.dim, [&](auto lanes, auto nv) {
+        return by_dim<true>(p.dim, [&](auto lanes, auto nv) {
             typedef decltype(e) E;
             constexpr int LANES = decltype(lanes)::value, NV = decltype(nv)::value;
             if (in.stream_dtype == SSD_F32)
-                residual_norm_bwd_kernel<E, ElemF32, LANES, NV><<<unsigned(n), kThreads, 0, stream>>>(p);
-            else residual_norm_bwd_kernel<E, E, LANES, NV><<<unsigned(n), kThreads, 0, stream>>>(p);
+                residual_norm_bwd_kernel<E, ElemF32, LANES, NV><<<unsigned(n), threads_of(LANES), 0, stream>>>(p);
+            else residual_norm_bwd_kernel<E, E, LANES, NV><<<unsigned(n), threads_of(LANES), 0, stream>>>(p);
             return hipGetLastError() == hipSuccess ? 0 : -7;
         });
     });
