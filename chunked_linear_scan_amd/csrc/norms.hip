@@ -5,7 +5,7 @@
 // All are bound by memory: a row is read once, kept in registers between its sum
 // and its output, and written once.  8 adjacent values (one or two 16-byte vectors)
 // to a lane at a time; a row has 8 to 1024 lanes, as few as it needs in one run for the
-// gradients, which keep several arrays of a row (8192 x 4096 in 256 lanes of two runs: 174 us, in 512 of one: 86), and two
+// gradients, which keep several arrays of a row (5461 x 6144 in 256 lanes of three runs: 174 us, in 1024 of one: 98), and two
 // or three runs otherwise, where barriers and the lanes behind a row's end cost more (1021 x 5120 in 1024 lanes of one run: 17 us,
 // in 256 of three: 10).  Workgroups walk over rows, so that w and s are read once (16384 x 4096: 102 us, 5.3 TB/s; one row to a
 // workgroup: 165).  The gradients of w and s are summed over the rows that a workgroup walks in its lanes, then over the
