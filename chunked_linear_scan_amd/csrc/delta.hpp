@@ -153,7 +153,7 @@ struct DeltaParams {
     const int32_t* seqlens;
     void *y, *dq, *dk_, *dv_;
     float *h_last, *dg, *dbeta, *dh0;
-    float* states;   // [batch, chunks, heads, dv, dk]: the state before each chunk (NULL = not kept)
+    float* states;   // [batch, chunks, heads, dv, kpitch]: the state before each chunk (NULL = not kept)
     float* fixes;    // [batch, chunks, heads, dv, chunk]: N, the corrections (NULL = not kept)
     void* mats;      // per (batch, chunk, head): (I + A)^-1 - I and D QK^T (forward: times scale), in one part or two
     float* vecs;     // per (batch, chunk, head): kVecs factors of each token
@@ -163,6 +163,7 @@ struct DeltaParams {
     Strided3 sq, sk, sv, sdy;
     int64_t g_batch, g_token, b_batch, b_token;
     int batch, L, Hk, H, dk, dv, nchunk;
+    int kpitch;  // of the kept states' rows: dk to whole vectors
     float scale;
     uint8_t vec_out;  // y or dv has rows of whole 16-byte vectors
     uint8_t vec_dqk;  // dq and dk start on 16 bytes
@@ -196,8 +197,8 @@ struct LdsTile {
     static constexpr bool kSwap = M::kSplit;
     static constexpr int kPitch = DIM + (kSwap ? 0 : 4);
     static constexpr int kSpan = DIM < 128 ? DIM : 128;  // columns that the exchange covers
-    static constexpr int kRows = kSwap ? kSpan / 32 : 1, kCols = kSwap ? kSpan / 16 : 1;
-    uint32_t r[kRows], c[kCols];  // bytes
+    static constexpr int kRows = kSwap ? kSpan / 32 : 1;
+    uint32_t r[kRows], c[kRows];  // bytes
 
     // A number of the row: its upper bits differ among four rows, its lower two among every fourth, in an order that
     // keeps the 16 lanes which a 16-byte read serves at a time apart (0-3, 12-15 and 20-27 of 32, so rows of two lane groups).
@@ -233,7 +234,7 @@ struct LdsTile {
 #pragma unroll
             for (int n = 0; n < kRows; ++n) r[n] = quad(l16, (first + 32 * n) % DIM + 4 * g) * sizeof(raw);
 #pragma unroll
-            for (int n = 0; n < kCols; ++n) c[n] = quad(4 * g + (l16 >> 2), (first + 16 * n) % DIM + 4 * (l16 & 3)) * sizeof(raw);
+            for (int n = 0; n < kRows; ++n) c[n] = quad(4 * g + (l16 >> 2), (first + 32 * n) % DIM + 4 * (l16 & 3)) * sizeof(raw);
         } else {
             r[0] = (l16 * kPitch + first + 4 * g) * sizeof(raw);
             c[0] = (4 * g * kPitch + first + l16) * sizeof(raw);
@@ -255,7 +256,7 @@ struct LdsTile {
         const char* p = reinterpret_cast<const char*>(m + 32 * s * kPitch);
         if constexpr (kSwap) {
             typedef __attribute__((address_space(3))) s16x4* lp;
-            p += 16 * t / kSpan * kSpan * sizeof(raw) + c[t % kCols];
+            p += 16 * t / kSpan * kSpan * sizeof(raw) + c[t / 2 % kRows] + t % 2 * 4 * sizeof(raw);
             const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p)));
             const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p + 16 * kPitch * sizeof(raw))));
             return u32x4{a[0], a[1], b[0], b[1]};

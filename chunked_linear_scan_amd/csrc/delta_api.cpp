@@ -109,7 +109,7 @@ DeltaSpace delta_space(const gated_delta_inputs& s) {
     d.k = d.q + (d.pack_q ? keys : 0);
     d.v = d.k + (d.pack_k ? keys : 0);
     d.fwd = d.v + (d.pack_v ? values : 0);
-    const size_t states = round_up(size_t(n) * s.dk * s.dv * 4, 256);
+    const size_t states = round_up(size_t(n) * round_up(size_t(s.dk), 4) * s.dv * 4, 256);
     const size_t tokens = round_up(size_t(n) * s.dv * C * 4, 256);
     const size_t parts = s.heads > s.kheads ? round_up(size_t(rows * s.heads) * s.dk * 4, 256) : 0;
     d.fixes = states;
@@ -128,7 +128,7 @@ DeltaParams delta_params(const gated_delta_inputs& in, void* workspace, void* ch
     p.g = in.g; p.beta = in.beta; p.h0 = in.h0; p.seqlens = in.seqlens;
     p.g_batch = in.g_batch; p.g_token = in.g_token; p.b_batch = in.beta_batch; p.b_token = in.beta_token;
     p.batch = int(in.batch); p.L = int(in.seqlen); p.Hk = int(in.kheads); p.H = int(in.heads);
-    p.dk = int(in.dk); p.dv = int(in.dv);
+    p.dk = int(in.dk); p.dv = int(in.dv); p.kpitch = (p.dk + 3) / 4 * 4;
     p.nchunk = int(ceil_div(in.seqlen, chunk_of(in.dtype)));
     p.scale = in.scale;
     char* ws = static_cast<char*>(workspace);

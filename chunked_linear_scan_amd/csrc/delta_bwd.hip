@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_bwd_kernel(DeltaParams p) 
             ex.put(3, qq.lo);
         }
         fence();
-        store_state<KT>(S, p.dstates, chunk, n, a * (DK / 2), p);
+        keep_state<KT>(S, p.dstates, chunk, n, a * (DK / 2), p);
         store_tokens<C>(Z, p.z, chunk, n, a, p);
         // the state's gradient, by the half's own tokens, then by the others; two tiles in turn, as a product waits for
         // the one before it on its tile

@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
             }
         };
         if constexpr (KEEP) {
-            store_state<KT>(S, p.states, chunk, n, a * (DK / 2), p);
+            keep_state<KT>(S, p.states, chunk, n, a * (DK / 2), p);
             store_tokens<C>(N, p.fixes, chunk, n, a, p);
         }
         add(a, nn, true);

@@ -15,6 +15,10 @@
 // leave as four adjacent values of a token, and the decays are factors of a lane.
 // What reaches dg and dbeta, fp32 outputs, takes computed operands in two parts;
 // pP and pB only reach dQ and dK and go in as one.
+// Bound by memory: a chunk's states, corrections and operands are read once, 32 of dv at a time, of the 288 KB that
+// it moves for 64 tokens and keys and values of 128 (192 KB of states and corrections; 4 x 2048 x 16 heads: 164 us, 3.7 TB/s; with the products with S and with dS
+// in two walks over dv: 196).  LDS has K and those tiles, and Q and the pairs in the tiles' place afterwards, so that two
+// workgroups fit a compute unit.
 #include <hip/hip_runtime.h>
 
 #include "delta.hpp"
@@ -38,30 +42,18 @@ struct Tile32 {
     static_assert(THREADS % PER_ROW == 0 && 32 % STEP == 0, "");
     static constexpr int kPart = 32 * Lds::kPitch;
     f32x4 r[N];
-    __device__ __forceinline__ void load(const float* m, int64_t dv, int row0, int cols) {
-        const Buffer b = buffer(m, dv * cols * 4);
-        const int col = threadIdx.x % PER_ROW * 4;
+    // cols: a multiple of 4
+    __device__ __forceinline__ void load(Buffer b, int row0, int cols) {
+        const int col = threadIdx.x % PER_ROW * 4, row = row0 + int(threadIdx.x) / PER_ROW;
+        const uint32_t at = col < cols ? uint32_t(row * cols + col) * 4 : kOutside;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int row = row0 + int(threadIdx.x) / PER_ROW + n * STEP;
-            const uint32_t at = uint32_t(row * cols + col) * 4;
-            if (cols % 4 == 0) {
-                r[n] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, int(col < cols ? at : kOutside), 0, 0));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) r[n][e] = as_float(load_one<ElemF32>(b, col + e < cols ? at + 4 * e : kOutside));
-            }
-        }
+        for (int n = 0; n < N; ++n)
+            r[n] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, int(at + uint32_t(n * STEP * cols * 4)), 0, 0));
     }
     __device__ __forceinline__ void store(typename E::raw* to) const {
         const int col = threadIdx.x % PER_ROW * 4;
 #pragma unroll
         for (int n = 0; n < N; ++n) put4<E>(to + Lds::quad(int(threadIdx.x) / PER_ROW + n * STEP, col), kPart, r[n]);
-    }
-    // times a factor of each column
-    __device__ __forceinline__ void scale(const f32x4& f) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) r[n] *= f;
     }
     __device__ __forceinline__ float dot(const Tile32& o) const {
         float v = 0.0f;
@@ -87,25 +79,26 @@ struct GradSize {
     typedef Mat<E> M;
     static constexpr int C = M::kChunk, KP = LdsTile<E, DK>::kPitch, MP = LdsTile<E, C>::kPitch;
     static constexpr int kParts = ChunkMats<E>::kParts;
-    static constexpr int kTiles = kParts * 32 * (KP + 2 * MP);  // tiles of S or dS, of N and of Z
-    static constexpr int kPairs = 2 * C * MP;                   // pB and pP, in the same place
+    static constexpr int kTiles = kParts * 32 * (2 * KP + 2 * MP);  // tiles of S, dS, N and Z
+    static constexpr int kPairs = C * KP + 2 * C * MP;              // Q, pB and pP, in the same place
     static constexpr int kUnion = kTiles > kPairs ? kTiles : kPairs;
-    static constexpr size_t bytes = (2 * C * KP + kUnion) * sizeof(typename M::raw) + (Decays<C>::kFloats + (2 + C / 16) * C + C / 16) * sizeof(float);
+    static constexpr size_t bytes = (C * KP + kUnion) * sizeof(typename M::raw) + (Decays<C>::kFloats + (2 + C / 16) * C + C / 16) * sizeof(float);
 };
 
 template <typename E, int DK>
-__global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_grad_kernel(DeltaParams p) {
+__global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2 : 1) void delta_grad_kernel(DeltaParams p) {
     typedef Mat<E> M;
     typedef typename M::raw raw;
     typedef GradSize<E, DK> G;
     constexpr int C = G::C, NT = C / 16, KT = DK / 16, THREADS = 64 * NT, KP = G::KP, MP = G::MP;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     raw* sK = reinterpret_cast<raw*>(lds);
-    raw* sQ = sK + C * KP;
-    raw* sS = sQ + C * KP;
-    raw* sN = sS + G::kParts * 32 * KP;
+    raw* sS = sK + C * KP;
+    raw* sD = sS + G::kParts * 32 * KP;
+    raw* sN = sD + G::kParts * 32 * KP;
     raw* sZ = sN + G::kParts * 32 * MP;
-    raw* sB = sS;  // once the tiles are done with
+    raw* sQ = sS;  // once the tiles are done with
+    raw* sB = sQ + C * KP;
     raw* sP = sB + C * MP;
     float* sG = reinterpret_cast<float*>(sS + G::kUnion);
     float* sRow = sG + Decays<C>::kFloats;  // read_i + sum_j F_ij
@@ -117,129 +110,156 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_g
     const UnitPart u = unit_part(p.batch * p.nchunk * p.Hk, rep);
     const int kh = u.unit % p.Hk, h = kh * rep + u.part, c = u.unit / p.Hk % p.nchunk, b = u.unit / p.Hk / p.nchunk;
     const int end = seq_end(p.seqlens, b, p.L), t0 = c * C;
-    const int tid = threadIdx.x, w = tid >> 6, l16 = lane16(), g4 = group4();
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane16(), g4 = group4();
     const int i = 16 * w + l16, tok = t0 + i;  // this lane's token
     const bool in = tok < end;
-    // rows of the outputs: of a token's head, or its part of a key head's sum
-    raw* dQ = static_cast<raw*>(p.dq) + ((int64_t(b) * p.L + tok) * p.Hk + kh) * p.dk;
-    raw* dK = static_cast<raw*>(p.dk_) + ((int64_t(b) * p.L + tok) * p.Hk + kh) * p.dk;
-    float* partQ = p.part_q + ((int64_t(b) * p.L + tok) * p.H + h) * p.dk;
-    float* partK = p.part_k + ((int64_t(b) * p.L + tok) * p.H + h) * p.dk;
-    const int64_t gat = (int64_t(b) * p.L + tok) * p.H + h;
 
-    const auto put_row = [&](raw* one, float* part, int d, const f32x4& v) {
-        if (tok >= p.L) return;
-        if (rep > 1) {
-            if (p.dk % 4 == 0) {
-                if (d < p.dk) *reinterpret_cast<f32x4*>(part + d) = v;
+    // rows of the outputs: of a token's head, or its part of a key head's sum
+    const auto put_rows = [&](auto&& q, auto&& k) {
+        int at = tok;
+        asm volatile("" : "+v"(at));  // addresses from here: those of all tiles would be kept from the padding's on
+        if (at >= p.L) return;
+        const int64_t one = ((int64_t(b) * p.L + at) * p.Hk + kh) * p.dk, part = ((int64_t(b) * p.L + at) * p.H + h) * p.dk;
+        const auto put = [&](raw* whole, float* parts, int d, const f32x4& v) {
+            if (rep > 1) {
+                if (p.dk % 4 == 0) {
+                    if (d < p.dk) *reinterpret_cast<f32x4*>(parts + part + d) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (d + e < p.dk) parts[part + d + e] = v[e];
+                }
+            } else if (p.dk % 4 == 0 && p.vec_dqk) {
+                if (d < p.dk) put4<E>(whole + one + d, 0, v);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (d + e < p.dk) part[d + e] = v[e];
+                    if (d + e < p.dk) whole[one + d + e] = E::put(v[e]);
             }
-        } else if (p.dk % 4 == 0 && p.vec_dqk) {
-            if (d < p.dk) put4<E>(one + d, 0, v);
-        } else {
+        };
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (d + e < p.dk) one[d + e] = E::put(v[e]);
+        for (int t = 0; t < KT; ++t) {
+            put(static_cast<raw*>(p.dq), p.part_q, 16 * t + 4 * g4, q(t));
+            put(static_cast<raw*>(p.dk_), p.part_k, 16 * t + 4 * g4, k(t));
         }
     };
     if (t0 >= end) {  // padding
-#pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            put_row(dQ, partQ, 16 * t + 4 * g4, f32x4{0, 0, 0, 0});
-            put_row(dK, partK, 16 * t + 4 * g4, f32x4{0, 0, 0, 0});
-        }
-        if (g4 == 0 && tok < p.L) p.dg[gat] = p.dbeta[gat] = 0.0f;
+        const auto none = [](int) { return f32x4{0, 0, 0, 0}; };
+        put_rows(none, none);
+        if (g4 == 0 && tok < p.L) p.dg[(int64_t(b) * p.L + tok) * p.H + h] = p.dbeta[(int64_t(b) * p.L + tok) * p.H + h] = 0.0f;
         return;
     }
 
     const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
     const float* vecs = p.vecs + chunk * kVecs * C;
-    const float start = vecs[kStart * C + i], beta = vecs[kBeta * C + i], fade = vecs[kStart * C + C - 1];
-    const float* S0 = p.states + chunk * p.dk * p.dv;
-    const float* dS = p.dstates + chunk * p.dk * p.dv;
-    const float* N = p.fixes + chunk * p.dv * C;
-    const float* Z = p.z + chunk * p.dv * C;
-    const raw* Yi = static_cast<const raw*>(p.dy) + b * p.sdy.batch + h * p.sdy.head + tok * p.sdy.token;
-    const raw* Vi = static_cast<const raw*>(p.v) + b * p.sv.batch + h * p.sv.head + tok * p.sv.token;
+    const Buffer bS = buffer(p.states + chunk * p.dv * p.kpitch, int64_t(p.dv) * p.kpitch * 4);
+    const Buffer bD = buffer(p.dstates + chunk * p.dv * p.kpitch, int64_t(p.dv) * p.kpitch * 4);
+    const Buffer bN = buffer(p.fixes + chunk * p.dv * C, int64_t(p.dv) * C * 4);
+    const Buffer bZ = buffer(p.z + chunk * p.dv * C, int64_t(p.dv) * C * 4);
     const int left = end - t0 < C ? end - t0 : C;  // tokens of the chunk
+    // dY and V: 16 columns of the lane's token to a load, an operand's depths in two
+    constexpr int SZ = sizeof(raw);
+    const auto rows_of = [&](const void* m, const Strided3& s) {
+        return buffer(static_cast<const raw*>(m) + b * s.batch + h * s.head + t0 * s.token, left * s.token * SZ);
+    };
+    const Buffer bY = rows_of(p.dy, p.sdy), bV = rows_of(p.v, p.sv);
+    const uint32_t oy = uint32_t((i * p.sdy.token + 4 * g4) * SZ), ov = uint32_t((i * p.sv.token + 4 * g4) * SZ);
+    const auto load_rows = [&](Buffer m, uint32_t at, int d0) {
+        const int a = int(d0 + 4 * g4 < p.dv ? at + d0 * SZ : kOutside);
+        const int c = int(d0 + 16 + 4 * g4 < p.dv ? at + (d0 + 16) * SZ : kOutside);
+        if constexpr (SZ == 4) {
+            return typename M::frag{__builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(m, a, 0, 0)),
+                                    __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(m, c, 0, 0))};
+        } else {
+            const u32x2 lo = __builtin_amdgcn_raw_buffer_load_b64(m, a, 0, 0), hi = __builtin_amdgcn_raw_buffer_load_b64(m, c, 0, 0);
+            return typename M::frag{lo[0], lo[1], hi[0], hi[1]};
+        }
+    };
     typedef LdsTile<E, DK> KTile;
     typedef LdsTile<E, C> MTile;
     const KTile kt;
-    const MTile mt;
+    const MTile mt, mw(16 * w);  // mw: of the wave's tokens
+    typedef TileRegs<E, C, DK, THREADS> Regs;
+    const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + t0 * p.sq.token + kh * p.sq.head;
     {
-        typedef TileRegs<E, C, DK, THREADS> Regs;
-        Regs k, q;
+        Regs k;
         const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + t0 * p.sk.token + kh * p.sk.head;
-        const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + t0 * p.sq.token + kh * p.sq.head;
         k.load(buffer(K, left * p.sk.token * sizeof(raw)), Regs::offset(p.sk.token, p.dk, tid), p.sk.token);
-        q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk, tid), p.sq.token);
         if (tid < C) Decays<C>::put(sG, t0 + tid < end ? p.g[b * p.g_batch + int64_t(t0 + tid) * p.g_token + h] : 0.0f);
         k.template store<KTile>(sK, tid);
-        q.template store<KTile>(sQ, tid);
     }
 
-    // with the state before the chunk: X1 = S dY^T, X2 = S Z^T; with the corrections: dP^T and M^T
-    f32x4 X1[KT], X2[KT], dP[NT], Mz[NT];
+    // 32 of dv at a time: X1 = S dY^T, X2 = S Z^T, X3 = dS N^T, <S, dS>, dP^T and M^T
+    f32x4 X1[KT], X2[KT], X3[KT], dP[NT], Mz[NT];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) X1[t] = X2[t] = f32x4{0, 0, 0, 0};
+    for (int t = 0; t < KT; ++t) X1[t] = X2[t] = X3[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int t = 0; t < NT; ++t) dP[t] = Mz[t] = f32x4{0, 0, 0, 0};
-    float zv = 0.0f;  // Z_i.V_i
+    float zv = 0.0f, both = 0.0f;  // Z_i.V_i
     typedef Tile32<E, DK, THREADS> STile;
     typedef Tile32<E, C, THREADS> NTile;
-    STile rs;
+    STile rs, rd;
     NTile rn, rz;
-    rs.load(S0, p.dv, 0, p.dk);
-    rn.load(N, p.dv, 0, C);
-    rz.load(Z, p.dv, 0, C);
-    f32x4 y1[2], v1[2];  // of dY and V, of the columns to come
+    typename M::frag y1, v1;  // of dY and V
     const auto ahead = [&](int d0) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int col = d0 + 16 * u + 4 * g4;
-            y1[u] = in ? load4<E>(Yi, col, p.dv, true) : f32x4{0, 0, 0, 0};
-            v1[u] = in ? load4<E>(Vi, col, p.dv, true) : f32x4{0, 0, 0, 0};
-        }
+        rs.load(bS, d0, p.kpitch);
+        rd.load(bD, d0, p.kpitch);
+        rn.load(bN, d0, C);
+        rz.load(bZ, d0, C);
+        y1 = load_rows(bY, oy, d0);
+        v1 = load_rows(bV, ov, d0);
     };
     ahead(0);
     for (int d0 = 0; d0 < p.dv; d0 += 32) {
         lds_meet();
         rs.store(sS);
+        rd.store(sD);
         rn.store(sN);
         rz.store(sZ);
-        const f32x4 y[2] = {y1[0], y1[1]}, v[2] = {v1[0], v1[1]};
+        both += rs.dot(rd);
+        const typename M::frag yf = y1, v = v1;
         lds_meet();
         if (d0 + 32 < p.dv) {
-            rs.load(S0, p.dv, d0 + 32, p.dk);
-            rn.load(N, p.dv, d0 + 32, C);
-            rz.load(Z, p.dv, d0 + 32, C);
             ahead(d0 + 32);
+        } else {  // Q, in registers of S
+            Regs q;
+            q.load(buffer(Q, left * p.sq.token * sizeof(raw)), Regs::offset(p.sq.token, p.dk, tid), p.sq.token);
+#pragma unroll
+            for (int n = 0; n < STile::N; ++n) rs.r[n] = __builtin_bit_cast(f32x4, q.r[n]);
         }
-        const Two<E> zf = two_cols<E>(mt, sZ, w);
-        const typename M::frag yf = M::cvt(y[0], y[1]);  // exact
+        const Two<E> zf = two_cols<E>(mw, sZ, 0), nf = two_cols<E>(mw, sN, 0);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float z = M::at(zf.hi, e);
             if constexpr (M::kSplit) z += M::at(zf.lo, e);
-            zv = fmaf(z, v[e >> 2][e & 3], zv);
+            zv = fmaf(z, M::at(v, e), zv);
         }
+        // operands are read a tile at a time and not further ahead: registers are what is short
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            const Two<E> s = two_cols<E>(kt, sS, t);
+            const Two<E> s = two_cols<E>(kt, sS, t), d = two_cols<E>(kt, sD, t);
             X1[t] = mma2<E>(s, yf, X1[t]);
             X2[t] = mma3<E>(s, zf, X2[t]);
+            X3[t] = mma3<E>(d, nf, X3[t]);
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (t > w) break;
+        for (int t = 0; t < NT; ++t) {  // without a branch: those of later tokens are not used
             const Two<E> nj = two_cols<E>(mt, sN, t);
             dP[t] = mma2<E>(nj, yf, dP[t]);
             Mz[t] = mma3<E>(nj, zf, Mz[t]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
+    lds_meet();  // the tiles are read
+    {
+        static_assert(Regs::N == STile::N, "");
+        Regs q;
+#pragma unroll
+        for (int n = 0; n < STile::N; ++n) q.r[n] = __builtin_bit_cast(u32x4, rs.r[n]);
+        q.template store<KTile>(sQ, tid);
+    }
+    lds_meet();
     zv = sum_groups(zv);
     const auto dot_row = [&](const raw* m, const f32x4 (&x)[KT]) {
         float v = 0.0f;
@@ -251,39 +271,22 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_g
         }
         return sum_groups(v);
     };
-    const float qx = p.scale * start * dot_row(sQ, X1), kx = start * dot_row(sK, X2);
+    const float start = vecs[kStart * C + i], beta = vecs[kBeta * C + i], fade = vecs[kStart * C + C - 1];
+    const float after = vecs[kWrite * C + i];
+    const float qx = p.scale * start * dot_row(sQ, X1), kx = start * dot_row(sK, X2), write = after * dot_row(sK, X3);
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
         X1[t] *= p.scale * start;
-        X2[t] *= -beta * start;
-    }
-
-    // with the gradient of the state behind it: + dS (e^(gamma_C - gamma) N)^T, and <S, dS>
-    float both = 0.0f;
-    {
-        STile r0;
-        const f32x4 after = *reinterpret_cast<const f32x4*>(vecs + kWrite * C + threadIdx.x % NTile::PER_ROW * 4);
-        rs.load(dS, p.dv, 0, p.dk);
-        r0.load(S0, p.dv, 0, p.dk);
-        rn.load(N, p.dv, 0, C);
-        for (int d0 = 0; d0 < p.dv; d0 += 32) {
-            lds_meet();
-            rs.store(sS);
-            rn.scale(after);
-            rn.store(sN);
-            both += rs.dot(r0);
-            lds_meet();
-            if (d0 + 32 < p.dv) {
-                rs.load(dS, p.dv, d0 + 32, p.dk);
-                r0.load(S0, p.dv, d0 + 32, p.dk);
-                rn.load(N, p.dv, d0 + 32, C);
-            }
-            const Two<E> nf = two_cols<E>(mt, sN, w);
+        X2[t] = after * X3[t] - beta * start * X2[t];
+        // here, not where it is used: both are kept until then otherwise
 #pragma unroll
-            for (int t = 0; t < KT; ++t) X2[t] = mma3<E>(two_cols<E>(kt, sS, t), nf, X2[t]);
+        for (int r = 0; r < 4; ++r) {
+            float v = X2[t][r], u = X1[t][r];
+            asm volatile("" : "+v"(v), "+v"(u));
+            X2[t][r] = v;
+            X1[t][r] = u;
         }
     }
-    const float write = dot_row(sK, X2) + beta * kx;
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) both += __shfl_xor(both, d, 64);
     if ((tid & 63) == 0) sDot[w] = both;
@@ -306,8 +309,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_g
     float rows = 0.0f, db = 0.0f;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-        if (t > w)
-            for (int r = 0; r < 4; ++r) kk[t][r] = 0.0f;
+        if (t > w) kk[t] = dP[t] = Mz[t] = f32x4{0, 0, 0, 0};
     Decays<C>::each(sG, w, [&](int t, const f32x4& d) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -334,9 +336,8 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_g
     if (g4 == 0) {
         sRow[i] = rows + qx - beta * kx;
         sWrite[i] = write;
-        if (tok < p.L) p.dbeta[gat] = in ? zv - kx - db : 0.0f;
+        if (tok < p.L) p.dbeta[(int64_t(b) * p.L + tok) * p.H + h] = in ? zv - kx - db : 0.0f;
     }
-    __syncthreads();  // the tiles are read
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         put4<E>(sB + MTile::quad(i, 16 * t + 4 * g4), 0, Mz[t]);  // zeros for the tiles behind w
@@ -374,8 +375,8 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_g
     for (int s = 0; s < NT / 2; ++s) {
         bi[s] = M::cvt(Mz[2 * s], Mz[2 * s + 1]);
         pi[s] = M::cvt(dP[2 * s], dP[2 * s + 1]);
-        bj[s] = mt.cols(sB, s, w);
-        pj[s] = mt.cols(sP, s, w);
+        bj[s] = mw.cols(sB, s, 0);
+        pj[s] = mw.cols(sP, s, 0);
     }
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
@@ -388,9 +389,8 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, DK <= 128 ? 2 : 1) void delta_g
             X2[t] = M::mma(qc, pj[s], X2[t]);
         }
         if (!in) X1[t] = X2[t] = f32x4{0, 0, 0, 0};
-        put_row(dQ, partQ, 16 * t + 4 * g4, X1[t]);
-        put_row(dK, partK, 16 * t + 4 * g4, X2[t]);
     }
+    put_rows([&](int t) { return X1[t]; }, [&](int t) { return X2[t]; });
 }
 
 // Sums over the heads of a key head.

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
     const int kh = u.unit % p.Hk, h = kh * rep + u.part, c = u.unit / p.Hk % p.nchunk, b = u.unit / p.Hk / p.nchunk;
     const int end = seq_end(p.seqlens, b, p.L), t0 = c * C;
     if (t0 >= end) return;
-    const int tid = threadIdx.x, w = tid >> 6, l16 = lane16(), g4 = group4();
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane16(), g4 = group4();
     {
         typedef TileRegs<E, C, DK, THREADS> Regs;
         Regs k, q;

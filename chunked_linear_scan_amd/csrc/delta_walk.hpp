@@ -363,6 +363,17 @@ __device__ __forceinline__ void load_state(f32x4 (&S)[KT], const float* from, in
             S[t][r] = v;
         }
 }
+// The same for the gradients: rows of kpitch elements.
+template <int KT>
+__device__ __forceinline__ void keep_state(const f32x4 (&S)[KT], float* to, int64_t of, int n, int first, const DeltaParams& p) {
+    const Buffer b = buffer(to + of * p.dv * p.kpitch, int64_t(p.dv) * p.kpitch * 4);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+        const int d = first + 16 * t + 4 * group4();
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[t]), b,
+                                               int(d < p.kpitch && n < p.dv ? uint32_t(n * p.kpitch + d) * 4 : kOutside), 0, 0);
+    }
+}
 template <int KT>
 __device__ __forceinline__ void store_state(const f32x4 (&S)[KT], float* to, int64_t of, int n, int first, const DeltaParams& p) {
     const Buffer b = buffer(to + of * p.dv * p.dk, int64_t(p.dv) * p.dk * 4);
