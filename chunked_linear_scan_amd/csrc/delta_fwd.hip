@@ -15,8 +15,8 @@ namespace cls {
 namespace {
 
 // KEEP: with the states and corrections that the gradients need.
-template <typename E, int DK, bool KEEP>
-__global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) {
+template <typename E, int DK, bool KEEP, int TILES>
+__global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaParams p) {
     typedef Mat<E> M;
     typedef HalfOps<E> Op;
     typedef typename M::frag frag;
@@ -28,20 +28,20 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
     constexpr int KT = DK / 32, KS = DK / 64;                   // of a wave's half of the keys' elements: tiles, steps
     extern __shared__ __attribute__((aligned(16))) char lds[];
 
-    const int nblk = (p.dv + kWalkCols - 1) / kWalkCols;
+    const int nblk = (p.dv + walk_cols(TILES) - 1) / walk_cols(TILES);
     const int rep = p.H / p.Hk;
     const UnitPart u = unit_part(p.batch * p.Hk, rep * nblk);
     const int blk = u.part % nblk, h = u.unit % p.Hk * rep + u.part / nblk, b = u.unit / p.Hk;
     const int end = seq_end(p.seqlens, b, p.L), chunks = (end + C - 1) / C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave >= 4) {
+    if (wave >= 2 * TILES) {
         const WalkColumns w{p.v, p.sv, p.y, bool(p.vec_out)};
-        walk_load<E, DK, NM>(p, w, lds, b, h, blk * kWalkCols, end, 0, 1, chunks);
+        walk_load<E, DK, NM, TILES>(p, w, lds, b, h, blk * walk_cols(TILES), end, 0, 1, chunks);
         return;
     }
     const int a = wave & 1, tile = wave >> 1;  // the wave's half, its tile of the columns
     const int l16 = lane16(), g4 = group4();
-    const int n = blk * kWalkCols + tile * 16 + l16;  // the lane's column
+    const int n = blk * walk_cols(TILES) + tile * 16 + l16;  // the lane's column
 
     f32x4 S[KT];
     load_state<KT>(S, p.h0, int64_t(b) * p.H + h, n, a * (DK / 2), p);
@@ -233,17 +233,17 @@ __global__ __launch_bounds__(kWalkThreads) void delta_fwd_kernel(DeltaParams p) 
     if (p.h_last) store_state<KT>(S, p.h_last, int64_t(b) * p.H + h, n, a * (DK / 2), p);
 }
 
-template <typename E, int DK, bool KEEP>
+template <typename E, int DK, bool KEEP, int TILES>
 int launch(const DeltaParams& p, hipStream_t stream) {
     typedef WalkLds<E, DK, ChunkMats<E>::kParts + 1> Lds;
     static DeviceOnce once;
     const int st = run_once_per_device(once, [] {
-        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_fwd_kernel<E, DK, KEEP>),
+        return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_fwd_kernel<E, DK, KEEP, TILES>),
                                    hipFuncAttributeMaxDynamicSharedMemorySize, Lds::kBytes) == hipSuccess ? 0 : -7;
     });
     if (st != 0) return st;
-    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + kWalkCols - 1) / kWalkCols));
-    delta_fwd_kernel<E, DK, KEEP><<<wgs, kWalkThreads, Lds::kBytes, stream>>>(p);
+    const unsigned wgs = unsigned(int64_t(p.batch) * p.H * ((p.dv + walk_cols(TILES) - 1) / walk_cols(TILES)));
+    delta_fwd_kernel<E, DK, KEEP, TILES><<<wgs, walk_threads(TILES), Lds::kBytes, stream>>>(p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
@@ -254,6 +254,9 @@ int cls_delta_fwd_launch(const cls::DeltaParams& p, int dtype, hipStream_t strea
     return cls::by_type(dtype, p.dk, [&](auto e, auto dk) {
         typedef decltype(e) E;
         constexpr int DK = decltype(dk)::value;
-        return p.states ? cls::launch<E, DK, true>(p, stream) : cls::launch<E, DK, false>(p, stream);
+        return cls::by_tiles(p, [&](auto tiles) {
+            constexpr int TILES = decltype(tiles)::value;
+            return p.states ? cls::launch<E, DK, true, TILES>(p, stream) : cls::launch<E, DK, false, TILES>(p, stream);
+        });
     });
 }

@@ -9,12 +9,14 @@
 //   - four more waves load, and store what is not kept for the gradients, two chunks ahead;
 //   - operands are read from LDS a step before their products, and products are
 //     interleaved with vector instructions.
-// A workgroup has 32 columns: four computing waves, one to a SIMD, and four that load.  A chunk of 64 tokens and keys of
-// 128 takes 1.7 us, 1.5 of them the computing waves'.  (One wave to 16 columns: 1.95 us with two computing waves to a workgroup,
+// A workgroup has 32 columns: four computing waves, one to a SIMD, and four that load; or 16, and two.  A chunk of 64 tokens and
+// keys of 128 takes 1.7 us, 1.5 of them the computing waves'.  (One wave to 16 columns: 1.95 us with two computing waves to a workgroup,
 // 2.3 with four, where their reads of LDS took 3200 cycles of the 5500.)
 #pragma once
 
 #include "delta.hpp"
+#include <type_traits>
+
 #include "device_once.hpp"
 
 namespace cls {
@@ -39,8 +41,18 @@ __device__ __forceinline__ void settle(f32x4& x) {
     x = f32x4{a, b, c, d};
 }
 
-constexpr int kWalkCols = 32;      // columns to a workgroup
-constexpr int kWalkThreads = 512;  // computing waves (16 (w / 2).. of the columns, half w % 2), then loading waves
+// A workgroup of TILES has 16 TILES columns: computing waves (16 (w / 2).. of the columns, half w % 2), then four that load.
+constexpr int walk_cols(int tiles) { return 16 * tiles; }
+constexpr int walk_threads(int tiles) { return 128 * tiles + 256; }
+
+// Calls f with the tiles of a walk's workgroups: two, or one, with the same rows of K, Q and matrices to load for half the columns,
+// where all of those have a compute unit of their own (1 x 32768 x 32 heads of 128: 842 us instead of 880; fp32 4096 x 8: 68
+// instead of 75).
+template <typename F>
+int by_tiles(const DeltaParams& p, F&& f) {
+    const int64_t columns = int64_t(p.batch) * p.H * ((p.dv + 15) / 16);
+    return columns <= 256 ? f(std::integral_constant<int, 1>()) : f(std::integral_constant<int, 2>());
+}
 
 // LDS of a walk: K, Q, NM triangular matrices of a chunk (32 columns of all rows, then the others of the last 32), its
 // columns of V and its factors; those of y; what waves exchange.  The first two twice where that fits.
@@ -51,7 +63,7 @@ struct WalkLds {
     typedef LdsTile<E, 32> MTile;  // of a block of 32 columns, and of V
     static constexpr int C = Mat<E>::kChunk;
     static constexpr int KS = C * KTile::kPitch, M1 = C * MTile::kPitch, MS = M1 + (C - 32) * MTile::kPitch;
-    static constexpr int YP = kWalkCols + 16 / int(sizeof(raw));  // pitch of y
+    static constexpr int YP = 32 + 16 / int(sizeof(raw));  // pitch of y
     static constexpr int kBuffer = int((2 * KS + NM * MS + M1) * sizeof(raw) + kVecs * C * sizeof(float));
     static constexpr int kOut = C * YP * int(sizeof(raw));
     static constexpr int kSlots = 6, kExchange = 4 * kSlots * 1024;
@@ -165,7 +177,7 @@ struct WalkColumns {
 };
 
 // Chunks first, first + step, .. (n of them).
-template <typename E, int DK, int NM>
+template <typename E, int DK, int NM, int TILES>
 __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumns& w, char* lds, int b, int h, int col0, int end,
                                           int first, int step, int n) {
     typedef Mat<E> M;
@@ -178,11 +190,11 @@ __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumn
     typedef TileRegs<E, C, 32, THREADS> XRegs;  // 32 columns: of a matrix, of V, of y
     static_assert(XRegs::N == 1, "");
     constexpr int LOW = (C - 32) * XRegs::PER_ROW;  // threads with a vector of the last 32 columns
-    const int kh = h / (p.H / p.Hk), tid = threadIdx.x % THREADS;
+    const int kh = h / (p.H / p.Hk), tid = threadIdx.x - 128 * TILES;
     const raw* K = static_cast<const raw*>(p.k) + b * p.sk.batch + kh * p.sk.head;
     const raw* Q = static_cast<const raw*>(p.q) + b * p.sq.batch + kh * p.sq.head;
     const raw* X = static_cast<const raw*>(w.x) + b * w.sx.batch + h * w.sx.head + col0;
-    const int cols = p.dv - col0 < kWalkCols ? p.dv - col0 : kWalkCols;
+    const int cols = p.dv - col0 < walk_cols(TILES) ? p.dv - col0 : walk_cols(TILES);
     const int xrow = tid / XRegs::PER_ROW, xcol = tid % XRegs::PER_ROW * XRegs::VE;  // a thread's vector of 32 columns
     const uint32_t ok = KRegs::offset(p.sk.token, p.dk, tid), oq = KRegs::offset(p.sq.token, p.dk, tid);
     // two chunks in flight, where LDS has two: a chunk may take less time than a load from memory
