@@ -330,6 +330,21 @@ __device__ __forceinline__ void store_one(Buffer b, uint32_t offset, float v) {
     else __builtin_amdgcn_raw_buffer_store_b16(E::put(v), b, int(offset), 0, 0);
 }
 
+// The lane's part of an operand of rows in memory: depths col.. of `dim`, of the row at byte offset `row`.
+template <typename E>
+__device__ __forceinline__ typename Mat<E>::frag load_frag(Buffer b, uint32_t row, int col, int dim) {
+    constexpr int SZ = sizeof(typename E::raw);
+    const int d = col + 4 * group4();
+    const int lo = int(d < dim ? row + d * SZ : kOutside), hi = int(d + 16 < dim ? row + (d + 16) * SZ : kOutside);
+    if constexpr (SZ == 4) {
+        return {__builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lo, 0, 0)),
+                __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, hi, 0, 0))};
+    } else {
+        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(b, lo, 0, 0), y = __builtin_amdgcn_raw_buffer_load_b64(b, hi, 0, 0);
+        return u32x4{x[0], x[1], y[0], y[1]};
+    }
+}
+
 // Four values of a row: elements col.. of `dim` (zeros past it).
 template <typename E>
 __device__ __forceinline__ f32x4 load4(const typename E::raw* row, int col, int dim, bool vec) {

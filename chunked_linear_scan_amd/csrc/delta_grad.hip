@@ -157,24 +157,13 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
     const Buffer bN = buffer(p.fixes + chunk * p.dv * C, int64_t(p.dv) * C * 4);
     const Buffer bZ = buffer(p.z + chunk * p.dv * C, int64_t(p.dv) * C * 4);
     const int left = end - t0 < C ? end - t0 : C;  // tokens of the chunk
-    // dY and V: 16 columns of the lane's token to a load, an operand's depths in two
+    // dY and V, of the lane's token
     constexpr int SZ = sizeof(raw);
     const auto rows_of = [&](const void* m, const Strided3& s) {
         return buffer(static_cast<const raw*>(m) + b * s.batch + h * s.head + t0 * s.token, left * s.token * SZ);
     };
     const Buffer bY = rows_of(p.dy, p.sdy), bV = rows_of(p.v, p.sv);
-    const uint32_t oy = uint32_t((i * p.sdy.token + 4 * g4) * SZ), ov = uint32_t((i * p.sv.token + 4 * g4) * SZ);
-    const auto load_rows = [&](Buffer m, uint32_t at, int d0) {
-        const int a = int(d0 + 4 * g4 < p.dv ? at + d0 * SZ : kOutside);
-        const int c = int(d0 + 16 + 4 * g4 < p.dv ? at + (d0 + 16) * SZ : kOutside);
-        if constexpr (SZ == 4) {
-            return typename M::frag{__builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(m, a, 0, 0)),
-                                    __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(m, c, 0, 0))};
-        } else {
-            const u32x2 lo = __builtin_amdgcn_raw_buffer_load_b64(m, a, 0, 0), hi = __builtin_amdgcn_raw_buffer_load_b64(m, c, 0, 0);
-            return typename M::frag{lo[0], lo[1], hi[0], hi[1]};
-        }
-    };
+    const uint32_t oy = uint32_t(i * p.sdy.token * SZ), ov = uint32_t(i * p.sv.token * SZ);
     typedef LdsTile<E, DK> KTile;
     typedef LdsTile<E, C> MTile;
     const KTile kt;
@@ -206,8 +195,8 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
         rd.load(bD, d0, p.kpitch);
         rn.load(bN, d0, C);
         rz.load(bZ, d0, C);
-        y1 = load_rows(bY, oy, d0);
-        v1 = load_rows(bV, ov, d0);
+        y1 = load_frag<E>(bY, oy, d0, p.dv);
+        v1 = load_frag<E>(bV, ov, d0, p.dv);
     };
     ahead(0);
     for (int d0 = 0; d0 < p.dv; d0 += 32) {
