@@ -149,7 +149,10 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_bwd_kernel(DeltaPar
         for (int j = 0; j < OT; ++j) Z[j] = dN[j];
         if constexpr (kSplit) {
 #pragma unroll
-            for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Tl[j], dn.hi, Z[j]);
+            for (int j = 0; j < OT; ++j) {
+                if (small_parts(DK)) Z[j] = Op::mma(Tl[j], dn.lo, Z[j]);
+                Z[j] = Op::mma(Tl[j], dn.hi, Z[j]);
+            }
 #pragma unroll
             for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Th[j], dn.lo, Z[j]);
         }
@@ -180,7 +183,10 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_bwd_kernel(DeltaPar
             if constexpr (kSplit) {
                 ex.get(5, xx.lo);
 #pragma unroll
-                for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Xl[j], xx.hi, Z[j]);
+                for (int j = 0; j < OT; ++j) {
+                    if (small_parts(DK)) Z[j] = Op::mma(Xl[j], xx.lo, Z[j]);
+                    Z[j] = Op::mma(Xl[j], xx.hi, Z[j]);
+                }
 #pragma unroll
                 for (int j = 0; j < OT; ++j) Z[j] = Op::mma(Xh[j], xx.lo, Z[j]);
             }

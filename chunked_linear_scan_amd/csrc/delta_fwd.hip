@@ -138,7 +138,10 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
         for (int j = 0; j < OT; ++j) N[j] = R[j];
         if constexpr (kSplit) {
 #pragma unroll
-            for (int j = 0; j < OT; ++j) N[j] = Op::mma(Tl[j], rr.hi, N[j]);
+            for (int j = 0; j < OT; ++j) {
+                if (small_parts(DK)) N[j] = Op::mma(Tl[j], rr.lo, N[j]);
+                N[j] = Op::mma(Tl[j], rr.hi, N[j]);
+            }
 #pragma unroll
             for (int j = 0; j < OT; ++j) N[j] = Op::mma(Th[j], rr.lo, N[j]);
         }
@@ -165,7 +168,10 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
             if constexpr (kSplit) {
                 ex.get(5, xx.lo);
 #pragma unroll
-                for (int j = 0; j < OT; ++j) N[j] = Op::mma(Xl[j], xx.hi, N[j]);
+                for (int j = 0; j < OT; ++j) {
+                    if (small_parts(DK)) N[j] = Op::mma(Xl[j], xx.lo, N[j]);
+                    N[j] = Op::mma(Xl[j], xx.hi, N[j]);
+                }
 #pragma unroll
                 for (int j = 0; j < OT; ++j) N[j] = Op::mma(Xh[j], xx.lo, N[j]);
             }
