@@ -87,6 +87,30 @@ def test_delta_and_gradients(shape, kind):
           label=str(shape))
 
 
+# more than 256 tiles of 16 columns, so workgroups of two; the last one of a head with one, or part of one
+MANY = [(3, 64, 2, 6, 64, 250), (2, 65, 10, 10, 128, 200), (1, 190, 3, 9, 24, 500), (3, 330, 1, 3, 72, 450),
+        (2, 129, 2, 6, 256, 360)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", MANY)
+def test_delta_many_columns(shape, kind):
+    seed = 200 + MANY.index(shape)
+    check(delta_case(seed, *shape, kind=kind, start=seed % 2 == 0, ragged=seed % 2 == 1), kind, label=str(shape))
+
+
+def test_delta_of_a_head_does_not_depend_on_the_others():
+    """Workgroups of one and of two tiles of columns: the same sums in the same order."""
+    c = on_gpu(delta_case(210, 2, 200, 9, 9, 64, 250, start=True))
+    want = run(c)
+    few = {k: v[:, :, :4] if k in ("q", "k", "v", "g", "beta", "dy") else v[:, :4].contiguous() if k in ("h0", "dh") else v
+           for k, v in c.items()}
+    got = run(few)
+    for n in got:
+        head = 1 if n in ("h", "dh0") else 2
+        assert torch.equal(got[n], want[n].narrow(head, 0, 4)), n
+
+
 @pytest.mark.parametrize("off", ["start", "dh", "ragged", "strong", "scale", "negative scale", "none"])
 def test_delta_options(off):
     c = delta_case(7, 2, 90, 2, 4, 64, 40, start=off != "start", ragged=off == "ragged", strong=off == "strong")

@@ -67,6 +67,13 @@ def test_gated_norm_of_many_rows():
     check_gated(gated_case(5, 3000, 1, 1100, "bf16"), True, "many long")
 
 
+@pytest.mark.parametrize("dim,rows", [(700, 2500), (2500, 700), (5000, 600), (9000, 300)])
+def test_norms_of_many_wide_rows(dim, rows):
+    """A row over 128 to 1024 lanes, and more rows than workgroups: the waves' sums of one row and the next do not meet."""
+    check_gated(gated_case(6 + dim, rows, 1, dim, "bf16"), False, "wide")
+    check_residual(residual_case(7 + dim, rows, dim, "bf16", "f32"), "wide")
+
+
 def test_gated_norm_row_of_zeros_and_large_values():
     """A zero row has the norm of eps alone; squares stay finite up to 2^63 (fp32), and gates saturate."""
     c = gated_case(6, 4, 2, 64, "f32")
