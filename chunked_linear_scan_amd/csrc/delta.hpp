@@ -287,6 +287,7 @@ __device__ __forceinline__ void lds_meet() { asm volatile("s_waitcnt lgkmcnt(0)\
 // written.  Strides are bounded by kDeltaMaxToken, so that the rows of a chunk lie within.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kOutside = 0x80000000u;
+constexpr int kStream = 2;  // of a load or store: not to be kept in the caches (nt)
 typedef __amdgpu_buffer_rsrc_t Buffer;
 __device__ __forceinline__ Buffer buffer(const void* p, int64_t bytes = kOutside) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes < int64_t(kOutside) ? int(bytes) : int(kOutside),

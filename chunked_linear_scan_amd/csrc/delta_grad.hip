@@ -16,8 +16,9 @@
 // What reaches dg and dbeta, fp32 outputs, takes computed operands in two parts;
 // pP and pB only reach dQ and dK and go in as one.
 // Bound by memory: a chunk's states, corrections and operands are read once, 32 of dv at a time, of the 288 KB that
-// it moves for 64 tokens and keys and values of 128 (192 KB of states and corrections; 4 x 2048 x 16 heads: 164 us, 3.7 TB/s; with the products with S and with dS
-// in two walks over dv: 196).  LDS has K and those tiles, and Q and the pairs in the tiles' place afterwards, so that two
+// it moves for 64 tokens and keys and values of 128 (192 KB of states and corrections; 4 x 2048 x 16 heads: 147 us, 4.1 TB/s; before they went past the
+// caches 164, and with the products with S and with dS
+// in two walks over dv as well 196).  LDS has K and those tiles, and Q and the pairs in the tiles' place afterwards, so that two
 // workgroups fit a compute unit.
 #include <hip/hip_runtime.h>
 
@@ -48,7 +49,7 @@ struct Tile32 {
         const uint32_t at = col < cols ? uint32_t(row * cols + col) * 4 : kOutside;
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            r[n] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, int(at + uint32_t(n * STEP * cols * 4)), 0, 0));
+            r[n] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, int(at + uint32_t(n * STEP * cols * 4)), 0, kStream));
     }
     __device__ __forceinline__ void store(typename E::raw* to) const {
         const int col = threadIdx.x % PER_ROW * 4;
