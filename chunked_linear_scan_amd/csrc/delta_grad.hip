@@ -15,11 +15,10 @@
 // leave as four adjacent values of a token, and the decays are factors of a lane.
 // What reaches dg and dbeta, fp32 outputs, takes computed operands in two parts;
 // pP and pB only reach dQ and dK and go in as one.
-// Bound by memory: a chunk's states, corrections and operands are read once, 32 of dv at a time, of the 288 KB that
-// it moves for 64 tokens and keys and values of 128 (192 KB of states and corrections; 4 x 2048 x 16 heads: 147 us, 4.1 TB/s; before they went past the
-// caches 164, and with the products with S and with dS
-// in two walks over dv as well 196).  LDS has K and those tiles, and Q and the pairs in the tiles' place afterwards, so that two
-// workgroups fit a compute unit.
+// Bound by memory: a chunk's states and corrections (192 KB of the 288 KB that it moves for 64 tokens, keys and values of 128)
+// are read once, 32 of dv at a time, past the caches: 4 x 2048 x 16 heads 150 us, 4.0 TB/s; through the caches 164; with the
+// products with S and with dS in two walks over dv as well 196.  LDS has K and those tiles, and Q and the pairs in the tiles'
+// place afterwards, so that two workgroups fit a compute unit.
 #include <hip/hip_runtime.h>
 
 #include "delta.hpp"

@@ -10,7 +10,7 @@
 //   - operands are read from LDS a step before their products, and products are
 //     interleaved with vector instructions.
 // A workgroup has 32 columns: four computing waves, one to a SIMD, and four that load; or 16, and two.  A chunk of 64 tokens and
-// keys of 128 takes 1.7 us, 1.5 of them the computing waves'.  (One wave to 16 columns: 1.95 us with two computing waves to a workgroup,
+// keys of 128 takes 1.7 us, 1.5 without its loads; with 16 columns 1.6.  (One wave to 16 columns: 1.95 us with two computing waves to a workgroup,
 // 2.3 with four, where their reads of LDS took 3200 cycles of the 5500.)
 #pragma once
 
@@ -376,7 +376,8 @@ __device__ __forceinline__ void load_state(f32x4 (&S)[KT], const float* from, in
         }
 }
 // The same for the gradients: rows of kpitch elements.  Past the caches, as all of it is written before any of it is read
-// (4 x 2048 x 16 heads of 128: the walks 121 and 136 -> 113 and 128 us, the gradients' kernel, which reads it once, 165 -> 147).
+// (4 x 2048 x 16 heads of 128: the walks 121 and 136 -> 115 and 130 us, the gradients'
+// kernel, which reads it once, 165 -> 150).
 template <int KT>
 __device__ __forceinline__ void keep_state(const f32x4 (&S)[KT], float* to, int64_t of, int n, int first, const DeltaParams& p) {
     const Buffer b = buffer(to + of * p.dv * p.kpitch, int64_t(p.dv) * p.kpitch * 4);
