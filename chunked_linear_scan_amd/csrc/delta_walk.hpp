@@ -10,13 +10,13 @@
 //   - operands are read from LDS a step before their products, and products are
 //     interleaved with vector instructions.
 // A workgroup has 32 columns: four computing waves, one to a SIMD, and four that load; or 16, and two.  A chunk of 64 tokens and
-// keys of 128 takes 1.7 us, 1.5 without its loads; with 16 columns 1.6.  (One wave to 16 columns: 1.95 us with two computing waves to a workgroup,
-// 2.3 with four, where their reads of LDS took 3200 cycles of the 5500.)
+// keys of 128 takes 1.7 us, 1.5 without its loads; with 16 columns 1.6.  (One wave to 16 columns: 1.95 us with two computing
+// waves to a workgroup, 2.3 with four, where their reads of LDS took 3200 cycles of the 5500.)
 #pragma once
 
-#include "delta.hpp"
 #include <type_traits>
 
+#include "delta.hpp"
 #include "device_once.hpp"
 
 namespace cls {
