@@ -160,7 +160,7 @@ struct DeltaParams {
     float *h_last, *dg, *dbeta, *dh0;
     float* states;   // [batch, chunks, heads, dv, kpitch]: the state before each chunk (NULL = not kept)
     float* fixes;    // [batch, chunks, heads, dv, chunk]: N, the corrections (NULL = not kept)
-    void* mats;      // per (batch, chunk, head): (I + A)^-1 - I and D QK^T (forward: times scale), in one part or two
+    void* mats;      // per (batch, chunk, head): (I + A)^-1 - I and D QK^T, each in its parts
     float* vecs;     // per (batch, chunk, head): kVecs factors of each token
     float* dstates;  // as states: the gradient of the state behind each chunk
     float* z;        // as fixes: (I + A)^-T dN

@@ -233,7 +233,7 @@ int gated_delta_fwd(const gated_delta_inputs* in, void* y, float* h_final, void*
     p.h_last = h_final;
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     int rc = delta_pack(*in, workspace, s, hs);
-    if (rc == 0) rc = cls_delta_prep_launch(p, in->dtype, false, hs);
+    if (rc == 0) rc = cls_delta_prep_launch(p, in->dtype, hs);
     if (rc == 0) rc = cls_delta_fwd_launch(p, in->dtype, hs);
     return launched(rc);
 }
@@ -274,7 +274,7 @@ int gated_delta_bwd(const gated_delta_inputs* in, const gated_delta_grads* g, vo
     if (rc == 0 && pack_dy)
         rc = cls_delta_pack_launch(g->dy, ws + s.dy, int64_t(elem_size(in->dtype)), in->batch, in->seqlen, in->heads, in->dv,
                                    dv, g->dy_batch, g->dy_token, g->dy_head, hs);
-    if (rc == 0) rc = cls_delta_prep_launch(p, in->dtype, true, hs);
+    if (rc == 0) rc = cls_delta_prep_launch(p, in->dtype, hs);
     if (rc == 0) rc = cls_delta_bwd_launch(p, in->dtype, hs);
     if (rc == 0) rc = cls_delta_grad_launch(p, in->dtype, hs);
     return launched(rc);

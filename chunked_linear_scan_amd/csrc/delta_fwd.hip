@@ -4,8 +4,8 @@
 // T - I, P and factors.  Per chunk
 //     R = beta (V - e^gamma K S),  N = R + (T - I) R,  Y = scale (e^gamma Q S + P N),
 //     S' = e^gamma_C S + K^T (e^(gamma_C - gamma) N)
-// where K S, T R and K^T N reach the state and take computed operands in two
-// parts, and Q S and P N only reach y and take them in one.
+// with all computed operands in two parts: y, too, is off by its own rounding and little else (with one part of
+// S, P and N where only y reads them its 2-norm error was 2.8e-3 in bf16, of which 1.7e-3 are its rounding).
 #include <hip/hip_runtime.h>
 
 #include "delta_walk.hpp"
@@ -22,7 +22,7 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
     typedef typename M::frag frag;
     typedef typename Op::op op;
     constexpr bool kSplit = M::kSplit;
-    constexpr int kParts = ChunkMats<E>::kParts, NM = kParts + 1;  // T - I in its parts, P
+    constexpr int kParts = ChunkMats<E>::kParts, NM = ChunkMats<E>::kAll;  // T - I, P, in their parts
     typedef WalkLds<E, DK, NM> Lds;
     constexpr int C = M::kChunk, NT = C / 16, OT = Op::OT;      // tiles of a chunk's tokens, of a half's
     constexpr int KT = DK / 32, KS = DK / 64;                   // of a wave's half of the keys' elements: tiles, steps
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
         Two<E> st[2];
         read(k[0], q[0], 0);
         const op v = Op::tokens(xt, m.x, a, 0);
-        op Th[OT], Tl[OT], P[OT], Xh[OT], Xl[OT], PX[OT];
+        op Th[OT], Tl[OT], Ph[OT], Pl[OT], Xh[OT], Xl[OT], Yh[OT], Yl[OT];
 #pragma unroll
         for (int j = 0; j < OT; ++j) be[j] = factors(kBeta, j);
 #pragma unroll
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
 #pragma unroll
                 for (int j = 0; j < OT; ++j) {
                     bs[j] = factors(kBetaStart, j);
-                    e[j] = factors(kRead, j);
+                    e[j] = factors(kStart, j);
                     Th[j] = Op::rows(mt, m.m, Lds::M1, a, a, j);
                     if constexpr (kSplit) Tl[j] = Op::rows(mt, m.m + Lds::MS, Lds::M1, a, a, j);
                 }
@@ -107,12 +107,14 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
             if constexpr (kSplit) {
 #pragma unroll
                 for (int t = NT - 1; t >= 0; --t) ks[t] = M::mma(k[s & 1][t], st[s & 1].lo, ks[t]);
+#pragma unroll
+                for (int t = NT - 1; t >= 0; --t) O[t] = M::mma(q[s & 1][t], st[s & 1].lo, O[t]);
             }
 #pragma unroll
             for (int t = NT - 1; t >= 0; --t) ks[t] = M::mma(k[s & 1][t], st[s & 1].hi, ks[t]);
 #pragma unroll
             for (int t = NT - 1; t >= 0; --t) O[t] = M::mma(q[s & 1][t], st[s & 1].hi, O[t]);
-            interleave<3 * NT, 4>();
+            interleave<4 * NT, 3>();
             fence();
         }
 #pragma unroll
@@ -151,11 +153,13 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
         for (int j = 0; j < OT; ++j) {
             O[j] = (O[j] + x[OT + j]) * e[j];
             e[j] = factors(kWrite, j);
-            P[j] = Op::rows(mt, m.m + kParts * Lds::MS, Lds::M1, a, a, j);
+            Ph[j] = Op::rows(mt, m.m + kParts * Lds::MS, Lds::M1, a, a, j);
+            if constexpr (kSplit) Pl[j] = Op::rows(mt, m.m + (kParts + 1) * Lds::MS, Lds::M1, a, a, j);
             if (a == 0) continue;
             Xh[j] = Op::rows(mt, m.m, Lds::M1, 1, 0, j);
             if constexpr (kSplit) Xl[j] = Op::rows(mt, m.m + Lds::MS, Lds::M1, 1, 0, j);
-            PX[j] = Op::rows(mt, m.m + kParts * Lds::MS, Lds::M1, 1, 0, j);
+            Yh[j] = Op::rows(mt, m.m + kParts * Lds::MS, Lds::M1, 1, 0, j);
+            if constexpr (kSplit) Yl[j] = Op::rows(mt, m.m + (kParts + 1) * Lds::MS, Lds::M1, 1, 0, j);
         }
         op kc[2][2];
         kc[0][0] = Op::tokens(kt, m.k, a, 0);
@@ -182,10 +186,13 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
 #pragma unroll
         for (int j = 0; j < OT; ++j) w[j] = N[j] * e[j];
         const auto nn = Op::two(w);
-        const op nf = Op::cvt(N);
+        const auto nf = Op::two(N);
         ex.put(0, nn.hi);
         if constexpr (kSplit) ex.put(1, nn.lo);
-        if (a == 0) ex.put(2, nf);
+        if (a == 0) {
+            ex.put(2, nf.hi);
+            if constexpr (kSplit) ex.put(3, nf.lo);
+        }
         fence();
         // the state, by the half's own tokens, then by the others; two tiles in turn, as a product waits for the one
         // before it on its tile
@@ -219,21 +226,30 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
             kc[0][0] = kc[1][0];
             kc[0][1] = kc[1][1];
         }
+        const auto read_out = [&](const op (&h)[OT], const op (&l)[OT], const auto& by) {
+            if constexpr (kSplit) {
 #pragma unroll
-        for (int j = 0; j < OT; ++j) O[j] = Op::mma(P[j], nf, O[j]);
+                for (int j = 0; j < OT; ++j) O[j] = Op::mma(l[j], by.hi, O[j]);
+#pragma unroll
+                for (int j = 0; j < OT; ++j) O[j] = Op::mma(h[j], by.lo, O[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < OT; ++j) O[j] = Op::mma(h[j], by.hi, O[j]);
+        };
+        read_out(Ph, Pl, nf);
         lds_meet();  // 3: the other half's corrections
         auto xx = nn;
-        op xf = nf;
         ex.get(0, xx.hi);
         if constexpr (kSplit) ex.get(1, xx.lo);
         if (a) {
-            ex.get(2, xf);
-#pragma unroll
-            for (int j = 0; j < OT; ++j) O[j] = Op::mma(PX[j], xf, O[j]);
+            auto xf = nf;
+            ex.get(2, xf.hi);
+            if constexpr (kSplit) ex.get(3, xf.lo);
+            read_out(Yh, Yl, xf);
         }
         add(1 - a, xx, false);
 #pragma unroll
-        for (int j = 0; j < OT; ++j) put_column<E, Lds::YP>(m.y + oy, j, O[j]);
+        for (int j = 0; j < OT; ++j) put_column<E, Lds::YP>(m.y + oy, j, p.scale * O[j]);
         settle(S[KT - 1]);
     });
     if (p.h_last) store_state<KT>(S, p.h_last, int64_t(b) * p.H + h, n, a * (DK / 2), p);
@@ -241,7 +257,7 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
 
 template <typename E, int DK, bool KEEP, int TILES>
 int launch(const DeltaParams& p, hipStream_t stream) {
-    typedef WalkLds<E, DK, ChunkMats<E>::kParts + 1> Lds;
+    typedef WalkLds<E, DK, ChunkMats<E>::kAll> Lds;
     static DeviceOnce once;
     const int st = run_once_per_device(once, [] {
         return hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_fwd_kernel<E, DK, KEEP, TILES>),

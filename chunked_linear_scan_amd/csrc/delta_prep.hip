@@ -4,9 +4,8 @@
 // here are T - I, T = (I + A)^-1, P_ij = D_ij q_i.k_j (j <= i) and the factors
 // e^gamma_i and e^(gamma_C - gamma_j) of reads and writes of the state.  The ones
 // of T's diagonal are left out so that what they multiply stays in fp32 (with two
-// bf16 numbers to an operand half of the states' error came from them).  For the
-// forward pass P is multiplied by the scale; for the backward pass, which takes it
-// in two parts, it is not, so that with fp16 fewer entries are subnormal.
+// bf16 numbers to an operand half of the states' error came from them).  P is without
+// the scale, so that with fp16 fewer entries are subnormal.
 //
 // T by blocks: the 16x16 diagonal blocks by forward substitution (a column to a
 // lane, in registers), then T10 = -T11 A10 T00 for pairs of blocks and pairs of
@@ -39,7 +38,7 @@ __device__ __forceinline__ void put16(float* t, int pitch, const f32x4& v) {
 }
 
 template <typename E, int DK>
-__global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaParams p, int p_parts) {
+__global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaParams p) {
     typedef Mat<E> M;
     typedef typename M::raw raw;
     constexpr int C = M::kChunk, NT = C / 16, THREADS = 64 * NT;
@@ -100,20 +99,18 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
     if (!(w & 1)) {  // above the diagonal, but within the 32 columns that products read
 #pragma unroll
         for (int part = 0; part < ChunkMats<E>::kParts; ++part)
-            if (part < p_parts)
-                put4<E>(P + part * ChunkMats<E>::kSize + i * C + 16 * (w + 1) + 4 * g4, 0, f32x4{0, 0, 0, 0});
+            put4<E>(P + part * ChunkMats<E>::kSize + i * C + 16 * (w + 1) + 4 * g4, 0, f32x4{0, 0, 0, 0});
     }
-    const float scale = p_parts > 1 ? 1.0f : p.scale;
     Decays<C>::each(sG, w, [&](int t, const f32x4& d) {
         f32x4 a, q;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int j = 16 * t + 4 * g4 + r;
             a[r] = j < i ? beta * d[r] * kk[t][r] : 0.0f;
-            q[r] = j <= i ? scale * d[r] * qk[t][r] : 0.0f;
+            q[r] = j <= i ? d[r] * qk[t][r] : 0.0f;
         }
         *reinterpret_cast<f32x4*>(sA + i * AP + 16 * t + 4 * g4) = a;
-        put4<E>(P + i * C + 16 * t + 4 * g4, p_parts > 1 ? ChunkMats<E>::kSize : 0, q);
+        put4<E>(P + i * C + 16 * t + 4 * g4, ChunkMats<E>::kSize, q);
     });
     if (g4 == 0) {
         float* vecs = p.vecs + chunk * kVecs * C;
@@ -177,17 +174,17 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4) void delta_prep_kernel(DeltaPar
 }
 
 template <typename E, int DK>
-int launch(const DeltaParams& p, bool backward, hipStream_t stream) {
+int launch(const DeltaParams& p, hipStream_t stream) {
     const unsigned wgs = unsigned(int64_t(p.batch) * p.nchunk * p.H);
-    delta_prep_kernel<E, DK><<<wgs, 4 * Mat<E>::kChunk, 0, stream>>>(p, backward ? 2 : 1);
+    delta_prep_kernel<E, DK><<<wgs, 4 * Mat<E>::kChunk, 0, stream>>>(p);
     return hipGetLastError() == hipSuccess ? 0 : -7;
 }
 
 }  // namespace
 }  // namespace cls
 
-int cls_delta_prep_launch(const cls::DeltaParams& p, int dtype, bool backward, hipStream_t stream) {
+int cls_delta_prep_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream) {
     return cls::by_type(dtype, p.dk, [&](auto e, auto dk) {
-        return cls::launch<decltype(e), decltype(dk)::value>(p, backward, stream);
+        return cls::launch<decltype(e), decltype(dk)::value>(p, stream);
     });
 }

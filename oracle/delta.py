@@ -5,9 +5,9 @@ float64 loops, with error bounds.  Test infrastructure only.
 kernels' chunk algebra in float64 to see how large the terms are whose rounding
 reaches each output, and returns absolute bounds to first order:
 
-* a product's computed operand that reaches a state or an fp32 gradient carries
-  a relative error of ``u2`` (two bf16 numbers 2^-16, two fp16 numbers 2^-22, fp32 2^-24), one
-  that only reaches a 16-bit output ``u1`` (half a step: 2^-8, 2^-11, 2^-24);
+* a product's computed operand carries a relative error of ``u2`` (two bf16 numbers 2^-16, two
+  fp16 numbers 2^-22, fp32 2^-24), the pairs of tokens that only reach dq and dk one of ``u1``
+  (half a step: 2^-8, 2^-11, 2^-24);
 * every product's fp32 sums and factors add ``W`` = 32 units of 2^-24 of the sum of its
   terms' magnitudes (sums run over at most 8 terms at a time in the unit, tiles after tiles
   in turn: 8 to 16 turns, and the decays' exponentials add 1 + |x| units, which fade with them);
@@ -138,8 +138,8 @@ def delta_bounds(kind, C, q, k, v, g, beta, h0=None, seqlens=None, scale=None, d
                 val["y"][b, at, n] = Y
                 aP = D * A_(Q @ K.T)
                 eP = W * D * np.outer(qn, kn)
-                err["y"][b, at, n] = A_(c) * (st[:, None] * (A_(Q) @ E1(S)) + (st * qn)[:, None] * eS
-                                              + (E1(aP) + eP) @ A_(N) + aP @ (E1(N) + eN))
+                err["y"][b, at, n] = A_(c) * (st[:, None] * (A_(Q) @ E2(S)) + (st * qn)[:, None] * eS
+                                              + (E2(aP) + eP) @ A_(N) + aP @ (E2(N) + eN)) + W * A_(Y)
                 kept.append((at, S, eS, N, eN, T, eT, P, eP, D, st, en, kk))
                 # what the chunk's own map makes of the error it got, and what it adds
                 grow = np.prod(np.exp(g[b, at, n]) * np.maximum(1.0, A_(1 - be * kn ** 2)))
