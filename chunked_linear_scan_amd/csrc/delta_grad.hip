@@ -13,8 +13,7 @@
 // rounding; sums of F are of the same numbers by rows and by columns.)
 // A wave has 16 tokens; products run transposed (tokens in the columns), so dQ and dK
 // leave as four adjacent values of a token, and the decays are factors of a lane.
-// What reaches dg and dbeta, fp32 outputs, takes computed operands in two parts;
-// pP and pB only reach dQ and dK and go in as one.
+// All computed operands go in as two parts, so 16-bit gradients are off by their own rounding and little else.
 // Bound by memory: a chunk's states and corrections (192 KB of the 288 KB that it moves for 64 tokens, keys and values of 128)
 // are read once, 32 of dv at a time, past the caches: 4 x 2048 x 16 heads 150 us, 4.0 TB/s; through the caches 164; with the
 // products with S and with dS in two walks over dv as well 196.  LDS has K and those tiles, and Q and the pairs in the tiles'
@@ -80,7 +79,7 @@ struct GradSize {
     static constexpr int C = M::kChunk, KP = LdsTile<E, DK>::kPitch, MP = LdsTile<E, C>::kPitch;
     static constexpr int kParts = ChunkMats<E>::kParts;
     static constexpr int kTiles = kParts * 32 * (2 * KP + 2 * MP);  // tiles of S, dS, N and Z
-    static constexpr int kPairs = C * KP + 2 * C * MP;              // Q, pB and pP, in the same place
+    static constexpr int kPairs = C * KP + 2 * kParts * C * MP;     // Q, pB and pP, in the same place
     static constexpr int kUnion = kTiles > kPairs ? kTiles : kPairs;
     static constexpr size_t bytes = (C * KP + kUnion) * sizeof(typename M::raw) + (Decays<C>::kFloats + (2 + C / 16) * C + C / 16) * sizeof(float);
 };
@@ -99,7 +98,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
     raw* sZ = sN + G::kParts * 32 * MP;
     raw* sQ = sS;  // once the tiles are done with
     raw* sB = sQ + C * KP;
-    raw* sP = sB + C * MP;
+    raw* sP = sB + G::kParts * C * MP;
     float* sG = reinterpret_cast<float*>(sS + G::kUnion);
     float* sRow = sG + Decays<C>::kFloats;  // read_i + sum_j F_ij
     float* sWrite = sRow + C;   // write_j
@@ -329,8 +328,8 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        put4<E>(sB + MTile::quad(i, 16 * t + 4 * g4), 0, Mz[t]);  // zeros for the tiles behind w
-        put4<E>(sP + MTile::quad(i, 16 * t + 4 * g4), 0, dP[t]);
+        put4<E>(sB + MTile::quad(i, 16 * t + 4 * g4), C * MP, Mz[t]);  // zeros for the tiles behind w
+        put4<E>(sP + MTile::quad(i, 16 * t + 4 * g4), C * MP, dP[t]);
     }
     __syncthreads();
     if (tid < 64) {  // dg of token tid, by the first wave
@@ -359,26 +358,28 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
         }
     }
     // the pairs' parts: as the later token (operands from the lanes), as the earlier one (from LDS)
-    typename M::frag bi[NT / 2], pi[NT / 2], bj[NT / 2], pj[NT / 2];
 #pragma unroll
     for (int s = 0; s < NT / 2; ++s) {
-        bi[s] = M::cvt(Mz[2 * s], Mz[2 * s + 1]);
-        pi[s] = M::cvt(dP[2 * s], dP[2 * s + 1]);
-        bj[s] = mw.cols(sB, s, 0);
-        pj[s] = mw.cols(sP, s, 0);
-    }
+        const Two<E> bi = two<E>(Mz[2 * s], Mz[2 * s + 1]), pi = two<E>(dP[2 * s], dP[2 * s + 1]);
+        const auto earlier = [&](const raw* m) {
+            Two<E> x;
+            x.hi = mw.cols(m, s, 0);
+            if constexpr (M::kSplit) x.lo = mw.cols(m + C * MP, s, 0);
+            return x;
+        };
+        const Two<E> bj = earlier(sB), pj = earlier(sP);
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-#pragma unroll
-        for (int s = 0; s < NT / 2; ++s) {
+        for (int t = 0; t < KT; ++t) {
             const typename M::frag kc = kt.cols(sK, s, t), qc = kt.cols(sQ, s, t);
-            X1[t] = M::mma(kc, pi[s], X1[t]);
-            X2[t] = M::mma(kc, bi[s], X2[t]);
-            X2[t] = M::mma(kc, bj[s], X2[t]);
-            X2[t] = M::mma(qc, pj[s], X2[t]);
+            X1[t] = mma2<E>(kc, pi, X1[t]);
+            X2[t] = mma2<E>(kc, bi, X2[t]);
+            X2[t] = mma2<E>(kc, bj, X2[t]);
+            X2[t] = mma2<E>(qc, pj, X2[t]);
         }
-        if (!in) X1[t] = X2[t] = f32x4{0, 0, 0, 0};
     }
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+        if (!in) X1[t] = X2[t] = f32x4{0, 0, 0, 0};
     put_rows([&](int t) { return X1[t]; }, [&](int t) { return X2[t]; });
 }
 

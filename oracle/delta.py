@@ -6,8 +6,7 @@ kernels' chunk algebra in float64 to see how large the terms are whose rounding
 reaches each output, and returns absolute bounds to first order:
 
 * a product's computed operand carries a relative error of ``u2`` (two bf16 numbers 2^-16, two
-  fp16 numbers 2^-22, fp32 2^-24), the pairs of tokens that only reach dq and dk one of ``u1``
-  (half a step: 2^-8, 2^-11, 2^-24);
+  fp16 numbers 2^-22, fp32 2^-24; one number's half step is ``U1``);
 * every product's fp32 sums and factors add ``W`` = 32 units of 2^-24 of the sum of its
   terms' magnitudes (sums run over at most 8 terms at a time in the unit, tiles after tiles
   in turn: 8 to 16 turns, and the decays' exponentials add 1 + |x| units, which fade with them);
@@ -104,8 +103,8 @@ def delta_bounds(kind, C, q, k, v, g, beta, h0=None, seqlens=None, scale=None, d
     nb, L, H, dv = v.shape
     dk, rep = q.shape[-1], H // q.shape[2]
     c = dk ** -0.5 if scale is None else scale
-    u1, u2, s = U1[kind] + W, U2[kind] + W, SUB[kind]
-    E1, E2 = (lambda x: u1 * np.abs(x) + s), (lambda x: u2 * np.abs(x) + s)
+    u2, s = U2[kind] + W, SUB[kind]
+    E2 = lambda x: u2 * np.abs(x) + s  # noqa: E731
     EN = lambda norm: u2 * norm + s * dk ** 0.5  # noqa: E731  of a column of dk elements, by its norm
     names = {"y": v, "h": np.zeros((nb, H, dv, dk))}
     if dy is not None:
@@ -185,10 +184,10 @@ def delta_bounds(kind, C, q, k, v, g, beta, h0=None, seqlens=None, scale=None, d
                 pP, pB = c * D * dP, -be[:, None] * D * Mz
                 epP, epB = ac * D * edP + W * A_(pP), ab[:, None] * D * eM + W * A_(pB)
                 val["dq"][b, at, m] += c * st[:, None] * X1 + pP @ K
-                err["dq"][b, at, m] += ac * st[:, None] * e1 + (E1(pP) + epP) @ A_(K)
+                err["dq"][b, at, m] += ac * st[:, None] * e1 + (E2(pP) + epP) @ A_(K)
                 val["dk"][b, at, m] += -(be * st)[:, None] * X2 + pB @ K + X3 + pB.T @ K + pP.T @ Q
-                err["dk"][b, at, m] += (ab * st)[:, None] * e2 + e3 + (E1(pB) + epB) @ A_(K) \
-                    + (E1(pB) + epB).T @ A_(K) + (E1(pP) + epP).T @ A_(Q)
+                err["dk"][b, at, m] += (ab * st)[:, None] * e2 + e3 + (E2(pB) + epB) @ A_(K) \
+                    + (E2(pB) + epB).T @ A_(K) + (E2(pP) + epP).T @ A_(Q)
                 k2 = (K * X2).sum(1)
                 val["dbeta"][b, at, n] = (Z * V).sum(1) - st * k2 - (D * kk * Mz).sum(1)
                 err["dbeta"][b, at, n] = (W * A_(Z) * A_(V) + eZ * A_(V)).sum(1) + st * d2 + W * st * A_(k2) \

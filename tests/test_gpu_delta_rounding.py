@@ -49,3 +49,13 @@ def test_fp16_y_of_a_small_scale():
     small, _ = cls.gated_delta(*(c[k] for k in KEYS), scale=2.0 ** -9)
     fits = y.abs() >= 2.0 ** -4  # a normal number of the type in both
     assert fits.any() and torch.equal((small * 512)[fits], y[fits])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", SHAPES[1:])
+def test_gradients_of_16_bits_are_off_by_their_rounding(shape, kind):
+    c = delta_case(320 + SHAPES.index(shape), *shape, kind=kind, start=False)
+    got = check(c, kind, label=str(shape), dh=False)
+    want = od.delta_grads(f64(c["dy"]), **oracle_args(c))
+    for n in ("dq", "dk", "dv"):
+        off_by_rounding(got[n], want[n], f"{shape} {n}")
