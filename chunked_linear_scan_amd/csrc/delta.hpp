@@ -162,12 +162,14 @@ struct DeltaParams {
     float* fixes;    // [batch, chunks, heads, dv, chunk]: N, the corrections (NULL = not kept)
     void* mats;      // per (batch, chunk, head): (I + A)^-1 - I and D QK^T, each in its parts
     float* vecs;     // per (batch, chunk, head): kVecs factors of each token
-    float* dstates;  // as states: the gradient of the state behind each chunk
-    float* z;        // as fixes: (I + A)^-T dN
+    float* dstates;  // as states: the gradient of the state behind each chunk, times grad_power
+    float* z;        // as fixes: (I + A)^-T dN, likewise
     float *part_q, *part_k;  // [batch, L, heads, dk], where key heads are shared
+    float* sizes;    // [batch, heads, 2, kSizes], the first nsize of each: largest values of parts of dY and of dh (fp16)
     Strided3 sq, sk, sv, sdy;
     int64_t g_batch, g_token, b_batch, b_token;
     int batch, L, Hk, H, dk, dv, nchunk;
+    int nsize;
     int kpitch;  // of the kept states' rows: dk to whole vectors
     float scale;
     uint8_t vec_out;  // y or dv has rows of whole 16-byte vectors
@@ -182,6 +184,62 @@ struct ChunkMats {
     static constexpr int kParts = M::kSplit ? 2 : 1;
     static constexpr int kAll = 2 * kParts;
 };
+
+// ---------------------------------------------------------------------------
+// powers of two in front of fp16 operands
+// ---------------------------------------------------------------------------
+// Two fp16 numbers hold 22 bits of what is 2^-3 and more, and of less what is left above 2^-25; past 65504 they hold nothing.
+// Gradients are as large as the loss makes them, often far below that, so the backward pass multiplies a head's gradients of
+// state, corrections and outputs by one power of two that brings the largest of scale dY and dh_final to 4..8, 2^13 below
+// the type's end, and divides what it writes by it: exactly, so gradients of 2^n dy are 2^n times those of dy.  (Without it
+// dg of dy about 1e-3 was 1.5e-4 off, of 1e-5 1.6e-2, and dh_final past 65504 gave NaN.)  dY itself goes in times another, at least 1, as
+// products of subnormal operands lose bits where the unit adds them up (1e-8 of the sums for dy of 2^-14, 7e-7 for 2^-18).
+template <typename E>
+constexpr bool kSized = std::is_same_v<E, ElemF16>;
+constexpr int kSizes = 64;  // at most, parts of a head that delta_size_kernel takes apart
+
+// The larger of m and |x|; values that are not finite do not count.
+__device__ __forceinline__ float larger(float m, float x) {
+    const float a = fabsf(x);
+    return a > m && a < __builtin_inff() ? a : m;
+}
+__device__ __forceinline__ float wave_max(float m) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+    return m;
+}
+
+struct Power { float up, down; };
+// 2^k, which brings m to 2^to up to twice that (k at most `most`), and 2^-k.
+__device__ __forceinline__ Power power_to(float m, int to, int most = 126) {
+    int k = to + 127 - int(as_uint(m) >> 23);
+    k = m == 0.0f ? 0 : k > most ? most : k < -126 ? -126 : k;
+    return {as_float(uint32_t(127 + k) << 23), as_float(uint32_t(127 - k) << 23)};
+}
+// Those of a head's gradients: of = batch * heads + head.
+struct GradPower {
+    float up, down;  // of all gradients
+    float dy;        // of dY as an operand: up to 2^15, which is in the type's range and takes its smallest number to 2^-9
+    float ratio;     // up / dy, of products with dY
+};
+template <typename E>
+__device__ __forceinline__ GradPower grad_power(const DeltaParams& p, int64_t of) {
+    if constexpr (kSized<E>) {
+        const float* sizes = p.sizes + of * 2 * kSizes;
+        const int lane = threadIdx.x & 63;
+        const float dy = wave_max(lane < p.nsize ? sizes[lane] : 0.0f);
+        const float dh = wave_max(lane < p.nsize ? sizes[kSizes + lane] : 0.0f);
+        const Power all = power_to(larger(dh, dy * p.scale), 2), y = power_to(fminf(dy, 4.0f), 2, 15);
+        return {all.up, all.down, y.up, all.up * y.down};
+    }
+    return {1.0f, 1.0f, 1.0f, 1.0f};
+}
+// Eight elements times such a power.
+template <typename E>
+__device__ __forceinline__ u32x4 times(const u32x4& x, float power) {
+    if constexpr (kSized<E>) return __builtin_bit_cast(u32x4, __builtin_bit_cast(f16x8, x) * (_Float16)power);
+    return x;
+}
 
 // Factors of a token in `vecs`, each for all of a chunk's: scale e^gamma, e^(gamma_C - gamma), beta, beta e^gamma, e^gamma.
 enum { kRead, kWrite, kBeta, kBetaStart, kStart, kVecs };

@@ -92,7 +92,7 @@ struct DeltaSpace {
     bool pack_q, pack_k, pack_v;
     size_t mats, vecs, q, k, v, fwd;             // both passes: matrices and factors of the chunks, copies
     size_t fixes, ckpt;                          // checkpoints: states, then corrections
-    size_t dstates, z, part_q, part_k, dy, bwd;  // backward
+    size_t dstates, z, part_q, part_k, dy, sizes, bwd;  // backward
 };
 
 DeltaSpace delta_space(const gated_delta_inputs& s) {
@@ -119,7 +119,8 @@ DeltaSpace delta_space(const gated_delta_inputs& s) {
     d.part_q = d.z + tokens;
     d.part_k = d.part_q + parts;
     d.dy = d.part_k + parts;
-    d.bwd = d.dy + values;
+    d.sizes = d.dy + values;
+    d.bwd = d.sizes + (s.dtype == SSD_F16 ? size_t(s.batch * s.heads) * 2 * cls::kSizes * 4 : 0);
     return d;
 }
 
@@ -269,12 +270,17 @@ int gated_delta_bwd(const gated_delta_inputs* in, const gated_delta_grads* g, vo
     p.z = reinterpret_cast<float*>(ws + s.z);
     p.part_q = reinterpret_cast<float*>(ws + s.part_q);
     p.part_k = reinterpret_cast<float*>(ws + s.part_k);
+    p.sizes = reinterpret_cast<float*>(ws + s.sizes);
+    // parts of a head, so that a few heads have workgroups for the whole device, too
+    const int64_t heads = in->batch * in->heads, parts = 2048 / heads;
+    p.nsize = int(parts < 1 ? 1 : parts < cls::kSizes ? parts : cls::kSizes);
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     int rc = delta_pack(*in, workspace, s, hs);
     if (rc == 0 && pack_dy)
         rc = cls_delta_pack_launch(g->dy, ws + s.dy, int64_t(elem_size(in->dtype)), in->batch, in->seqlen, in->heads, in->dv,
                                    dv, g->dy_batch, g->dy_token, g->dy_head, hs);
     if (rc == 0) rc = cls_delta_prep_launch(p, in->dtype, hs);
+    if (rc == 0 && in->dtype == SSD_F16) rc = cls_delta_size_launch(p, hs);
     if (rc == 0) rc = cls_delta_bwd_launch(p, in->dtype, hs);
     if (rc == 0) rc = cls_delta_grad_launch(p, in->dtype, hs);
     return launched(rc);

@@ -4,7 +4,8 @@
 //     dN = e^(gamma_C - gamma) K dS + scale P^T dY,  Z = T^T dN,  dV = dR = beta Z,
 //     dS' = e^gamma_C dS + scale Q^T e^gamma dY - K^T e^gamma dR.
 // dS of every chunk and Z go to memory for the kernel that takes the chunks'
-// other gradients all at once (delta_grad.hip).
+// other gradients all at once (delta_grad.hip).  All of it is times a power of two
+// in fp16 (grad_power), which what leaves is divided by.
 #include <hip/hip_runtime.h>
 
 #include "delta_walk.hpp"
@@ -33,16 +34,20 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_bwd_kernel(DeltaPar
     const int end = seq_end(p.seqlens, b, p.L), chunks = (end + C - 1) / C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= 2 * TILES) {
-        const WalkColumns w{p.dy, p.sdy, p.dv_, bool(p.vec_out)};
-        walk_load<E, DK, NM, TILES>(p, w, lds, b, h, blk * walk_cols(TILES), end, chunks - 1, -1, chunks);
+        const WalkColumns w{p.dy, p.sdy, p.dv_, bool(p.vec_out), grad_power<E>(p, int64_t(b) * p.H + h).dy};
+        walk_load<E, DK, NM, TILES, true>(p, w, lds, b, h, blk * walk_cols(TILES), end, chunks - 1, -1, chunks);
         return;
     }
     const int a = wave & 1, tile = wave >> 1;  // the wave's half, its tile of the columns
     const int l16 = lane16(), g4 = group4();
     const int n = blk * walk_cols(TILES) + tile * 16 + l16;  // the lane's column
 
+    const GradPower size = grad_power<E>(p, int64_t(b) * p.H + h);
+    const float scale = p.scale * size.ratio;
     f32x4 S[KT];
     load_state<KT>(S, p.dh_last, int64_t(b) * p.H + h, n, a * (DK / 2), p);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) S[t] *= size.up;
     const typename Lds::KTile kt(a * (DK / 2));
     const typename Lds::MTile mt, xt(16 * tile);
     const Exchange ex(lds, wave, Lds::kSlots);
@@ -76,7 +81,7 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_bwd_kernel(DeltaPar
             Ph[j] = Op::cols(mt, m.m + kParts * Lds::MS, Lds::M1, a, a, j);
             if constexpr (kSplit) Pl[j] = Op::cols(mt, m.m + (kParts + 1) * Lds::MS, Lds::M1, a, a, j);
             later[j] = f32x4{0, 0, 0, 0};
-            rd[j] = factors(kRead, j);
+            rd[j] = factors(kRead, j) * size.ratio;
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) kd[t] = f32x4{0, 0, 0, 0};
@@ -138,7 +143,7 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_bwd_kernel(DeltaPar
 #pragma unroll
         for (int j = 0; j < OT; ++j)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dN[j][r] = fmaf(kd[j][r] + x[j][r], e[j][r], p.scale * later[j][r]);
+            for (int r = 0; r < 4; ++r) dN[j][r] = fmaf(kd[j][r] + x[j][r], e[j][r], scale * later[j][r]);
         // Z = dN + (T - I)^T dN: the second half's tokens reach the first's
         const auto dn = Op::two(dN);
         if (a) {
@@ -248,9 +253,11 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_bwd_kernel(DeltaPar
         }
         add(1 - a, xa, xq, false);
 #pragma unroll
-        for (int j = 0; j < OT; ++j) put_column<E, Lds::YP>(m.y + oy, j, be[j] * Z[j]);
+        for (int j = 0; j < OT; ++j) put_column<E, Lds::YP>(m.y + oy, j, size.down * (be[j] * Z[j]));
         settle(S[KT - 1]);
     });
+#pragma unroll
+    for (int t = 0; t < KT; ++t) S[t] *= size.down;
     if (p.dh0) store_state<KT>(S, p.dh0, int64_t(b) * p.H + h, n, a * (DK / 2), p);
 }
 

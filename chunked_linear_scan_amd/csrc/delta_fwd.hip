@@ -35,8 +35,8 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
     const int end = seq_end(p.seqlens, b, p.L), chunks = (end + C - 1) / C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= 2 * TILES) {
-        const WalkColumns w{p.v, p.sv, p.y, bool(p.vec_out)};
-        walk_load<E, DK, NM, TILES>(p, w, lds, b, h, blk * walk_cols(TILES), end, 0, 1, chunks);
+        const WalkColumns w{p.v, p.sv, p.y, bool(p.vec_out), 1.0f};
+        walk_load<E, DK, NM, TILES, false>(p, w, lds, b, h, blk * walk_cols(TILES), end, 0, 1, chunks);
         return;
     }
     const int a = wave & 1, tile = wave >> 1;  // the wave's half, its tile of the columns

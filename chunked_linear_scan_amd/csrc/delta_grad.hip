@@ -81,7 +81,7 @@ struct GradSize {
     static constexpr int kTiles = kParts * 32 * (2 * KP + 2 * MP);  // tiles of S, dS, N and Z
     static constexpr int kPairs = C * KP + 2 * kParts * C * MP;     // Q, pB and pP, in the same place
     static constexpr int kUnion = kTiles > kPairs ? kTiles : kPairs;
-    static constexpr size_t bytes = (C * KP + kUnion) * sizeof(typename M::raw) + (Decays<C>::kFloats + (2 + C / 16) * C + C / 16) * sizeof(float);
+    static constexpr size_t bytes = (C * KP + kUnion) * sizeof(typename M::raw) + (Decays<C>::kFloats + (2 + C / 16) * C + 2 * (C / 16)) * sizeof(float);
 };
 
 template <typename E, int DK>
@@ -104,6 +104,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
     float* sWrite = sRow + C;   // write_j
     float* sCol = sWrite + C;   // [NT][C]: sums of F over a wave's tokens
     float* sDot = sCol + NT * C;
+    float* sMost = sDot + NT;  // the waves' largest pairs
 
     const int rep = p.H / p.Hk;
     const UnitPart u = unit_part(p.batch * p.nchunk * p.Hk, rep);
@@ -149,6 +150,9 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
         return;
     }
 
+    // dS, Z and what comes of them are times a power of two, and so are products with dY times `scale`
+    const GradPower size = grad_power<E>(p, int64_t(b) * p.H + h);
+    const float scale = p.scale * size.ratio;
     const int64_t chunk = (int64_t(b) * p.nchunk + c) * p.H + h;
     const float* vecs = p.vecs + chunk * kVecs * C;
     const Buffer bS = buffer(p.states + chunk * p.dv * p.kpitch, int64_t(p.dv) * p.kpitch * 4);
@@ -205,7 +209,9 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
         rn.store(sN);
         rz.store(sZ);
         both += rs.dot(rd);
-        const typename M::frag yf = y1, v = v1;
+        typename M::frag yf = y1;
+        const typename M::frag v = v1;
+        if constexpr (kSized<E>) yf = times<E>(yf, size.dy);
         lds_meet();
         if (d0 + 32 < p.dv) {
             ahead(d0 + 32);
@@ -261,10 +267,10 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
     };
     const float start = vecs[kStart * C + i], beta = vecs[kBeta * C + i], fade = vecs[kStart * C + C - 1];
     const float after = vecs[kWrite * C + i];
-    const float qx = p.scale * start * dot_row(sQ, X1), kx = start * dot_row(sK, X2), write = after * dot_row(sK, X3);
+    const float qx = scale * start * dot_row(sQ, X1), kx = start * dot_row(sK, X2), write = after * dot_row(sK, X3);
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-        X1[t] *= p.scale * start;
+        X1[t] *= scale * start;
         X2[t] = after * X3[t] - beta * start * X2[t];
         // here, not where it is used: both are kept until then otherwise
 #pragma unroll
@@ -303,7 +309,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
         for (int r = 0; r < 4; ++r) {
             const int j = 16 * t + 4 * g4 + r;
             const float m = j < i ? d[r] * Mz[t][r] : 0.0f;
-            dP[t][r] = j <= i ? p.scale * d[r] * dP[t][r] : 0.0f;
+            dP[t][r] = j <= i ? scale * d[r] * dP[t][r] : 0.0f;
             Mz[t][r] = -beta * m;
             db = fmaf(m, kk[t][r], db);
             const float f = j < i ? fmaf(dP[t][r], qk[t][r], Mz[t][r] * kk[t][r]) : 0.0f;
@@ -324,7 +330,33 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
     if (g4 == 0) {
         sRow[i] = rows + qx - beta * kx;
         sWrite[i] = write;
-        if (tok < p.L) p.dbeta[(int64_t(b) * p.L + tok) * p.H + h] = in ? zv - kx - db : 0.0f;
+        if (tok < p.L) p.dbeta[(int64_t(b) * p.L + tok) * p.H + h] = in ? size.down * (zv - kx - db) : 0.0f;
+    }
+    // The pairs are products of dY or Z with the corrections, which may be of any size: a power of two of the chunk's
+    // own brings them to 2^10, at most 2^15 as they only add to the states' parts.
+    Power pairs{1.0f, 1.0f};
+    if constexpr (kSized<E>) {
+        float most = 0.0f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) most = larger(larger(most, dP[t][r]), Mz[t][r]);
+        most = wave_max(most);
+        if ((tid & 63) == 0) sMost[w] = most;
+        lds_meet();
+#pragma unroll
+        for (int k = 0; k < NT; ++k) most = fmaxf(most, sMost[k]);
+        pairs = power_to(most, 10, 15);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            dP[t] *= pairs.up;
+            Mz[t] *= pairs.up;
+        }
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+            X1[t] *= pairs.up;
+            X2[t] *= pairs.up;
+        }
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -354,7 +386,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
         float v = both + from + before;
         if (tid < C && t0 + tid < p.L) {
             if (fexp(sG[tid]) == 0.0f) v = 0.0f;  // nothing passes: not the sums' roundings either
-            p.dg[(int64_t(b) * p.L + t0 + tid) * p.H + h] = t0 + tid < end ? v : 0.0f;
+            p.dg[(int64_t(b) * p.L + t0 + tid) * p.H + h] = t0 + tid < end ? size.down * v : 0.0f;
         }
     }
     // the pairs' parts: as the later token (operands from the lanes), as the earlier one (from LDS)
@@ -380,7 +412,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
 #pragma unroll
     for (int t = 0; t < KT; ++t)
         if (!in) X1[t] = X2[t] = f32x4{0, 0, 0, 0};
-    put_rows([&](int t) { return X1[t]; }, [&](int t) { return X2[t]; });
+    put_rows([&](int t) { return size.down * (pairs.down * X1[t]); }, [&](int t) { return size.down * (pairs.down * X2[t]); });
 }
 
 // Sums over the heads of a key head.

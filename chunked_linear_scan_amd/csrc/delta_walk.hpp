@@ -174,10 +174,11 @@ struct WalkColumns {
     Strided3 sx;
     void* y;
     bool vec_y;
+    float power;  // of X as an operand, where it is a gradient (GRADS)
 };
 
 // Chunks first, first + step, .. (n of them).
-template <typename E, int DK, int NM, int TILES>
+template <typename E, int DK, int NM, int TILES, bool GRADS>
 __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumns& w, char* lds, int b, int h, int col0, int end,
                                           int first, int step, int n) {
     typedef Mat<E> M;
@@ -241,7 +242,7 @@ __device__ __forceinline__ void walk_load(const DeltaParams& p, const WalkColumn
             Lds::MTile::put(to.m + m * Lds::MS, xrow, xcol, r.m[m]);
             if (LOW > 0 && tid < LOW) Lds::MTile::put(to.m + m * Lds::MS + Lds::M1, xrow, xcol, r.low[m]);
         }
-        Lds::MTile::put(to.x, xrow, xcol, r.x);
+        Lds::MTile::put(to.x, xrow, xcol, GRADS ? times<E>(r.x, w.power) : r.x);
         if (tid < kVecs * C / 4) *reinterpret_cast<u32x4*>(to.v + 4 * tid) = r.v;
     };
     const int64_t row = int64_t(p.H) * p.dv;  // of a token of y

@@ -15,6 +15,7 @@ struct DeltaParams;
 int cls_delta_pack_launch(const void* from, void* to, int64_t size, int64_t batch, int64_t L, int64_t heads, int64_t dim,
                           int64_t padded, int64_t sb, int64_t st, int64_t sh, hipStream_t stream);
 int cls_delta_prep_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream);
+int cls_delta_size_launch(const cls::DeltaParams& p, hipStream_t stream);
 int cls_delta_fwd_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream);
 int cls_delta_bwd_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream);
 int cls_delta_grad_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream);

@@ -6,7 +6,8 @@ kernels' chunk algebra in float64 to see how large the terms are whose rounding
 reaches each output, and returns absolute bounds to first order:
 
 * a product's computed operand carries a relative error of ``u2`` (two bf16 numbers 2^-16, two
-  fp16 numbers 2^-22, fp32 2^-24; one number's half step is ``U1``);
+  fp16 numbers 2^-22, and ``SUB`` as long as gradients are scaled to be of the size of 4 and more, fp32 2^-24;
+  one number's half step is ``U1``);
 * every product's fp32 sums and factors add ``W`` = 32 units of 2^-24 of the sum of its
   terms' magnitudes (sums run over at most 8 terms at a time in the unit, tiles after tiles
   in turn: 8 to 16 turns, and the decays' exponentials add 1 + |x| units, which fade with them);
@@ -105,7 +106,7 @@ def delta_bounds(kind, C, q, k, v, g, beta, h0=None, seqlens=None, scale=None, d
     c = dk ** -0.5 if scale is None else scale
     u2, s = U2[kind] + W, SUB[kind]
     E2 = lambda x: u2 * np.abs(x) + s  # noqa: E731
-    EN = lambda norm: u2 * norm + s * dk ** 0.5  # noqa: E731  of a column of dk elements, by its norm
+    EN = lambda norm, s=s: u2 * norm + s * dk ** 0.5  # noqa: E731  of a column of dk elements, by its norm
     names = {"y": v, "h": np.zeros((nb, H, dv, dk))}
     if dy is not None:
         names |= {"dq": q, "dk": k, "dv": v, "dg": g, "dbeta": beta, "dh0": names["h"]}
@@ -151,6 +152,11 @@ def delta_bounds(kind, C, q, k, v, g, beta, h0=None, seqlens=None, scale=None, d
                 continue
             dS = np.zeros((dk, dv)) if dh is None else dh[b, n].T
             eD = np.zeros(dv)
+            # fp16: operands that are gradients are held to 2^-25 where the largest of c dY and dh is 4 at least, and
+            # the chunk's pairs where their largest is 2^10 or all of them are multiplied by 2^15
+            top = max(abs(c) * A_(dy[b, :end, n]).max(initial=0.0), A_(dS).max())
+            sg = s * top / 4
+            G2 = lambda x: u2 * np.abs(x) + sg  # noqa: E731
             for at, S, eS, N, eN, T, eT, P, eP, D, st, en, kk in reversed(kept):
                 Q, K, V, be, dY = q[b, at, m], k[b, at, m], v[b, at, n], beta[b, at, n], dy[b, at, n]
                 kn, qn = np.linalg.norm(K, axis=1), np.linalg.norm(Q, axis=1)
@@ -158,36 +164,38 @@ def delta_bounds(kind, C, q, k, v, g, beta, h0=None, seqlens=None, scale=None, d
                 aT, low, aP = A_(T), np.tril(A_(T), -1), A_(P)
                 dN = en[:, None] * (K @ dS) + c * P.T @ dY
                 Z = T.T @ dN
-                edN0 = (en * kn)[:, None] * EN(Dn) + ac * (E2(aP) + eP).T @ A_(dY) + W * A_(dN)
+                edN0 = (en * kn)[:, None] * EN(Dn, sg) + ac * (E2(aP) + eP).T @ A_(dY) + W * A_(dN)
                 edN = edN0 + (en * kn)[:, None] * eD
-                more = (E2(low) + eT).T @ A_(dN) + low.T @ E2(dN) + W * A_(Z)
+                more = (E2(low) + eT).T @ A_(dN) + low.T @ G2(dN) + W * A_(Z)
                 eZ = aT.T @ edN + more
                 val["dv"][b, at, n] = be[:, None] * Z
                 err["dv"][b, at, n] = ab[:, None] * eZ
                 # the state's parts
                 X1, X2, X3 = dY @ S.T, Z @ S.T, (en[:, None] * N) @ dS.T
                 e1 = A_(dY) @ E2(S).T + (A_(dY) @ eS)[:, None] * np.ones(dk)
-                e2 = A_(Z) @ E2(S).T + E2(Z) @ A_(S).T + (A_(Z) @ eS)[:, None] + eZ @ A_(S).T
+                e2 = A_(Z) @ E2(S).T + G2(Z) @ A_(S).T + (A_(Z) @ eS)[:, None] + eZ @ A_(S).T
                 aNe = en[:, None] * A_(N)
-                e3 = aNe @ E2(dS).T + E2(aNe) @ A_(dS).T + (aNe @ eD)[:, None] + en[:, None] * (eN @ A_(dS).T)
+                e3 = aNe @ G2(dS).T + E2(aNe) @ A_(dS).T + (aNe @ eD)[:, None] + en[:, None] * (eN @ A_(dS).T)
                 # as dots with a key or query the states' errors count by their norm
                 d1 = (A_(Q) * (A_(dY) @ E2(S).T)).sum(1) + qn * (A_(dY) @ eS)
-                d2 = (A_(K) * (A_(Z) @ E2(S).T + E2(Z) @ A_(S).T)).sum(1) + kn * (A_(Z) @ eS) \
+                d2 = (A_(K) * (A_(Z) @ E2(S).T + G2(Z) @ A_(S).T)).sum(1) + kn * (A_(Z) @ eS) \
                     + (A_(K) * (eZ @ A_(S).T)).sum(1)
-                d3 = (A_(K) * (aNe @ E2(dS).T + E2(aNe) @ A_(dS).T)).sum(1) + kn * (aNe @ eD) \
+                d3 = (A_(K) * (aNe @ G2(dS).T + E2(aNe) @ A_(dS).T)).sum(1) + kn * (aNe @ eD) \
                     + en * (A_(K) * (eN @ A_(dS).T)).sum(1)
                 # the write terms are taken as a difference from the read terms
                 d3 = d3 + W * (ab * st * (A_(K) * A_(X2)).sum(1))
                 dP, Mz = np.tril(dY @ N.T), np.tril(Z @ N.T, -1)
                 edP = np.tril(A_(dY) @ (E2(N) + eN).T)
-                eM = np.tril(A_(Z) @ (E2(N) + eN).T + (E2(Z) + eZ) @ A_(N).T, -1)
+                eM = np.tril(A_(Z) @ (E2(N) + eN).T + (G2(Z) + eZ) @ A_(N).T, -1)
                 pP, pB = c * D * dP, -be[:, None] * D * Mz
+                sp = s * (2.0 ** -10 * max(A_(pP).max(), A_(pB).max()) + 2.0 ** -15 * top / 4)
+                P2 = lambda x: u2 * np.abs(x) + sp  # noqa: E731
                 epP, epB = ac * D * edP + W * A_(pP), ab[:, None] * D * eM + W * A_(pB)
                 val["dq"][b, at, m] += c * st[:, None] * X1 + pP @ K
-                err["dq"][b, at, m] += ac * st[:, None] * e1 + (E2(pP) + epP) @ A_(K)
+                err["dq"][b, at, m] += ac * st[:, None] * e1 + (P2(pP) + epP) @ A_(K)
                 val["dk"][b, at, m] += -(be * st)[:, None] * X2 + pB @ K + X3 + pB.T @ K + pP.T @ Q
-                err["dk"][b, at, m] += (ab * st)[:, None] * e2 + e3 + (E2(pB) + epB) @ A_(K) \
-                    + (E2(pB) + epB).T @ A_(K) + (E2(pP) + epP).T @ A_(Q)
+                err["dk"][b, at, m] += (ab * st)[:, None] * e2 + e3 + (P2(pB) + epB) @ A_(K) \
+                    + (P2(pB) + epB).T @ A_(K) + (P2(pP) + epP).T @ A_(Q)
                 k2 = (K * X2).sum(1)
                 val["dbeta"][b, at, n] = (Z * V).sum(1) - st * k2 - (D * kk * Mz).sum(1)
                 err["dbeta"][b, at, n] = (W * A_(Z) * A_(V) + eZ * A_(V)).sum(1) + st * d2 + W * st * A_(k2) \
@@ -207,7 +215,7 @@ def delta_bounds(kind, C, q, k, v, g, beta, h0=None, seqlens=None, scale=None, d
                 grow = np.prod(np.exp(g[b, at, n]) * np.maximum(1.0, A_(1 - be * kn ** 2)))
                 dR = be[:, None] * Z
                 dS = st[-1] * dS + c * (st[:, None] * Q).T @ dY - (st[:, None] * K).T @ dR
-                eD = grow * eD + qn @ E2(c * st[:, None] * dY) + kn @ E2(st[:, None] * dR) \
+                eD = grow * eD + qn @ G2(c * st[:, None] * dY) + kn @ G2(st[:, None] * dR) \
                     + (st * kn * ab) @ (aT.T @ edN0 + more) + W * st[-1] * Dn
             val["dh0"][b, n], err["dh0"][b, n] = dS.T, np.broadcast_to(eD[:, None], (dv, dk))
     return val, err
