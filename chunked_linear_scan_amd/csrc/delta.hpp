@@ -340,6 +340,19 @@ struct LdsTile {
 // stores of memory stay in flight across it.
 __device__ __forceinline__ void lds_meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// Nothing is scheduled across it.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// At the end of a loop that carries results of matrix products: they are all written before it goes on or ends.  The
+// compiler (AMD clang 22.0.0git of ROCm 7.2.0) left out the wait states on a loop's way out: copies of a result
+// (v_mov_b64) stood there two instructions behind its product, which needs 8 (16-bit) or 10 (fp32) between them.
+// Within a block, and on the way back to a loop's start, it has them.
+__device__ __forceinline__ void settle() {
+    fence();
+    asm volatile("s_nop 15");
+    fence();
+}
+
 // ---------------------------------------------------------------------------
 // matrices in memory: buffers of up to 2^31 bytes from a row on, where what lies outside reads as zeros and is not
 // written.  Strides are bounded by kDeltaMaxToken, so that the rows of a chunk lie within.

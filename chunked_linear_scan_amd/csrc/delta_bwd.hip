@@ -254,7 +254,6 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_bwd_kernel(DeltaPar
         add(1 - a, xa, xq, false);
 #pragma unroll
         for (int j = 0; j < OT; ++j) put_column<E, Lds::YP>(m.y + oy, j, size.down * (be[j] * Z[j]));
-        settle(S[KT - 1]);
     });
 #pragma unroll
     for (int t = 0; t < KT; ++t) S[t] *= size.down;

@@ -250,7 +250,6 @@ __global__ __launch_bounds__(walk_threads(TILES)) void delta_fwd_kernel(DeltaPar
         add(1 - a, xx, false);
 #pragma unroll
         for (int j = 0; j < OT; ++j) put_column<E, Lds::YP>(m.y + oy, j, p.scale * O[j]);
-        settle(S[KT - 1]);
     });
     if (p.h_last) store_state<KT>(S, p.h_last, int64_t(b) * p.H + h, n, a * (DK / 2), p);
 }

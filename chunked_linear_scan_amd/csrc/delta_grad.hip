@@ -235,15 +235,16 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
             X1[t] = mma2<E>(s, yf, X1[t]);
             X2[t] = mma3<E, small_parts(DK)>(s, zf, X2[t]);
             X3[t] = mma3<E, small_parts(DK)>(d, nf, X3[t]);
-            __builtin_amdgcn_sched_barrier(0);
+            fence();
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {  // without a branch: those of later tokens are not used
             const Two<E> nj = two_cols<E>(mt, sN, t);
             dP[t] = mma2<E>(nj, yf, dP[t]);
             Mz[t] = mma3<E, small_parts(DK)>(nj, zf, Mz[t]);
-            __builtin_amdgcn_sched_barrier(0);
+            fence();
         }
+        settle();
     }
     lds_meet();  // the tiles are read
     {

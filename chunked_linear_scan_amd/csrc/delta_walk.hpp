@@ -31,16 +31,6 @@ __device__ __forceinline__ void interleave() {
         interleave<N - 1, V>();
     }
 }
-__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
-
-// Lets the last product's result be written: the compiler's copies of it at a loop's end (v_mov_b64) were seen two
-// instructions behind the product, without the wait for its last two registers.
-__device__ __forceinline__ void settle(f32x4& x) {
-    float a = x[0], b = x[1], c = x[2], d = x[3];
-    asm volatile("s_nop 15" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
-    x = f32x4{a, b, c, d};
-}
-
 // A workgroup of TILES has 16 TILES columns: computing waves (16 (w / 2).. of the columns, half w % 2), then four that load.
 constexpr int walk_cols(int tiles) { return 16 * tiles; }
 constexpr int walk_threads(int tiles) { return 128 * tiles + 256; }
@@ -330,6 +320,7 @@ __device__ __forceinline__ void walk(char* lds, int n, F&& f) {
         lds_meet();
         for (int i = 0; i < n; ++i) {
             f(i, Lds(lds, i));
+            settle();
             lds_meet();
         }
     } else {
@@ -337,6 +328,7 @@ __device__ __forceinline__ void walk(char* lds, int n, F&& f) {
             lds_meet();
             lds_meet();
             f(i, Lds(lds, i));
+            settle();
         }
         lds_meet();
     }
