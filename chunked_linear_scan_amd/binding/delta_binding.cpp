@@ -184,11 +184,12 @@ py::dict gated_bwd(const Tensor& dy, const Tensor& x, const Maybe& weight, const
     return got;
 }
 
-residual_norm_inputs residual_inputs(const Tensor& x, const Maybe& weight, const Maybe& scale, double eps) {
+// `name`: that of the tensor which the others are held to.
+residual_norm_inputs residual_inputs(const char* name, const Tensor& x, const Maybe& weight, const Maybe& scale, double eps) {
     residual_norm_inputs s{};
-    s.dtype = element_code("x", x);
-    if (x.dim() < 1) throw py::value_error("x must be [..., dim]");
-    s.dtype = check_lead("x", x, x.dim(), "..., dim");
+    s.dtype = element_code(name, x);
+    if (x.dim() < 1) throw py::value_error(std::string(name) + " must be [..., dim]");
+    s.dtype = check_lead(name, x, x.dim(), "..., dim");
     s.dim = x.size(-1);
     s.rows = 1;
     for (int64_t d = 0; d < x.dim() - 1; ++d) s.rows *= x.size(d);
@@ -196,7 +197,7 @@ residual_norm_inputs residual_inputs(const Tensor& x, const Maybe& weight, const
     check("scale", scale, x.device(), at::kFloat, {s.dim});
     s.eps = float(eps);
     s.x = ptr(x); s.scale = ptr<float>(scale); s.weight = ptr<float>(weight);
-    s.x_row = row_stride("x", x, 1);
+    s.x_row = row_stride(name, x, 1);
     return s;
 }
 
@@ -211,7 +212,7 @@ at::ScalarType stream_kind(const char* name, const Tensor& t, const Tensor& x) {
 
 std::tuple<Tensor, Tensor, Maybe> residual(const Tensor& x, const Maybe& res, const Maybe& weight, const Maybe& scale,
                                            double eps, bool want_rstd) {
-    residual_norm_inputs s = residual_inputs(x, weight, scale, eps);
+    residual_norm_inputs s = residual_inputs("x", x, weight, scale, eps);
     const at::Device dev = x.device();
     const at::ScalarType kind = res ? stream_kind("residual", *res, x) : x.scalar_type();
     check("residual", res, dev, kind, x.sizes(), true);
@@ -232,7 +233,7 @@ std::tuple<Tensor, Tensor, Maybe> residual(const Tensor& x, const Maybe& res, co
 
 py::dict residual_bwd(const Tensor& dy, const Tensor& r, const Maybe& weight, const Tensor& rstd, const Maybe& dr,
                       const Maybe& x, const Maybe& scale) {
-    residual_norm_inputs s = residual_inputs(dy, weight, scale, 0.0);
+    residual_norm_inputs s = residual_inputs("dy", dy, weight, scale, 0.0);
     const at::Device dev = dy.device();
     const at::ScalarType kind = stream_kind("r", r, dy);
     s.stream_dtype = kind == at::kFloat ? int32_t(SSD_F32) : s.dtype;
