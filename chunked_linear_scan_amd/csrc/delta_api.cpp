@@ -69,7 +69,7 @@ int delta_check(const gated_delta_inputs* in, bool step) {
     if (!in || !in->q || !in->k || !in->v || !in->g || !in->beta) return SSD_ERR_NULL;
     const int st = (step ? delta_dims : delta_sizes)(*in);
     if (st != SSD_OK) return st;
-    if (step && in->batch * in->heads * ceil_div(in->dv, 4) >= kMaxThreads / 256) return SSD_ERR_SHAPE;
+    if (step && cls_delta_step_groups(in->batch * in->heads, in->dk, in->dv) >= kMaxThreads / 256) return SSD_ERR_SHAPE;
     if (!strides_ok({in->q_batch, in->q_token, in->q_head, in->k_batch, in->k_token, in->k_head, in->v_batch, in->v_token,
                      in->v_head, in->g_batch, in->g_token, in->beta_batch, in->beta_token}))
         return SSD_ERR_SHAPE;

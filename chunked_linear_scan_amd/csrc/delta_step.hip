@@ -92,15 +92,23 @@ __global__ __launch_bounds__(256) void delta_step_kernel(StepParams p) {
     }
 }
 
+int lanes_of(int64_t dk) { return dk <= 32 ? 8 : dk <= 64 ? 16 : dk <= 128 ? 32 : 64; }
+
+// Rows of a state to a workgroup: four to a thread once that still leaves eight workgroups to a compute unit.
+int rows_of(int64_t heads, int64_t dk, int64_t dv) {
+    const int pass = 256 / lanes_of(dk);
+    return heads * ((dv + 4 * pass - 1) / (4 * pass)) >= 2048 ? 4 * pass : pass;
+}
+int64_t groups_of(int64_t heads, int64_t dk, int64_t dv) {
+    const int rows = rows_of(heads, dk, dv);
+    return heads * ((dv + rows - 1) / rows);
+}
+
 template <typename E, int LANES>
 int launch(const StepParams& p, hipStream_t stream) {
-    constexpr int PASS = 256 / LANES;
     const int64_t heads = int64_t(p.batch) * p.H;
-    const bool whole = p.dk % 4 == 0;
-    // four rows to a thread once that still leaves eight workgroups to a compute unit
-    const bool four = heads * ((p.dv + 4 * PASS - 1) / (4 * PASS)) >= 2048;
-    const int rows = PASS * (four ? 4 : 1);
-    const unsigned wgs = unsigned(heads * ((p.dv + rows - 1) / rows));
+    const bool whole = p.dk % 4 == 0, four = rows_of(heads, p.dk, p.dv) > 256 / LANES;
+    const unsigned wgs = unsigned(groups_of(heads, p.dk, p.dv));
     if (four && whole) delta_step_kernel<E, LANES, 4, true><<<wgs, 256, 0, stream>>>(p);
     else if (four) delta_step_kernel<E, LANES, 4, false><<<wgs, 256, 0, stream>>>(p);
     else if (whole) delta_step_kernel<E, LANES, 1, true><<<wgs, 256, 0, stream>>>(p);
@@ -110,13 +118,18 @@ int launch(const StepParams& p, hipStream_t stream) {
 
 template <typename E>
 int launch(const StepParams& p, hipStream_t stream) {
-    if (p.dk <= 32) return launch<E, 8>(p, stream);
-    if (p.dk <= 64) return launch<E, 16>(p, stream);
-    return p.dk <= 128 ? launch<E, 32>(p, stream) : launch<E, 64>(p, stream);
+    switch (lanes_of(p.dk)) {
+        case 8: return launch<E, 8>(p, stream);
+        case 16: return launch<E, 16>(p, stream);
+        case 32: return launch<E, 32>(p, stream);
+        default: return launch<E, 64>(p, stream);
+    }
 }
 
 }  // namespace
 }  // namespace cls
+
+int64_t cls_delta_step_groups(int64_t heads, int64_t dk, int64_t dv) { return cls::groups_of(heads, dk, dv); }
 
 int cls_delta_step_launch(const gated_delta_inputs& in, float* h, void* y, hipStream_t stream) {
     cls::StepParams p{};

@@ -19,6 +19,8 @@ int cls_delta_size_launch(const cls::DeltaParams& p, hipStream_t stream);
 int cls_delta_fwd_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream);
 int cls_delta_bwd_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream);
 int cls_delta_grad_launch(const cls::DeltaParams& p, int dtype, hipStream_t stream);
+// Workgroups of 256 threads that a step of `heads` states (of all sequences) launches.
+int64_t cls_delta_step_groups(int64_t heads, int64_t dk, int64_t dv);
 int cls_delta_step_launch(const gated_delta_inputs& in, float* h, void* y, hipStream_t stream);
 
 // The partial sums of parameters' gradients: rows of a norm's backward workspace.

@@ -127,7 +127,9 @@ int gated_delta_bwd(const gated_delta_inputs* in, const gated_delta_grads* g, vo
  * One token for every sequence: the state h [batch, heads, dv, dk] (fp32,
  * contiguous, 16-byte aligned where dk is a multiple of 4) is updated in place.
  * `in` is read with seqlen 1: its token strides, h0 and seqlens are not used.
- * y [batch, heads, dv], contiguous.  All arithmetic is fp32.
+ * y [batch, heads, dv], contiguous.  All arithmetic is fp32.  Sizes are bounded
+ * by this launch's threads alone: 256 for each 128, 64, 32 or 16 rows of a state
+ * with dk up to 32, 64, 128 or 256.
  */
 int gated_delta_step(const gated_delta_inputs* in, float* h, void* y, void* stream);
 
