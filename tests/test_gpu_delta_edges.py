@@ -1,10 +1,10 @@
-"""GPU tests of the gated delta rule's step at its limits, and of states that went through the 8-bit cache."""
+"""GPU tests of the gated delta rule: orders of dimensions, the step at its limits, states from the 8-bit cache."""
 import pytest
 import torch
 
 import chunked_linear_scan_amd as cls
 from oracle import delta as od
-from test_gpu_delta import KEYS, delta_case, oracle_args
+from test_gpu_delta import KEYS, delta_case, oracle_args, run
 from test_gpu_selective import U, close, f64, on_gpu
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +42,24 @@ def test_a_state_from_the_cache_is_continued():
     _, err = od.delta_bounds("bf16", 64, **a)
     close(y, ry, err["y"] / U, "y")
     close(h2, rh, err["h"] / U, "h")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_orders_of_dimensions(kind):
+    """Heads in front of tokens, tokens that overlap (windows of one signal), one key head for all: the same bits as
+    contiguous tensors give."""
+    c = on_gpu(delta_case(61, 2, 150, 2, 4, 64, 48, kind=kind))
+    c = {k: v.contiguous() if isinstance(v, torch.Tensor) else v for k, v in c.items()}
+    want = run(c)
+    names = ("q", "k", "v", "dy")
+    got = run({**c, **{k: c[k].transpose(1, 2).contiguous().transpose(1, 2) for k in names}})
+    got2 = run({**c, **{k: c[k].permute(1, 2, 0, 3).contiguous().permute(2, 0, 1, 3) for k in names}})
+    for n in want:
+        assert torch.equal(got[n], want[n]) and torch.equal(got2[n], want[n]), n
+    signal = torch.randn(2, 2, 8 * 149 + 64, generator=torch.Generator().manual_seed(62)).to(c["q"].dtype).cuda() / 8
+    over = signal.as_strided((2, 150, 2, 64), (signal.stride(0), 8, signal.stride(1), 1))
+    shared = c["q"][:, :, :1].expand(2, 150, 2, 64)
+    want = run({**c, "k": over.contiguous(), "q": shared.contiguous()})
+    got = run({**c, "k": over, "q": shared})
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
