@@ -6,8 +6,8 @@
 // both the depths 16 (j/4) + 4 (l/16) + j%4, j = 0..7: the order in which two
 // result tiles, one below the other, lie in the lanes (rows 4 (l/16) + r of
 // column l%16).  So a result goes on as the right operand of the next product
-// without leaving its lanes: the states, the corrections and the gradients of a
-// chunk never pass through LDS.
+// without leaving its lanes: in the walks LDS only has what waves that share
+// columns exchange of them, and states stay in registers.
 #pragma once
 
 #include <type_traits>
@@ -379,13 +379,10 @@ struct TileRegs {
         const int row = tid / PER_ROW, col = tid % PER_ROW * VE;
         return col < dim ? uint32_t((row * pitch + col) * sizeof(raw)) : kOutside;
     }
-    __device__ __forceinline__ void load(Buffer b, uint32_t offset, int64_t pitch) { load(b, offset, pitch, offset); }
-    // `first`: the offset for rows before 32.
-    __device__ __forceinline__ void load(Buffer b, uint32_t offset, int64_t pitch, uint32_t first) {
+    __device__ __forceinline__ void load(Buffer b, uint32_t offset, int64_t pitch) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            r[n] = __builtin_amdgcn_raw_buffer_load_b128(
-                b, int((n * STEP < 32 ? first : offset) + uint32_t(n * STEP * pitch * sizeof(raw))), 0, 0);
+            r[n] = __builtin_amdgcn_raw_buffer_load_b128(b, int(offset + uint32_t(n * STEP * pitch * sizeof(raw))), 0, 0);
     }
     template <typename T>
     __device__ __forceinline__ void store(raw* lds, int tid) const {
@@ -422,28 +419,21 @@ __device__ __forceinline__ typename Mat<E>::frag load_frag(Buffer b, uint32_t ro
     }
 }
 
-// Four values of a row: elements col.. of `dim` (zeros past it).
+// Four adjacent elements.
 template <typename E>
-__device__ __forceinline__ f32x4 load4(const typename E::raw* row, int col, int dim, bool vec) {
-    f32x4 v{0, 0, 0, 0};
-    if (vec) {
-        if (col >= dim) return v;
-        if constexpr (sizeof(typename E::raw) == 4) {
-            return *reinterpret_cast<const f32x4*>(row + col);
-        } else {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(row + col);
+__device__ __forceinline__ f32x4 load4(const typename E::raw* p) {
+    if constexpr (sizeof(typename E::raw) == 4) {
+        return *reinterpret_cast<const f32x4*>(p);
+    } else {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+        f32x4 v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t x = w[e >> 1];
-                v[e] = Mat<E>::part(x, e & 1);
-            }
-            return v;
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t x = w[e >> 1];
+            v[e] = Mat<E>::part(x, e & 1);
         }
+        return v;
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (col + e < dim) v[e] = E::get(row[col + e]);
-    return v;
 }
 
 // Four adjacent computed values as an operand's parts, `lo` elements after the first for the small ones.

@@ -1,6 +1,7 @@
 // Gradients of the gated delta rule, the part that walks the chunks: from the
-// last to the first, a wave with 16 columns of dS, the gradient of the state, as
-// the forward walk has them of S.  Per chunk, dS being that of the state behind it,
+// last to the first, two waves with 16 columns of dS, the gradient of the state, as
+// the forward walk has them of S.  They exchange their halves of K dS, dN, and what
+// their tokens add to dS.  Per chunk, dS being that of the state behind it,
 //     dN = e^(gamma_C - gamma) K dS + scale P^T dY,  Z = T^T dN,  dV = dR = beta Z,
 //     dS' = e^gamma_C dS + scale Q^T e^gamma dY - K^T e^gamma dR.
 // dS of every chunk and Z go to memory for the kernel that takes the chunks'

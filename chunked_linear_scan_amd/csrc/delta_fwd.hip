@@ -1,7 +1,8 @@
 // Gated delta rule over whole sequences: the walk over the chunks.  Columns of the
-// state S [dk, dv] stay in registers and go through all chunks of a sequence; they do not
-// meet, so waves only share what is staged in LDS for them: the chunk's K, Q,
-// T - I, P and factors.  Per chunk
+// state S [dk, dv] stay in registers, 16 of them in two waves, and go through all
+// chunks of a sequence.  Columns do not meet: a workgroup's waves share the chunk's
+// K, Q, T - I, P and factors in LDS, and the two waves of the same columns exchange
+// their halves of K S and Q S, R, and N.  Per chunk
 //     R = beta (V - e^gamma K S),  N = R + (T - I) R,  Y = scale (e^gamma Q S + P N),
 //     S' = e^gamma_C S + K^T (e^(gamma_C - gamma) N)
 // with all computed operands in two parts: y, too, is off by its own rounding and little else (with one part of

@@ -15,9 +15,9 @@
 // leave as four adjacent values of a token, and the decays are factors of a lane.
 // All computed operands go in as two parts, so 16-bit gradients are off by their own rounding and little else.
 // Bound by memory: a chunk's states and corrections (192 KB of the 288 KB that it moves for 64 tokens, keys and values of 128)
-// are read once, 32 of dv at a time, past the caches: 4 x 2048 x 16 heads 150 us, 4.0 TB/s; through the caches 164; with the
-// products with S and with dS in two walks over dv as well 196.  LDS has K and those tiles, and Q and the pairs in the tiles'
-// place afterwards, so that two workgroups fit a compute unit.
+// are read once, 32 of dv at a time, past the caches: 4 x 2048 x 16 heads 152 us, 4.0 TB/s; through the caches 163 (with the
+// products with S and with dS in two walks over dv, a fifth longer).  LDS has K and those tiles, and Q and the pairs in the
+// tiles' place afterwards, so that two workgroups fit a compute unit.
 #include <hip/hip_runtime.h>
 
 #include "delta.hpp"
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(Mat<E>::kChunk * 4, Mat<E>::kSplit && DK <= 128 ? 2
         float v = 0.0f;
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            const f32x4 a = load4<E>(m, KTile::quad(i, 16 * t + 4 * g4), 1 << 30, true);
+            const f32x4 a = load4<E>(m + KTile::quad(i, 16 * t + 4 * g4));
 #pragma unroll
             for (int r = 0; r < 4; ++r) v = fmaf(a[r], x[t][r], v);
         }

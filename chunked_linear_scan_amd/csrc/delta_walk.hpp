@@ -1,17 +1,21 @@
-// What the forward and the backward walk over the chunks share.  A chunk's work
-// on a column of the state is one long chain of products, and of vector instructions on
-// their results, of which a wave issues one in 8.5 cycles: that chain's
-// latency bounds a walk, not any unit's rate.  So
-//   - two waves have 16 columns of a state between them, each the rows of one half of the
-//     keys' elements and the tokens of one half of a chunk.  Products with the state are sums of two halves, which the
-//     waves exchange through LDS, as they do what the other half's tokens add to the state: four
-//     meetings a chunk, and half the instructions between them;
-//   - four more waves load, and store what is not kept for the gradients, two chunks ahead;
+// What the forward and the backward walk over the chunks share.  A chunk's work on a
+// column of the state is one long chain of products, and of vector instructions on
+// their results, of which a wave issues one in 8.5 cycles: that chain's latency
+// bounds a walk, not any unit's rate.  So
+//   - two waves have 16 columns of a state between them, each the rows of one half
+//     of the keys' elements and the tokens of one half of a chunk.  Products with
+//     the state are sums of two halves, which the waves exchange through LDS, as
+//     they do what the other half's tokens add to the state: four meetings a chunk,
+//     and half the instructions between them;
+//   - four more waves load, and store what is not kept for the gradients, two
+//     chunks ahead;
 //   - operands are read from LDS a step before their products, and products are
 //     interleaved with vector instructions.
-// A workgroup has 32 columns: four computing waves, one to a SIMD, and four that load; or 16, and two.  A chunk of 64 tokens and
-// keys of 128 takes 1.7 us, 1.5 without its loads; with 16 columns 1.6.  (One wave to 16 columns: 1.95 us with two computing
-// waves to a workgroup, 2.3 with four, where their reads of LDS took 3200 cycles of the 5500.)
+// A workgroup has 32 columns: four computing waves, one to a SIMD, and four that
+// load; or 16, and two.  A chunk of 64 tokens and keys of 128 takes 2.0 us, with 16
+// columns 1.8 (0.2 more than with y's operands in one part each; then, one wave to
+// 16 columns took 1.95 us with two computing waves to a workgroup, and 2.3 with
+// four, where their reads of LDS took 3200 cycles of the 5500).
 #pragma once
 
 #include <type_traits>
@@ -31,13 +35,14 @@ __device__ __forceinline__ void interleave() {
         interleave<N - 1, V>();
     }
 }
+
 // A workgroup of TILES has 16 TILES columns: computing waves (16 (w / 2).. of the columns, half w % 2), then four that load.
 constexpr int walk_cols(int tiles) { return 16 * tiles; }
 constexpr int walk_threads(int tiles) { return 128 * tiles + 256; }
 
-// Calls f with the tiles of a walk's workgroups: two, or one, with the same rows of K, Q and matrices to load for half the columns,
-// where all of those have a compute unit of their own (1 x 32768 x 32 heads of 128: 842 us instead of 880; fp32 4096 x 8: 68
-// instead of 75).
+// Calls f with the tiles of a walk's workgroups: two, or one, with the same rows of K, Q and matrices to load for half
+// the columns, where all of those have a compute unit of their own (1 x 32768 x 32 heads of 128: 929 us instead of
+// 1020; fp32 3 x 1000 x 8, values of 72: 69 instead of 75).
 template <typename F>
 int by_tiles(const DeltaParams& p, F&& f) {
     const int64_t columns = int64_t(p.batch) * p.H * ((p.dv + 15) / 16);
@@ -369,8 +374,7 @@ __device__ __forceinline__ void load_state(f32x4 (&S)[KT], const float* from, in
         }
 }
 // The same for the gradients: rows of kpitch elements.  Past the caches, as all of it is written before any of it is read
-// (4 x 2048 x 16 heads of 128: the walks 121 and 136 -> 115 and 130 us, the gradients'
-// kernel, which reads it once, 165 -> 150).
+// (4 x 2048 x 16 heads of 128: the walks 128 and 135 -> 124 and 129 us, the gradients' kernel, which reads it once, 163 -> 152).
 template <int KT>
 __device__ __forceinline__ void keep_state(const f32x4 (&S)[KT], float* to, int64_t of, int n, int first, const DeltaParams& p) {
     const Buffer b = buffer(to + of * p.dv * p.kpitch, int64_t(p.dv) * p.kpitch * 4);

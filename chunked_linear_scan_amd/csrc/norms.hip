@@ -4,12 +4,17 @@
 //     unit(u) = u / sqrt(mean(u^2) + eps),  du = rstd (a - unit mean(a unit)), a the gradient of unit.
 // All are bound by memory: a row is read once, kept in registers between its sum
 // and its output, and written once.  8 adjacent values (one or two 16-byte vectors)
-// to a lane at a time; a row has 8 to 1024 lanes, as few as it needs in one run for the
-// gradients, which keep several arrays of a row (5461 x 6144 in 256 lanes of three runs: 174 us, in 1024 of one: 98), and two
-// or three runs otherwise, where barriers and the lanes behind a row's end cost more (1021 x 5120 in 1024 lanes of one run: 17 us,
-// in 256 of three: 10).  Workgroups walk over rows, so that w and s are read once (16384 x 4096: 102 us, 5.3 TB/s; one row to a
-// workgroup: 165).  The gradients of w and s are summed over the rows that a workgroup walks in its lanes, then over the
-// workgroups by a second launch in a fixed order.
+// to a lane at a time; a row has 8, 16, 64 or more lanes, up to 1024: one run of
+// them for the gradients of up to 8192 values, which keep several arrays of a row
+// (5461 x 6144 in 256 lanes of three runs: 174 us, in 1024 of one: 98), and up to
+// three otherwise, where barriers and the lanes behind a row's end cost more (1021
+// x 5120 in 1024 lanes of one run: 17 us, in 256 of three: 10).  Rows of 129 to 256
+// values leave half of their lanes or more without any (bf16 65536 x 256: 34 us,
+// 2.9 TB/s; gradients and their sums 60), and rows off 8 values go one element at a
+// time (16384 x 4095: 352 us, 4096: 103).  Workgroups walk over rows, so that w and
+// s are read once (16384 x 4096: 102 us, 5.3 TB/s; one row to a workgroup: 165).
+// The gradients of w and s are summed over the rows that a workgroup walks in its
+// lanes, then over the workgroups by a second launch in a fixed order.
 //
 //     bf16             forward          gradients           their sums over workgroups
 //     131072 x 128     19.4 us  5.2 TB/s  30.7 us  5.5 TB/s   4.7 us    gated_norm
@@ -74,8 +79,10 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int left, bool ve
         if (e < left) p[e] = E::put(v[e]);
 }
 
-// Where a lane has several runs of a row its gradients do not keep them all: they are read one at a time, and again, from
-// the cache, when the row's sum is there (gated_norm of 2048 x 16384: 157 us; all kept, and spilled: 286).
+// Where a lane has two runs of a row (more than 8192 values) its gradients do not keep both: they are read one at a
+// time, and again, from the cache, when the row's sum is there (gated_norm of 2048 x 16384 in bf16: 146 us; all kept: 286).
+// The factors and their gradients' sums stay in registers from row to row and do not fit the 128 that 1024 lanes have
+// each: up to 36 are spilled, of residual_norm's up to 192 (bf16 230 us, 1.8 TB/s; with the stream in fp32 269; fp32 259).
 template <int NV>
 __device__ __forceinline__ void again() {
     if constexpr (NV > 1) {

@@ -59,12 +59,12 @@ extern "C" {
  * |dh_final| to 4..8: any size of those gives the same bits behind the exponent,
  * but a gradient that grows to 8000 times the largest is not finite.
  * A value that is not finite reaches its head's outputs from the start of its
- * chunk on (and its gradients up to the end of its chunk).
+ * chunk on, one of dy its head's gradients up to the end of its chunk.
  *
  * heads is a multiple of kheads; dk is 1..256 and dv 1..65536
  * (SSD_ERR_UNSUPPORTED above).  SSD_ERR_SHAPE, too, for batch or heads above
- * 2^20, seqlen above 2^30, heads * dv (dv to whole vectors) or
- * kheads * 256 above 2^23, strides above 2^40, and where a launch would have 2^32 threads or more
+ * 2^20, seqlen above 2^30, heads * dv (dv to whole vectors) or kheads * 256 above
+ * 2^23, strides above 2^40, and where a launch would have 2^32 threads or more
  * (512 for each 32 of dv, head and sequence; 256 for each chunk, head and
  * sequence; with gradients and heads > kheads one for each element of q).
  */
