@@ -188,12 +188,13 @@ struct ChunkMats {
 // ---------------------------------------------------------------------------
 // powers of two in front of fp16 operands
 // ---------------------------------------------------------------------------
-// Two fp16 numbers hold 22 bits of what is 2^-3 and more, and of less what is left above 2^-25; past 65504 they hold nothing.
-// Gradients are as large as the loss makes them, often far below that, so the backward pass multiplies a head's gradients of
-// state, corrections and outputs by one power of two that brings the largest of scale dY and dh_final to 4..8, 2^13 below
-// the type's end, and divides what it writes by it: exactly, so gradients of 2^n dy are 2^n times those of dy.  (Without it
-// dg of dy about 1e-3 was 1.5e-4 off, of 1e-5 1.6e-2, and dh_final past 65504 gave NaN.)  dY itself goes in times another, at least 1, as
-// products of subnormal operands lose bits where the unit adds them up (1e-8 of the sums for dy of 2^-14, 7e-7 for 2^-18).
+// Two fp16 numbers hold 22 bits of what is 2^-3 and more, and of less what is left above 2^-25; past 65504 they hold
+// nothing.  Gradients are as large as the loss makes them, often far below that, so the backward pass multiplies a head's
+// gradients of states, corrections and outputs by one power of two that brings the largest of scale dY and dh_final to
+// 4..8, 2^13 below the type's end, and divides what it writes by it: exactly, so gradients of 2^n dy are 2^n times those
+// of dy.  (Without it dg of dy about 1e-3 was 1.5e-4 off, of 1e-5 1.6e-2, and dh_final past 65504 gave NaN.)  dY itself
+// goes in times another, at least 1, as products of subnormal operands lose bits where the unit adds them up (1e-8 of the
+// sums for dy of 2^-14, 7e-7 for 2^-18).
 template <typename E>
 constexpr bool kSized = std::is_same_v<E, ElemF16>;
 constexpr int kSizes = 64;  // at most, parts of a head that delta_size_kernel takes apart

@@ -51,13 +51,14 @@ extern "C" {
  * Tokens are taken gated_delta_chunk(dtype) at a time through matrix products.
  * States, their updates and all sums are fp32; with 16-bit elements a computed
  * operand of a product goes in as the sum of two numbers of that type (bf16: 16
- * bits in all).  With SSD_F16 such operands have that type's range.  States and
- * corrections of values go in at their own size: what they reach is not finite
- * where they are past 65504, and they are held to 2^-25 at best, so below 2^-3
- * they have fewer good bits than 22.  Gradients go in times a power of two, one
- * for each sequence and head, that takes the largest of |scale dy| and
- * |dh_final| to 4..8: any size of those gives the same bits behind the exponent,
- * but a gradient that grows to 8000 times the largest is not finite.
+ * bits in all).  With SSD_F16 such operands have that type's range.  States,
+ * corrections of values and products of a chunk's keys and queries go in at their
+ * own size: what they reach is not finite where they are past 65504, and they are
+ * held to 2^-25 at best, so below 2^-3 they have fewer good bits than 22.
+ * Gradients go in times a power of two, one for each sequence and head, that takes
+ * the largest of |scale dy| and |dh_final| to 4..8: any size of those gives the
+ * same bits behind the exponent, but a gradient of a state or of corrections that
+ * grows to 8000 times the largest is not finite.
  * A value that is not finite reaches its head's outputs from the start of its
  * chunk on, one of dy its head's gradients up to the end of its chunk.
  *
